@@ -242,6 +242,17 @@ tp_status launch_gqa_attention_bwd(const void* qkv, const void* o, const float* 
                                    int heads, int kv_heads, int N, int d, int causal, tp_dtype dt,
                                    cudaStream_t st);
 
+// paged key/value cache (kv_cache.cu); page size 2^ps_log2
+constexpr int64_t kKvMaxRequests = 8192;  // requests of one tables call (shared memory)
+tp_status launch_kv_tables(const int32_t* ctx, const int32_t* add, const int32_t* free_pages,
+                           int n_free, const int32_t* head, int32_t* head_out, int32_t* table,
+                           int32_t* total, int32_t* cu, int32_t* slots, int32_t* pos,
+                           int32_t* counts, int64_t R, int64_t T, int ps_log2, int max_pages,
+                           cudaStream_t st);
+tp_status launch_kv_append(const void* qkv, const int32_t* slots, void* kc, void* vc, int64_t T,
+                           int d, int Hkv, int hkv, int hq, int rep, int64_t W, int64_t n_slots,
+                           int ps_log2, tp_dtype dt, cudaStream_t st);
+
 // vocabulary-parallel embedding / cross-entropy and AdamW (vocab.cu)
 tp_status launch_vocab_embed_fwd(const int32_t* ids, const void* E, void* x, int64_t M, int64_t v,
                                  int64_t h, int N, tp_dtype dt, cudaStream_t st);

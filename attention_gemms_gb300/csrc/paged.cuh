@@ -1,0 +1,278 @@
+// Work division of the paged attention kernels (paged_attention.cu and the kernels beside
+// it): which request, key/value head, query rows and keys each CTA takes.
+//
+// The work of one call is a line of key tiles. Request r with n new tokens has, for each
+// of Hv head groups, ceil(n / tpu) units of tpu tokens x Gv query heads that share a
+// key/value head; a unit's tiles are the KT-key tiles that its last token may see (at
+// least one, so that rows that see no key are written too). CTA i of g takes tiles
+// [i total / g, (i + 1) total / g) of the line, whatever units they fall into: every CTA
+// gets the same number of tiles for any mix of lengths, and a long context is split over
+// the whole GPU without a setting. A unit that lies in one CTA is finished there; else
+// each CTA leaves its rows' (maximum, sum, unnormalised output) in its slot of the
+// workspace and the combine kernel joins them in key order. At most one unit begins and
+// one ends inside other CTAs' ranges, so two slots per CTA are enough for any lengths.
+//
+// Lengths live on the device (a captured step replays with new ones), so each CTA finds
+// its own place: one pass over the lengths with a block-wide scan, and within a request
+// by the closed form of the tile counts' sum. Nothing is planned ahead, so no plan can go
+// stale. Lengths and page ids are not trusted: rows end at T, keys at the table's width,
+// and a page id outside the cache is a page of masked keys.
+#pragma once
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "internal.h"
+
+namespace tp {
+
+struct PagedParams {
+  const void *qkv, *kc, *vc;
+  const int32_t *table, *total, *cu;
+  void* o;
+  float* lse;              // (H, T), may be null
+  float* part;             // partial results: per slot m (rows), l (rows), O (rows, d)
+  struct PagedRec* rec;    // one per CTA
+  int64_t T;               // rows of qkv, o, lse
+  int64_t ldq, S;          // qkv row pitch, shard block width (elements)
+  int R, H, Hkv, G, hq;    // G = H / Hkv; hq query heads per shard block
+  int n_pages, ps_log2, max_pages;
+  int causal;
+  float scale_log2;        // log2(e) / sqrt(d)
+  int hs, Gv, Hv;          // head groups per key/value head, heads per group, Hkv * hs
+  int tpu, kt_log2;        // tokens per unit, keys per tile
+  int only_rows;           // > 0: only requests of at most that many rows per head group;
+                           // < 0: only requests of more than -only_rows
+};
+
+// What CTA i left in its two slots: slot 0 the piece of a unit that began in an earlier
+// CTA (head: 1 the unit goes on after this CTA, 2 it ends here), slot 1 the first piece of
+// a unit that goes on after this CTA (tail = 1; r, vh, u name it). 0: nothing.
+struct PagedRec {
+  int head, tail, r, vh, u;
+};
+
+#ifdef __CUDACC__
+
+struct PagedReq {
+  int row0, n, rows, total, kv_end;  // rows: those below T; kv_end: keys the table can hold
+};
+
+__device__ __forceinline__ PagedReq paged_req(const PagedParams& p, int r) {
+  PagedReq q;
+  const int c0 = p.cu[r], c1 = p.cu[r + 1];
+  q.row0 = c0;
+  q.n = (c0 >= 0 && c1 > c0) ? c1 - c0 : 0;
+  q.rows = static_cast<int>(min(static_cast<int64_t>(q.n), max(p.T - c0, static_cast<int64_t>(0))));
+  q.total = max(p.total[r], 0);
+  q.kv_end = static_cast<int>(
+      min(static_cast<int64_t>(q.total), static_cast<int64_t>(p.max_pages) << p.ps_log2));
+  const int64_t gr = static_cast<int64_t>(q.rows) * p.Gv;
+  if (p.only_rows > 0 ? gr > p.only_rows : (p.only_rows < 0 && gr <= -p.only_rows)) q.rows = 0;
+  return q;
+}
+
+__device__ __forceinline__ int paged_units(const PagedParams& p, const PagedReq& q) {
+  return (q.rows + p.tpu - 1) / p.tpu;
+}
+
+// first key that no row of unit u sees
+__device__ __forceinline__ int paged_unit_kend(const PagedParams& p, const PagedReq& q, int u) {
+  if (!p.causal) return q.kv_end;
+  const int64_t tokens = min(static_cast<int64_t>(u + 1) * p.tpu, static_cast<int64_t>(q.rows));
+  const int64_t end = static_cast<int64_t>(q.total) - q.n + tokens;
+  return static_cast<int>(max(static_cast<int64_t>(0), min(end, static_cast<int64_t>(q.kv_end))));
+}
+__device__ __forceinline__ int paged_unit_tiles(const PagedParams& p, const PagedReq& q, int u) {
+  return max(1, static_cast<int>((static_cast<int64_t>(paged_unit_kend(p, q, u)) +
+                                  (1 << p.kt_log2) - 1) >> p.kt_log2));
+}
+
+// sum over i < n of floor((a i + b) / m), b >= 0 (the Euclid-like recurrence on the
+// lattice points under a line)
+__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+  int64_t ans = 0;
+  while (n > 0) {
+    if (a >= m) {
+      ans += (n - 1) * n / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      ans += n * (b / m);
+      b %= m;
+    }
+    const int64_t y = a * n + b;
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const int64_t t = m;
+    m = a;
+    a = t;
+  }
+  return ans;
+}
+
+// tiles of the first `u` units of a request's head group
+__device__ __forceinline__ int64_t paged_prefix(const PagedParams& p, const PagedReq& q, int u) {
+  if (u <= 0) return 0;
+  if (u == 1) return paged_unit_tiles(p, q, 0);
+  const int units = paged_units(p, q);
+  const int c = q.total - q.n;
+  if (!p.causal) return static_cast<int64_t>(u) * paged_unit_tiles(p, q, 0);
+  if (c < 0 || q.kv_end < q.total) {  // tokens outside the cache: no closed form, rare
+    int64_t s = 0;
+    for (int i = 0; i < u; ++i) s += paged_unit_tiles(p, q, i);
+    return s;
+  }
+  const int full = min(u, units - 1);  // the last unit may hold fewer tokens
+  const int64_t kt = static_cast<int64_t>(1) << p.kt_log2;
+  int64_t s = floor_sum(full, kt, p.tpu, static_cast<int64_t>(c) + p.tpu + kt - 1);
+  if (u > full) s += paged_unit_tiles(p, q, units - 1);
+  return s;
+}
+
+// A CTA's walk over its tiles: segment by segment, a segment being tiles [lo, hi) of unit u.
+struct PagedWalk {
+  int64_t left;  // tiles left after the current segment
+  PagedReq q;
+  int r, vh, u, units, tiles, lo, hi;
+
+  __device__ __forceinline__ bool valid() const { return hi > lo; }
+  __device__ __forceinline__ void take(const PagedParams& p, int first) {
+    tiles = paged_unit_tiles(p, q, u);
+    lo = first;
+    hi = static_cast<int>(min(static_cast<int64_t>(tiles), lo + left));
+    left -= hi - lo;
+  }
+  __device__ __forceinline__ void next(const PagedParams& p) {
+    if (left <= 0) {
+      lo = hi = 0;
+      return;
+    }
+    if (++u >= units) {
+      u = 0;
+      if (++vh >= p.Hv) {
+        vh = 0;
+        do {
+          if (++r >= p.R) {  // lengths changed under the call: nothing left
+            left = 0;
+            lo = hi = 0;
+            return;
+          }
+          q = paged_req(p, r);
+        } while (q.rows == 0);
+        units = paged_units(p, q);
+      }
+    }
+    take(p, 0);
+  }
+};
+
+// Scratch of the schedule (shared memory).
+struct PagedSched {
+  int64_t warp_sum[32];
+  int64_t first, x, count;  // first tile in request r, tiles of this CTA
+  int r, vh, u, tile;
+};
+
+// Every thread of the CTA (blockDim.x a multiple of 32, at most 1024) calls it; returns
+// the CTA's first segment. Two block-wide barriers.
+__device__ __forceinline__ PagedWalk paged_schedule(const PagedParams& p, PagedSched& sc, int cta,
+                                                    int ctas) {
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.R + nt - 1) / nt;
+  const int r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
+  int64_t sum = 0;
+  for (int r = r0; r < r1; ++r) {
+    const PagedReq q = paged_req(p, r);
+    if (q.rows > 0) sum += p.Hv * paged_prefix(p, q, paged_units(p, q));
+  }
+  int64_t inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xFFFFFFFFu, inc, o);
+    if (lane >= o) inc += v;
+  }
+  if (lane == 31) sc.warp_sum[warp] = inc;
+  if (tid == 0) sc.r = -1;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+  for (int w = 0; w < (nt >> 5); ++w) {
+    const int64_t v = sc.warp_sum[w];
+    before += w < warp ? v : 0;
+    total += v;
+  }
+  const int64_t begin = total * cta / ctas, end = total * (cta + 1) / ctas;
+  const int64_t mine = before + inc - sum;  // tiles before this thread's requests
+  if (end > begin && begin >= mine && begin < mine + sum) {
+    int64_t x = begin - mine;
+    int r = r0;
+    for (; r < r1; ++r) {
+      const PagedReq q = paged_req(p, r);
+      const int64_t w = q.rows > 0 ? p.Hv * paged_prefix(p, q, paged_units(p, q)) : 0;
+      if (x < w) break;
+      x -= w;
+    }
+    sc.r = r;
+    sc.x = x;
+  }
+  __syncthreads();
+  PagedWalk w;
+  w.lo = w.hi = 0;
+  w.left = end - begin;
+  w.r = sc.r;
+  if (w.left <= 0 || w.r < 0 || w.r >= p.R) {
+    w.left = 0;
+    return w;
+  }
+  // every warp finds the unit on its own (32 candidates at a time)
+  w.q = paged_req(p, w.r);
+  w.units = paged_units(p, w.q);
+  const int64_t per_head = paged_prefix(p, w.q, w.units);
+  int64_t x = sc.x;
+  w.vh = static_cast<int>(x / per_head);
+  x -= w.vh * per_head;
+  int lo = 0, hi = w.units;  // prefix(lo) <= x < prefix(hi)
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32;
+    const int cand = min(lo + lane * step, hi);
+    const bool le = cand < hi && paged_prefix(p, w.q, cand) <= x;
+    const int k = __popc(__ballot_sync(0xFFFFFFFFu, le)) - 1;  // lane 0 always holds
+    const int base = lo;
+    lo = base + k * step;
+    hi = min(hi, base + (k + 1) * step);
+  }
+  w.u = lo;
+  w.take(p, static_cast<int>(x - paged_prefix(p, w.q, lo)));
+  return w;
+}
+
+// column of query head t in a qkv row
+template <int D>
+__device__ __forceinline__ int64_t paged_qcol(const PagedParams& p, int t) {
+  const int i = t / p.hq;
+  return i * p.S + static_cast<int64_t>(t - i * p.hq) * D;
+}
+
+// cache row (of D elements) of key `key` of the request whose table row is `tab`, head j;
+// -1 when its page id is not one of the cache's
+__device__ __forceinline__ int64_t paged_row(const PagedParams& p, const int32_t* tab, int j,
+                                             int key) {
+  const int page = tab[key >> p.ps_log2];
+  if (page < 0 || page >= p.n_pages) return -1;
+  return (((static_cast<int64_t>(page) * p.Hkv + j) << p.ps_log2)) + (key & ((1 << p.ps_log2) - 1));
+}
+
+#endif  // __CUDACC__
+
+// kernels (bf16 / fp32, CUDA cores) and the join of the partial results
+constexpr int kPagedMaxCtas = 304;
+tp_status launch_paged_simt(PagedParams p, int d, bool wide, tp_dtype dt, cudaStream_t st);
+// unit_rows: rows of a slot; tile_rows: rows of its tiles (whole tokens each)
+tp_status launch_paged_combine(const PagedParams& p, int d, int unit_rows, int tile_rows, int ctas,
+                               tp_dtype dt, cudaStream_t st);
+// units of unit_rows rows in tiles of tile_rows, 2^kt_log2 keys per tile
+void paged_set_units(PagedParams& p, int tile_rows, int unit_rows, int kt_log2);
+size_t paged_workspace_bytes(int d, tp_dtype dt);
+
+}  // namespace tp

@@ -1,0 +1,364 @@
+// Grouped-query attention of each request's new tokens over a paged key/value cache, on
+// CUDA cores (fp32, and the reference path of every shape), and the join of the partial
+// results of all paged kernels. The division of the work is paged.cuh's.
+//
+//   o_i = sum_k softmax_k(q_i . K_k / sqrt(d)) V_k over the keys that row i sees, in one
+//   pass: for each tile of keys the scores s (base 2), the running maximum m and sum l,
+//     m' = max(m, max s), w = 2^(m - m'), l' = w l + sum 2^(s - m'), O' = w O + 2^(s - m') V,
+//   and o = O / l, lse = ln 2 (m + log2 l). Statistics and O are fp32.
+// Pieces (m_j, l_j, O_j) of one row join the same way: M = max m_j, o = sum 2^(m_j - M) O_j
+// / sum 2^(m_j - M) l_j, in the order of their keys, so a call's result does not depend on
+// which CTA finished first.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "internal.h"
+#include "paged.cuh"
+
+namespace tp {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kKT = 64;  // keys per tile
+
+template <typename T>
+__device__ __forceinline__ void load4(const T* src, float (&f)[4]);
+template <>
+__device__ __forceinline__ void load4<float>(const float* src, float (&f)[4]) {
+  const float4 v = *reinterpret_cast<const float4*>(src);
+  f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
+}
+template <>
+__device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16* src, float (&f)[4]) {
+  const uint2 v = *reinterpret_cast<const uint2*>(src);
+  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.x));
+  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.y));
+  f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
+}
+__device__ __forceinline__ void store4(float* dst, const float (&f)[4]) {
+  *reinterpret_cast<float4*>(dst) = make_float4(f[0], f[1], f[2], f[3]);
+}
+// the output's one rounding: to nearest
+__device__ __forceinline__ void store4(__nv_bfloat16* dst, const float (&f)[4]) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(f[0], f[1]), b = __floats2bfloat162_rn(f[2], f[3]);
+  *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                              *reinterpret_cast<const uint32_t*>(&b));
+}
+
+// Row i of a unit (tiles of tile_rows rows, each of whole tokens): its token and query
+// head; false when the row is none.
+__device__ __forceinline__ bool unit_row(const PagedParams& p, const PagedReq& q, int u, int vh,
+                                         int tile_rows, int i, int* token, int* head) {
+  const int tpt = tile_rows / p.Gv;
+  const int tile = i / tile_rows, x = i - tile * tile_rows;
+  const int tt = x / p.Gv, hh = x - tt * p.Gv;
+  const int j = vh / p.hs, g = (vh - j * p.hs) * p.Gv + hh;
+  *token = u * p.tpu + tile * tpt + tt;
+  *head = j * p.G + g;
+  return tt < tpt && g < p.G && *token < q.rows;
+}
+
+// RT rows per unit: 16 for a token or a few, 64 for chunks (a key tile is then read from
+// L2 once per 64 rows instead of 16).
+template <typename T, int D, int RT>
+struct SimtLayout {
+  static constexpr int LD = D + 4;  // padded row: float4 accesses of 8 rows hit 32 banks
+  static constexpr int kQ = 0, kK = RT * LD, kV = kK + kKT * LD, kP = kV + kKT * LD,
+                       kStat = kP + RT * (kKT + 4), kEnd = kStat + 3 * RT + kKT;
+  static constexpr int kSmem = kEnd * 4;
+};
+
+template <typename T, int D, int RT>
+__global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams p) {
+  using Lay = SimtLayout<T, D, RT>;
+  constexpr int LD = Lay::LD, PLD = kKT + 4;
+  extern __shared__ __align__(16) float sm[];
+  float *Qs = sm + Lay::kQ, *Ks = sm + Lay::kK, *Vs = sm + Lay::kV, *Ps = sm + Lay::kP;
+  float *ms = sm + Lay::kStat, *ls = ms + RT, *ws = ls + RT;
+  int* ok = reinterpret_cast<int*>(ws + RT);  // key is in the cache
+  __shared__ PagedSched sc;
+  pdl_wait();  // the previous kernel's results are complete and visible
+  pdl_trigger();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // scores: RT / RY rows x 64 / KX keys per thread; output: D / 4 column groups
+  constexpr int KX = RT == 16 ? 32 : 16, RY = kThreads / KX, SR = RT / RY, SK = kKT / KX;
+  constexpr int CG = D / 4, OY = (kThreads / CG) < RT ? (kThreads / CG) : RT, OR = RT / OY;
+  const int kx = tid % KX, ry = tid / KX, cg = tid % CG, oy = tid / CG;
+  PagedRec rec{0, 0, 0, 0, 0};
+  PagedWalk w = paged_schedule(p, sc, blockIdx.x, gridDim.x);
+  for (; w.valid(); w.next(p)) {
+    const int j = w.vh / p.hs;
+    const int32_t* tab = p.table + static_cast<int64_t>(w.r) * p.max_pages;
+    const int kend = paged_unit_kend(p, w.q, w.u);
+    __syncthreads();  // the previous segment's readers are done
+    for (int e = tid; e < RT * CG; e += kThreads) {
+      const int i = e / CG, c = (e - i * CG) * 4;
+      int token, head;
+      float f[4] = {0.f, 0.f, 0.f, 0.f};
+      if (unit_row(p, w.q, w.u, w.vh, RT, i, &token, &head)) {
+        load4(static_cast<const T*>(p.qkv) + (static_cast<int64_t>(w.q.row0) + token) * p.ldq +
+                  paged_qcol<D>(p, head) + c, f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) f[k] *= p.scale_log2;
+      }
+      store4(Qs + i * LD + c, f);
+    }
+    for (int i = tid; i < RT; i += kThreads) {
+      ms[i] = -INFINITY;
+      ls[i] = 0.0f;
+    }
+    float acc[OR][4];
+#pragma unroll
+    for (int i = 0; i < OR; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[i][k] = 0.0f;
+    for (int tile = w.lo; tile < w.hi; ++tile) {
+      const int k0 = tile * kKT;
+      __syncthreads();
+      for (int e = tid; e < kKT * CG; e += kThreads) {
+        const int k = e / CG, c = (e - k * CG) * 4;
+        float fk[4] = {0.f, 0.f, 0.f, 0.f}, fv[4] = {0.f, 0.f, 0.f, 0.f};
+        const int64_t row = k0 + k < kend ? paged_row(p, tab, j, k0 + k) : -1;
+        if (row >= 0) {
+          load4(static_cast<const T*>(p.kc) + row * D + c, fk);
+          load4(static_cast<const T*>(p.vc) + row * D + c, fv);
+        }
+        store4(Ks + k * LD + c, fk);
+        store4(Vs + k * LD + c, fv);
+        if (c == 0) ok[k] = row >= 0;
+      }
+      __syncthreads();
+      {
+        float s[SR][SK];
+#pragma unroll
+        for (int a = 0; a < SR; ++a)
+#pragma unroll
+          for (int b = 0; b < SK; ++b) s[a][b] = 0.0f;
+#pragma unroll 4
+        for (int c = 0; c < D; c += 4) {
+          float4 kv[SK];
+#pragma unroll
+          for (int b = 0; b < SK; ++b)
+            kv[b] = *reinterpret_cast<const float4*>(Ks + (kx + b * KX) * LD + c);
+#pragma unroll
+          for (int a = 0; a < SR; ++a) {
+            const float4 q = *reinterpret_cast<const float4*>(Qs + (ry + a * RY) * LD + c);
+#pragma unroll
+            for (int b = 0; b < SK; ++b)
+              s[a][b] += q.x * kv[b].x + q.y * kv[b].y + q.z * kv[b].z + q.w * kv[b].w;
+          }
+        }
+#pragma unroll
+        for (int a = 0; a < SR; ++a) {
+          const int i = ry + a * RY;
+          // keys the row's token sees: all, or up to its own position
+          const int64_t lim = p.causal ? static_cast<int64_t>(w.q.total) - w.q.n + w.u * p.tpu +
+                                             i / p.Gv + 1
+                                       : w.q.kv_end;
+#pragma unroll
+          for (int b = 0; b < SK; ++b) {
+            const int k = kx + b * KX;
+            Ps[i * PLD + k] = (ok[k] && k0 + k < lim) ? s[a][b] : -INFINITY;
+          }
+        }
+      }
+      __syncthreads();
+      for (int i = warp; i < RT; i += kThreads / 32) {
+        const float a = Ps[i * PLD + lane], b = Ps[i * PLD + lane + 32];
+        float mx = fmaxf(a, b);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
+        const float m0 = ms[i], m1 = fmaxf(m0, mx), mu = m1 == -INFINITY ? 0.0f : m1;
+        const float ea = exp2f(a - mu), eb = exp2f(b - mu);
+        Ps[i * PLD + lane] = ea;
+        Ps[i * PLD + lane + 32] = eb;
+        float sum = ea + eb;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        __syncwarp();
+        if (lane == 0) {
+          const float wt = exp2f(m0 - mu);
+          ws[i] = wt;
+          ls[i] = ls[i] * wt + sum;
+          ms[i] = m1;
+        }
+      }
+      __syncthreads();
+      if (oy < OY) {
+#pragma unroll
+        for (int i = 0; i < OR; ++i) {
+          const float wt = ws[oy + i * OY];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[i][k] *= wt;
+        }
+#pragma unroll 4
+        for (int k = 0; k < kKT; ++k) {
+          const float4 v = *reinterpret_cast<const float4*>(Vs + k * LD + cg * 4);
+#pragma unroll
+          for (int i = 0; i < OR; ++i) {
+            const float e = Ps[(oy + i * OY) * PLD + k];
+            acc[i][0] += e * v.x;
+            acc[i][1] += e * v.y;
+            acc[i][2] += e * v.z;
+            acc[i][3] += e * v.w;
+          }
+        }
+      }
+    }
+    const bool begins = w.lo == 0, ends = w.hi == w.tiles;
+    if (!begins) rec.head = ends ? 2 : 1;
+    if (begins && !ends) rec.tail = 1, rec.r = w.r, rec.vh = w.vh, rec.u = w.u;
+    float* slot = p.part + static_cast<int64_t>(2 * blockIdx.x + (begins ? 1 : 0)) * RT * (D + 2);
+    if (oy < OY) {
+#pragma unroll
+      for (int i = 0; i < OR; ++i) {
+        const int row = oy + i * OY;
+        int token, head;
+        if (!unit_row(p, w.q, w.u, w.vh, RT, row, &token, &head)) continue;
+        if (begins && ends) {
+          const float l = ls[row], inv = l > 0.0f ? 1.0f / l : 0.0f;
+          float f[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) f[k] = acc[i][k] * inv;
+          const int64_t t = static_cast<int64_t>(w.q.row0) + token;
+          store4(static_cast<T*>(p.o) + t * p.H * D + static_cast<int64_t>(head) * D + cg * 4, f);
+          if (cg == 0 && p.lse)
+            p.lse[head * p.T + t] = l > 0.0f ? (ms[row] + log2f(l)) * 0.6931471805599453f : -INFINITY;
+        } else {
+          store4(slot + 2 * RT + row * D + cg * 4, acc[i]);
+          if (cg == 0) {
+            slot[row] = ms[row];
+            slot[RT + row] = ls[row];
+          }
+        }
+      }
+    }
+  }
+  if (tid == 0) p.rec[blockIdx.x] = rec;
+}
+
+// CTA i joins the unit whose first piece is CTA i's tail: that piece, then the heads of the
+// following CTAs up to the one where the unit ends. Thread: one row, 4 columns.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedParams p,
+                                                                 const int unit_rows,
+                                                                 const int tile_rows) {
+  __shared__ int last;
+  pdl_wait();  // the previous kernel's results are complete and visible
+  pdl_trigger();
+  const int i = blockIdx.x, n = gridDim.x, tid = threadIdx.x;
+  const PagedRec rec = p.rec[i];
+  if (!rec.tail) return;
+  if (tid == 0) last = n;
+  __syncthreads();
+  for (int k = i + 1 + tid; k < n; k += kThreads)
+    if (p.rec[k].head == 2) atomicMin(&last, k);
+  __syncthreads();
+  const int end = min(last, n - 1);
+  const PagedReq q = paged_req(p, rec.r);
+  const int64_t floats = static_cast<int64_t>(unit_rows) * (D + 2);
+  auto slot_of = [&](int k) { return p.part + (2 * static_cast<int64_t>(k) + (k == i ? 1 : 0)) * floats; };
+  constexpr int CG = D / 4;
+  for (int e = blockIdx.y * kThreads + tid; e < unit_rows * CG; e += kThreads * gridDim.y) {
+    const int row = e / CG, c = (e - row * CG) * 4;
+    int token, head;
+    if (!unit_row(p, q, rec.u, rec.vh, tile_rows, row, &token, &head)) continue;
+    float m = -INFINITY, l = 0.0f, f[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int k = i; k <= end; ++k) {
+      if (k != i && p.rec[k].head == 0) continue;  // a CTA without tiles
+      const float* s = slot_of(k);
+      const float mk = s[row], lk = s[unit_rows + row];
+      float ok[4];
+      load4(s + 2 * unit_rows + row * D + c, ok);
+      const float m1 = fmaxf(m, mk), mu = m1 == -INFINITY ? 0.0f : m1;
+      const float w0 = exp2f(m - mu), w1 = exp2f(mk - mu);
+      l = l * w0 + lk * w1;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) f[x] = f[x] * w0 + ok[x] * w1;
+      m = m1;
+    }
+    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) f[x] *= inv;
+    const int64_t t = static_cast<int64_t>(q.row0) + token;
+    store4(static_cast<T*>(p.o) + t * p.H * D + static_cast<int64_t>(head) * D + c, f);
+    if (c == 0 && p.lse)
+      p.lse[head * p.T + t] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  }
+}
+
+template <typename T, int D>
+tp_status combine_t(const PagedParams& p, int unit_rows, int tile_rows, int ctas, cudaStream_t st) {
+  const dim3 grid(ctas, std::max(1, unit_rows * (D / 4) / (4 * kThreads)));
+  TP_CUDA_TRY(launch_kernel(paged_combine_kernel<T, D>, grid, dim3(kThreads), 0, st, p, unit_rows,
+                            tile_rows));
+  count_launch();
+  return TP_OK;
+}
+
+template <typename T, int D, int RT>
+tp_status simt_t(PagedParams& p, cudaStream_t st) {
+  using Lay = SimtLayout<T, D, RT>;
+  paged_set_units(p, RT, RT, 6);
+  static std::atomic<uint64_t> attr_set{0};
+  if (needs_setup(attr_set)) {
+    TP_CUDA_TRY(cudaFuncSetAttribute(paged_simt_kernel<T, D, RT>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kSmem));
+    mark_device(attr_set);
+  }
+  const int ctas = std::min(kPagedMaxCtas, device_sm_count() * (Lay::kSmem <= 100 * 1024 ? 2 : 1));
+  TP_CUDA_TRY(launch_kernel(paged_simt_kernel<T, D, RT>, dim3(ctas), dim3(kThreads),
+                            static_cast<size_t>(Lay::kSmem), st, p));
+  count_launch();
+  return launch_paged_combine(p, D, RT, RT, ctas, sizeof(T) == 2 ? TP_BF16 : TP_F32, st);
+}
+
+template <typename T>
+tp_status simt_d(PagedParams& p, int d, bool wide, cudaStream_t st) {
+  switch (d) {
+    case 16: return wide ? simt_t<T, 16, 64>(p, st) : simt_t<T, 16, 16>(p, st);
+    case 32: return wide ? simt_t<T, 32, 64>(p, st) : simt_t<T, 32, 16>(p, st);
+    case 64: return wide ? simt_t<T, 64, 64>(p, st) : simt_t<T, 64, 16>(p, st);
+    case 128: return wide ? simt_t<T, 128, 64>(p, st) : simt_t<T, 128, 16>(p, st);
+  }
+  return fail(TP_ERR_SHAPE, "head_dim must be 16, 32, 64 or 128");
+}
+
+}  // namespace
+
+tp_status launch_paged_simt(PagedParams p, int d, bool wide, tp_dtype dt, cudaStream_t st) {
+  return dt == TP_BF16 ? simt_d<__nv_bfloat16>(p, d, wide, st) : simt_d<float>(p, d, wide, st);
+}
+
+tp_status launch_paged_combine(const PagedParams& p, int d, int unit_rows, int tile_rows, int ctas,
+                               tp_dtype dt, cudaStream_t st) {
+  auto go = [&](auto dim) -> tp_status {
+    constexpr int D = decltype(dim)::value;
+    return dt == TP_BF16 ? combine_t<__nv_bfloat16, D>(p, unit_rows, tile_rows, ctas, st)
+                         : combine_t<float, D>(p, unit_rows, tile_rows, ctas, st);
+  };
+  switch (d) {
+    case 16: return go(std::integral_constant<int, 16>{});
+    case 32: return go(std::integral_constant<int, 32>{});
+    case 64: return go(std::integral_constant<int, 64>{});
+    default: return go(std::integral_constant<int, 128>{});
+  }
+}
+
+void paged_set_units(PagedParams& p, int tile_rows, int unit_rows, int kt_log2) {
+  p.hs = (p.G + tile_rows - 1) / tile_rows;
+  p.Gv = (p.G + p.hs - 1) / p.hs;
+  p.Hv = p.Hkv * p.hs;
+  p.tpu = tile_rows / p.Gv * (unit_rows / tile_rows);
+  p.kt_log2 = kt_log2;
+}
+
+size_t paged_workspace_bytes(int d, tp_dtype) {
+  return align_up(kPagedMaxCtas * sizeof(PagedRec), 256) +
+         static_cast<size_t>(kPagedMaxCtas) * 2 * 64 * (d + 2) * 4;
+}
+
+}  // namespace tp

@@ -159,6 +159,14 @@ _SIGS = {
                                                _ST, _ST, _P, _SZ, _P]),
     "tp_gqa_attn_proj_bwd": (_ST, [_P] * 16 + [_I64, _I64, _I64, _I32, _I32, _I32, ctypes.c_int,
                                                _ST, _ST, _P, _SZ, _P]),
+    "tp_kv_tables": (_ST, [_P] * 3 + [_I64] + [_P] * 8 + [_I64] * 4 + [_P]),
+    "tp_kv_append": (_ST, [_P] * 4 + [_I64, _I64, _I32, _I32, _I32, _I64, _I64, _ST, _P]),
+    "tp_gqa_paged_attention_workspace_size": (_SZ, [_I64, _I32, _I32, _I32, _ST]),
+    "tp_gqa_paged_attention_fwd": (_ST, [_P] * 8 + [_I64, _I64, _I64, _I32, _I32, _I32] +
+                                   [_I64] * 4 + [ctypes.c_int, _ST, _P, _SZ, _P]),
+    "tp_gqa_paged_workspace_size": (_SZ, [_I64, _I64, _I32, _I32, _I32, _ST, _ST]),
+    "tp_gqa_paged_attn_proj_fwd": (_ST, [_P] * 18 + [_I64, _I64, _I64, _I32, _I32, _I32] +
+                                   [_I64] * 4 + [ctypes.c_int, _ST, _ST, _P, _SZ, _P]),
     "tp_sp_mlp_fwd": (_ST, [_P] * 13 + [_I64, _I64, _I64, _I32, _ST, _ST, _ST, _P, _SZ, _P]),
     "tp_sp_mlp_bwd": (_ST, [_P] * 20 + [_I64, _I64, _I64, _I32, _ST, _ST, _ST, _P, _SZ, _P]),
     "tp_layer_fwd": (_ST, [_P, ctypes.POINTER(LayerWeights), ctypes.POINTER(LayerSaved), _P, _I64,
@@ -380,6 +388,51 @@ def tp_gqa_attn_proj_bwd(x, gamma, Wqkv, Wo, xn, mean, rstd, qkv, o, lse, dout, 
                                                           dWqkv, dWo)],
                                       b, s, h, n_heads, n_kv_heads, N, int(causal), int(dtype),
                                       int(mode), _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def tp_kv_tables(ctx_lens, new_lens, free_pages, n_free, free_head, free_head_out, block_table,
+                 total_lens, cu_new, slots, positions, counts, R, T, page_size, max_pages,
+                 stream=None):
+    _check(lib().tp_kv_tables(_ptr(ctx_lens), _ptr(new_lens), _ptr(free_pages), n_free,
+                              _ptr(free_head), _ptr(free_head_out), _ptr(block_table),
+                              _ptr(total_lens), _ptr(cu_new), _ptr(slots), _ptr(positions),
+                              _ptr(counts), R, T, page_size, max_pages, _stream(stream)))
+
+
+def tp_kv_append(qkv, slots, kcache, vcache, T, h, n_heads, n_kv_heads, N, n_pages, page_size,
+                 dtype, stream=None):
+    _check(lib().tp_kv_append(_ptr(qkv), _ptr(slots), _ptr(kcache), _ptr(vcache), T, h, n_heads,
+                              n_kv_heads, N, n_pages, page_size, int(dtype), _stream(stream)))
+
+
+def tp_gqa_paged_attention_workspace_size(h, n_heads, n_kv_heads, N, dtype):
+    return int(lib().tp_gqa_paged_attention_workspace_size(h, n_heads, n_kv_heads, N, int(dtype)))
+
+
+def tp_gqa_paged_attention_fwd(qkv, kcache, vcache, block_table, total_lens, cu_new, o, lse, T, R,
+                               h, n_heads, n_kv_heads, N, n_pages, page_size, max_pages, max_new,
+                               causal, dtype, ws, ws_bytes, stream=None):
+    _check(lib().tp_gqa_paged_attention_fwd(*[_ptr(t) for t in (qkv, kcache, vcache, block_table,
+                                                                total_lens, cu_new, o, lse)],
+                                            T, R, h, n_heads, n_kv_heads, N, n_pages, page_size,
+                                            max_pages, max_new, int(causal), int(dtype), _ptr(ws),
+                                            int(ws_bytes), _stream(stream)))
+
+
+def tp_gqa_paged_workspace_size(T, h, n_heads, n_kv_heads, N, dtype, mode):
+    return int(lib().tp_gqa_paged_workspace_size(T, h, n_heads, n_kv_heads, N, int(dtype),
+                                                 int(mode)))
+
+
+def tp_gqa_paged_attn_proj_fwd(x, gamma, beta, Wqkv, Wo, xn, mean, rstd, qkv, kcache, vcache,
+                               block_table, total_lens, cu_new, slots, o, lse, out, T, R, h,
+                               n_heads, n_kv_heads, N, n_pages, page_size, max_pages, max_new,
+                               causal, dtype, mode, ws, ws_bytes, stream=None):
+    _check(lib().tp_gqa_paged_attn_proj_fwd(*[_ptr(t) for t in (
+        x, gamma, beta, Wqkv, Wo, xn, mean, rstd, qkv, kcache, vcache, block_table, total_lens,
+        cu_new, slots, o, lse, out)], T, R, h, n_heads, n_kv_heads, N, n_pages, page_size,
+        max_pages, max_new, int(causal), int(dtype), int(mode), _ptr(ws), int(ws_bytes),
+        _stream(stream)))
 
 
 def tp_sp_mlp_fwd(x, gamma, beta, W1, W1_up, W2, xn, mean, rstd, Y, Y_up, H, out, M, h, f, N,

@@ -552,6 +552,98 @@ TP_API tp_status tp_gqa_attn_proj_bwd(const void* x, const float* gamma, const v
                                       int32_t n_kv_heads, int32_t N, int causal, tp_dtype dtype,
                                       tp_reduce mode, void* ws, size_t ws_bytes, void* stream);
 
+/* ------------------------------------------------------------------ paged key/value cache
+ * Serving the grouped-query block: the keys and values of earlier tokens stay in a cache
+ * of pages, and each step computes only its new tokens' rows, from one per request
+ * (decode) to a prompt's chunk [20260402-parallelism, Decode 阶段 / Prefill 阶段].
+ *
+ * Cache: kcache, vcache (n_pages, n_kv_heads, page_size, head_dim), one copy of each
+ * key/value head (replicas of N > n_kv_heads hold equal values); head_dim 16, 32, 64 or
+ * 128; page_size a power of two from 8 to 256; n_pages * page_size * n_kv_heads < 2^31.
+ * block_table (R, max_pages) int32: row r lists request r's pages in order of position.
+ * slot = page * page_size + offset. Step: request r has total_lens[r] tokens, the last
+ * cu_new[r+1] - cu_new[r] of them new, in rows cu_new[r] .. cu_new[r+1] - 1 of the packed
+ * rows; rows from cu_new[R] to T are padding (a captured graph's fixed size).
+ * All of these int32 arrays are device memory (4-byte aligned) and are read when the work
+ * runs, so a captured step replays with new lengths. Values that do not fit are no error
+ * and nothing is read or written outside the buffers: rows >= T do not exist, a page id
+ * outside [0, n_pages) is a page whose keys no row sees, keys past max_pages pages do
+ * not exist, negative lengths are zero.
+ */
+
+/* A step's set-up from the requests' lengths. c = ctx_lens[r], n = new_lens[r] (each at
+ * most 2^30, the new ones together below 2^31), P = page_size:
+ *   cu_new[0] = 0, cu_new[r+1] = cu_new[r] + n;  total_lens[r] = c + n
+ *   request r takes the pages it lacks, entries ceil(c/P) .. ceil((c+n)/P) - 1 (below
+ *     max_pages) of its row, off free_pages (n_free), from position *free_head on, in
+ *     request order; -1 where the list has run out. Other entries are left as they were.
+ *   row t = cu_new[r] + i: positions[t] = c + i, slots[t] = its slot (-1 without a page);
+ *   padding rows: -1 and -1.  *free_head_out: the list's new position (at most n_free)
+ *   counts (4): new rows, pages taken, pages missing, new rows that T has no room for.
+ * total_lens may be ctx_lens and free_head_out may be free_head (updated in place); no
+ * other buffers may overlap. positions and counts may be NULL. R <= 8192.
+ * Errors: TP_ERR_INVALID_ARG, TP_ERR_SHAPE, TP_ERR_CUDA, TP_ERR_UNSUPPORTED. */
+TP_API tp_status tp_kv_tables(const int32_t* ctx_lens, const int32_t* new_lens,
+                              const int32_t* free_pages, int64_t n_free,
+                              const int32_t* free_head, int32_t* free_head_out,
+                              int32_t* block_table, int32_t* total_lens, int32_t* cu_new,
+                              int32_t* slots, int32_t* positions, int32_t* counts, int64_t R,
+                              int64_t T, int64_t page_size, int64_t max_pages, void* stream);
+
+/* K and V of row t of qkv (T, tp_gqa sharded columns: N blocks of [hq Q | hkv K | hkv V]
+ * heads; a replicated head from its first replica) into slot slots[t]; slots outside
+ * [0, n_pages * page_size) are skipped. The slots of one call are distinct (two rows with
+ * one slot: the slot ends with elements of either). Other slots are left as they were.
+ * Errors: TP_ERR_INVALID_ARG, SHAPE, DTYPE, ALIGNMENT (qkv, caches), CUDA, UNSUPPORTED. */
+TP_API tp_status tp_kv_append(const void* qkv, const int32_t* slots, void* kcache, void* vcache,
+                              int64_t T, int64_t h, int32_t n_heads, int32_t n_kv_heads,
+                              int32_t N, int64_t n_pages, int64_t page_size, tp_dtype dtype,
+                              void* stream);
+
+/* Attention of the new rows over the cache (their own keys included, so after
+ * tp_kv_append): row i of request r sits at position total_lens[r] - n + i and sees the
+ * keys up to its position (causal != 0) or all total_lens[r].
+ *   qkv (T, W): the Q columns are read;  o (T, h) written;  lse (n_heads, T) fp32
+ *   written, or NULL. A row that sees no key gets o = 0 and lse = -inf; padding rows of o
+ *   and lse are left as they were.
+ *   max_new: the largest number of new tokens of a request. It chooses kernels only: the
+ *   result is right for any value, and the wrong one costs time.
+ *   K and V of the positions that a request's rows see must be finite; other positions'
+ *   values (unused slots, the rest of a last page) are never used.
+ *   ws: tp_gqa_paged_attention_workspace_size(...) bytes, uninitialised, for one call at a
+ *   time (calls on one stream may share it).
+ * The result does not depend on the order in which blocks run.
+ * Errors: TP_ERR_INVALID_ARG, SHAPE, DTYPE, ALIGNMENT, WORKSPACE, CUDA, UNSUPPORTED. */
+TP_API size_t tp_gqa_paged_attention_workspace_size(int64_t h, int32_t n_heads,
+                                                    int32_t n_kv_heads, int32_t N,
+                                                    tp_dtype dtype);
+TP_API tp_status tp_gqa_paged_attention_fwd(const void* qkv, const void* kcache,
+                                            const void* vcache, const int32_t* block_table,
+                                            const int32_t* total_lens, const int32_t* cu_new,
+                                            void* o, float* lse, int64_t T, int64_t R, int64_t h,
+                                            int32_t n_heads, int32_t n_kv_heads, int32_t N,
+                                            int64_t n_pages, int64_t page_size,
+                                            int64_t max_pages, int64_t max_new, int causal,
+                                            tp_dtype dtype, void* ws, size_t ws_bytes,
+                                            void* stream);
+
+/* One serving step of the pre-LN block of tp_gqa_attn_proj_fwd over the cache:
+ * out = x + Attn(LN(x)): LN, column-parallel QKV, the new keys and values into the cache,
+ * the attention above, row-parallel W_o with the residual. x, xn, out, o (T, h); qkv (T,
+ * W); mean, rstd (T), lse may be NULL. Padding rows of out depend on x and o of that row
+ * only. ws: tp_gqa_paged_workspace_size(...) bytes. Errors: as tp_gqa_attn_proj_fwd. */
+TP_API size_t tp_gqa_paged_workspace_size(int64_t T, int64_t h, int32_t n_heads,
+                                          int32_t n_kv_heads, int32_t N, tp_dtype dtype,
+                                          tp_reduce mode);
+TP_API tp_status tp_gqa_paged_attn_proj_fwd(
+    const void* x, const float* gamma, const float* beta, const void* Wqkv, const void* Wo,
+    void* xn, float* mean, float* rstd, void* qkv, void* kcache, void* vcache,
+    const int32_t* block_table, const int32_t* total_lens, const int32_t* cu_new,
+    const int32_t* slots, void* o, float* lse, void* out, int64_t T, int64_t R, int64_t h,
+    int32_t n_heads, int32_t n_kv_heads, int32_t N, int64_t n_pages, int64_t page_size,
+    int64_t max_pages, int64_t max_new, int causal, tp_dtype dtype, tp_reduce mode, void* ws,
+    size_t ws_bytes, void* stream);
+
 /*
  * Sequence-parallel pre-LN MLP sub-block, out = x + MLP(LN(x))
  * [20260402-parallelism, §5 Sequence Parallelism]. The rows are split over the N
