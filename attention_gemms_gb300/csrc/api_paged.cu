@@ -47,8 +47,8 @@ tp_status check_pages(int64_t n_pages, int64_t page_size, int64_t max_pages, int
   TP_TRY(need(n_pages >= 1 && max_pages >= 1, TP_ERR_INVALID_ARG, "need n_pages, max_pages >= 1"));
   TP_TRY(need(page_size >= 8 && page_size <= 256 && (page_size & (page_size - 1)) == 0,
               TP_ERR_SHAPE, "page_size must be a power of two from 8 to 256"));
-  TP_TRY(need(n_pages < (1ll << 31) && n_pages * page_size <= 2147483647ll / Hkv, TP_ERR_SHAPE,
-              "n_pages * page_size * n_kv_heads must be below 2^31"));
+  TP_TRY(need(n_pages < (1ll << 31) && n_pages * page_size <= 2147482623ll / Hkv, TP_ERR_SHAPE,
+              "n_pages * page_size * n_kv_heads must be below 2^31 - 1024"));
   return need(max_pages <= 2147483647ll / page_size, TP_ERR_SHAPE,
               "max_pages * page_size must be below 2^31");
 }
@@ -97,6 +97,7 @@ tp_status launch_paged(const PagedArgs& a, const PagedGqa& g, void* ws, cudaStre
   p.max_pages = static_cast<int>(a.max_pages);
   p.causal = a.causal != 0;
   p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(g.d));
+  if (a.dt == TP_BF16) return launch_paged_decode(p, g.d, st);
   return launch_paged_simt(p, g.d, a.max_new * p.G > 16, a.dt, st);
 }
 

@@ -18,6 +18,7 @@
 // stale. Lengths and page ids are not trusted: rows end at T, keys at the table's width,
 // and a page id outside the cache is a page of masked keys.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -273,6 +274,10 @@ tp_status launch_paged_combine(const PagedParams& p, int d, int unit_rows, int t
                                tp_dtype dt, cudaStream_t st);
 // units of unit_rows rows in tiles of tile_rows, 2^kt_log2 keys per tile
 void paged_set_units(PagedParams& p, int tile_rows, int unit_rows, int kt_log2);
+// bf16, few rows per key/value head (paged_decode.cu)
+tp_status launch_paged_decode(const PagedParams& p, int d, cudaStream_t st);
+// tensor map of a cache (rows of d bf16, swizzled): boxes of box_rows x min(64, d)
+tp_status paged_cache_map(CUtensorMap* m, const void* cache, int64_t rows, int d, int box_rows);
 size_t paged_workspace_bytes(int d, tp_dtype dt);
 
 }  // namespace tp

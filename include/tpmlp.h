@@ -559,7 +559,8 @@ TP_API tp_status tp_gqa_attn_proj_bwd(const void* x, const float* gamma, const v
  *
  * Cache: kcache, vcache (n_pages, n_kv_heads, page_size, head_dim), one copy of each
  * key/value head (replicas of N > n_kv_heads hold equal values); head_dim 16, 32, 64 or
- * 128; page_size a power of two from 8 to 256; n_pages * page_size * n_kv_heads < 2^31.
+ * 128; page_size a power of two from 8 to 256; n_pages * page_size * n_kv_heads below
+ * 2^31 - 1024.
  * block_table (R, max_pages) int32: row r lists request r's pages in order of position.
  * slot = page * page_size + offset. Step: request r has total_lens[r] tokens, the last
  * cu_new[r+1] - cu_new[r] of them new, in rows cu_new[r] .. cu_new[r+1] - 1 of the packed
