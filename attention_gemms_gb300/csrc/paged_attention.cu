@@ -356,9 +356,10 @@ void paged_set_units(PagedParams& p, int tile_rows, int unit_rows, int kt_log2) 
   p.kt_log2 = kt_log2;
 }
 
-size_t paged_workspace_bytes(int d, tp_dtype) {
-  return align_up(kPagedMaxCtas * sizeof(PagedRec), 256) +
-         static_cast<size_t>(kPagedMaxCtas) * 2 * 64 * (d + 2) * 4;
+size_t paged_workspace_bytes(int d, tp_dtype dt) {
+  size_t floats = static_cast<size_t>(kPagedMaxCtas) * 2 * 64 * (d + 2);
+  if (dt == TP_BF16 && d >= 64) floats = std::max(floats, paged_tc_floats(d));
+  return align_up(kPagedMaxCtas * sizeof(PagedRec), 256) + floats * 4;
 }
 
 }  // namespace tp

@@ -1,0 +1,614 @@
+// Paged grouped-query attention for chunks of new tokens, bf16, head_dim 64 or 128, on the
+// tensor cores (tcgen05). One persistent CTA per SM; paged.cuh divides the work.
+//
+// A unit is 256 rows, two TMEM tiles of 128 rows (whole tokens x the query heads of one
+// key/value head, so a key tile serves the whole group), keys in tiles of 128.
+//   producer warp: page ids 32 at a time, one TMA box per page, 64-column half and tensor
+//     into a ring of K and V tiles (K0 V0 K1 V1 ...); pages outside the cache or past the
+//     unit's keys are boxes outside the tensor and arrive as zeros;
+//   MMA warp (one lane): S = Q K^T into TMEM, and O += P V with P read from TMEM;
+//   eight softmax warps, four per tile, a thread per row: S out of TMEM, the running
+//     maximum (moved lazily) and sum, P as bf16 back into TMEM, O rescaled there when the
+//     maximum moves; at a segment's end O / l, or the piece for the join.
+// The tiles take turns: while one tile's softmax runs, the tensor cores do the other's
+// O += P V and next S. At d = 128, P lies over the S it came from: the MMAs of a thread run
+// in order, so the next S of the tile is written after the P V that reads P. At d = 64 the
+// two products have different shapes and P has columns of its own.
+// A unit of at most 128 rows (drafts, decoding requests beside a chunk, a chunk's end) would
+// leave the second tile idle and the chain S, softmax, P V bare; then both tiles take the
+// same rows, the first the even key tiles, the second the odd ones, and the second's piece
+// joins the first's at the end of the segment through the workspace.
+// Every wait is bounded; on a timeout the CTA records TP_ERR_TIMEOUT, stops issuing, waits
+// (bounded) for its own copies and MMAs, frees TMEM and returns.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "internal.h"
+#include "paged.cuh"
+#include "ptx.cuh"
+
+namespace tp {
+namespace {
+
+constexpr int kTile = 128;  // rows of a TMEM tile, keys of a key tile
+constexpr int kUnitRows = 2 * kTile;
+constexpr int kProd = 8, kMma = 9, kThreads = 320;  // warps 0-3: tile 0, 4-7: tile 1
+constexpr int kBadRing = 16;
+constexpr uint64_t kDrainNs = 20000000ull;
+
+struct PagedTcParams {
+  CUtensorMap tk, tv;  // (n_pages * Hkv * page, d), box 64 x min(page, 128)
+  PagedParams p;
+  float* joins;        // per CTA: m (128), l (128), O (128, d) of the second tile's piece
+  int cache_rows;
+  int* status;
+  uint64_t timeout_ns;
+  int debug_hang;
+};
+
+template <int D>
+struct Lay {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kOp = kTile * D * 2;  // a Q, K or V tile
+  static constexpr int kRing = D == 128 ? 5 : 10;
+  static constexpr int kOffRing = 2 * kOp;
+  static constexpr int kOffBar = kOffRing + kRing * kOp;
+  static constexpr int kBars = 2 * kRing + 11;
+  static constexpr int kSmem = kOffBar + kBars * 8 + kBadRing * 4 + 16 + 1024;
+  static constexpr uint32_t kO = 256, kOStep = D;                     // TMEM columns
+  static constexpr uint32_t kP = D == 128 ? 0 : 384, kPStep = D == 128 ? 128 : 64;
+};
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+      "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]: A's row is the TMEM lane, two bf16 per column
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {  // relative error about 2^-22
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// P rounded to bf16 (relative 2^-8 of each weight), the operand of the second product
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// A segment as every role sees it: key tiles of each row tile. pair: tile t takes the tiles
+// lo .. hi_t - 1 of its own rows; else tile t takes lo + t, lo + t + 2, ... of the same rows.
+struct Seg {
+  bool pair;
+  int lo, hi[2], step;
+  __device__ __forceinline__ Seg(const PagedParams& p, const PagedWalk& w) {
+    const int tpt = p.tpu / 2, tokens = min(p.tpu, w.q.rows - w.u * p.tpu);
+    pair = tokens > tpt;
+    lo = w.lo;
+    hi[1] = w.hi;
+    hi[0] = w.hi;
+    step = pair ? 1 : 2;
+    if (pair && p.causal) {  // the first tile's rows see no key of the last tiles
+      const int64_t end = static_cast<int64_t>(w.q.total) - w.q.n + w.u * p.tpu + tpt;
+      const int64_t own = (min(end, static_cast<int64_t>(w.q.kv_end)) + kTile - 1) >> 7;
+      hi[0] = static_cast<int>(min(static_cast<int64_t>(w.hi),
+                                   max(own, static_cast<int64_t>(w.lo))));
+    }
+  }
+  __device__ __forceinline__ int first(int t) const { return pair ? lo : lo + t; }
+  __device__ __forceinline__ int count(int t) const {  // tile t's key tiles
+    const int f = first(t);
+    return hi[t] > f ? (hi[t] - f + step - 1) / step : 0;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_tc_kernel(const __grid_constant__ PagedTcParams tp_) {
+  using L = Lay<D>;
+  const PagedParams& p = tp_.p;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sb = smem_u32(smem);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  volatile uint32_t* bad = reinterpret_cast<volatile uint32_t*>(bars + L::kBars);
+  uint32_t* tmem_slot = const_cast<uint32_t*>(bad) + kBadRing;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const uint32_t bar0 = smem_u32(bars);
+  auto full = [&](int e) { return bar0 + 8u * e; };
+  auto empty = [&](int e) { return bar0 + 8u * (L::kRing + e); };
+  auto bar_at = [&](int i) { return bar0 + 8u * (2 * L::kRing + i); };
+  auto q_full = [&](int t) { return bar_at(t); };
+  auto s_full = [&](int t) { return bar_at(2 + t); };
+  auto p_full = [&](int t) { return bar_at(4 + t); };
+  auto o_done = [&](int t) { return bar_at(6 + t); };
+  const uint32_t j_full = bar_at(8), j_free = bar_at(9), drain = bar_at(10);
+  __shared__ PagedSched sc;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int e = 0; e < L::kRing; ++e) {
+      mbar_init(full(e), 1);
+      mbar_init(empty(e), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(q_full(t), 4);
+      mbar_init(s_full(t), 1);
+      mbar_init(p_full(t), 4);
+      mbar_init(o_done(t), 1);
+    }
+    mbar_init(j_full, 4);
+    mbar_init(j_free, 4);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == kMma) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_slot);
+  pdl_wait();  // the set-up above overlaps the previous kernel
+  pdl_trigger();
+  PagedWalk w = paged_schedule(p, sc, blockIdx.x, gridDim.x);
+  auto tS = [&](int t) { return tmem + 128u * t; };
+  auto tP = [&](int t) { return tmem + L::kP + L::kPStep * t; };
+  auto tO = [&](int t) { return tmem + L::kO + L::kOStep * t; };
+  auto entry_at = [&](int e) { return sb + L::kOffRing + e * L::kOp; };
+  auto timed_out = [&] {
+    atomicCAS(tp_.status, 0, static_cast<int>(TP_ERR_TIMEOUT));
+    atomicAdd(tp_.status + 1, 1);
+  };
+  int issued = 0;  // producer: ring entries issued
+
+  if (warp == kProd) {
+    // ---------------------------------------------------------------- TMA producer
+    const int ps = 1 << p.ps_log2, box = min(ps, kTile), boxes = kTile / box;
+    bool ok = true;
+    int tiles = 0;
+    for (; w.valid() && ok; w.next(p)) {
+      const int j = w.vh / p.hs;
+      const int kend = paged_unit_kend(p, w.q, w.u);
+      const int32_t* tab = p.table + static_cast<int64_t>(w.r) * p.max_pages;
+      const int npages = (kend + ps - 1) >> p.ps_log2;
+      auto fetch = [&](int first) {
+        const int i = first + lane;
+        const int id = i < npages ? tab[i] : -1;
+        return id >= 0 && id < p.n_pages ? id : -1;
+      };
+      int base = (w.lo * kTile) >> p.ps_log2;
+      int ids = fetch(base), ahead = fetch(base + 32);
+      for (int tile = w.lo; tile < w.hi && ok; ++tile, ++tiles) {
+        const int k0 = tile * kTile, pg0 = k0 >> p.ps_log2;
+        if (pg0 - base >= 32) {  // tiles are whole groups of at most 16 pages
+          base += 32;
+          ids = ahead;
+          ahead = fetch(base + 32);
+        }
+        const int src = __shfl_sync(0xFFFFFFFFu, ids, (pg0 - base + min(lane, boxes - 1)) & 31);
+        const uint32_t missing = __ballot_sync(0xFFFFFFFFu, lane < boxes && src < 0);
+        const int y = src < 0 ? tp_.cache_rows
+                              : (((src * p.Hkv + j) << p.ps_log2) + (k0 & (ps - 1)));
+#pragma unroll
+        for (int is_v = 0; is_v < 2; ++is_v) {
+          const int e = issued % L::kRing, round = issued / L::kRing;
+          if (round > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(empty(e), (round - 1) & 1,
+                                                              tp_.timeout_ns, abort_flag))) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
+            if (!is_v) bad[tiles % kBadRing] = missing;
+            mbar_arrive_expect_tx(full(e), L::kOp);
+          }
+          __syncwarp();
+          if (lane < boxes)
+#pragma unroll
+            for (int h = 0; h < L::kHalves; ++h)
+              tma_load_2d(entry_at(e) + h * (kTile * 128) + lane * box * 128,
+                          is_v ? &tp_.tv : &tp_.tk, full(e), h * 64, y);
+          ++issued;
+        }
+      }
+    }
+    if (!ok && lane == 0) timed_out();
+  } else if (warp == kMma) {
+    // ---------------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      const uint32_t id_s = idesc_bf16_f32(128, kTile, 0, 0);  // Q, K both K-major
+      const uint32_t id_o = idesc_bf16_f32(128, D, 0, 1);      // P in TMEM, V MN-major
+      bool ok = true;
+      if (tp_.debug_hang) ok = mbar_wait(drain, 0, tp_.timeout_ns, abort_flag);
+      int seg_q[2] = {0, 0}, np[2] = {0, 0};  // Q tiles and P tiles taken so far
+      int ring0 = 0;                          // ring entries before this segment
+      auto ring_wait = [&](int n) {           // n-th entry of the segment has landed
+        const int i = ring0 + n;
+        return mbar_wait(full(i % L::kRing), (i / L::kRing) & 1, tp_.timeout_ns, abort_flag);
+      };
+      for (; w.valid() && ok; w.next(p)) {
+        const Seg g(p, w);
+        const int n0 = g.count(0), n1 = g.count(1);
+        const int most = max(n0, n1);
+        // S of tile t's k-th key tile
+        auto issue_s = [&](int t, int k) -> bool {
+          const int rel = g.first(t) + k * g.step - g.lo;  // key tile within the segment
+          if (!ring_wait(2 * rel)) return false;
+          tc_fence_after();
+          const uint32_t ka = entry_at((ring0 + 2 * rel) % L::kRing);
+          const uint32_t qa = sb + (g.pair ? t : 0) * L::kOp;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
+            mma_bf16_ss(tS(t), sw128_desc(qa + off, 16u, 1024u), sw128_desc(ka + off, 16u, 1024u),
+                        id_s, kk > 0 ? 1u : 0u);
+          }
+          mma_commit(s_full(t));
+          // the key tile's last reader frees it
+          if (!g.pair || t == 1) mma_commit(empty((ring0 + 2 * rel) % L::kRing));
+          return true;
+        };
+        auto issue_pv = [&](int t, int k) -> bool {
+          const int rel = g.first(t) + k * g.step - g.lo;
+          if (!ring_wait(2 * rel + 1)) return false;
+          if (!mbar_wait(p_full(t), np[t] & 1, tp_.timeout_ns, abort_flag)) return false;
+          ++np[t];
+          tc_fence_after();
+          const uint32_t va = entry_at((ring0 + 2 * rel + 1) % L::kRing);
+#pragma unroll
+          for (int kk = 0; kk < kTile / 16; ++kk)
+            mma_bf16_ts(tO(t), tP(t) + kk * 8, sw128_desc(va + kk * 2048, kTile * 128, 1024u), id_o,
+                        (k > 0 || kk > 0) ? 1u : 0u);
+          if (k + 1 == (t ? n1 : n0)) mma_commit(o_done(t));
+          if (!g.pair || t == 1) mma_commit(empty((ring0 + 2 * rel + 1) % L::kRing));
+          return true;
+        };
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (t == 0 || g.pair) {  // the rows' Q; in the other form both tiles read the first
+            ok = mbar_wait(q_full(t), seg_q[t] & 1, tp_.timeout_ns, abort_flag);
+            ++seg_q[t];
+          }
+          if (ok && (t ? n1 : n0) > 0) ok = issue_s(t, 0);
+        }
+        for (int k = 0; k < most && ok; ++k)
+          for (int t = 0; t < 2 && ok; ++t) {
+            const int n = t ? n1 : n0;
+            if (k < n) ok = issue_pv(t, k);
+            if (k + 1 < n && ok) ok = issue_s(t, k + 1);
+          }
+        ring0 += 2 * (w.hi - w.lo);
+      }
+      if (!ok) timed_out();
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- softmax
+    const int t = warp >> 2, x = threadIdx.x & 127;  // tile, row within it = TMEM lane
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int tpt = p.tpu / 2, tt = x / p.Gv, hh = x - tt * p.Gv;
+    float* piece = tp_.joins + static_cast<int64_t>(blockIdx.x) * kTile * (D + 2);
+    PagedRec rec{0, 0, 0, 0, 0};
+    int ns = 0, segs_o = 0, joined = 0, tiles0 = 0;
+    bool ok = true;
+    auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool {
+      return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, tp_.timeout_ns, abort_flag)) != 0;
+    };
+    for (; w.valid() && ok; w.next(p)) {
+      const Seg g(p, w);
+      const int j = w.vh / p.hs, gh = (w.vh - j * p.hs) * p.Gv + hh;
+      const int token = w.u * p.tpu + (g.pair ? t * tpt : 0) + tt, head = j * p.G + gh;
+      const bool live = tt < tpt && gh < p.G && token < w.q.rows;
+      const bool busy = __any_sync(0xFFFFFFFFu, live);  // a warp without rows computes nothing
+      const int64_t row = static_cast<int64_t>(w.q.row0) + token;
+      const int kv_end = w.q.kv_end;
+      const int lim = !live ? kv_end
+                            : p.causal ? min(kv_end, w.q.total - w.q.n + token + 1) : kv_end;
+      const int lim_min = __reduce_min_sync(0xFFFFFFFFu, lim);
+      if (t == 0 || g.pair) {
+        // this row's Q: every S of the tile's previous segment has been read (s_full seen)
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.qkv) + row * p.ldq +
+                                   paged_qcol<D>(p, live ? head : 0);
+        const uint32_t dst = sb + t * L::kOp + x * 128;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (live) v = *reinterpret_cast<const uint4*>(src + c * 8);
+          st_shared_v4(dst + (c >> 3) * (kTile * 128) + (((c & 7) ^ (x & 7)) << 4), v.x, v.y, v.z,
+                       v.w);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full(t));
+      }
+      const int n = g.count(t);
+      float m = -INFINITY, l = 0.0f;
+      for (int k = 0; k < n; ++k, ++ns) {
+        const int tile = g.first(t) + k * g.step, k0 = tile * kTile;
+        if (!wait_all(s_full(t), ns & 1)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int seg_tile = tiles0 + tile - g.lo;
+        if (k0 + kTile > kv_end) {
+          // V rows past the request's keys may hold anything and 0 * NaN would spoil O
+          const int e = 2 * seg_tile + 1;
+          if (!wait_all(full(e % L::kRing), (e / L::kRing) & 1)) {
+            ok = false;
+            break;
+          }
+          const uint32_t va = entry_at(e % L::kRing);
+          if (k0 + x >= kv_end)
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+              st_shared_v4(va + (c >> 3) * (kTile * 128) + x * 128 + ((c & 7) << 4), 0, 0, 0, 0);
+          fence_proxy_async_smem();
+        }
+        if (busy) {
+          uint32_t v[kTile];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            tmem_ld32(tS(t) + lanes + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
+          tmem_ld_wait();
+          const uint32_t miss = bad[seg_tile % kBadRing];
+          if (k0 + kTile > lim_min || miss) {
+#pragma unroll
+            for (int i = 0; i < kTile; ++i) {
+              const bool hidden = k0 + i >= lim || ((miss >> (i >> min(p.ps_log2, 7))) & 1);
+              if (hidden) v[i] = 0xff800000u;  // -inf
+            }
+          }
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < kTile; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(v[i]));
+          const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+          // The maximum moves only when it grows by more than 8 (weights up to 2^8 are
+          // harmless in bf16 and fp32): o / l does not depend on it.
+          const bool move = mb > m + 8.0f;
+          const float m1 = move ? mb : m, mu = m1 == -INFINITY ? 0.0f : m1;
+          const float f = move ? ex2(m - mu) : 1.0f;
+          m = m1;
+          if (k > 0 && __any_sync(0xFFFFFFFFu, move)) {
+            // the tile's previous P V has completed: s_full's commit came after it
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tO(t) + lanes + 32 * c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st32(tO(t) + lanes + 32 * c, o);
+            }
+          }
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float a = ex2(fmaf(__uint_as_float(v[64 * c + 2 * i]), p.scale_log2, -mu));
+              const float b = ex2(fmaf(__uint_as_float(v[64 * c + 2 * i + 1]), p.scale_log2, -mu));
+              sum[(2 * i) & 3] += a;
+              sum[(2 * i + 1) & 3] += b;
+              pk[i] = pack2(a, b);
+            }
+            tmem_st32(tP(t) + lanes + 32 * c, pk);
+          }
+          l = l * f + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+          tmem_st_wait();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(t));
+      }
+      tiles0 += w.hi - w.lo;
+      if (!ok) break;
+      if (n > 0) {  // the last P V
+        if (!wait_all(o_done(t), segs_o & 1)) {
+          ok = false;
+          break;
+        }
+        ++segs_o;
+        tc_fence_after();
+      }
+      const bool begins = w.lo == 0, ends = w.hi == w.tiles;
+      if (!begins) rec.head = ends ? 2 : 1;
+      if (begins && !ends) rec.tail = 1, rec.r = w.r, rec.vh = w.vh, rec.u = w.u;
+      const bool joins = !g.pair && g.count(1) > 0;
+      if (!g.pair && t == 1) {
+        if (joins) {
+          // the second tile's piece of the same rows, for the first tile's warps
+          if (joined > 0 && !wait_all(j_free, (joined - 1) & 1)) {
+            ok = false;
+            break;
+          }
+#pragma unroll 1
+          for (int c = 0; c < D / 32 && busy; ++c) {
+            uint32_t o[32];
+            __syncwarp();
+            tmem_ld32(tO(t) + lanes + 32 * c, o);
+            tmem_ld_wait();
+            if (live)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4*>(piece + 2 * kTile + x * D + 32 * c + 4 * i) =
+                    make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+          piece[x] = m;
+          piece[kTile + x] = l;
+          __threadfence();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(j_full);
+          ++joined;
+        }
+        continue;
+      }
+      float mj = m, lj = l, fa = 1.0f, fb = 0.0f;
+      if (joins) {
+        if (!wait_all(j_full, joined & 1)) {
+          ok = false;
+          break;
+        }
+        ++joined;
+        const float m2 = __ldcg(piece + x), l2 = __ldcg(piece + kTile + x);
+        mj = fmaxf(m, m2);
+        const float mu = mj == -INFINITY ? 0.0f : mj;
+        fa = ex2(m - mu);
+        fb = ex2(m2 - mu);
+        lj = l * fa + l2 * fb;
+      }
+      const bool whole = begins && ends;
+      const float inv = lj > 0.0f ? 1.0f / lj : 0.0f;
+      const float ga = whole ? fa * inv : fa, gb = whole ? fb * inv : fb;
+      float* slot =
+          p.part + static_cast<int64_t>(2 * blockIdx.x + (begins ? 1 : 0)) * kUnitRows * (D + 2);
+      const int ur = (g.pair ? t : 0) * kTile + x;
+#pragma unroll 1
+      for (int c = 0; c < D / 32 && busy; ++c) {
+        uint32_t o[32];
+        __syncwarp();
+        if (n > 0) {
+          tmem_ld32(tO(t) + lanes + 32 * c, o);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0u;
+        }
+        if (live) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * ga);
+          if (joins)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 y =
+                  __ldcg(reinterpret_cast<const float4*>(piece + 2 * kTile + x * D + 32 * c + 4 * i));
+              o[4 * i] = __float_as_uint(__uint_as_float(o[4 * i]) + y.x * gb);
+              o[4 * i + 1] = __float_as_uint(__uint_as_float(o[4 * i + 1]) + y.y * gb);
+              o[4 * i + 2] = __float_as_uint(__uint_as_float(o[4 * i + 2]) + y.z * gb);
+              o[4 * i + 3] = __float_as_uint(__uint_as_float(o[4 * i + 3]) + y.w * gb);
+            }
+          if (whole) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + row * p.H * D +
+                                                  static_cast<int64_t>(head) * D + 32 * c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float* s = reinterpret_cast<const float*>(o + 8 * i);
+              dst[i] = make_uint4(pack2(s[0], s[1]), pack2(s[2], s[3]), pack2(s[4], s[5]),
+                                  pack2(s[6], s[7]));
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(slot + 2 * kUnitRows + static_cast<int64_t>(ur) * D + 32 * c +
+                                        4 * i) =
+                  make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+      }
+      if (joins) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(j_free);
+      }
+      if (live) {
+        if (whole) {
+          if (p.lse)
+            p.lse[head * p.T + row] = lj > 0.0f ? (mj + log2f(lj)) * 0.6931471805599453f : -INFINITY;
+        } else {
+          slot[ur] = mj;
+          slot[kUnitRows + ur] = lj;
+        }
+      }
+      tc_fence_before();  // O has been read before the next segment's P is handed over
+    }
+    if (!ok && lane == 0) timed_out();
+    if (threadIdx.x == 0) p.rec[blockIdx.x] = rec;
+  }
+
+  // ------------------------------------------------------------------ teardown
+  __syncthreads();
+  if (*abort_flag) {
+    volatile int no_abort = 0;
+    if (warp == kProd && lane == 0)  // the copies this CTA issued have landed
+      for (int e = 0; e < L::kRing; ++e) {
+        const int n = issued > e ? (issued - 1 - e) / L::kRing : -1;  // last round of entry e
+        if (n >= 0) mbar_wait(full(e), n & 1, kDrainNs, &no_abort);
+      }
+    if (warp == kMma && lane == 0) {  // and the MMAs it issued have completed
+      mma_commit(drain);
+      mbar_wait(drain, 0, kDrainNs, &no_abort);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D>
+tp_status tc_t(PagedTcParams& t, cudaStream_t st) {
+  using L = Lay<D>;
+  static std::atomic<uint64_t> attr_set{0};
+  if (needs_setup(attr_set)) {
+    TP_CUDA_TRY(cudaFuncSetAttribute(paged_tc_kernel<D>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem));
+    mark_device(attr_set);
+  }
+  const int ctas = std::min(kPagedTcCtas, device_sm_count());
+  t.joins = t.p.part + static_cast<int64_t>(kPagedTcCtas) * 2 * kUnitRows * (D + 2);
+  TP_CUDA_TRY(launch_kernel(paged_tc_kernel<D>, dim3(ctas), dim3(kThreads),
+                            static_cast<size_t>(L::kSmem), st, t));
+  count_launch();
+  return launch_paged_combine(t.p, D, kUnitRows, kTile, ctas, TP_BF16, st);
+}
+
+}  // namespace
+
+tp_status launch_paged_tc(const PagedParams& p, int d, cudaStream_t st) {
+  PagedTcParams t{};
+  t.p = p;
+  paged_set_units(t.p, kTile, kUnitRows, 7);
+  const int64_t rows = (static_cast<int64_t>(p.n_pages) * p.Hkv) << p.ps_log2;
+  t.cache_rows = static_cast<int>(rows);
+  const int box = std::min(1 << p.ps_log2, kTile);
+  TP_TRY(paged_cache_map(&t.tk, p.kc, rows, d, box));
+  TP_TRY(paged_cache_map(&t.tv, p.vc, rows, d, box));
+  t.status = device_status_word();
+  if (!t.status) return fail(TP_ERR_CUDA, "device status word unavailable");
+  t.timeout_ns = wait_timeout_ns();
+  t.debug_hang = debug_hang_flag();
+  return d == 64 ? tc_t<64>(t, st) : tc_t<128>(t, st);
+}
+
+size_t paged_tc_floats(int d) {
+  return static_cast<size_t>(kPagedTcCtas) * (2 * kUnitRows + kTile) * (d + 2);
+}
+
+}  // namespace tp
