@@ -98,8 +98,9 @@ tp_status launch_paged(const PagedArgs& a, const PagedGqa& g, void* ws, cudaStre
   p.causal = a.causal != 0;
   p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(g.d));
   if (a.dt == TP_BF16)
-    return g.d >= 64 && a.max_new * p.G > 16 ? launch_paged_tc(p, g.d, st)
-                                             : launch_paged_decode(p, g.d, st);
+    return g.d >= 64 && p.G <= 128 && a.max_new * p.G > 16
+               ? launch_paged_tc(p, g.d, a.N, st)
+               : launch_paged_decode(p, g.d, st);
   return launch_paged_simt(p, g.d, a.max_new * p.G > 16, a.dt, st);
 }
 

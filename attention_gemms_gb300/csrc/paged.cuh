@@ -276,9 +276,13 @@ tp_status launch_paged_combine(const PagedParams& p, int d, int unit_rows, int t
 void paged_set_units(PagedParams& p, int tile_rows, int unit_rows, int kt_log2);
 // bf16, few rows per key/value head (paged_decode.cu)
 tp_status launch_paged_decode(const PagedParams& p, int d, cudaStream_t st);
-// bf16, head_dim 64 or 128, chunks (paged_attention_tc.cu)
+// bf16, head_dim 64 or 128, chunks, at most 128 query heads per key/value head
+// (paged_attention_tc.cu)
 constexpr int kPagedTcCtas = 152;
-tp_status launch_paged_tc(const PagedParams& p, int d, cudaStream_t st);
+tp_status launch_paged_tc(const PagedParams& p, int d, int N, cudaStream_t st);
+// tensor map of the queries: rows, shard blocks, heads, dims; box: tpu / 2 tokens x the
+// query heads of one key/value head x 64
+tp_status paged_q_map(CUtensorMap* m, const PagedParams& p, int d, int N);
 size_t paged_tc_floats(int d);  // partial results it may leave
 // tensor map of a cache (rows of d bf16, swizzled): boxes of box_rows x min(64, d)
 tp_status paged_cache_map(CUtensorMap* m, const void* cache, int64_t rows, int d, int box_rows);

@@ -36,12 +36,18 @@ namespace {
 
 constexpr int kTile = 128;  // rows of a TMEM tile, keys of a key tile
 constexpr int kUnitRows = 2 * kTile;
-constexpr int kProd = 8, kMma = 9, kThreads = 320;  // warps 0-3: tile 0, 4-7: tile 1
+// warps 0-3: softmax of tile 0, 4-7: of tile 1, 8: K and V loads, 9: MMA, 10: Q loads
+constexpr int kProd = 8, kMma = 9, kLoadQ = 10, kThreads = 384;
+// Registers: 384 threads launch with 168 each; the third warpgroup gives up its share
+// (128 x 80 + 256 x 208 = 63488 of the launch's 64512) so that a row's 128 scores stay in
+// the softmax threads' registers.
+constexpr int kRegsLoad = 80, kRegsSoftmax = 208;
 constexpr int kBadRing = 16;
 constexpr uint64_t kDrainNs = 20000000ull;
 
 struct PagedTcParams {
   CUtensorMap tk, tv;  // (n_pages * Hkv * page, d), box 64 x min(page, 128)
+  CUtensorMap tq;      // (T, N blocks, hq heads, d) of the qkv rows, box: a row tile x 64
   PagedParams p;
   float* joins;        // per CTA: m (128), l (128), O (128, d) of the second tile's piece
   int cache_rows;
@@ -57,7 +63,7 @@ struct Lay {
   static constexpr int kRing = D == 128 ? 5 : 10;
   static constexpr int kOffRing = 2 * kOp;
   static constexpr int kOffBar = kOffRing + kRing * kOp;
-  static constexpr int kBars = 2 * kRing + 11;
+  static constexpr int kBars = 2 * kRing + 13;
   static constexpr int kSmem = kOffBar + kBars * 8 + kBadRing * 4 + 16 + 1024;
   static constexpr uint32_t kO = 256, kOStep = D;                     // TMEM columns
   static constexpr uint32_t kP = D == 128 ? 0 : 384, kPStep = D == 128 ? 128 : 64;
@@ -87,6 +93,43 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, uint32_t bar,
+                                            int32_t x, int32_t y, int32_t z, int32_t w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// two fp32 values per instruction
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 __device__ __forceinline__ float ex2(float x) {  // relative error about 2^-22
   float y;
@@ -147,6 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto p_full = [&](int t) { return bar_at(4 + t); };
   auto o_done = [&](int t) { return bar_at(6 + t); };
   const uint32_t j_full = bar_at(8), j_free = bar_at(9), drain = bar_at(10);
+  auto q_empty = [&](int t) { return bar_at(11 + t); };
   __shared__ PagedSched sc;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -155,7 +199,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(empty(e), 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(q_full(t), 4);
+      mbar_init(q_full(t), 1);
+      mbar_init(q_empty(t), 1);
       mbar_init(s_full(t), 1);
       mbar_init(p_full(t), 4);
       mbar_init(o_done(t), 1);
@@ -185,129 +230,164 @@ __global__ void __launch_bounds__(kThreads, 1)
     atomicCAS(tp_.status, 0, static_cast<int>(TP_ERR_TIMEOUT));
     atomicAdd(tp_.status + 1, 1);
   };
-  int issued = 0;  // producer: ring entries issued
+  int issued = 0;             // K/V loads: ring entries issued
+  int issued_q[2] = {0, 0};   // Q loads: tiles issued
 
-  if (warp == kProd) {
-    // ---------------------------------------------------------------- TMA producer
-    const int ps = 1 << p.ps_log2, box = min(ps, kTile), boxes = kTile / box;
-    bool ok = true;
-    int tiles = 0;
-    for (; w.valid() && ok; w.next(p)) {
-      const int j = w.vh / p.hs;
-      const int kend = paged_unit_kend(p, w.q, w.u);
-      const int32_t* tab = p.table + static_cast<int64_t>(w.r) * p.max_pages;
-      const int npages = (kend + ps - 1) >> p.ps_log2;
-      auto fetch = [&](int first) {
-        const int i = first + lane;
-        const int id = i < npages ? tab[i] : -1;
-        return id >= 0 && id < p.n_pages ? id : -1;
-      };
-      int base = (w.lo * kTile) >> p.ps_log2;
-      int ids = fetch(base), ahead = fetch(base + 32);
-      for (int tile = w.lo; tile < w.hi && ok; ++tile, ++tiles) {
-        const int k0 = tile * kTile, pg0 = k0 >> p.ps_log2;
-        if (pg0 - base >= 32) {  // tiles are whole groups of at most 16 pages
-          base += 32;
-          ids = ahead;
-          ahead = fetch(base + 32);
-        }
-        const int src = __shfl_sync(0xFFFFFFFFu, ids, (pg0 - base + min(lane, boxes - 1)) & 31);
-        const uint32_t missing = __ballot_sync(0xFFFFFFFFu, lane < boxes && src < 0);
-        const int y = src < 0 ? tp_.cache_rows
-                              : (((src * p.Hkv + j) << p.ps_log2) + (k0 & (ps - 1)));
-#pragma unroll
-        for (int is_v = 0; is_v < 2; ++is_v) {
-          const int e = issued % L::kRing, round = issued / L::kRing;
-          if (round > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(empty(e), (round - 1) & 1,
-                                                              tp_.timeout_ns, abort_flag))) {
-            ok = false;
-            break;
-          }
-          if (lane == 0) {
-            if (!is_v) bad[tiles % kBadRing] = missing;
-            mbar_arrive_expect_tx(full(e), L::kOp);
-          }
-          __syncwarp();
-          if (lane < boxes)
-#pragma unroll
-            for (int h = 0; h < L::kHalves; ++h)
-              tma_load_2d(entry_at(e) + h * (kTile * 128) + lane * box * 128,
-                          is_v ? &tp_.tv : &tp_.tk, full(e), h * 64, y);
-          ++issued;
-        }
-      }
-    }
-    if (!ok && lane == 0) timed_out();
-  } else if (warp == kMma) {
-    // ---------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
-      const uint32_t id_s = idesc_bf16_f32(128, kTile, 0, 0);  // Q, K both K-major
-      const uint32_t id_o = idesc_bf16_f32(128, D, 0, 1);      // P in TMEM, V MN-major
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsLoad));
+    if (warp == kProd) {
+      // ---------------------------------------------------------------- TMA producer
+      const int ps = 1 << p.ps_log2, box = min(ps, kTile), boxes = kTile / box;
       bool ok = true;
-      if (tp_.debug_hang) ok = mbar_wait(drain, 0, tp_.timeout_ns, abort_flag);
-      int seg_q[2] = {0, 0}, np[2] = {0, 0};  // Q tiles and P tiles taken so far
-      int ring0 = 0;                          // ring entries before this segment
-      auto ring_wait = [&](int n) {           // n-th entry of the segment has landed
-        const int i = ring0 + n;
-        return mbar_wait(full(i % L::kRing), (i / L::kRing) & 1, tp_.timeout_ns, abort_flag);
-      };
+      int tiles = 0;
       for (; w.valid() && ok; w.next(p)) {
-        const Seg g(p, w);
-        const int n0 = g.count(0), n1 = g.count(1);
-        const int most = max(n0, n1);
-        // S of tile t's k-th key tile
-        auto issue_s = [&](int t, int k) -> bool {
-          const int rel = g.first(t) + k * g.step - g.lo;  // key tile within the segment
-          if (!ring_wait(2 * rel)) return false;
-          tc_fence_after();
-          const uint32_t ka = entry_at((ring0 + 2 * rel) % L::kRing);
-          const uint32_t qa = sb + (g.pair ? t : 0) * L::kOp;
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
-            mma_bf16_ss(tS(t), sw128_desc(qa + off, 16u, 1024u), sw128_desc(ka + off, 16u, 1024u),
-                        id_s, kk > 0 ? 1u : 0u);
-          }
-          mma_commit(s_full(t));
-          // the key tile's last reader frees it
-          if (!g.pair || t == 1) mma_commit(empty((ring0 + 2 * rel) % L::kRing));
-          return true;
+        const int j = w.vh / p.hs;
+        const int kend = paged_unit_kend(p, w.q, w.u);
+        const int32_t* tab = p.table + static_cast<int64_t>(w.r) * p.max_pages;
+        const int npages = (kend + ps - 1) >> p.ps_log2;
+        auto fetch = [&](int first) {
+          const int i = first + lane;
+          const int id = i < npages ? tab[i] : -1;
+          return id >= 0 && id < p.n_pages ? id : -1;
         };
-        auto issue_pv = [&](int t, int k) -> bool {
-          const int rel = g.first(t) + k * g.step - g.lo;
-          if (!ring_wait(2 * rel + 1)) return false;
-          if (!mbar_wait(p_full(t), np[t] & 1, tp_.timeout_ns, abort_flag)) return false;
-          ++np[t];
-          tc_fence_after();
-          const uint32_t va = entry_at((ring0 + 2 * rel + 1) % L::kRing);
-#pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            mma_bf16_ts(tO(t), tP(t) + kk * 8, sw128_desc(va + kk * 2048, kTile * 128, 1024u), id_o,
-                        (k > 0 || kk > 0) ? 1u : 0u);
-          if (k + 1 == (t ? n1 : n0)) mma_commit(o_done(t));
-          if (!g.pair || t == 1) mma_commit(empty((ring0 + 2 * rel + 1) % L::kRing));
-          return true;
-        };
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (t == 0 || g.pair) {  // the rows' Q; in the other form both tiles read the first
-            ok = mbar_wait(q_full(t), seg_q[t] & 1, tp_.timeout_ns, abort_flag);
-            ++seg_q[t];
+        int base = (w.lo * kTile) >> p.ps_log2;
+        int ids = fetch(base), ahead = fetch(base + 32);
+        for (int tile = w.lo; tile < w.hi && ok; ++tile, ++tiles) {
+          const int k0 = tile * kTile, pg0 = k0 >> p.ps_log2;
+          if (pg0 - base >= 32) {  // tiles are whole groups of at most 16 pages
+            base += 32;
+            ids = ahead;
+            ahead = fetch(base + 32);
           }
-          if (ok && (t ? n1 : n0) > 0) ok = issue_s(t, 0);
+          const int src = __shfl_sync(0xFFFFFFFFu, ids, (pg0 - base + min(lane, boxes - 1)) & 31);
+          const uint32_t missing = __ballot_sync(0xFFFFFFFFu, lane < boxes && src < 0);
+          const int y = src < 0 ? tp_.cache_rows
+                                : (((src * p.Hkv + j) << p.ps_log2) + (k0 & (ps - 1)));
+#pragma unroll
+          for (int is_v = 0; is_v < 2; ++is_v) {
+            const int e = issued % L::kRing, round = issued / L::kRing;
+            if (round > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(empty(e), (round - 1) & 1,
+                                                                tp_.timeout_ns, abort_flag))) {
+              ok = false;
+              break;
+            }
+            if (lane == 0) {
+              if (!is_v) bad[tiles % kBadRing] = missing;
+              mbar_arrive_expect_tx(full(e), L::kOp);
+            }
+            __syncwarp();
+            if (lane < boxes)
+#pragma unroll
+              for (int h = 0; h < L::kHalves; ++h)
+                tma_load_2d(entry_at(e) + h * (kTile * 128) + lane * box * 128,
+                            is_v ? &tp_.tv : &tp_.tk, full(e), h * 64, y);
+            ++issued;
+          }
         }
-        for (int k = 0; k < most && ok; ++k)
-          for (int t = 0; t < 2 && ok; ++t) {
-            const int n = t ? n1 : n0;
-            if (k < n) ok = issue_pv(t, k);
-            if (k + 1 < n && ok) ok = issue_s(t, k + 1);
-          }
-        ring0 += 2 * (w.hi - w.lo);
       }
-      if (!ok) timed_out();
+      if (!ok && lane == 0) timed_out();
+    } else if (warp == kMma) {
+      // ---------------------------------------------------------------- MMA issuer
+      if (lane == 0) {
+        const uint32_t id_s = idesc_bf16_f32(128, kTile, 0, 0);  // Q, K both K-major
+        const uint32_t id_o = idesc_bf16_f32(128, D, 0, 1);      // P in TMEM, V MN-major
+        bool ok = true;
+        if (tp_.debug_hang) ok = mbar_wait(drain, 0, tp_.timeout_ns, abort_flag);
+        int seg_q[2] = {0, 0}, np[2] = {0, 0};  // Q tiles and P tiles taken so far
+        int ring0 = 0;                          // ring entries before this segment
+        auto ring_wait = [&](int n) {           // n-th entry of the segment has landed
+          const int i = ring0 + n;
+          return mbar_wait(full(i % L::kRing), (i / L::kRing) & 1, tp_.timeout_ns, abort_flag);
+        };
+        for (; w.valid() && ok; w.next(p)) {
+          const Seg g(p, w);
+          const int n0 = g.count(0), n1 = g.count(1);
+          const int most = max(n0, n1);
+          // S of tile t's k-th key tile
+          auto issue_s = [&](int t, int k) -> bool {
+            const int rel = g.first(t) + k * g.step - g.lo;  // key tile within the segment
+            if (!ring_wait(2 * rel)) return false;
+            tc_fence_after();
+            const uint32_t ka = entry_at((ring0 + 2 * rel) % L::kRing);
+            const uint32_t qa = sb + (g.pair ? t : 0) * L::kOp;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
+              mma_bf16_ss(tS(t), sw128_desc(qa + off, 16u, 1024u), sw128_desc(ka + off, 16u, 1024u),
+                          id_s, kk > 0 ? 1u : 0u);
+            }
+            mma_commit(s_full(t));
+            // the last reader of the segment's Q, and of the key tile, frees them
+            if (g.pair ? k + 1 == (t ? n1 : n0) : rel + 1 == g.hi[1] - g.lo)
+              mma_commit(q_empty(g.pair ? t : 0));
+            if (!g.pair || t == 1) mma_commit(empty((ring0 + 2 * rel) % L::kRing));
+            return true;
+          };
+          auto issue_pv = [&](int t, int k) -> bool {
+            const int rel = g.first(t) + k * g.step - g.lo;
+            if (!ring_wait(2 * rel + 1)) return false;
+            if (!mbar_wait(p_full(t), np[t] & 1, tp_.timeout_ns, abort_flag)) return false;
+            ++np[t];
+            tc_fence_after();
+            const uint32_t va = entry_at((ring0 + 2 * rel + 1) % L::kRing);
+#pragma unroll
+            for (int kk = 0; kk < kTile / 16; ++kk)
+              mma_bf16_ts(tO(t), tP(t) + kk * 8, sw128_desc(va + kk * 2048, kTile * 128, 1024u), id_o,
+                          (k > 0 || kk > 0) ? 1u : 0u);
+            if (k + 1 == (t ? n1 : n0)) mma_commit(o_done(t));
+            if (!g.pair || t == 1) mma_commit(empty((ring0 + 2 * rel + 1) % L::kRing));
+            return true;
+          };
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (t == 0 || g.pair) {  // the rows' Q; in the other form both tiles read the first
+              ok = mbar_wait(q_full(t), seg_q[t] & 1, tp_.timeout_ns, abort_flag);
+              ++seg_q[t];
+            }
+            if (ok && (t ? n1 : n0) > 0)
+              ok = issue_s(t, 0);
+            else if (ok && g.pair)
+              mma_commit(q_empty(t));  // a tile whose rows see no key of the segment
+          }
+          for (int k = 0; k < most && ok; ++k)
+            for (int t = 0; t < 2 && ok; ++t) {
+              const int n = t ? n1 : n0;
+              if (k < n) ok = issue_pv(t, k);
+              if (k + 1 < n && ok) ok = issue_s(t, k + 1);
+            }
+          ring0 += 2 * (w.hi - w.lo);
+        }
+        if (!ok) timed_out();
+      }
+      __syncwarp();
+    } else if (warp == kLoadQ) {
+      // ---------------------------------------------------------------- Q loads
+      // A row tile is tpt tokens x G heads, in that order: a box of the qkv rows. Rows past
+      // the request's tokens are other requests' or zeros; nothing of them is written.
+      if (lane == 0) {
+        bool ok = true;
+        const int tpt = p.tpu / 2;
+        const uint32_t bytes = static_cast<uint32_t>(tpt) * p.G * D * 2;
+        for (; w.valid() && ok; w.next(p)) {
+          const Seg g(p, w);
+          const int head = w.vh * p.G, blk = head / p.hq;
+          for (int t = 0; t < (g.pair ? 2 : 1) && ok; ++t) {
+            if (issued_q[t] > 0)
+              ok = mbar_wait(q_empty(t), (issued_q[t] - 1) & 1, tp_.timeout_ns, abort_flag);
+            if (!ok) break;
+            mbar_arrive_expect_tx(q_full(t), bytes);
+            for (int h = 0; h < L::kHalves; ++h)
+              tma_load_4d(sb + t * L::kOp + h * (kTile * 128), &tp_.tq, q_full(t), h * 64,
+                          head - blk * p.hq, blk, w.q.row0 + w.u * p.tpu + t * tpt);
+            ++issued_q[t];
+          }
+        }
+        if (!ok) timed_out();
+      }
+      __syncwarp();
     }
-    __syncwarp();
   } else {
     // ---------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int t = warp >> 2, x = threadIdx.x & 127;  // tile, row within it = TMEM lane
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int tpt = p.tpu / 2, tt = x / p.Gv, hh = x - tt * p.Gv;
@@ -329,22 +409,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lim = !live ? kv_end
                             : p.causal ? min(kv_end, w.q.total - w.q.n + token + 1) : kv_end;
       const int lim_min = __reduce_min_sync(0xFFFFFFFFu, lim);
-      if (t == 0 || g.pair) {
-        // this row's Q: every S of the tile's previous segment has been read (s_full seen)
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.qkv) + row * p.ldq +
-                                   paged_qcol<D>(p, live ? head : 0);
-        const uint32_t dst = sb + t * L::kOp + x * 128;
-#pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          uint4 v = make_uint4(0, 0, 0, 0);
-          if (live) v = *reinterpret_cast<const uint4*>(src + c * 8);
-          st_shared_v4(dst + (c >> 3) * (kTile * 128) + (((c & 7) ^ (x & 7)) << 4), v.x, v.y, v.z,
-                       v.w);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full(t));
-      }
       const int n = g.count(t);
       float m = -INFINITY, l = 0.0f;
       for (int k = 0; k < n; ++k, ++ns) {
@@ -378,14 +442,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t miss = bad[seg_tile % kBadRing];
           if (k0 + kTile > lim_min || miss) {
 #pragma unroll
-            for (int i = 0; i < kTile; ++i) {
-              const bool hidden = k0 + i >= lim || ((miss >> (i >> min(p.ps_log2, 7))) & 1);
-              if (hidden) v[i] = 0xff800000u;  // -inf
+            for (int c = 0; c < 4; ++c) {  // bit i: key 32 c + i is seen
+              const int seen = min(max(lim - (k0 + 32 * c), 0), 32);
+              uint32_t bits = seen == 32 ? ~0u : (1u << seen) - 1u;
+              if (miss) {
+                const int sh = min(p.ps_log2, 5), span = 32 >> sh;  // pages within the 32 keys
+                for (int b = 0; b < span; ++b)
+                  if ((miss >> ((32 * c + (b << sh)) >> min(p.ps_log2, 7))) & 1)
+                    bits &= ~((sh == 5 ? ~0u : (1u << (1 << sh)) - 1u) << (b << sh));
+              }
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (!(bits & (1u << i))) v[32 * c + i] = 0xff800000u;  // -inf
             }
           }
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-          for (int i = 0; i < kTile; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(v[i]));
+          for (int i = 0; i < kTile; i += 8)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              mx[y] = max3(mx[y], __uint_as_float(v[i + 2 * y]), __uint_as_float(v[i + 2 * y + 1]));
           const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
           // The maximum moves only when it grows by more than 8 (weights up to 2^8 are
           // harmless in bf16 and fp32): o / l does not depend on it.
@@ -395,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           m = m1;
           if (k > 0 && __any_sync(0xFFFFFFFFu, move)) {
             // the tile's previous P V has completed: s_full's commit came after it
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[32];
               tmem_ld32(tO(t) + lanes + 32 * c, o);
@@ -405,21 +481,26 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st32(tO(t) + lanes + 32 * c, o);
             }
           }
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t sc2 = pair_of(p.scale_log2, p.scale_log2), mu2 = pair_of(-mu, -mu);
+          uint64_t sum[2] = {0, 0};
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             uint32_t pk[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const float a = ex2(fmaf(__uint_as_float(v[64 * c + 2 * i]), p.scale_log2, -mu));
-              const float b = ex2(fmaf(__uint_as_float(v[64 * c + 2 * i + 1]), p.scale_log2, -mu));
-              sum[(2 * i) & 3] += a;
-              sum[(2 * i + 1) & 3] += b;
+              float a, b;
+              split(fma2(pair_of(__uint_as_float(v[64 * c + 2 * i]),
+                                 __uint_as_float(v[64 * c + 2 * i + 1])), sc2, mu2), a, b);
+              a = ex2(a);
+              b = ex2(b);
+              sum[i & 1] = add2(sum[i & 1], pair_of(a, b));
               pk[i] = pack2(a, b);
             }
             tmem_st32(tP(t) + lanes + 32 * c, pk);
           }
-          l = l * f + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+          float sa, sb2;
+          split(add2(sum[0], sum[1]), sa, sb2);
+          l = l * f + (sa + sb2);
           tmem_st_wait();
         }
         tc_fence_before();
@@ -554,7 +635,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (*abort_flag) {
     volatile int no_abort = 0;
-    if (warp == kProd && lane == 0)  // the copies this CTA issued have landed
+    if (warp == kLoadQ && lane == 0)  // the copies this CTA issued have landed
+      for (int t = 0; t < 2; ++t)
+        if (issued_q[t] > 0) mbar_wait(q_full(t), (issued_q[t] - 1) & 1, kDrainNs, &no_abort);
+    if (warp == kProd && lane == 0)
       for (int e = 0; e < L::kRing; ++e) {
         const int n = issued > e ? (issued - 1 - e) / L::kRing : -1;  // last round of entry e
         if (n >= 0) mbar_wait(full(e), n & 1, kDrainNs, &no_abort);
@@ -591,7 +675,7 @@ tp_status tc_t(PagedTcParams& t, cudaStream_t st) {
 
 }  // namespace
 
-tp_status launch_paged_tc(const PagedParams& p, int d, cudaStream_t st) {
+tp_status launch_paged_tc(const PagedParams& p, int d, int N, cudaStream_t st) {
   PagedTcParams t{};
   t.p = p;
   paged_set_units(t.p, kTile, kUnitRows, 7);
@@ -600,6 +684,7 @@ tp_status launch_paged_tc(const PagedParams& p, int d, cudaStream_t st) {
   const int box = std::min(1 << p.ps_log2, kTile);
   TP_TRY(paged_cache_map(&t.tk, p.kc, rows, d, box));
   TP_TRY(paged_cache_map(&t.tv, p.vc, rows, d, box));
+  TP_TRY(paged_q_map(&t.tq, t.p, d, N));
   t.status = device_status_word();
   if (!t.status) return fail(TP_ERR_CUDA, "device status word unavailable");
   t.timeout_ns = wait_timeout_ns();

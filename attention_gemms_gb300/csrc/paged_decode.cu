@@ -478,6 +478,27 @@ tp_status paged_cache_map(CUtensorMap* m, const void* cache, int64_t rows, int d
   return TP_OK;
 }
 
+tp_status paged_q_map(CUtensorMap* m, const PagedParams& p, int d, int N) {
+  EncodeFn enc = encoder();
+  if (!enc) return fail(TP_ERR_CUDA, "cuTensorMapEncodeTiled entry point not available");
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(p.hq),
+                              static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(p.T)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(p.S) * 2,
+                                 static_cast<cuuint64_t>(p.ldq) * 2};
+  const int heads = std::min(p.G, p.hq);  // of one shard block
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(heads),
+                             static_cast<cuuint32_t>(p.G / heads),
+                             static_cast<cuuint32_t>(p.tpu / 2)};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p.qkv), dims,
+                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(TP_ERR_CUDA, "cuTensorMapEncodeTiled failed (code " + std::to_string(r) + ")");
+  return TP_OK;
+}
+
 tp_status launch_paged_decode(const PagedParams& p, int d, cudaStream_t st) {
   DecodeParams dp{};
   dp.p = p;
