@@ -84,16 +84,56 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32
 __device__ __forceinline__ void tmem_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-// D[tmem] (+)= A[tmem] * B[smem]: A's row is the TMEM lane, two bf16 per column
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                            uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
+// The products of one key tile, issued back to back. An MMA takes its operands from uniform
+// registers: issued inside a one-lane branch, each cost 80 to 100 cycles of moves, more
+// than the 64 that the tensor cores need for it. So the whole warp runs the MMA role on
+// values that the compiler can see to be the same in every lane, and only the instruction
+// itself is predicated to the leader; descriptors advance by constants in their low words
+// (addresses in 16-byte units).
+constexpr uint32_t kDescHi = 1024u >> 4 | 1u << 14 | 2u << 29;  // SBO 1024, version 1, SW128
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((lbo >> 4) << 16);
 }
+// D[tmem] = A[smem] * B[smem], both K-major, 16 steps' k at 32-byte steps and 64-wide halves
+template <int STEPS>
+__device__ __forceinline__ void mma_qk(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
+#pragma unroll
+  for (int kk = 0; kk < STEPS; ++kk) {
+    const uint32_t off = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d),
+        "r"(a_lo + off), "r"(b_lo + off), "n"(kDescHi), "r"(idesc), "r"(kk > 0 ? 1u : 0u)
+        : "memory");
+  }
+}
+// D[tmem] (+)= A[tmem] * B[smem]: A's row is the TMEM lane, two bf16 per column (8 columns
+// per step of 16 keys); B MN-major, 16 keys are 2048 bytes
+template <int STEPS>
+__device__ __forceinline__ void mma_pv(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t idesc,
+                                       uint32_t accumulate) {
+#pragma unroll
+  for (int kk = 0; kk < STEPS; ++kk)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+        "mov.b64 db, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
+        "r"(a + kk * 8), "r"(b_lo + kk * (2048 >> 4)), "n"(kDescHi), "r"(idesc),
+        "r"(kk > 0 ? 1u : accumulate)
+        : "memory");
+}
+// one lane of the converged warp, always the same one
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+__device__ __forceinline__ int same(int v) { return __shfl_sync(0xFFFFFFFFu, v, 0); }
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* m, uint32_t bar,
                                             int32_t x, int32_t y, int32_t z, int32_t w) {
   asm volatile(
@@ -124,11 +164,6 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ float ex2(float x) {  // relative error about 2^-22
@@ -288,75 +323,79 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok && lane == 0) timed_out();
     } else if (warp == kMma) {
       // ---------------------------------------------------------------- MMA issuer
-      if (lane == 0) {
+      {
         const uint32_t id_s = idesc_bf16_f32(128, kTile, 0, 0);  // Q, K both K-major
         const uint32_t id_o = idesc_bf16_f32(128, D, 0, 1);      // P in TMEM, V MN-major
-        bool ok = true;
-        if (tp_.debug_hang) ok = mbar_wait(drain, 0, tp_.timeout_ns, abort_flag);
-        int seg_q[2] = {0, 0}, np[2] = {0, 0};  // Q tiles and P tiles taken so far
-        int ring0 = 0;                          // ring entries before this segment
-        auto ring_wait = [&](int n) {           // n-th entry of the segment has landed
-          const int i = ring0 + n;
-          return mbar_wait(full(i % L::kRing), (i / L::kRing) & 1, tp_.timeout_ns, abort_flag);
+        const uint32_t tm = same(tmem), sbase = same(sb);
+        auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+          return same(mbar_wait(bar, parity, tp_.timeout_ns, abort_flag)) != 0;
         };
-        for (; w.valid() && ok; w.next(p)) {
+        bool ok = true;
+        if (tp_.debug_hang) ok = wait(drain, 0);
+        uint32_t seg_q = 0, np = 0;  // bit t: parity of tile t's next Q, next P
+        uint32_t base = 0;           // ring entries before the segment
+        for (; same(w.valid() && ok); w.next(p)) {
           const Seg g(p, w);
-          const int n0 = g.count(0), n1 = g.count(1);
+          const int n0 = same(g.count(0)), n1 = same(g.count(1));
+          const int tiles = same(w.hi - w.lo);
+          const bool pair = same(g.pair) != 0;
           const int most = max(n0, n1);
-          // S of tile t's k-th key tile
-          auto issue_s = [&](int t, int k) -> bool {
-            const int rel = g.first(t) + k * g.step - g.lo;  // key tile within the segment
-            if (!ring_wait(2 * rel)) return false;
-            tc_fence_after();
-            const uint32_t ka = entry_at((ring0 + 2 * rel) % L::kRing);
-            const uint32_t qa = sb + (g.pair ? t : 0) * L::kOp;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
-              mma_bf16_ss(tS(t), sw128_desc(qa + off, 16u, 1024u), sw128_desc(ka + off, 16u, 1024u),
-                          id_s, kk > 0 ? 1u : 0u);
-            }
-            mma_commit(s_full(t));
-            // the last reader of the segment's Q, and of the key tile, frees them
-            if (g.pair ? k + 1 == (t ? n1 : n0) : rel + 1 == g.hi[1] - g.lo)
-              mma_commit(q_empty(g.pair ? t : 0));
-            if (!g.pair || t == 1) mma_commit(empty((ring0 + 2 * rel) % L::kRing));
-            return true;
-          };
-          auto issue_pv = [&](int t, int k) -> bool {
-            const int rel = g.first(t) + k * g.step - g.lo;
-            if (!ring_wait(2 * rel + 1)) return false;
-            if (!mbar_wait(p_full(t), np[t] & 1, tp_.timeout_ns, abort_flag)) return false;
-            ++np[t];
-            tc_fence_after();
-            const uint32_t va = entry_at((ring0 + 2 * rel + 1) % L::kRing);
-#pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-              mma_bf16_ts(tO(t), tP(t) + kk * 8, sw128_desc(va + kk * 2048, kTile * 128, 1024u), id_o,
-                          (k > 0 || kk > 0) ? 1u : 0u);
-            if (k + 1 == (t ? n1 : n0)) mma_commit(o_done(t));
-            if (!g.pair || t == 1) mma_commit(empty((ring0 + 2 * rel + 1) % L::kRing));
-            return true;
-          };
-          for (int t = 0; t < 2 && ok; ++t) {
-            if (t == 0 || g.pair) {  // the rows' Q; in the other form both tiles read the first
-              ok = mbar_wait(q_full(t), seg_q[t] & 1, tp_.timeout_ns, abort_flag);
-              ++seg_q[t];
-            }
-            if (ok && (t ? n1 : n0) > 0)
-              ok = issue_s(t, 0);
-            else if (ok && g.pair)
-              mma_commit(q_empty(t));  // a tile whose rows see no key of the segment
-          }
-          for (int k = 0; k < most && ok; ++k)
-            for (int t = 0; t < 2 && ok; ++t) {
+          // One copy of the code, rolled over the tiles: unrolled, the role's instructions
+          // fell out of the instruction cache that the softmax warps fill.
+          // Step k of tile t: O += P V of its k-th key tile, then S of the next.
+#pragma unroll 1
+          for (int k = -1; k < most && ok; ++k)
+#pragma unroll 1
+            for (int t = 0; t < 2; ++t) {
               const int n = t ? n1 : n0;
-              if (k < n) ok = issue_pv(t, k);
-              if (k + 1 < n && ok) ok = issue_s(t, k + 1);
+              // a tile's key tiles come one after the other, or every second one; the second
+              // tile of a pair finds them there: the first has waited, unless it ended
+              const bool late = t == 0 || !pair;
+              if (k >= 0 && k < n) {
+                const uint32_t i = base + 2 * (pair ? k : 2 * k + t) + 1, e = i % L::kRing;
+                ok = ok && (!(late || k >= n0) || wait(bar0 + 8 * e, (i / L::kRing) & 1));
+                ok = ok && wait(p_full(t), (np >> t) & 1);
+                if (!ok) break;
+                np ^= 1u << t;
+                tc_fence_after();
+                if (elect_one()) {
+                  mma_pv<kTile / 16>(tm + L::kO + L::kOStep * t, tm + L::kP + L::kPStep * t,
+                                     desc_lo(sbase + L::kOffRing + e * L::kOp, kTile * 128), id_o,
+                                     k > 0);
+                  if (k + 1 == n) mma_commit(o_done(t));
+                  if (!pair || t == 1) mma_commit(empty(e));
+                }
+                __syncwarp();
+              }
+              if (k < 0 && (t == 0 || pair)) {  // the rows' Q; one for both tiles of the other form
+                ok = wait(q_full(t), (seg_q >> t) & 1);
+                if (!ok) break;
+                seg_q ^= 1u << t;
+                if (n == 0 && elect_one()) mma_commit(q_empty(t));  // its rows see no key here
+                __syncwarp();
+              }
+              if (k + 1 < n) {
+                const uint32_t i = base + 2 * (pair ? k + 1 : 2 * (k + 1) + t), e = i % L::kRing;
+                if ((late || k + 1 >= n0) && !wait(bar0 + 8 * e, (i / L::kRing) & 1)) {
+                  ok = false;
+                  break;
+                }
+                tc_fence_after();
+                if (elect_one()) {
+                  mma_qk<D / 16>(tm + 128 * t, desc_lo(sbase + (pair ? t : 0) * L::kOp, 16),
+                                 desc_lo(sbase + L::kOffRing + e * L::kOp, 16), id_s);
+                  mma_commit(s_full(t));
+                  // the last reader of the segment's Q, and of the key tile, frees them
+                  if (pair ? k + 2 == n : 2 * (k + 1) + t + 1 == n0 + n1)
+                    mma_commit(q_empty(pair ? t : 0));
+                  if (!pair || t == 1) mma_commit(empty(e));
+                }
+                __syncwarp();
+              }
             }
-          ring0 += 2 * (w.hi - w.lo);
+          base += 2 * tiles;
         }
-        if (!ok) timed_out();
+        if (!ok && lane == 0) timed_out();
       }
       __syncwarp();
     } else if (warp == kLoadQ) {
@@ -643,8 +682,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = issued > e ? (issued - 1 - e) / L::kRing : -1;  // last round of entry e
         if (n >= 0) mbar_wait(full(e), n & 1, kDrainNs, &no_abort);
       }
-    if (warp == kMma && lane == 0) {  // and the MMAs it issued have completed
-      mma_commit(drain);
+    if (warp == kMma) {  // and the MMAs it issued have completed
+      if (elect_one()) mma_commit(drain);
+      __syncwarp();
       mbar_wait(drain, 0, kDrainNs, &no_abort);
     }
   }
