@@ -4,7 +4,8 @@
 // A unit is 256 rows, two TMEM tiles of 128 rows (whole tokens x the query heads of one
 // key/value head, so a key tile serves the whole group), keys in tiles of 128.
 //   producer warp: page ids 32 at a time, one TMA box per page, 64-column half and tensor
-//     into a ring of K and V tiles (K0 V0 K1 V1 ...); pages outside the cache or past the
+//     into a ring of K and V tiles, V of a key tile and K of the next one to be multiplied
+//     under one barrier (the operands of one turn); pages outside the cache or past the
 //     unit's keys are boxes outside the tensor and arrive as zeros;
 //   MMA warp (one lane): S = Q K^T into TMEM, and O += P V with P read from TMEM;
 //   eight softmax warps, four per tile, a thread per row: S out of TMEM, the running
@@ -42,6 +43,7 @@ constexpr int kProd = 8, kMma = 9, kLoadQ = 10, kThreads = 384;
 // (128 x 80 + 256 x 208 = 63488 of the launch's 64512) so that a row's 128 scores stay in
 // the softmax threads' registers.
 constexpr int kRegsLoad = 80, kRegsSoftmax = 208;
+constexpr int kLoads = 16;  // barriers of loads in flight (at most a ring's tiles)
 constexpr int kBadRing = 16;
 constexpr uint64_t kDrainNs = 20000000ull;
 
@@ -63,7 +65,7 @@ struct Lay {
   static constexpr int kRing = D == 128 ? 5 : 10;
   static constexpr int kOffRing = 2 * kOp;
   static constexpr int kOffBar = kOffRing + kRing * kOp;
-  static constexpr int kBars = 2 * kRing + 13;
+  static constexpr int kBars = 2 * kLoads + 13;
   static constexpr int kSmem = kOffBar + kBars * 8 + kBadRing * 4 + 16 + 1024;
   static constexpr uint32_t kO = 256, kOStep = D;                     // TMEM columns
   static constexpr uint32_t kP = D == 128 ? 0 : 384, kPStep = D == 128 ? 128 : 64;
@@ -217,9 +219,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* tmem_slot = const_cast<uint32_t*>(bad) + kBadRing;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const uint32_t bar0 = smem_u32(bars);
-  auto full = [&](int e) { return bar0 + 8u * e; };
-  auto empty = [&](int e) { return bar0 + 8u * (L::kRing + e); };
-  auto bar_at = [&](int i) { return bar0 + 8u * (2 * L::kRing + i); };
+  auto full = [&](uint32_t l) { return bar0 + 8u * (l % kLoads); };
+  auto empty = [&](uint32_t l) { return bar0 + 8u * (kLoads + l % kLoads); };
+  auto round_of = [](uint32_t l) { return (l / kLoads) & 1u; };
+  auto bar_at = [&](int i) { return bar0 + 8u * (2 * kLoads + i); };
   auto q_full = [&](int t) { return bar_at(t); };
   auto s_full = [&](int t) { return bar_at(2 + t); };
   auto p_full = [&](int t) { return bar_at(4 + t); };
@@ -229,9 +232,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ PagedSched sc;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int e = 0; e < L::kRing; ++e) {
-      mbar_init(full(e), 1);
-      mbar_init(empty(e), 1);
+    for (int l = 0; l < kLoads; ++l) {
+      mbar_init(full(l), 1);
+      mbar_init(empty(l), 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(q_full(t), 1);
@@ -265,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     atomicCAS(tp_.status, 0, static_cast<int>(TP_ERR_TIMEOUT));
     atomicAdd(tp_.status + 1, 1);
   };
-  int issued = 0;             // K/V loads: ring entries issued
+  uint32_t issued = 0;        // K/V loads issued
   int issued_q[2] = {0, 0};   // Q loads: tiles issued
 
   if (warp >= 8) {
@@ -274,8 +277,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------------- TMA producer
       const int ps = 1 << p.ps_log2, box = min(ps, kTile), boxes = kTile / box;
       bool ok = true;
-      int tiles = 0;
+      uint32_t tiles = 0, slot = 0, freed = 0, sizes = 0;  // bit l % 32: load l has two tiles
+      int room = L::kRing;
       for (; w.valid() && ok; w.next(p)) {
+        const Seg g(p, w);
+        const int n = w.hi - w.lo, c = g.pair ? 1 : 2;
         const int j = w.vh / p.hs;
         const int kend = paged_unit_kend(p, w.q, w.u);
         const int32_t* tab = p.table + static_cast<int64_t>(w.r) * p.max_pages;
@@ -287,37 +293,63 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         int base = (w.lo * kTile) >> p.ps_log2;
         int ids = fetch(base), ahead = fetch(base + 32);
-        for (int tile = w.lo; tile < w.hi && ok; ++tile, ++tiles) {
-          const int k0 = tile * kTile, pg0 = k0 >> p.ps_log2;
-          if (pg0 - base >= 32) {  // tiles are whole groups of at most 16 pages
+        int next = w.lo, y0 = 0, y1 = 0, y = 0;  // cache rows of this lane's page: the last tiles
+        // the next key tile's rows (tiles are whole groups of at most 16 pages)
+        auto locate = [&] {
+          const int k0 = next * kTile, pg0 = k0 >> p.ps_log2;
+          if (pg0 - base >= 32) {
             base += 32;
             ids = ahead;
             ahead = fetch(base + 32);
           }
           const int src = __shfl_sync(0xFFFFFFFFu, ids, (pg0 - base + min(lane, boxes - 1)) & 31);
           const uint32_t missing = __ballot_sync(0xFFFFFFFFu, lane < boxes && src < 0);
-          const int y = src < 0 ? tp_.cache_rows
-                                : (((src * p.Hkv + j) << p.ps_log2) + (k0 & (ps - 1)));
-#pragma unroll
-          for (int is_v = 0; is_v < 2; ++is_v) {
-            const int e = issued % L::kRing, round = issued / L::kRing;
-            if (round > 0 && !__all_sync(0xFFFFFFFFu, mbar_wait(empty(e), (round - 1) & 1,
-                                                                tp_.timeout_ns, abort_flag))) {
-              ok = false;
-              break;
-            }
-            if (lane == 0) {
-              if (!is_v) bad[tiles % kBadRing] = missing;
-              mbar_arrive_expect_tx(full(e), L::kOp);
-            }
-            __syncwarp();
-            if (lane < boxes)
-#pragma unroll
-              for (int h = 0; h < L::kHalves; ++h)
-                tma_load_2d(entry_at(e) + h * (kTile * 128) + lane * box * 128,
-                            is_v ? &tp_.tv : &tp_.tk, full(e), h * 64, y);
-            ++issued;
+          if (lane == 0) bad[tiles % kBadRing] = missing;
+          y0 = y1;
+          y1 = y;
+          y = src < 0 ? tp_.cache_rows
+                      : (((src * p.Hkv + j) << p.ps_log2) + (k0 & (ps - 1)));
+          ++next;
+          ++tiles;
+        };
+        // room for a load's tiles, then its barrier's count
+        auto begin = [&](int size) -> bool {
+          while (room < size) {
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(empty(freed), round_of(freed), tp_.timeout_ns,
+                                                   abort_flag)))
+              return false;
+            room += 1 + ((sizes >> (freed % 32)) & 1);
+            ++freed;
           }
+          room -= size;
+          sizes = (sizes & ~(1u << (issued % 32))) | static_cast<uint32_t>(size - 1) << (issued % 32);
+          if (lane == 0) mbar_arrive_expect_tx(full(issued), size * L::kOp);
+          __syncwarp();
+          return true;
+        };
+        auto copy = [&](const CUtensorMap* m, int row) {
+          if (lane < boxes)
+#pragma unroll
+            for (int h = 0; h < L::kHalves; ++h)
+              tma_load_2d(entry_at(slot) + h * (kTile * 128) + lane * box * 128, m, full(issued),
+                          h * 64, row);
+          if (++slot == L::kRing) slot = 0;
+        };
+        const int lead = min(c, n);
+        for (int i = 0; i < lead; ++i) locate();
+        if (!(ok = begin(lead))) break;
+        if (lead > 1) copy(&tp_.tk, y1);
+        copy(&tp_.tk, y);
+        ++issued;
+        for (int m = 0; m < n; ++m) {
+          const bool more = m + c < n;
+          if (more) locate();  // its mask is written before the barrier's arrival
+          if (!(ok = begin(more ? 2 : 1))) break;
+          // V of tile m: c tiles (fewer at the end) before the last located one
+          const int back = next - 1 - (w.lo + m);
+          copy(&tp_.tv, back == 0 ? y : back == 1 ? y1 : y0);
+          if (more) copy(&tp_.tk, y);
+          ++issued;
         }
       }
       if (!ok && lane == 0) timed_out();
@@ -333,67 +365,72 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         if (tp_.debug_hang) ok = wait(drain, 0);
         uint32_t seg_q = 0, np = 0;  // bit t: parity of tile t's next Q, next P
-        uint32_t base = 0;           // ring entries before the segment
+        uint32_t load = 0, slot = 0;
+        auto s_of = [&](uint32_t t, uint32_t q, uint32_t ks) {
+          mma_qk<D / 16>(tm + 128 * t, desc_lo(sbase + q * L::kOp, 16),
+                         desc_lo(sbase + L::kOffRing + ks * L::kOp, 16), id_s);
+          mma_commit(s_full(t));
+        };
         for (; same(w.valid() && ok); w.next(p)) {
           const Seg g(p, w);
-          const int n0 = same(g.count(0)), n1 = same(g.count(1));
-          const int tiles = same(w.hi - w.lo);
+          const int n0 = same(g.count(0)), n = same(w.hi - w.lo);
           const bool pair = same(g.pair) != 0;
-          const int most = max(n0, n1);
-          // One copy of the code, rolled over the tiles: unrolled, the role's instructions
-          // fell out of the instruction cache that the softmax warps fill.
-          // Step k of tile t: O += P V of its k-th key tile, then S of the next.
-#pragma unroll 1
-          for (int k = -1; k < most && ok; ++k)
-#pragma unroll 1
-            for (int t = 0; t < 2; ++t) {
-              const int n = t ? n1 : n0;
-              // a tile's key tiles come one after the other, or every second one; the second
-              // tile of a pair finds them there: the first has waited, unless it ended
-              const bool late = t == 0 || !pair;
-              if (k >= 0 && k < n) {
-                const uint32_t i = base + 2 * (pair ? k : 2 * k + t) + 1, e = i % L::kRing;
-                ok = ok && (!(late || k >= n0) || wait(bar0 + 8 * e, (i / L::kRing) & 1));
-                ok = ok && wait(p_full(t), (np >> t) & 1);
-                if (!ok) break;
-                np ^= 1u << t;
-                tc_fence_after();
-                if (elect_one()) {
-                  mma_pv<kTile / 16>(tm + L::kO + L::kOStep * t, tm + L::kP + L::kPStep * t,
-                                     desc_lo(sbase + L::kOffRing + e * L::kOp, kTile * 128), id_o,
-                                     k > 0);
-                  if (k + 1 == n) mma_commit(o_done(t));
-                  if (!pair || t == 1) mma_commit(empty(e));
-                }
-                __syncwarp();
-              }
-              if (k < 0 && (t == 0 || pair)) {  // the rows' Q; one for both tiles of the other form
-                ok = wait(q_full(t), (seg_q >> t) & 1);
-                if (!ok) break;
-                seg_q ^= 1u << t;
-                if (n == 0 && elect_one()) mma_commit(q_empty(t));  // its rows see no key here
-                __syncwarp();
-              }
-              if (k + 1 < n) {
-                const uint32_t i = base + 2 * (pair ? k + 1 : 2 * (k + 1) + t), e = i % L::kRing;
-                if ((late || k + 1 >= n0) && !wait(bar0 + 8 * e, (i / L::kRing) & 1)) {
-                  ok = false;
-                  break;
-                }
-                tc_fence_after();
-                if (elect_one()) {
-                  mma_qk<D / 16>(tm + 128 * t, desc_lo(sbase + (pair ? t : 0) * L::kOp, 16),
-                                 desc_lo(sbase + L::kOffRing + e * L::kOp, 16), id_s);
-                  mma_commit(s_full(t));
-                  // the last reader of the segment's Q, and of the key tile, frees them
-                  if (pair ? k + 2 == n : 2 * (k + 1) + t + 1 == n0 + n1)
-                    mma_commit(q_empty(pair ? t : 0));
-                  if (!pair || t == 1) mma_commit(empty(e));
-                }
-                __syncwarp();
-              }
+          const int c = pair ? 1 : 2, lead = min(c, n);
+          // the rows' Q (one for both tiles when they share rows) and the first key tiles
+          ok = wait(q_full(0), seg_q & 1) && (!pair || wait(q_full(1), seg_q >> 1)) &&
+               wait(full(load), round_of(load));
+          seg_q ^= pair ? 3 : 1;
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            if (pair ? n0 > 0 : true) s_of(0, 0, slot);
+            if (pair ? n0 < 2 : n == 1) mma_commit(q_empty(0));
+            if (pair || n > 1) {
+              const uint32_t ks = slot + (pair ? 0 : 1);
+              s_of(1, pair, ks < L::kRing ? ks : 0);
+              if (pair ? n == 1 : n == 2) mma_commit(q_empty(pair));
             }
-          base += 2 * tiles;
+            mma_commit(empty(load));
+          }
+          __syncwarp();
+          ++load;
+          slot += lead;
+          if (slot >= L::kRing) slot -= L::kRing;
+          // Load m + 1: V of key tile m and K of tile m + c, the operands of one turn (of two
+          // turns for a pair): O += P V of the tile, then S of the row tile's next one.
+#pragma unroll 1
+          for (int m = 0; m < n; ++m) {
+            const uint32_t ks = slot + 1 < L::kRing ? slot + 1 : 0;
+            ok = wait(full(load), round_of(load));
+            if (!ok) break;
+            const int t1 = pair ? 1 : m & 1;
+#pragma unroll 1
+            for (int t = pair ? 0 : t1; t <= t1; ++t) {
+              const int left = pair ? (t ? n : n0) - m : (n - m + 1) >> 1;  // the row tile's own
+              if (left <= 0) continue;
+              ok = wait(p_full(t), (np >> t) & 1);
+              if (!ok) break;
+              np ^= 1u << t;
+              tc_fence_after();
+              if (elect_one()) {
+                mma_pv<kTile / 16>(tm + L::kO + L::kOStep * t, tm + L::kP + L::kPStep * t,
+                                   desc_lo(sbase + L::kOffRing + slot * L::kOp, kTile * 128), id_o,
+                                   m >= c);
+                if (left > 1)
+                  s_of(t, pair ? t : 0, ks);
+                else
+                  mma_commit(o_done(t));
+                if (t == t1) mma_commit(empty(load));
+                // the last S of the segment frees its Q
+                if (pair ? left == 2 : m + 3 == n) mma_commit(q_empty(pair ? t : 0));
+              }
+              __syncwarp();
+            }
+            if (!ok) break;
+            ++load;
+            slot += m + c < n ? 2 : 1;
+            if (slot >= L::kRing) slot -= L::kRing;
+          }
         }
         if (!ok && lane == 0) timed_out();
       }
@@ -432,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tpt = p.tpu / 2, tt = x / p.Gv, hh = x - tt * p.Gv;
     float* piece = tp_.joins + static_cast<int64_t>(blockIdx.x) * kTile * (D + 2);
     PagedRec rec{0, 0, 0, 0, 0};
-    int ns = 0, segs_o = 0, joined = 0, tiles0 = 0;
+    int ns = 0, segs_o = 0, joined = 0, tiles0 = 0, segs = 0;
     bool ok = true;
     auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool {
       return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, tp_.timeout_ns, abort_flag)) != 0;
@@ -460,12 +497,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int seg_tile = tiles0 + tile - g.lo;
         if (k0 + kTile > kv_end) {
           // V rows past the request's keys may hold anything and 0 * NaN would spoil O
-          const int e = 2 * seg_tile + 1;
-          if (!wait_all(full(e % L::kRing), (e / L::kRing) & 1)) {
+          const int mm = tile - g.lo, nn = w.hi - w.lo;  // V's load and place in the ring
+          const uint32_t l = static_cast<uint32_t>(tiles0 + segs + 1 + mm);
+          const int at = 2 * tiles0 + (mm == nn - 1 ? 2 * nn - 1 : g.pair ? 1 + 2 * mm : 2 + 2 * mm);
+          if (!wait_all(full(l), round_of(l))) {
             ok = false;
             break;
           }
-          const uint32_t va = entry_at(e % L::kRing);
+          const uint32_t va = entry_at(at % L::kRing);
           if (k0 + x >= kv_end)
 #pragma unroll
             for (int c = 0; c < D / 8; ++c)
@@ -547,6 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(p_full(t));
       }
       tiles0 += w.hi - w.lo;
+      ++segs;
       if (!ok) break;
       if (n > 0) {  // the last P V
         if (!wait_all(o_done(t), segs_o & 1)) {
@@ -678,10 +718,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int t = 0; t < 2; ++t)
         if (issued_q[t] > 0) mbar_wait(q_full(t), (issued_q[t] - 1) & 1, kDrainNs, &no_abort);
     if (warp == kProd && lane == 0)
-      for (int e = 0; e < L::kRing; ++e) {
-        const int n = issued > e ? (issued - 1 - e) / L::kRing : -1;  // last round of entry e
-        if (n >= 0) mbar_wait(full(e), n & 1, kDrainNs, &no_abort);
-      }
+      for (uint32_t l = issued > kLoads ? issued - kLoads : 0; l < issued; ++l)
+        mbar_wait(full(l), round_of(l), kDrainNs, &no_abort);
     if (warp == kMma) {  // and the MMAs it issued have completed
       if (elect_one()) mma_commit(drain);
       __syncwarp();
