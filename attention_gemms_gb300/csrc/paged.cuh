@@ -32,7 +32,7 @@ struct PagedParams {
   const int32_t *table, *total, *cu;
   void* o;
   float* lse;              // (H, T), may be null
-  float* part;             // partial results: per slot m (rows), l (rows), O (rows, d)
+  float* part;             // partial results: per slot m (rows), l (rows), O (rows x d)
   struct PagedRec* rec;    // one per CTA
   int64_t T;               // rows of qkv, o, lse
   int64_t ldq, S;          // qkv row pitch, shard block width (elements)

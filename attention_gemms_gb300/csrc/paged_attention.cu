@@ -262,8 +262,12 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedPara
   const int64_t floats = static_cast<int64_t>(unit_rows) * (D + 2);
   auto slot_of = [&](int k) { return p.part + (2 * static_cast<int64_t>(k) + (k == i ? 1 : 0)) * floats; };
   constexpr int CG = D / 4;
+  // Slots of two tiles hold O by groups of 4 columns, (d / 4, rows, 4), as their kernel has a
+  // thread per row; the others by rows. Threads follow the slots' order.
+  const bool by_cols = unit_rows > tile_rows;
   for (int e = blockIdx.y * kThreads + tid; e < unit_rows * CG; e += kThreads * gridDim.y) {
-    const int row = e / CG, c = (e - row * CG) * 4;
+    const int row = by_cols ? e % unit_rows : e / CG;
+    const int c = (by_cols ? e / unit_rows : e % CG) * 4;
     int token, head;
     if (!unit_row(p, q, rec.u, rec.vh, tile_rows, row, &token, &head)) continue;
     float m = -INFINITY, l = 0.0f, f[4] = {0.f, 0.f, 0.f, 0.f};
@@ -272,7 +276,7 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedPara
       const float* s = slot_of(k);
       const float mk = s[row], lk = s[unit_rows + row];
       float ok[4];
-      load4(s + 2 * unit_rows + row * D + c, ok);
+      load4(s + 2 * unit_rows + 4 * e, ok);
       const float m1 = fmaxf(m, mk), mu = m1 == -INFINITY ? 0.0f : m1;
       const float w0 = exp2f(m - mu), w1 = exp2f(mk - mu);
       l = l * w0 + lk * w1;

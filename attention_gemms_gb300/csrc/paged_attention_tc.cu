@@ -179,6 +179,28 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// 4 x 4 transpose over the lanes of a quad: chunk i of lane y becomes chunk y of lane i
+__device__ __forceinline__ void quad_transpose(uint32_t (&q)[4][4]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int s = 1; s <= 2; s <<= 1) {
+    const bool up = lane & s;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & s) continue;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const uint32_t give = up ? q[i][y] : q[i | s][y];
+        const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, give, s);
+        if (up)
+          q[i][y] = got;
+        else
+          q[i | s][y] = got;
+      }
+    }
+  }
+}
+
 // A segment as every role sees it: key tiles of each row tile. pair: tile t takes the tiles
 // lo .. hi_t - 1 of its own rows; else tile t takes lo + t, lo + t + 2, ... of the same rows.
 struct Seg {
@@ -616,7 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (live)
 #pragma unroll
               for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint4*>(piece + 2 * kTile + x * D + 32 * c + 4 * i) =
+                *reinterpret_cast<uint4*>(piece + 2 * kTile + ((8 * c + i) * kTile + x) * 4) =
                     make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
           piece[x] = m;
@@ -649,6 +671,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* slot =
           p.part + static_cast<int64_t>(2 * blockIdx.x + (begins ? 1 : 0)) * kUnitRows * (D + 2);
       const int ur = (g.pair ? t : 0) * kTile + x;
+      int64_t quad_dst[4];  // where the quad's rows go, -1: nowhere
+      {
+        const int64_t dst = live ? row * p.H * D + static_cast<int64_t>(head) * D : -1;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) quad_dst[i] = __shfl_sync(0xFFFFFFFFu, dst, (lane & ~3) + i);
+      }
 #pragma unroll 1
       for (int c = 0; c < D / 32 && busy; ++c) {
         uint32_t o[32];
@@ -667,28 +695,36 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
               const float4 y =
-                  __ldcg(reinterpret_cast<const float4*>(piece + 2 * kTile + x * D + 32 * c + 4 * i));
+                  __ldcg(reinterpret_cast<const float4*>(piece + 2 * kTile + ((8 * c + i) * kTile + x) * 4));
               o[4 * i] = __float_as_uint(__uint_as_float(o[4 * i]) + y.x * gb);
               o[4 * i + 1] = __float_as_uint(__uint_as_float(o[4 * i + 1]) + y.y * gb);
               o[4 * i + 2] = __float_as_uint(__uint_as_float(o[4 * i + 2]) + y.z * gb);
               o[4 * i + 3] = __float_as_uint(__uint_as_float(o[4 * i + 3]) + y.w * gb);
             }
-          if (whole) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + row * p.H * D +
-                                                  static_cast<int64_t>(head) * D + 32 * c);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float* s = reinterpret_cast<const float*>(o + 8 * i);
-              dst[i] = make_uint4(pack2(s[0], s[1]), pack2(s[2], s[3]), pack2(s[4], s[5]),
-                                  pack2(s[6], s[7]));
-            }
-          } else {
+          if (!whole) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<uint4*>(slot + 2 * kUnitRows + static_cast<int64_t>(ur) * D + 32 * c +
-                                        4 * i) =
+              *reinterpret_cast<uint4*>(slot + 2 * kUnitRows + ((8 * c + i) * kUnitRows + ur) * 4) =
                   make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
+        }
+        if (whole) {
+          // Four lanes trade 16-byte chunks so that they store 64 bytes of one row at once:
+          // a store instruction then touches 8 lines instead of 32, whose accesses cost a
+          // unit's end about 5000 cycles.
+          uint32_t q[4][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+              q[i][y] = pack2(__uint_as_float(o[8 * i + 2 * y]), __uint_as_float(o[8 * i + 2 * y + 1]));
+          quad_transpose(q);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)  // row of lane (lane & ~3) + i, its chunk lane & 3
+            if (quad_dst[i] >= 0)
+              *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + quad_dst[i] + 32 * c +
+                                        8 * (lane & 3)) =
+                  make_uint4(q[i][0], q[i][1], q[i][2], q[i][3]);
         }
       }
       if (joins) {
