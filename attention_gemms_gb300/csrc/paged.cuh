@@ -4,10 +4,11 @@
 // The work of one call is a line of key tiles. Request r with n new tokens has, for each
 // of Hv head groups, ceil(n / tpu) units of tpu tokens x Gv query heads that share a
 // key/value head; a unit's tiles are the KT-key tiles that its last token may see (at
-// least one, so that rows that see no key are written too). CTA i of g takes tiles
-// [i total / g, (i + 1) total / g) of the line, whatever units they fall into: every CTA
-// gets the same number of tiles for any mix of lengths, and a long context is split over
-// the whole GPU without a setting. A unit that lies in one CTA is finished there; else
+// least one, so that rows that see no key are written too), after a start cost of unit_cost
+// tiles (queries, first loads, the output: what a unit takes beside its tiles). CTA i of g
+// takes [i total / g, (i + 1) total / g) of the line, whatever units that falls into: every
+// CTA gets the same work for any mix of lengths, and a long context is split over the whole
+// GPU without a setting. A unit that lies in one CTA is finished there; else
 // each CTA leaves its rows' (maximum, sum, unnormalised output) in its slot of the
 // workspace and the combine kernel joins them in key order. At most one unit begins and
 // one ends inside other CTAs' ranges, so two slots per CTA are enough for any lengths.
@@ -42,6 +43,8 @@ struct PagedParams {
   float scale_log2;        // log2(e) / sqrt(d)
   int hs, Gv, Hv;          // head groups per key/value head, heads per group, Hkv * hs
   int tpu, kt_log2;        // tokens per unit, keys per tile
+  int tpu_log2;            // -1: not a power of two
+  int unit_cost;           // of a unit, beside its tiles, in tiles
   int only_rows;           // > 0: only requests of at most that many rows per head group;
                            // < 0: only requests of more than -only_rows
 };
@@ -89,61 +92,86 @@ __device__ __forceinline__ int paged_unit_tiles(const PagedParams& p, const Page
                                   (1 << p.kt_log2) - 1) >> p.kt_log2));
 }
 
-// sum over i < n of floor((a i + b) / m), b >= 0 (the Euclid-like recurrence on the
-// lattice points under a line)
-__device__ __forceinline__ int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+// division by a small number, in 32 bits where that holds it (64 bits: a long call)
+__device__ __forceinline__ int64_t div_by(int64_t a, int b) {
+  return (static_cast<uint64_t>(a) >> 32) == 0
+             ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b))
+             : a / b;
+}
+
+// sum over i < n of floor((a i + b) / 2^k), b >= 0: the Euclid-like recurrence on the
+// lattice points under a line
+__device__ __forceinline__ int64_t floor_sum(int64_t n, int k, int a, int64_t b) {
   int64_t ans = 0;
+  int m = 1 << k;
   while (n > 0) {
     if (a >= m) {
       ans += (n - 1) * n / 2 * (a / m);
       a %= m;
     }
     if (b >= m) {
-      ans += n * (b / m);
-      b %= m;
+      const int64_t d = div_by(b, m);
+      ans += n * d;
+      b -= d * m;
     }
     const int64_t y = a * n + b;
     if (y < m) break;
-    n = y / m;
-    b = y % m;
-    const int64_t t = m;
+    n = div_by(y, m);
+    b = y - n * m;
+    const int t = m;
     m = a;
     a = t;
   }
   return ans;
 }
 
-// tiles of the first `u` units of a request's head group
+// cost of the first `u` units of a request's head group
 __device__ __forceinline__ int64_t paged_prefix(const PagedParams& p, const PagedReq& q, int u) {
   if (u <= 0) return 0;
-  if (u == 1) return paged_unit_tiles(p, q, 0);
+  const int64_t starts = static_cast<int64_t>(u) * p.unit_cost;
+  if (u == 1) return starts + paged_unit_tiles(p, q, 0);
   const int units = paged_units(p, q);
   const int c = q.total - q.n;
-  if (!p.causal) return static_cast<int64_t>(u) * paged_unit_tiles(p, q, 0);
+  if (!p.causal) return starts + static_cast<int64_t>(u) * paged_unit_tiles(p, q, 0);
+  int64_t s = starts;
   if (c < 0 || q.kv_end < q.total) {  // tokens outside the cache: no closed form, rare
-    int64_t s = 0;
     for (int i = 0; i < u; ++i) s += paged_unit_tiles(p, q, i);
     return s;
   }
-  const int full = min(u, units - 1);  // the last unit may hold fewer tokens
-  const int64_t kt = static_cast<int64_t>(1) << p.kt_log2;
-  int64_t s = floor_sum(full, kt, p.tpu, static_cast<int64_t>(c) + p.tpu + kt - 1);
+  const int64_t full = min(u, units - 1);  // the last unit may hold fewer tokens
+  const int64_t b = static_cast<int64_t>(c) + p.tpu + (1 << p.kt_log2) - 1;
+  if (p.tpu_log2 >= p.kt_log2) {  // a whole number of tiles more per unit
+    s += ((full * (full - 1) / 2) << (p.tpu_log2 - p.kt_log2)) + full * (b >> p.kt_log2);
+  } else if (p.tpu_log2 >= 0) {  // a tile more every 2^k units
+    const int k = p.kt_log2 - p.tpu_log2;
+    auto below = [&](int64_t n) {  // sum over x < n of x >> k
+      const int64_t a = n >> k, r = n & ((1 << k) - 1);
+      return ((a * (a - 1) / 2) << k) + a * r;
+    };
+    const int64_t x = b >> p.tpu_log2;
+    s += below(x + full) - below(x);
+  } else {
+    s += floor_sum(full, p.kt_log2, p.tpu, b);
+  }
   if (u > full) s += paged_unit_tiles(p, q, units - 1);
   return s;
 }
 
-// A CTA's walk over its tiles: segment by segment, a segment being tiles [lo, hi) of unit u.
+// A CTA's walk over its work: segment by segment, a segment being tiles [lo, hi) of unit u
+// (never none of them: a share that ends within a unit's start cost leaves it to the next).
 struct PagedWalk {
-  int64_t left;  // tiles left after the current segment
+  int64_t left;  // work left after the current segment
   PagedReq q;
   int r, vh, u, units, tiles, lo, hi;
 
   __device__ __forceinline__ bool valid() const { return hi > lo; }
-  __device__ __forceinline__ void take(const PagedParams& p, int first) {
+  // from `x` on, counted from the unit's beginning
+  __device__ __forceinline__ void take(const PagedParams& p, int x) {
     tiles = paged_unit_tiles(p, q, u);
-    lo = first;
-    hi = static_cast<int>(min(static_cast<int64_t>(tiles), lo + left));
-    left -= hi - lo;
+    const int end = static_cast<int>(min(static_cast<int64_t>(tiles) + p.unit_cost, x + left));
+    left -= end - x;
+    lo = max(x - p.unit_cost, 0);
+    hi = max(end - p.unit_cost, 0);
   }
   __device__ __forceinline__ void next(const PagedParams& p) {
     if (left <= 0) {
@@ -172,8 +200,8 @@ struct PagedWalk {
 // Scratch of the schedule (shared memory).
 struct PagedSched {
   int64_t warp_sum[32];
-  int64_t first, x, count;  // first tile in request r, tiles of this CTA
-  int r, vh, u, tile;
+  int64_t x;  // the CTA's first work, from the beginning of request r
+  int r;
 };
 
 // Every thread of the CTA (blockDim.x a multiple of 32, at most 1024) calls it; returns
@@ -203,7 +231,7 @@ __device__ __forceinline__ PagedWalk paged_schedule(const PagedParams& p, PagedS
     before += w < warp ? v : 0;
     total += v;
   }
-  const int64_t begin = total * cta / ctas, end = total * (cta + 1) / ctas;
+  const int64_t begin = div_by(total * cta, ctas), end = div_by(total * (cta + 1), ctas);
   const int64_t mine = before + inc - sum;  // tiles before this thread's requests
   if (end > begin && begin >= mine && begin < mine + sum) {
     int64_t x = begin - mine;
@@ -231,7 +259,9 @@ __device__ __forceinline__ PagedWalk paged_schedule(const PagedParams& p, PagedS
   w.units = paged_units(p, w.q);
   const int64_t per_head = paged_prefix(p, w.q, w.units);
   int64_t x = sc.x;
-  w.vh = static_cast<int>(x / per_head);
+  w.vh = static_cast<int>((static_cast<uint64_t>(x) | static_cast<uint64_t>(per_head)) >> 32
+                              ? x / per_head
+                              : static_cast<uint32_t>(x) / static_cast<uint32_t>(per_head));
   x -= w.vh * per_head;
   int lo = 0, hi = w.units;  // prefix(lo) <= x < prefix(hi)
   while (hi - lo > 1) {
@@ -273,7 +303,7 @@ tp_status launch_paged_simt(PagedParams p, int d, bool wide, tp_dtype dt, cudaSt
 tp_status launch_paged_combine(const PagedParams& p, int d, int unit_rows, int tile_rows, int ctas,
                                tp_dtype dt, cudaStream_t st);
 // units of unit_rows rows in tiles of tile_rows, 2^kt_log2 keys per tile
-void paged_set_units(PagedParams& p, int tile_rows, int unit_rows, int kt_log2);
+void paged_set_units(PagedParams& p, int tile_rows, int unit_rows, int kt_log2, int unit_cost);
 // bf16, few rows per key/value head (paged_decode.cu)
 tp_status launch_paged_decode(const PagedParams& p, int d, cudaStream_t st);
 // bf16, head_dim 64 or 128, chunks, at most 128 query heads per key/value head

@@ -240,63 +240,102 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
   if (tid == 0) p.rec[blockIdx.x] = rec;
 }
 
-// CTA i joins the unit whose first piece is CTA i's tail: that piece, then the heads of the
-// following CTAs up to the one where the unit ends. Thread: one row, 4 columns.
+// CTA (i, y) joins rows [16 y, 16 y + 16) of the unit whose first piece is CTA i's tail: that
+// piece, then the heads of the following CTAs up to the one where the unit ends. First all
+// pieces' maxima and sums at once (a weight per piece and row, into shared memory), then
+// each thread sums its columns over the pieces, whose loads do not wait for one another. A
+// loop that rescaled piece by piece took 21 us for 25 pieces of 16 x 128.
+constexpr int kJoinRows = 16;
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedParams p,
                                                                  const int unit_rows,
                                                                  const int tile_rows) {
   __shared__ int last;
+  __shared__ float wt[kPagedMaxCtas][kJoinRows];
+  __shared__ float ms[kJoinRows][kThreads / kJoinRows + 1], mrow[kJoinRows];
+  __shared__ float ls[kJoinRows][kThreads / kJoinRows + 1];
   pdl_wait();  // the previous kernel's results are complete and visible
   pdl_trigger();
   const int i = blockIdx.x, n = gridDim.x, tid = threadIdx.x;
   const PagedRec rec = p.rec[i];
   if (!rec.tail) return;
+  const PagedReq q = paged_req(p, rec.r);
+  int token, head;
+  unit_row(p, q, rec.u, rec.vh, tile_rows, blockIdx.y * kJoinRows, &token, &head);
+  if (token >= q.rows) return;  // tokens ascend with the rows: none of these is one
   if (tid == 0) last = n;
   __syncthreads();
   for (int k = i + 1 + tid; k < n; k += kThreads)
     if (p.rec[k].head == 2) atomicMin(&last, k);
   __syncthreads();
-  const int end = min(last, n - 1);
-  const PagedReq q = paged_req(p, rec.r);
+  const int pieces = min(last, n - 1) - i + 1;
   const int64_t floats = static_cast<int64_t>(unit_rows) * (D + 2);
-  auto slot_of = [&](int k) { return p.part + (2 * static_cast<int64_t>(k) + (k == i ? 1 : 0)) * floats; };
-  constexpr int CG = D / 4;
+  auto slot_of = [&](int k) { return p.part + (2 * static_cast<int64_t>(i + k) + (k == 0)) * floats; };
+  {
+    const int r = tid % kJoinRows, first = tid / kJoinRows;
+    const int row = blockIdx.y * kJoinRows + r;
+    const bool live = unit_row(p, q, rec.u, rec.vh, tile_rows, row, &token, &head);
+    float m = -INFINITY;
+    for (int k = first; k < pieces; k += kThreads / kJoinRows) {
+      // a CTA without tiles left no piece; rows that are none have none
+      const bool has = live && (k == 0 || p.rec[i + k].head != 0);
+      const float mk = has ? slot_of(k)[row] : -INFINITY;
+      wt[k][r] = mk;
+      m = fmaxf(m, mk);
+    }
+    ms[r][first] = m;
+    __syncthreads();
+    float M = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kThreads / kJoinRows; ++k) M = fmaxf(M, ms[r][k]);
+    float l = 0.0f;
+    for (int k = first; k < pieces; k += kThreads / kJoinRows) {
+      const float mk = wt[k][r];
+      const float e = mk == -INFINITY ? 0.0f : exp2f(mk - M);
+      if (e > 0.0f) l += slot_of(k)[unit_rows + row] * e;
+      wt[k][r] = e;
+    }
+    ls[r][first] = l;
+    if (first == 0) mrow[r] = M;
+    __syncthreads();
+  }
   // Slots of two tiles hold O by groups of 4 columns, (d / 4, rows, 4), as their kernel has a
   // thread per row; the others by rows. Threads follow the slots' order.
   const bool by_cols = unit_rows > tile_rows;
-  for (int e = blockIdx.y * kThreads + tid; e < unit_rows * CG; e += kThreads * gridDim.y) {
-    const int row = by_cols ? e % unit_rows : e / CG;
-    const int c = (by_cols ? e / unit_rows : e % CG) * 4;
-    int token, head;
+  constexpr int CG = D / 4;
+  for (int e = tid; e < kJoinRows * CG; e += kThreads) {
+    const int r = by_cols ? e % kJoinRows : e / CG, cg = by_cols ? e / kJoinRows : e % CG;
+    const int row = blockIdx.y * kJoinRows + r;
     if (!unit_row(p, q, rec.u, rec.vh, tile_rows, row, &token, &head)) continue;
-    float m = -INFINITY, l = 0.0f, f[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int k = i; k <= end; ++k) {
-      if (k != i && p.rec[k].head == 0) continue;  // a CTA without tiles
-      const float* s = slot_of(k);
-      const float mk = s[row], lk = s[unit_rows + row];
+    const int64_t at = 2 * unit_rows +
+                       4 * (by_cols ? static_cast<int64_t>(cg) * unit_rows + row
+                                    : static_cast<int64_t>(row) * CG + cg);
+    float f[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int k = 0; k < pieces; ++k) {
+      const float w = wt[k][r];
+      if (w == 0.0f) continue;
       float ok[4];
-      load4(s + 2 * unit_rows + 4 * e, ok);
-      const float m1 = fmaxf(m, mk), mu = m1 == -INFINITY ? 0.0f : m1;
-      const float w0 = exp2f(m - mu), w1 = exp2f(mk - mu);
-      l = l * w0 + lk * w1;
+      load4(slot_of(k) + at, ok);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) f[x] = f[x] * w0 + ok[x] * w1;
-      m = m1;
+      for (int x = 0; x < 4; ++x) f[x] += ok[x] * w;
     }
+    float l = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kThreads / kJoinRows; ++k) l += ls[r][k];
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
     for (int x = 0; x < 4; ++x) f[x] *= inv;
     const int64_t t = static_cast<int64_t>(q.row0) + token;
-    store4(static_cast<T*>(p.o) + t * p.H * D + static_cast<int64_t>(head) * D + c, f);
-    if (c == 0 && p.lse)
-      p.lse[head * p.T + t] = l > 0.0f ? (m + log2f(l)) * 0.6931471805599453f : -INFINITY;
+    store4(static_cast<T*>(p.o) + t * p.H * D + static_cast<int64_t>(head) * D + 4 * cg, f);
+    if (cg == 0 && p.lse)
+      p.lse[head * p.T + t] = l > 0.0f ? (mrow[r] + log2f(l)) * 0.6931471805599453f : -INFINITY;
   }
 }
 
 template <typename T, int D>
 tp_status combine_t(const PagedParams& p, int unit_rows, int tile_rows, int ctas, cudaStream_t st) {
-  const dim3 grid(ctas, std::max(1, unit_rows * (D / 4) / (4 * kThreads)));
+  const dim3 grid(ctas, unit_rows / kJoinRows);
   TP_CUDA_TRY(launch_kernel(paged_combine_kernel<T, D>, grid, dim3(kThreads), 0, st, p, unit_rows,
                             tile_rows));
   count_launch();
@@ -306,7 +345,7 @@ tp_status combine_t(const PagedParams& p, int unit_rows, int tile_rows, int ctas
 template <typename T, int D, int RT>
 tp_status simt_t(PagedParams& p, cudaStream_t st) {
   using Lay = SimtLayout<T, D, RT>;
-  paged_set_units(p, RT, RT, 6);
+  paged_set_units(p, RT, RT, 6, 1);
   static std::atomic<uint64_t> attr_set{0};
   if (needs_setup(attr_set)) {
     TP_CUDA_TRY(cudaFuncSetAttribute(paged_simt_kernel<T, D, RT>,
@@ -352,12 +391,16 @@ tp_status launch_paged_combine(const PagedParams& p, int d, int unit_rows, int t
   }
 }
 
-void paged_set_units(PagedParams& p, int tile_rows, int unit_rows, int kt_log2) {
+void paged_set_units(PagedParams& p, int tile_rows, int unit_rows, int kt_log2, int unit_cost) {
   p.hs = (p.G + tile_rows - 1) / tile_rows;
   p.Gv = (p.G + p.hs - 1) / p.hs;
   p.Hv = p.Hkv * p.hs;
   p.tpu = tile_rows / p.Gv * (unit_rows / tile_rows);
   p.kt_log2 = kt_log2;
+  p.tpu_log2 = -1;
+  for (int k = 0; k < 16; ++k)
+    if (p.tpu == 1 << k) p.tpu_log2 = k;
+  p.unit_cost = unit_cost;
 }
 
 size_t paged_workspace_bytes(int d, tp_dtype dt) {

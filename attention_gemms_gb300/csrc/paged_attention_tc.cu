@@ -17,8 +17,8 @@
 // two products have different shapes and P has columns of its own.
 // A unit of at most 128 rows (drafts, decoding requests beside a chunk, a chunk's end) would
 // leave the second tile idle and the chain S, softmax, P V bare; then both tiles take the
-// same rows, the first the even key tiles, the second the odd ones, and the second's piece
-// joins the first's at the end of the segment through the workspace.
+// same rows, the first the even key tiles, the second the odd ones, and at the segment's end
+// the first tile's warps read both O.
 // Every wait is bounded; on a timeout the CTA records TP_ERR_TIMEOUT, stops issuing, waits
 // (bounded) for its own copies and MMAs, frees TMEM and returns.
 #include <cuda.h>
@@ -51,7 +51,6 @@ struct PagedTcParams {
   CUtensorMap tk, tv;  // (n_pages * Hkv * page, d), box 64 x min(page, 128)
   CUtensorMap tq;      // (T, N blocks, hq heads, d) of the qkv rows, box: a row tile x 64
   PagedParams p;
-  float* joins;        // per CTA: m (128), l (128), O (128, d) of the second tile's piece
   int cache_rows;
   int* status;
   uint64_t timeout_ns;
@@ -66,7 +65,8 @@ struct Lay {
   static constexpr int kOffRing = 2 * kOp;
   static constexpr int kOffBar = kOffRing + kRing * kOp;
   static constexpr int kBars = 2 * kLoads + 13;
-  static constexpr int kSmem = kOffBar + kBars * 8 + kBadRing * 4 + 16 + 1024;
+  static constexpr int kOffJoin = kOffBar + kBars * 8 + kBadRing * 4 + 16;
+  static constexpr int kSmem = kOffJoin + kTile * 8 + 1024;
   static constexpr uint32_t kO = 256, kOStep = D;                     // TMEM columns
   static constexpr uint32_t kP = D == 128 ? 0 : 384, kPStep = D == 128 ? 128 : 64;
 };
@@ -251,7 +251,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto o_done = [&](int t) { return bar_at(6 + t); };
   const uint32_t j_full = bar_at(8), j_free = bar_at(9), drain = bar_at(10);
   auto q_empty = [&](int t) { return bar_at(11 + t); };
-  __shared__ PagedSched sc;
+  float2* join = reinterpret_cast<float2*>(smem + L::kOffJoin);  // the second tile's (m, l)
+  PagedSched& sc = *reinterpret_cast<PagedSched*>(join);         // before any segment
+  static_assert(sizeof(PagedSched) <= kTile * 8, "the schedule's scratch lies in the join's");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int l = 0; l < kLoads; ++l) {
@@ -282,6 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   pdl_wait();  // the set-up above overlaps the previous kernel
   pdl_trigger();
   PagedWalk w = paged_schedule(p, sc, blockIdx.x, gridDim.x);
+  __syncthreads();  // the scratch has been read
   auto tS = [&](int t) { return tmem + 128u * t; };
   auto tP = [&](int t) { return tmem + L::kP + L::kPStep * t; };
   auto tO = [&](int t) { return tmem + L::kO + L::kOStep * t; };
@@ -489,10 +492,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = warp >> 2, x = threadIdx.x & 127;  // tile, row within it = TMEM lane
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int tpt = p.tpu / 2, tt = x / p.Gv, hh = x - tt * p.Gv;
-    float* piece = tp_.joins + static_cast<int64_t>(blockIdx.x) * kTile * (D + 2);
     PagedRec rec{0, 0, 0, 0, 0};
     int ns = 0, segs_o = 0, joined = 0, tiles0 = 0, segs = 0;
-    bool ok = true;
+    bool ok = true, taken = true;
     auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool {
       return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, tp_.timeout_ns, abort_flag)) != 0;
     };
@@ -603,6 +605,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           l = l * f + (sa + sb2);
           tmem_st_wait();
         }
+        // the next P V overwrites this tile's O: a join has read it
+        if (k == 0 && !taken) {
+          if (!wait_all(j_free, (joined - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          taken = true;
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full(t));
@@ -624,30 +634,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool joins = !g.pair && g.count(1) > 0;
       if (!g.pair && t == 1) {
         if (joins) {
-          // the second tile's piece of the same rows, for the first tile's warps
-          if (joined > 0 && !wait_all(j_free, (joined - 1) & 1)) {
-            ok = false;
-            break;
-          }
-#pragma unroll 1
-          for (int c = 0; c < D / 32 && busy; ++c) {
-            uint32_t o[32];
-            __syncwarp();
-            tmem_ld32(tO(t) + lanes + 32 * c, o);
-            tmem_ld_wait();
-            if (live)
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                *reinterpret_cast<uint4*>(piece + 2 * kTile + ((8 * c + i) * kTile + x) * 4) =
-                    make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-          }
-          piece[x] = m;
-          piece[kTile + x] = l;
-          __threadfence();
+          // the first tile's warps read this tile's O, in the same TMEM lanes as their own
+          join[x] = make_float2(m, l);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(j_full);
           ++joined;
+          taken = false;
         }
         continue;
       }
@@ -658,12 +651,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         ++joined;
-        const float m2 = __ldcg(piece + x), l2 = __ldcg(piece + kTile + x);
-        mj = fmaxf(m, m2);
+        tc_fence_after();
+        const float2 ml = join[x];
+        mj = fmaxf(m, ml.x);
         const float mu = mj == -INFINITY ? 0.0f : mj;
         fa = ex2(m - mu);
-        fb = ex2(m2 - mu);
-        lj = l * fa + l2 * fb;
+        fb = ex2(ml.x - mu);
+        lj = l * fa + ml.y * fb;
       }
       const bool whole = begins && ends;
       const float inv = lj > 0.0f ? 1.0f / lj : 0.0f;
@@ -683,24 +677,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (n > 0) {
           tmem_ld32(tO(t) + lanes + 32 * c, o);
+          uint32_t o2[32];
+          if (joins) tmem_ld32(tO(1) + lanes + 32 * c, o2);
           tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * ga);
+          if (joins)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              o[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(o2[i]) * gb);
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0u;
         }
         if (live) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * ga);
-          if (joins)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 y =
-                  __ldcg(reinterpret_cast<const float4*>(piece + 2 * kTile + ((8 * c + i) * kTile + x) * 4));
-              o[4 * i] = __float_as_uint(__uint_as_float(o[4 * i]) + y.x * gb);
-              o[4 * i + 1] = __float_as_uint(__uint_as_float(o[4 * i + 1]) + y.y * gb);
-              o[4 * i + 2] = __float_as_uint(__uint_as_float(o[4 * i + 2]) + y.z * gb);
-              o[4 * i + 3] = __float_as_uint(__uint_as_float(o[4 * i + 3]) + y.w * gb);
-            }
           if (!whole) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
@@ -728,6 +718,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (joins) {
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(j_free);
       }
@@ -780,7 +771,6 @@ tp_status tc_t(PagedTcParams& t, cudaStream_t st) {
     mark_device(attr_set);
   }
   const int ctas = std::min(kPagedTcCtas, device_sm_count());
-  t.joins = t.p.part + static_cast<int64_t>(kPagedTcCtas) * 2 * kUnitRows * (D + 2);
   TP_CUDA_TRY(launch_kernel(paged_tc_kernel<D>, dim3(ctas), dim3(kThreads),
                             static_cast<size_t>(L::kSmem), st, t));
   count_launch();
@@ -792,7 +782,7 @@ tp_status tc_t(PagedTcParams& t, cudaStream_t st) {
 tp_status launch_paged_tc(const PagedParams& p, int d, int N, cudaStream_t st) {
   PagedTcParams t{};
   t.p = p;
-  paged_set_units(t.p, kTile, kUnitRows, 7);
+  paged_set_units(t.p, kTile, kUnitRows, 7, 3);
   const int64_t rows = (static_cast<int64_t>(p.n_pages) * p.Hkv) << p.ps_log2;
   t.cache_rows = static_cast<int>(rows);
   const int box = std::min(1 << p.ps_log2, kTile);
@@ -807,7 +797,7 @@ tp_status launch_paged_tc(const PagedParams& p, int d, int N, cudaStream_t st) {
 }
 
 size_t paged_tc_floats(int d) {
-  return static_cast<size_t>(kPagedTcCtas) * (2 * kUnitRows + kTile) * (d + 2);
+  return static_cast<size_t>(kPagedTcCtas) * 2 * kUnitRows * (d + 2);
 }
 
 }  // namespace tp
