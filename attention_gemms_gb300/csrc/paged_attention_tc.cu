@@ -37,12 +37,15 @@ namespace {
 
 constexpr int kTile = 128;  // rows of a TMEM tile, keys of a key tile
 constexpr int kUnitRows = 2 * kTile;
-// warps 0-3: softmax of tile 0, 4-7: of tile 1, 8: K and V loads, 9: MMA, 10: Q loads
-constexpr int kProd = 8, kMma = 9, kLoadQ = 10, kThreads = 384;
+// warps 0-3: softmax of tile 0, 4-7: of tile 1, 8: K and V loads, 9: MMA, 10: Q loads, 11:
+// the walk over the CTA's work
+constexpr int kProd = 8, kMma = 9, kLoadQ = 10, kWalk = 11, kThreads = 384;
 // Registers: 384 threads launch with 168 each; the third warpgroup gives up its share
 // (128 x 80 + 256 x 208 = 63488 of the launch's 64512) so that a row's 128 scores stay in
 // the softmax threads' registers.
 constexpr int kRegsLoad = 80, kRegsSoftmax = 208;
+constexpr int kSegs = 4;            // segment descriptors in flight
+constexpr int kSegReaders = 8 + 3;  // softmax warps, K/V loads, MMA, Q loads
 constexpr int kLoads = 16;  // barriers of loads in flight (at most a ring's tiles)
 constexpr int kBadRing = 16;
 constexpr uint64_t kDrainNs = 20000000ull;
@@ -64,9 +67,10 @@ struct Lay {
   static constexpr int kRing = D == 128 ? 5 : 10;
   static constexpr int kOffRing = 2 * kOp;
   static constexpr int kOffBar = kOffRing + kRing * kOp;
-  static constexpr int kBars = 2 * kLoads + 13;
+  static constexpr int kBars = 2 * kLoads + 13 + 2 * kSegs + 1;  // even: 16-byte alignment after
   static constexpr int kOffJoin = kOffBar + kBars * 8 + kBadRing * 4 + 16;
-  static constexpr int kSmem = kOffJoin + kTile * 8 + 1024;
+  static constexpr int kOffSeg = kOffJoin + kTile * 8;
+  static constexpr int kSmem = kOffSeg + kSegs * 64 + 1024;
   static constexpr uint32_t kO = 256, kOStep = D;                     // TMEM columns
   static constexpr uint32_t kP = D == 128 ? 0 : 384, kPStep = D == 128 ? 128 : 64;
 };
@@ -201,31 +205,46 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&q)[4][4]) {
   }
 }
 
-// A segment as every role sees it: key tiles of each row tile. pair: tile t takes the tiles
-// lo .. hi_t - 1 of its own rows; else tile t takes lo + t, lo + t + 2, ... of the same rows.
-struct Seg {
-  bool pair;
-  int lo, hi[2], step;
-  __device__ __forceinline__ Seg(const PagedParams& p, const PagedWalk& w) {
-    const int tpt = p.tpu / 2, tokens = min(p.tpu, w.q.rows - w.u * p.tpu);
-    pair = tokens > tpt;
-    lo = w.lo;
-    hi[1] = w.hi;
-    hi[0] = w.hi;
-    step = pair ? 1 : 2;
-    if (pair && p.causal) {  // the first tile's rows see no key of the last tiles
-      const int64_t end = static_cast<int64_t>(w.q.total) - w.q.n + w.u * p.tpu + tpt;
-      const int64_t own = (min(end, static_cast<int64_t>(w.q.kv_end)) + kTile - 1) >> 7;
-      hi[0] = static_cast<int>(min(static_cast<int64_t>(w.hi),
-                                   max(own, static_cast<int64_t>(w.lo))));
-    }
-  }
-  __device__ __forceinline__ int first(int t) const { return pair ? lo : lo + t; }
-  __device__ __forceinline__ int count(int t) const {  // tile t's key tiles
-    const int f = first(t);
-    return hi[t] > f ? (hi[t] - f + step - 1) / step : 0;
+// A segment, as one warp works it out for all roles (through shared memory: the walk's scalar
+// arithmetic in every role took longer than a key tile). pair: the row tiles hold different
+// rows and tile t takes key tiles 0 .. n_t - 1 of the segment (n_1 = n); else both hold the
+// same rows and tile t takes key tiles t, t + 2, ... of n.
+struct __align__(16) Seg {
+  int n, n0, pair, lo;              // n = 0: no more segments; lo: the first key tile
+  int row0, tokens, pos0, kv_end;   // first token's row and position, tokens, keys
+  int head0, heads, j, kend;        // first query head, heads, key/value head, unit's keys
+  int r, vh, u, ends;               // the unit; bit 0: begins here, bit 1: ends here
+  __device__ __forceinline__ int count(int t) const {  // row tile t's key tiles
+    return pair ? (t ? n : n0) : (n + 1 - t) >> 1;
   }
 };
+
+__device__ __forceinline__ Seg make_seg(const PagedParams& p, const PagedWalk& w) {
+  Seg g;
+  const int tpt = p.tpu / 2, j = w.vh / p.hs;
+  g.n = w.hi - w.lo;
+  g.lo = w.lo;
+  g.tokens = min(p.tpu, w.q.rows - w.u * p.tpu);
+  g.pair = g.tokens > tpt;
+  g.row0 = w.q.row0 + w.u * p.tpu;
+  g.pos0 = w.q.total - w.q.n + w.u * p.tpu;
+  g.kv_end = w.q.kv_end;
+  g.head0 = j * p.G + (w.vh - j * p.hs) * p.Gv;
+  g.heads = min(p.Gv, (j + 1) * p.G - g.head0);
+  g.j = j;
+  g.kend = paged_unit_kend(p, w.q, w.u);
+  g.r = w.r;
+  g.vh = w.vh;
+  g.u = w.u;
+  g.ends = (w.lo == 0 ? 1 : 0) | (w.hi == w.tiles ? 2 : 0);
+  g.n0 = g.n;
+  if (g.pair && p.causal) {  // the first tile's rows see no key of the last tiles
+    const int64_t end = min(static_cast<int64_t>(g.pos0) + tpt, static_cast<int64_t>(g.kv_end));
+    g.n0 = static_cast<int>(min(static_cast<int64_t>(g.n),
+                                max(((end + kTile - 1) >> 7) - g.lo, static_cast<int64_t>(0))));
+  }
+  return g;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -251,6 +270,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto o_done = [&](int t) { return bar_at(6 + t); };
   const uint32_t j_full = bar_at(8), j_free = bar_at(9), drain = bar_at(10);
   auto q_empty = [&](int t) { return bar_at(11 + t); };
+  auto seg_full = [&](uint32_t i) { return bar_at(13 + i % kSegs); };
+  auto seg_empty = [&](uint32_t i) { return bar_at(13 + kSegs + i % kSegs); };
+  Seg* segs = reinterpret_cast<Seg*>(smem + L::kOffSeg);
   float2* join = reinterpret_cast<float2*>(smem + L::kOffJoin);  // the second tile's (m, l)
   PagedSched& sc = *reinterpret_cast<PagedSched*>(join);         // before any segment
   static_assert(sizeof(PagedSched) <= kTile * 8, "the schedule's scratch lies in the join's");
@@ -266,6 +288,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(s_full(t), 1);
       mbar_init(p_full(t), 4);
       mbar_init(o_done(t), 1);
+    }
+    for (int i = 0; i < kSegs; ++i) {
+      mbar_init(seg_full(i), 1);
+      mbar_init(seg_empty(i), kSegReaders);
     }
     mbar_init(j_full, 4);
     mbar_init(j_free, 4);
@@ -293,6 +319,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     atomicCAS(tp_.status, 0, static_cast<int>(TP_ERR_TIMEOUT));
     atomicAdd(tp_.status + 1, 1);
   };
+  // the i-th segment, read by a whole warp; false: none left, or a wait expired (ok = false)
+  auto get_seg = [&](uint32_t i, Seg& g, bool& ok) -> bool {
+    ok = __all_sync(0xFFFFFFFFu, mbar_wait(seg_full(i), (i / kSegs) & 1, tp_.timeout_ns,
+                                           abort_flag)) != 0;
+    if (!ok) return false;
+    g = segs[i % kSegs];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(seg_empty(i));
+    return g.n > 0;
+  };
   uint32_t issued = 0;        // K/V loads issued
   int issued_q[2] = {0, 0};   // Q loads: tiles issued
 
@@ -304,21 +340,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool ok = true;
       uint32_t tiles = 0, slot = 0, freed = 0, sizes = 0;  // bit l % 32: load l has two tiles
       int room = L::kRing;
-      for (; w.valid() && ok; w.next(p)) {
-        const Seg g(p, w);
-        const int n = w.hi - w.lo, c = g.pair ? 1 : 2;
-        const int j = w.vh / p.hs;
-        const int kend = paged_unit_kend(p, w.q, w.u);
-        const int32_t* tab = p.table + static_cast<int64_t>(w.r) * p.max_pages;
-        const int npages = (kend + ps - 1) >> p.ps_log2;
+      Seg g;
+      for (uint32_t i = 0; ok && get_seg(i, g, ok); ++i) {
+        const int n = g.n, c = g.pair ? 1 : 2;
+        const int32_t* tab = p.table + static_cast<int64_t>(g.r) * p.max_pages;
+        const int npages = (g.kend + ps - 1) >> p.ps_log2;
         auto fetch = [&](int first) {
           const int i = first + lane;
           const int id = i < npages ? tab[i] : -1;
           return id >= 0 && id < p.n_pages ? id : -1;
         };
-        int base = (w.lo * kTile) >> p.ps_log2;
+        int base = (g.lo * kTile) >> p.ps_log2;
         int ids = fetch(base), ahead = fetch(base + 32);
-        int next = w.lo, y0 = 0, y1 = 0, y = 0;  // cache rows of this lane's page: the last tiles
+        int next = g.lo, y0 = 0, y1 = 0, y = 0;  // cache rows of this lane's page: the last tiles
         // the next key tile's rows (tiles are whole groups of at most 16 pages)
         auto locate = [&] {
           const int k0 = next * kTile, pg0 = k0 >> p.ps_log2;
@@ -333,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           y0 = y1;
           y1 = y;
           y = src < 0 ? tp_.cache_rows
-                      : (((src * p.Hkv + j) << p.ps_log2) + (k0 & (ps - 1)));
+                      : (((src * p.Hkv + g.j) << p.ps_log2) + (k0 & (ps - 1)));
           ++next;
           ++tiles;
         };
@@ -371,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (more) locate();  // its mask is written before the barrier's arrival
           if (!(ok = begin(more ? 2 : 1))) break;
           // V of tile m: c tiles (fewer at the end) before the last located one
-          const int back = next - 1 - (w.lo + m);
+          const int back = next - 1 - (g.lo + m);
           copy(&tp_.tv, back == 0 ? y : back == 1 ? y1 : y0);
           if (more) copy(&tp_.tk, y);
           ++issued;
@@ -396,9 +430,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                          desc_lo(sbase + L::kOffRing + ks * L::kOp, 16), id_s);
           mma_commit(s_full(t));
         };
-        for (; same(w.valid() && ok); w.next(p)) {
-          const Seg g(p, w);
-          const int n0 = same(g.count(0)), n = same(w.hi - w.lo);
+        Seg g;
+        for (uint32_t i = 0; same(ok && get_seg(i, g, ok)); ++i) {
+          const int n0 = same(g.n0), n = same(g.n);
           const bool pair = same(g.pair) != 0;
           const int c = pair ? 1 : 2, lead = min(c, n);
           // the rows' Q (one for both tiles when they share rows) and the first key tiles
@@ -464,27 +498,53 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ---------------------------------------------------------------- Q loads
       // A row tile is tpt tokens x G heads, in that order: a box of the qkv rows. Rows past
       // the request's tokens are other requests' or zeros; nothing of them is written.
-      if (lane == 0) {
-        bool ok = true;
-        const int tpt = p.tpu / 2;
-        const uint32_t bytes = static_cast<uint32_t>(tpt) * p.G * D * 2;
-        for (; w.valid() && ok; w.next(p)) {
-          const Seg g(p, w);
-          const int head = w.vh * p.G, blk = head / p.hq;
-          for (int t = 0; t < (g.pair ? 2 : 1) && ok; ++t) {
-            if (issued_q[t] > 0)
-              ok = mbar_wait(q_empty(t), (issued_q[t] - 1) & 1, tp_.timeout_ns, abort_flag);
-            if (!ok) break;
+      bool ok = true;
+      const int tpt = p.tpu / 2;
+      const uint32_t bytes = static_cast<uint32_t>(tpt) * p.G * D * 2;
+      Seg g;
+      for (uint32_t i = 0; ok && get_seg(i, g, ok); ++i) {
+        const int blk = g.head0 / p.hq;
+        for (int t = 0; t < (g.pair ? 2 : 1); ++t) {
+          if (issued_q[t] > 0 &&
+              !__all_sync(0xFFFFFFFFu, mbar_wait(q_empty(t), (issued_q[t] - 1) & 1, tp_.timeout_ns,
+                                                 abort_flag))) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) {
             mbar_arrive_expect_tx(q_full(t), bytes);
             for (int h = 0; h < L::kHalves; ++h)
               tma_load_4d(sb + t * L::kOp + h * (kTile * 128), &tp_.tq, q_full(t), h * 64,
-                          head - blk * p.hq, blk, w.q.row0 + w.u * p.tpu + t * tpt);
-            ++issued_q[t];
+                          g.head0 - blk * p.hq, blk, g.row0 + t * tpt);
           }
+          __syncwarp();
+          ++issued_q[t];
         }
-        if (!ok) timed_out();
       }
-      __syncwarp();
+      if (!ok && lane == 0) timed_out();
+    } else {
+      // ---------------------------------------------------------------- the walk
+      bool ok = true;
+      for (uint32_t i = 0; ok; ++i) {
+        Seg g;
+        const bool more = w.valid();
+        if (more)
+          g = make_seg(p, w);
+        else
+          g.n = 0;
+        if (i >= kSegs)
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(seg_empty(i), (i / kSegs - 1) & 1, tp_.timeout_ns,
+                                                 abort_flag)) != 0;
+        if (!ok) break;
+        if (lane == 0) {
+          segs[i % kSegs] = g;
+          mbar_arrive(seg_full(i));
+        }
+        __syncwarp();
+        if (!more) break;
+        w.next(p);
+      }
+      if (!ok && lane == 0) timed_out();
     }
   } else {
     // ---------------------------------------------------------------- softmax
@@ -493,37 +553,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int tpt = p.tpu / 2, tt = x / p.Gv, hh = x - tt * p.Gv;
     PagedRec rec{0, 0, 0, 0, 0};
-    int ns = 0, segs_o = 0, joined = 0, tiles0 = 0, segs = 0;
+    int ns = 0, segs_o = 0, joined = 0;
+    uint32_t tiles0 = 0;  // key tiles of earlier segments
     bool ok = true, taken = true;
     auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool {
       return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, tp_.timeout_ns, abort_flag)) != 0;
     };
-    for (; w.valid() && ok; w.next(p)) {
-      const Seg g(p, w);
-      const int j = w.vh / p.hs, gh = (w.vh - j * p.hs) * p.Gv + hh;
-      const int token = w.u * p.tpu + (g.pair ? t * tpt : 0) + tt, head = j * p.G + gh;
-      const bool live = tt < tpt && gh < p.G && token < w.q.rows;
+    Seg g;
+    for (uint32_t i = 0; ok && get_seg(i, g, ok); ++i) {
+      const int token = (g.pair ? t * tpt : 0) + tt, head = g.head0 + hh;  // of the unit's tokens
+      const bool live = tt < tpt && hh < g.heads && token < g.tokens;
       const bool busy = __any_sync(0xFFFFFFFFu, live);  // a warp without rows computes nothing
-      const int64_t row = static_cast<int64_t>(w.q.row0) + token;
-      const int kv_end = w.q.kv_end;
-      const int lim = !live ? kv_end
-                            : p.causal ? min(kv_end, w.q.total - w.q.n + token + 1) : kv_end;
+      const int64_t row = static_cast<int64_t>(g.row0) + token;
+      const int kv_end = g.kv_end;
+      const int lim = live && p.causal ? min(kv_end, g.pos0 + token + 1) : kv_end;
       const int lim_min = __reduce_min_sync(0xFFFFFFFFu, lim);
       const int n = g.count(t);
       float m = -INFINITY, l = 0.0f;
       for (int k = 0; k < n; ++k, ++ns) {
-        const int tile = g.first(t) + k * g.step, k0 = tile * kTile;
+        const int mm = g.pair ? k : 2 * k + t, k0 = (g.lo + mm) * kTile;  // tile of the segment
         if (!wait_all(s_full(t), ns & 1)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const int seg_tile = tiles0 + tile - g.lo;
         if (k0 + kTile > kv_end) {
           // V rows past the request's keys may hold anything and 0 * NaN would spoil O
-          const int mm = tile - g.lo, nn = w.hi - w.lo;  // V's load and place in the ring
-          const uint32_t l = static_cast<uint32_t>(tiles0 + segs + 1 + mm);
-          const int at = 2 * tiles0 + (mm == nn - 1 ? 2 * nn - 1 : g.pair ? 1 + 2 * mm : 2 + 2 * mm);
+          const uint32_t l = tiles0 + i + 1 + mm;  // V's load and place in the ring
+          const uint32_t at =
+              2 * tiles0 + (mm == g.n - 1 ? 2 * g.n - 1 : g.pair ? 1 + 2 * mm : 2 + 2 * mm);
           if (!wait_all(full(l), round_of(l))) {
             ok = false;
             break;
@@ -541,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < 4; ++c)
             tmem_ld32(tS(t) + lanes + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
           tmem_ld_wait();
-          const uint32_t miss = bad[seg_tile % kBadRing];
+          const uint32_t miss = bad[(tiles0 + mm) % kBadRing];
           if (k0 + kTile > lim_min || miss) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) {  // bit i: key 32 c + i is seen
@@ -617,8 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full(t));
       }
-      tiles0 += w.hi - w.lo;
-      ++segs;
+      tiles0 += g.n;
       if (!ok) break;
       if (n > 0) {  // the last P V
         if (!wait_all(o_done(t), segs_o & 1)) {
@@ -628,9 +685,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++segs_o;
         tc_fence_after();
       }
-      const bool begins = w.lo == 0, ends = w.hi == w.tiles;
+      const bool begins = g.ends & 1, ends = g.ends & 2;
       if (!begins) rec.head = ends ? 2 : 1;
-      if (begins && !ends) rec.tail = 1, rec.r = w.r, rec.vh = w.vh, rec.u = w.u;
+      if (begins && !ends) rec.tail = 1, rec.r = g.r, rec.vh = g.vh, rec.u = g.u;
       const bool joins = !g.pair && g.count(1) > 0;
       if (!g.pair && t == 1) {
         if (joins) {
@@ -677,15 +734,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (n > 0) {
           tmem_ld32(tO(t) + lanes + 32 * c, o);
-          uint32_t o2[32];
-          if (joins) tmem_ld32(tO(1) + lanes + 32 * c, o2);
           tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * ga);
-          if (joins)
+          if (joins) {
+            uint32_t o2[32];
+            tmem_ld32(tO(1) + lanes + 32 * c, o2);
+            tmem_ld_wait();
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               o[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(o2[i]) * gb);
+          }
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0u;
@@ -782,7 +841,7 @@ tp_status tc_t(PagedTcParams& t, cudaStream_t st) {
 tp_status launch_paged_tc(const PagedParams& p, int d, int N, cudaStream_t st) {
   PagedTcParams t{};
   t.p = p;
-  paged_set_units(t.p, kTile, kUnitRows, 7, 3);
+  paged_set_units(t.p, kTile, kUnitRows, 7, 2);
   const int64_t rows = (static_cast<int64_t>(p.n_pages) * p.Hkv) << p.ps_log2;
   t.cache_rows = static_cast<int>(rows);
   const int box = std::min(1 << p.ps_log2, kTile);

@@ -502,7 +502,7 @@ tp_status paged_q_map(CUtensorMap* m, const PagedParams& p, int d, int N) {
 tp_status launch_paged_decode(const PagedParams& p, int d, cudaStream_t st) {
   DecodeParams dp{};
   dp.p = p;
-  paged_set_units(dp.p, kRows, kRows, 6, 1);
+  paged_set_units(dp.p, kRows, kRows, 6, 2);
   const int64_t rows = (static_cast<int64_t>(p.n_pages) * p.Hkv) << p.ps_log2;
   dp.cache_rows = static_cast<int>(rows);
   const int box = std::min(1 << p.ps_log2, kKT);
