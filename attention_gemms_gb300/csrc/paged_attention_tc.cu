@@ -7,7 +7,8 @@
 //     into a ring of K and V tiles, V of a key tile and K of the next one to be multiplied
 //     under one barrier (the operands of one turn); pages outside the cache or past the
 //     unit's keys are boxes outside the tensor and arrive as zeros;
-//   MMA warp (one lane): S = Q K^T into TMEM, and O += P V with P read from TMEM;
+//   two MMA warps, one per tile: S = Q K^T into TMEM, and O += P V with P read from TMEM;
+//   a warp that walks the CTA's work, publishes its segments and loads their Q;
 //   eight softmax warps, four per tile, a thread per row: S out of TMEM, the running
 //     maximum (moved lazily) and sum, P as bf16 back into TMEM, O rescaled there when the
 //     maximum moves; at a segment's end O / l, or the piece for the join.
@@ -37,15 +38,15 @@ namespace {
 
 constexpr int kTile = 128;  // rows of a TMEM tile, keys of a key tile
 constexpr int kUnitRows = 2 * kTile;
-// warps 0-3: softmax of tile 0, 4-7: of tile 1, 8: K and V loads, 9: MMA, 10: Q loads, 11:
-// the walk over the CTA's work
-constexpr int kProd = 8, kMma = 9, kLoadQ = 10, kWalk = 11, kThreads = 384;
+// warps 0-3: softmax of tile 0, 4-7: of tile 1, 8: K and V loads, 9 and 10: MMA of tile 0
+// and 1, 11: the walk over the CTA's work, and Q loads
+constexpr int kProd = 8, kMma = 9, kWalk = 11, kThreads = 384;
 // Registers: 384 threads launch with 168 each; the third warpgroup gives up its share
 // (128 x 80 + 256 x 208 = 63488 of the launch's 64512) so that a row's 128 scores stay in
 // the softmax threads' registers.
 constexpr int kRegsLoad = 80, kRegsSoftmax = 208;
 constexpr int kSegs = 4;            // segment descriptors in flight
-constexpr int kSegReaders = 8 + 3;  // softmax warps, K/V loads, MMA, Q loads
+constexpr int kSegReaders = 8 + 3;  // softmax warps, K/V loads, MMA
 constexpr int kLoads = 16;  // barriers of loads in flight (at most a ring's tiles)
 constexpr int kBadRing = 16;
 constexpr uint64_t kDrainNs = 20000000ull;
@@ -67,12 +68,12 @@ struct Lay {
   static constexpr int kRing = D == 128 ? 5 : 10;
   static constexpr int kOffRing = 2 * kOp;
   static constexpr int kOffBar = kOffRing + kRing * kOp;
-  static constexpr int kBars = 2 * kLoads + 13 + 2 * kSegs + 1;  // even: 16-byte alignment after
+  static constexpr int kBars = 2 * kLoads + 18 + 2 * kSegs;  // even: 16-byte alignment after
   static constexpr int kOffJoin = kOffBar + kBars * 8 + kBadRing * 4 + 16;
   static constexpr int kOffSeg = kOffJoin + kTile * 8;
   static constexpr int kSmem = kOffSeg + kSegs * 64 + 1024;
   static constexpr uint32_t kO = 256, kOStep = D;                     // TMEM columns
-  static constexpr uint32_t kP = D == 128 ? 0 : 384, kPStep = D == 128 ? 128 : 64;
+  static constexpr uint32_t kP = 0, kPStep = 128, kPHalf = 64;  // over the half's own S
 };
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -265,11 +266,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto round_of = [](uint32_t l) { return (l / kLoads) & 1u; };
   auto bar_at = [&](int i) { return bar0 + 8u * (2 * kLoads + i); };
   auto q_full = [&](int t) { return bar_at(t); };
-  auto s_full = [&](int t) { return bar_at(2 + t); };
-  auto p_full = [&](int t) { return bar_at(4 + t); };
+  auto s_full = [&](int t, int h) { return bar_at((h ? 14 + 2 * kSegs : 2) + t); };
+  auto p_full = [&](int t, int h) { return bar_at((h ? 16 + 2 * kSegs : 4) + t); };
   auto o_done = [&](int t) { return bar_at(6 + t); };
   const uint32_t j_full = bar_at(8), j_free = bar_at(9), drain = bar_at(10);
   auto q_empty = [&](int t) { return bar_at(11 + t); };
+  const uint32_t q_other = bar_at(13 + 2 * kSegs);  // the second tile is done with the first's Q
   auto seg_full = [&](uint32_t i) { return bar_at(13 + i % kSegs); };
   auto seg_empty = [&](uint32_t i) { return bar_at(13 + kSegs + i % kSegs); };
   Seg* segs = reinterpret_cast<Seg*>(smem + L::kOffSeg);
@@ -280,13 +282,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int l = 0; l < kLoads; ++l) {
       mbar_init(full(l), 1);
-      mbar_init(empty(l), 1);
+      mbar_init(empty(l), 2);  // one arrival per row tile
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(q_full(t), 1);
       mbar_init(q_empty(t), 1);
-      mbar_init(s_full(t), 1);
-      mbar_init(p_full(t), 4);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(s_full(t, h), 1);
+        mbar_init(p_full(t, h), 4);
+      }
       mbar_init(o_done(t), 1);
     }
     for (int i = 0; i < kSegs; ++i) {
@@ -295,7 +299,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(j_full, 4);
     mbar_init(j_free, 4);
-    mbar_init(drain, 1);
+    mbar_init(q_other, 1);
+    mbar_init(drain, 2);
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -412,105 +417,141 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok && lane == 0) timed_out();
-    } else if (warp == kMma) {
-      // ---------------------------------------------------------------- MMA issuer
-      {
-        const uint32_t id_s = idesc_bf16_f32(128, kTile, 0, 0);  // Q, K both K-major
-        const uint32_t id_o = idesc_bf16_f32(128, D, 0, 1);      // P in TMEM, V MN-major
-        const uint32_t tm = same(tmem), sbase = same(sb);
-        auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-          return same(mbar_wait(bar, parity, tp_.timeout_ns, abort_flag)) != 0;
+    } else if (warp != kWalk) {
+      // ---------------------------------------------------------------- MMA issuers
+      // One warp per row tile: the tensor cores' queue holds about five MMAs, so a warp's
+      // waits and loop between its products (about 700 cycles of one turn's 1024) would leave
+      // them idle; now the other tile's products run meanwhile.
+      const int t = same(warp - kMma);
+      const uint32_t id_s = idesc_bf16_f32(128, kTile / 2, 0, 0);  // Q, K both K-major
+      const uint32_t id_o = idesc_bf16_f32(128, D, 0, 1);      // P in TMEM, V MN-major
+      const uint32_t tm = same(tmem), sbase = same(sb);
+      const uint32_t ts = tm + 128 * t, to = tm + L::kO + L::kOStep * t;
+      auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+        return same(mbar_wait(bar, parity, tp_.timeout_ns, abort_flag)) != 0;
+      };
+      bool ok = true;
+      if (tp_.debug_hang) ok = wait(drain, 0);
+      uint32_t q_par[2] = {0, 0}, p_par = 0;  // parities of the next Q tiles, the next P
+      uint32_t load = 0, slot = 0;
+      auto advance = [&](uint32_t n) {
+        ++load;
+        slot += n;
+        if (slot >= L::kRing) slot -= L::kRing;
+      };
+      Seg g;
+      for (uint32_t i = 0; same(ok && get_seg(i, g, ok)); ++i) {
+        const int n = same(g.n), own = same(g.count(t));
+        const bool pair = same(g.pair) != 0;
+        const int c = pair ? 1 : 2, lead = min(c, n);
+        const int qt = pair ? t : 0;  // the rows' Q: one for both tiles when they share rows
+        const uint32_t q_done = qt == t ? q_empty(t) : q_other;
+        auto s_of = [&](uint32_t ks, int h) {  // half h of S, by the elected lane
+          mma_qk<D / 16>(ts + 64 * h, desc_lo(sbase + qt * L::kOp, 16),
+                         desc_lo(sbase + L::kOffRing + ks * L::kOp + h * 8192, 16), id_s);
         };
-        bool ok = true;
-        if (tp_.debug_hang) ok = wait(drain, 0);
-        uint32_t seg_q = 0, np = 0;  // bit t: parity of tile t's next Q, next P
-        uint32_t load = 0, slot = 0;
-        auto s_of = [&](uint32_t t, uint32_t q, uint32_t ks) {
-          mma_qk<D / 16>(tm + 128 * t, desc_lo(sbase + q * L::kOp, 16),
-                         desc_lo(sbase + L::kOffRing + ks * L::kOp, 16), id_s);
-          mma_commit(s_full(t));
-        };
-        Seg g;
-        for (uint32_t i = 0; same(ok && get_seg(i, g, ok)); ++i) {
-          const int n0 = same(g.n0), n = same(g.n);
-          const bool pair = same(g.pair) != 0;
-          const int c = pair ? 1 : 2, lead = min(c, n);
-          // the rows' Q (one for both tiles when they share rows) and the first key tiles
-          ok = wait(q_full(0), seg_q & 1) && (!pair || wait(q_full(1), seg_q >> 1)) &&
-               wait(full(load), round_of(load));
-          seg_q ^= pair ? 3 : 1;
-          if (!ok) break;
-          tc_fence_after();
-          if (elect_one()) {
-            if (pair ? n0 > 0 : true) s_of(0, 0, slot);
-            if (pair ? n0 < 2 : n == 1) mma_commit(q_empty(0));
-            if (pair || n > 1) {
-              const uint32_t ks = slot + (pair ? 0 : 1);
-              s_of(1, pair, ks < L::kRing ? ks : 0);
-              if (pair ? n == 1 : n == 2) mma_commit(q_empty(pair));
-            }
-            mma_commit(empty(load));
+        ok = wait(q_full(qt), q_par[qt]) && wait(full(load), round_of(load));
+        q_par[0] ^= 1;  // every segment's first Q, whether this warp waited for it or not
+        q_par[1] ^= pair;
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          if (own > 0) {
+            uint32_t ks = slot + (pair ? 0 : t);
+            if (ks >= L::kRing) ks = 0;
+            s_of(ks, 0);
+            mma_commit(s_full(t, 0));
+            s_of(ks, 1);
+            mma_commit(s_full(t, 1));
           }
-          __syncwarp();
-          ++load;
-          slot += lead;
-          if (slot >= L::kRing) slot -= L::kRing;
-          // Load m + 1: V of key tile m and K of tile m + c, the operands of one turn (of two
-          // turns for a pair): O += P V of the tile, then S of the row tile's next one.
-#pragma unroll 1
-          for (int m = 0; m < n; ++m) {
-            const uint32_t ks = slot + 1 < L::kRing ? slot + 1 : 0;
-            ok = wait(full(load), round_of(load));
-            if (!ok) break;
-            const int t1 = pair ? 1 : m & 1;
-#pragma unroll 1
-            for (int t = pair ? 0 : t1; t <= t1; ++t) {
-              const int left = pair ? (t ? n : n0) - m : (n - m + 1) >> 1;  // the row tile's own
-              if (left <= 0) continue;
-              ok = wait(p_full(t), (np >> t) & 1);
-              if (!ok) break;
-              np ^= 1u << t;
-              tc_fence_after();
-              if (elect_one()) {
-                mma_pv<kTile / 16>(tm + L::kO + L::kOStep * t, tm + L::kP + L::kPStep * t,
-                                   desc_lo(sbase + L::kOffRing + slot * L::kOp, kTile * 128), id_o,
-                                   m >= c);
-                if (left > 1)
-                  s_of(t, pair ? t : 0, ks);
-                else
-                  mma_commit(o_done(t));
-                if (t == t1) mma_commit(empty(load));
-                // the last S of the segment frees its Q
-                if (pair ? left == 2 : m + 3 == n) mma_commit(q_empty(pair ? t : 0));
-              }
-              __syncwarp();
-            }
-            if (!ok) break;
-            ++load;
-            slot += m + c < n ? 2 : 1;
-            if (slot >= L::kRing) slot -= L::kRing;
-          }
+          if (own < 2) mma_commit(q_done);
+          mma_commit(empty(load));
         }
-        if (!ok && lane == 0) timed_out();
+        __syncwarp();
+        advance(lead);
+        // Load m + 1: V of key tile m and K of tile m + c, the operands of one turn of the
+        // tile (of both tiles for a pair): O += P V, then S of the row tile's next one.
+        int left = own;
+#pragma unroll 1
+        for (int m = 0; m < n; ++m) {
+          const uint32_t size = m + c < n ? 2 : 1;
+          if (pair ? left == 0 : (m & 1) != t) {  // not this tile's
+            if (elect_one()) mbar_arrive(empty(load));
+            __syncwarp();
+            advance(size);
+            continue;
+          }
+          const uint32_t ks = slot + 1 < L::kRing ? slot + 1 : 0;
+          ok = wait(full(load), round_of(load));
+          if (!ok) break;
+          // by halves of 64 keys: P V of the half, then the next S of the half, which lies over it
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            ok = wait(p_full(t, h), p_par);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              mma_pv<4>(to, ts + L::kPHalf * h,
+                        desc_lo(sbase + L::kOffRing + slot * L::kOp + h * 8192, kTile * 128), id_o,
+                        left < own || h > 0);
+              if (left > 1) s_of(ks, h);
+              // committed after the last key tile's first half too: its P V is then complete
+              if (left > 1 || h == 0) mma_commit(s_full(t, h));
+              if (h == 1) {
+                if (left == 2) mma_commit(q_done);
+                if (left == 1) mma_commit(o_done(t));
+                mma_commit(empty(load));
+              }
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          p_par ^= 1;
+          --left;
+          advance(size);
+        }
       }
-      __syncwarp();
-    } else if (warp == kLoadQ) {
-      // ---------------------------------------------------------------- Q loads
-      // A row tile is tpt tokens x G heads, in that order: a box of the qkv rows. Rows past
-      // the request's tokens are other requests' or zeros; nothing of them is written.
+      if (!ok && lane == 0) timed_out();
+    } else {
+      // ---------------------------------------------------------------- the walk, Q loads
+      // Segment i + 1 is published before segment i's Q is loaded. A Q tile is tpt tokens x G
+      // heads, in that order: a box of the qkv rows. Rows past the request's tokens are
+      // other requests' or zeros; nothing of them is written.
       bool ok = true;
       const int tpt = p.tpu / 2;
       const uint32_t bytes = static_cast<uint32_t>(tpt) * p.G * D * 2;
-      Seg g;
-      for (uint32_t i = 0; ok && get_seg(i, g, ok); ++i) {
+      Seg g, next;
+      g.n = 0;
+      bool shared = false;  // the first Q tile in use serves both row tiles
+      uint32_t other = 0;
+      for (uint32_t i = 0; ok; ++i) {
+        const bool more = w.valid();
+        if (more) {
+          next = make_seg(p, w);
+          w.next(p);
+        } else {
+          next.n = 0;
+        }
+        if (i >= kSegs)
+          ok = __all_sync(0xFFFFFFFFu, mbar_wait(seg_empty(i), (i / kSegs - 1) & 1, tp_.timeout_ns,
+                                                 abort_flag)) != 0;
+        if (!ok) break;
+        if (lane == 0) {
+          segs[i % kSegs] = next;
+          mbar_arrive(seg_full(i));
+        }
+        __syncwarp();
         const int blk = g.head0 / p.hq;
-        for (int t = 0; t < (g.pair ? 2 : 1); ++t) {
-          if (issued_q[t] > 0 &&
-              !__all_sync(0xFFFFFFFFu, mbar_wait(q_empty(t), (issued_q[t] - 1) & 1, tp_.timeout_ns,
-                                                 abort_flag))) {
-            ok = false;
-            break;
+        for (int t = 0; g.n > 0 && t < (g.pair ? 2 : 1); ++t) {
+          if (issued_q[t] > 0)
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(q_empty(t), (issued_q[t] - 1) & 1,
+                                                   tp_.timeout_ns, abort_flag)) != 0;
+          if (ok && t == 0 && shared) {  // and the second tile has let go of it
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(q_other, other, tp_.timeout_ns, abort_flag)) != 0;
+            other ^= 1;
           }
+          if (!ok) break;
+          if (t == 0) shared = !g.pair;
           if (lane == 0) {
             mbar_arrive_expect_tx(q_full(t), bytes);
             for (int h = 0; h < L::kHalves; ++h)
@@ -520,29 +561,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           ++issued_q[t];
         }
-      }
-      if (!ok && lane == 0) timed_out();
-    } else {
-      // ---------------------------------------------------------------- the walk
-      bool ok = true;
-      for (uint32_t i = 0; ok; ++i) {
-        Seg g;
-        const bool more = w.valid();
-        if (more)
-          g = make_seg(p, w);
-        else
-          g.n = 0;
-        if (i >= kSegs)
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait(seg_empty(i), (i / kSegs - 1) & 1, tp_.timeout_ns,
-                                                 abort_flag)) != 0;
-        if (!ok) break;
-        if (lane == 0) {
-          segs[i % kSegs] = g;
-          mbar_arrive(seg_full(i));
-        }
-        __syncwarp();
-        if (!more) break;
-        w.next(p);
+        if (i > 0 && g.n == 0) break;
+        g = next;
+        if (i == 0 && !more) break;
       }
       if (!ok && lane == 0) timed_out();
     }
@@ -553,7 +574,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int tpt = p.tpu / 2, tt = x / p.Gv, hh = x - tt * p.Gv;
     PagedRec rec{0, 0, 0, 0, 0};
-    int ns = 0, segs_o = 0, joined = 0;
+    int ns0 = 0, ns1 = 0, segs_o = 0, joined = 0;  // S halves' completions before the segment
     uint32_t tiles0 = 0;  // key tiles of earlier segments
     bool ok = true, taken = true;
     auto wait_all = [&](uint32_t bar, uint32_t parity) -> bool {
@@ -570,19 +591,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lim_min = __reduce_min_sync(0xFFFFFFFFu, lim);
       const int n = g.count(t);
       float m = -INFINITY, l = 0.0f;
-      for (int k = 0; k < n; ++k, ++ns) {
-        const int mm = g.pair ? k : 2 * k + t, k0 = (g.lo + mm) * kTile;  // tile of the segment
-        if (!wait_all(s_full(t), ns & 1)) {
+      const uint64_t sc2 = pair_of(p.scale_log2, p.scale_log2);
+#pragma unroll 1
+      for (int s = 0; s < 2 * n; ++s) {  // half h of the tile's k-th key tile
+        const int k = s >> 1, h = s & 1;
+        const int mm = g.pair ? k : 2 * k + t, k0 = (g.lo + mm) * kTile + 64 * h;
+        if (!wait_all(s_full(t, h), (h ? ns1 : ns0) + k & 1)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        if (k0 + kTile > kv_end) {
+        if (h == 0 && k0 + kTile > kv_end) {
           // V rows past the request's keys may hold anything and 0 * NaN would spoil O
-          const uint32_t l = tiles0 + i + 1 + mm;  // V's load and place in the ring
+          const uint32_t ld = tiles0 + i + 1 + mm;  // V's load and place in the ring
           const uint32_t at =
               2 * tiles0 + (mm == g.n - 1 ? 2 * g.n - 1 : g.pair ? 1 + 2 * mm : 2 + 2 * mm);
-          if (!wait_all(full(l), round_of(l))) {
+          if (!wait_all(full(ld), round_of(ld))) {
             ok = false;
             break;
           }
@@ -594,77 +618,86 @@ __global__ void __launch_bounds__(kThreads, 1)
           fence_proxy_async_smem();
         }
         if (busy) {
-          uint32_t v[kTile];
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            tmem_ld32(tS(t) + lanes + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * c));
-          tmem_ld_wait();
           const uint32_t miss = bad[(tiles0 + mm) % kBadRing];
-          if (k0 + kTile > lim_min || miss) {
+          const bool masked = k0 + 64 > lim_min || miss;
+          const uint32_t src = tS(t) + lanes + 64 * h;
+          uint32_t v[64], pk[32];
+          tmem_ld32(src, *reinterpret_cast<uint32_t(*)[32]>(v));
+          tmem_ld32(src + 32, *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+          tmem_ld_wait();
+          if (masked) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {  // bit i: key 32 c + i is seen
+            for (int c = 0; c < 2; ++c) {  // bit y: key 32 c + y of the half is seen
               const int seen = min(max(lim - (k0 + 32 * c), 0), 32);
               uint32_t bits = seen == 32 ? ~0u : (1u << seen) - 1u;
               if (miss) {
-                const int sh = min(p.ps_log2, 5), span = 32 >> sh;  // pages within the 32 keys
+                const int sh = min(p.ps_log2, 5), span = 32 >> sh;  // pages of the 32 keys
                 for (int b = 0; b < span; ++b)
-                  if ((miss >> ((32 * c + (b << sh)) >> min(p.ps_log2, 7))) & 1)
+                  if ((miss >> ((64 * h + 32 * c + (b << sh)) >> min(p.ps_log2, 7))) & 1)
                     bits &= ~((sh == 5 ? ~0u : (1u << (1 << sh)) - 1u) << (b << sh));
               }
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!(bits & (1u << i))) v[32 * c + i] = 0xff800000u;  // -inf
+              for (int y = 0; y < 32; ++y)
+                if (!(bits & (1u << y))) v[32 * c + y] = 0xff800000u;  // -inf
             }
           }
+          // The weights from the maximum so far; this half's is searched for beside the
+          // exponentials. They hold for every row of the warp unless one's maximum has to
+          // move (by more than 8: weights up to 2^8 are harmless in bf16 and fp32, and o / l
+          // does not depend on m); then they are formed again.
+          float f = 1.0f;
+          uint64_t sum[2];
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          auto weights = [&](bool search) {
+            const float mu = m == -INFINITY ? 0.0f : m;
+            const uint64_t mu2 = pair_of(-mu, -mu);
+            sum[0] = sum[1] = 0;
 #pragma unroll
-          for (int i = 0; i < kTile; i += 8)
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-              mx[y] = max3(mx[y], __uint_as_float(v[i + 2 * y]), __uint_as_float(v[i + 2 * y + 1]));
-          const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-          // The maximum moves only when it grows by more than 8 (weights up to 2^8 are
-          // harmless in bf16 and fp32): o / l does not depend on it.
-          const bool move = mb > m + 8.0f;
-          const float m1 = move ? mb : m, mu = m1 == -INFINITY ? 0.0f : m1;
-          const float f = move ? ex2(m - mu) : 1.0f;
-          m = m1;
-          if (k > 0 && __any_sync(0xFFFFFFFFu, move)) {
-            // the tile's previous P V has completed: s_full's commit came after it
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(tO(t) + lanes + 32 * c, o);
-              tmem_ld_wait();
-#pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st32(tO(t) + lanes + 32 * c, o);
-            }
-          }
-          const uint64_t sc2 = pair_of(p.scale_log2, p.scale_log2), mu2 = pair_of(-mu, -mu);
-          uint64_t sum[2] = {0, 0};
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t pk[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
+            for (int y = 0; y < 32; ++y) {
+              const float s0 = __uint_as_float(v[2 * y]), s1 = __uint_as_float(v[2 * y + 1]);
+              if (search) mx[y & 3] = max3(mx[y & 3], s0, s1);
               float a, b;
-              split(fma2(pair_of(__uint_as_float(v[64 * c + 2 * i]),
-                                 __uint_as_float(v[64 * c + 2 * i + 1])), sc2, mu2), a, b);
+              split(fma2(pair_of(s0, s1), sc2, mu2), a, b);
               a = ex2(a);
               b = ex2(b);
-              sum[i & 1] = add2(sum[i & 1], pair_of(a, b));
-              pk[i] = pack2(a, b);
+              sum[y & 1] = add2(sum[y & 1], pair_of(a, b));
+              pk[y] = pack2(a, b);
             }
-            tmem_st32(tP(t) + lanes + 32 * c, pk);
+          };
+          weights(true);
+          const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+          const bool move = mb > m + 8.0f;
+          if (__any_sync(0xFFFFFFFFu, move)) {
+            const float m1 = move ? mb : m;
+            f = move ? ex2(m - m1) : 1.0f;
+            m = m1;
+            if (s > 0) {
+              // all earlier P V of the tile have completed when the other half's next S has
+              if (!wait_all(s_full(t, h ^ 1), (h ? ns0 + k + 1 : ns1 + k) & 1)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(tO(t) + lanes + 32 * c, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+                tmem_st32(tO(t) + lanes + 32 * c, o);
+              }
+            }
+            weights(false);
           }
+          tmem_st32(tP(t) + lanes + L::kPHalf * h, pk);
           float sa, sb2;
           split(add2(sum[0], sum[1]), sa, sb2);
           l = l * f + (sa + sb2);
           tmem_st_wait();
         }
-        // the next P V overwrites this tile's O: a join has read it
-        if (k == 0 && !taken) {
+        // the segment's first P V overwrites this tile's O: a join has read it
+        if (!taken) {
           if (!wait_all(j_free, (joined - 1) & 1)) {
             ok = false;
             break;
@@ -673,7 +706,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(p_full(t));
+        if (lane == 0) mbar_arrive(p_full(t, h));
+      }
+      if (n > 0) {
+        ns0 += n + 1;
+        ns1 += n;
       }
       tiles0 += g.n;
       if (!ok) break;
@@ -800,13 +837,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   if (*abort_flag) {
     volatile int no_abort = 0;
-    if (warp == kLoadQ && lane == 0)  // the copies this CTA issued have landed
+    if (warp == kWalk && lane == 0)  // the copies this CTA issued have landed
       for (int t = 0; t < 2; ++t)
         if (issued_q[t] > 0) mbar_wait(q_full(t), (issued_q[t] - 1) & 1, kDrainNs, &no_abort);
     if (warp == kProd && lane == 0)
       for (uint32_t l = issued > kLoads ? issued - kLoads : 0; l < issued; ++l)
         mbar_wait(full(l), round_of(l), kDrainNs, &no_abort);
-    if (warp == kMma) {  // and the MMAs it issued have completed
+    if (warp == kMma || warp == kMma + 1) {  // and the MMAs it issued have completed
       if (elect_one()) mma_commit(drain);
       __syncwarp();
       mbar_wait(drain, 0, kDrainNs, &no_abort);
