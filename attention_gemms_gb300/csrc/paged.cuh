@@ -51,9 +51,10 @@ struct PagedParams {
 
 // What CTA i left in its two slots: slot 0 the piece of a unit that began in an earlier
 // CTA (head: 1 the unit goes on after this CTA, 2 it ends here), slot 1 the first piece of
-// a unit that goes on after this CTA (tail = 1; r, vh, u name it). 0: nothing.
-struct PagedRec {
-  int head, tail, r, vh, u;
+// a unit that goes on after this CTA (tail = 1, with the unit's first row, its tokens, its
+// first query head and their number). 0: nothing.
+struct __align__(8) PagedRec {
+  int head, tail, row0, tokens, head0, heads;
 };
 
 #ifdef __CUDACC__
@@ -276,6 +277,17 @@ __device__ __forceinline__ PagedWalk paged_schedule(const PagedParams& p, PagedS
   w.u = lo;
   w.take(p, static_cast<int>(x - paged_prefix(p, w.q, lo)));
   return w;
+}
+
+// the tail entry of a unit
+__device__ __forceinline__ void paged_tail(const PagedParams& p, PagedRec& rec, const PagedReq& q,
+                                           int vh, int u) {
+  const int j = vh / p.hs;
+  rec.tail = 1;
+  rec.row0 = q.row0 + u * p.tpu;
+  rec.tokens = min(p.tpu, q.rows - u * p.tpu);
+  rec.head0 = j * p.G + (vh - j * p.hs) * p.Gv;
+  rec.heads = min(p.Gv, (j + 1) * p.G - rec.head0);
 }
 
 // column of query head t in a qkv row

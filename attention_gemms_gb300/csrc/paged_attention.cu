@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
   constexpr int KX = RT == 16 ? 32 : 16, RY = kThreads / KX, SR = RT / RY, SK = kKT / KX;
   constexpr int CG = D / 4, OY = (kThreads / CG) < RT ? (kThreads / CG) : RT, OR = RT / OY;
   const int kx = tid % KX, ry = tid / KX, cg = tid % CG, oy = tid / CG;
-  PagedRec rec{0, 0, 0, 0, 0};
+  PagedRec rec{0, 0, 0, 0, 0, 0};
   PagedWalk w = paged_schedule(p, sc, blockIdx.x, gridDim.x);
   for (; w.valid(); w.next(p)) {
     const int j = w.vh / p.hs;
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
     }
     const bool begins = w.lo == 0, ends = w.hi == w.tiles;
     if (!begins) rec.head = ends ? 2 : 1;
-    if (begins && !ends) rec.tail = 1, rec.r = w.r, rec.vh = w.vh, rec.u = w.u;
+    if (begins && !ends) paged_tail(p, rec, w.q, w.vh, w.u);
     float* slot = p.part + static_cast<int64_t>(2 * blockIdx.x + (begins ? 1 : 0)) * RT * (D + 2);
     if (oy < OY) {
 #pragma unroll
@@ -250,19 +250,27 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedParams p,
                                                                  const int unit_rows,
                                                                  const int tile_rows) {
+  constexpr int kLanes = kThreads / kJoinRows;  // threads of a row in the first part
   __shared__ int last;
-  __shared__ float wt[kPagedMaxCtas][kJoinRows];
-  __shared__ float ms[kJoinRows][kThreads / kJoinRows + 1], mrow[kJoinRows];
-  __shared__ float ls[kJoinRows][kThreads / kJoinRows + 1];
+  __shared__ float wt[kPagedMaxCtas][kJoinRows], lk[kPagedMaxCtas][kJoinRows];
+  __shared__ float ms[kJoinRows][kLanes + 1], ls[kJoinRows][kLanes + 1];
   pdl_wait();  // the previous kernel's results are complete and visible
   pdl_trigger();
   const int i = blockIdx.x, n = gridDim.x, tid = threadIdx.x;
   const PagedRec rec = p.rec[i];
   if (!rec.tail) return;
-  const PagedReq q = paged_req(p, rec.r);
+  // row of the unit: tiles of tile_rows rows, each of whole tokens
+  const int tpt = tile_rows / p.Gv;
+  auto place = [&](int row, int* token, int* head) -> bool {
+    const int tile = row / tile_rows, x = row - tile * tile_rows;
+    const int tt = x / p.Gv, hh = x - tt * p.Gv;
+    *token = tile * tpt + tt;
+    *head = rec.head0 + hh;
+    return tt < tpt && hh < rec.heads && *token < rec.tokens;
+  };
   int token, head;
-  unit_row(p, q, rec.u, rec.vh, tile_rows, blockIdx.y * kJoinRows, &token, &head);
-  if (token >= q.rows) return;  // tokens ascend with the rows: none of these is one
+  place(blockIdx.y * kJoinRows, &token, &head);
+  if (token >= rec.tokens) return;  // tokens ascend with the rows: none of these is one
   if (tid == 0) last = n;
   __syncthreads();
   for (int k = i + 1 + tid; k < n; k += kThreads)
@@ -274,12 +282,14 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedPara
   {
     const int r = tid % kJoinRows, first = tid / kJoinRows;
     const int row = blockIdx.y * kJoinRows + r;
-    const bool live = unit_row(p, q, rec.u, rec.vh, tile_rows, row, &token, &head);
+    const bool live = place(row, &token, &head);
     float m = -INFINITY;
-    for (int k = first; k < pieces; k += kThreads / kJoinRows) {
+    for (int k = first; k < pieces; k += kLanes) {
       // a CTA without tiles left no piece; rows that are none have none
       const bool has = live && (k == 0 || p.rec[i + k].head != 0);
-      const float mk = has ? slot_of(k)[row] : -INFINITY;
+      const float* s = slot_of(k) + row;
+      const float mk = has ? s[0] : -INFINITY;
+      lk[k][r] = has ? s[unit_rows] : 0.0f;
       wt[k][r] = mk;
       m = fmaxf(m, mk);
     }
@@ -287,16 +297,15 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedPara
     __syncthreads();
     float M = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < kThreads / kJoinRows; ++k) M = fmaxf(M, ms[r][k]);
+    for (int k = 0; k < kLanes; ++k) M = fmaxf(M, ms[r][k]);
     float l = 0.0f;
-    for (int k = first; k < pieces; k += kThreads / kJoinRows) {
+    for (int k = first; k < pieces; k += kLanes) {
       const float mk = wt[k][r];
       const float e = mk == -INFINITY ? 0.0f : exp2f(mk - M);
-      if (e > 0.0f) l += slot_of(k)[unit_rows + row] * e;
+      l += lk[k][r] * e;
       wt[k][r] = e;
     }
     ls[r][first] = l;
-    if (first == 0) mrow[r] = M;
     __syncthreads();
   }
   // Slots of two tiles hold O by groups of 4 columns, (d / 4, rows, 4), as their kernel has a
@@ -306,30 +315,32 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedPara
   for (int e = tid; e < kJoinRows * CG; e += kThreads) {
     const int r = by_cols ? e % kJoinRows : e / CG, cg = by_cols ? e / kJoinRows : e % CG;
     const int row = blockIdx.y * kJoinRows + r;
-    if (!unit_row(p, q, rec.u, rec.vh, tile_rows, row, &token, &head)) continue;
+    if (!place(row, &token, &head)) continue;
     const int64_t at = 2 * unit_rows +
                        4 * (by_cols ? static_cast<int64_t>(cg) * unit_rows + row
                                     : static_cast<int64_t>(row) * CG + cg);
     float f[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
+#pragma unroll 8
     for (int k = 0; k < pieces; ++k) {
       const float w = wt[k][r];
-      if (w == 0.0f) continue;
       float ok[4];
-      load4(slot_of(k) + at, ok);
+      load4(slot_of(k) + at, ok);  // of a piece that is none: anything, not used
 #pragma unroll
-      for (int x = 0; x < 4; ++x) f[x] += ok[x] * w;
+      for (int x = 0; x < 4; ++x) f[x] += w == 0.0f ? 0.0f : ok[x] * w;
     }
-    float l = 0.0f;
+    float l = 0.0f, M = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < kThreads / kJoinRows; ++k) l += ls[r][k];
+    for (int k = 0; k < kLanes; ++k) {
+      l += ls[r][k];
+      M = fmaxf(M, ms[r][k]);
+    }
     const float inv = l > 0.0f ? 1.0f / l : 0.0f;
 #pragma unroll
     for (int x = 0; x < 4; ++x) f[x] *= inv;
-    const int64_t t = static_cast<int64_t>(q.row0) + token;
+    const int64_t t = static_cast<int64_t>(rec.row0) + token;
     store4(static_cast<T*>(p.o) + t * p.H * D + static_cast<int64_t>(head) * D + 4 * cg, f);
     if (cg == 0 && p.lse)
-      p.lse[head * p.T + t] = l > 0.0f ? (mrow[r] + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      p.lse[head * p.T + t] = l > 0.0f ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
   }
 }
 

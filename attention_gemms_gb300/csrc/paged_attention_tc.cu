@@ -214,7 +214,7 @@ struct __align__(16) Seg {
   int n, n0, pair, lo;              // n = 0: no more segments; lo: the first key tile
   int row0, tokens, pos0, kv_end;   // first token's row and position, tokens, keys
   int head0, heads, j, kend;        // first query head, heads, key/value head, unit's keys
-  int r, vh, u, ends;               // the unit; bit 0: begins here, bit 1: ends here
+  int r, ends, pad0, pad1;          // request; bit 0: the unit begins here, bit 1: it ends here
   __device__ __forceinline__ int count(int t) const {  // row tile t's key tiles
     return pair ? (t ? n : n0) : (n + 1 - t) >> 1;
   }
@@ -235,8 +235,6 @@ __device__ __forceinline__ Seg make_seg(const PagedParams& p, const PagedWalk& w
   g.j = j;
   g.kend = paged_unit_kend(p, w.q, w.u);
   g.r = w.r;
-  g.vh = w.vh;
-  g.u = w.u;
   g.ends = (w.lo == 0 ? 1 : 0) | (w.hi == w.tiles ? 2 : 0);
   g.n0 = g.n;
   if (g.pair && p.causal) {  // the first tile's rows see no key of the last tiles
@@ -573,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = warp >> 2, x = threadIdx.x & 127;  // tile, row within it = TMEM lane
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int tpt = p.tpu / 2, tt = x / p.Gv, hh = x - tt * p.Gv;
-    PagedRec rec{0, 0, 0, 0, 0};
+    PagedRec rec{0, 0, 0, 0, 0, 0};
     int ns0 = 0, ns1 = 0, segs_o = 0, joined = 0;  // S halves' completions before the segment
     uint32_t tiles0 = 0;  // key tiles of earlier segments
     bool ok = true, taken = true;
@@ -724,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const bool begins = g.ends & 1, ends = g.ends & 2;
       if (!begins) rec.head = ends ? 2 : 1;
-      if (begins && !ends) rec.tail = 1, rec.r = g.r, rec.vh = g.vh, rec.u = g.u;
+      if (begins && !ends) rec = {rec.head, 1, g.row0, g.tokens, g.head0, g.heads};
       const bool joins = !g.pair && g.count(1) > 0;
       if (!g.pair && t == 1) {
         if (joins) {

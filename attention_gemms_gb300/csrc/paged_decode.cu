@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (dp.debug_hang && warp == 0)
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(never, 0, dp.timeout_ns, abort_flag));
     const int row0 = lane >> 2, col = (lane & 3) * 2;
-    PagedRec rec{0, 0, 0, 0, 0};
+    PagedRec rec{0, 0, 0, 0, 0, 0};
     for (; w.valid(); w.next(p)) {
       const int j = w.vh / p.hs;
       const int kend = paged_unit_kend(p, w.q, w.u);
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int tid = threadIdx.x, jr = tid / TPR, jc = (tid % TPR) * 4;
       const bool begins = w.lo == 0, ends = w.hi == w.tiles;
       if (!begins) rec.head = ends ? 2 : 1;
-      if (begins && !ends) rec.tail = 1, rec.r = w.r, rec.vh = w.vh, rec.u = w.u;
+      if (begins && !ends) paged_tail(p, rec, w.q, w.vh, w.u);
       float M = -INFINITY, lsum = 0.0f;
       int jtoken = 0, jhead = 0;
       bool jlive = false;

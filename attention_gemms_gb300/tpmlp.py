@@ -219,10 +219,18 @@ def _ptr(x):
     return x.data_ptr()
 
 
+_current_stream = None  # torch.cuda.current_stream, once a GPU has been seen
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream if torch.cuda.is_available() else None
+        global _current_stream
+        if _current_stream is None:
+            import torch
+            if not torch.cuda.is_available():
+                return None
+            _current_stream = torch.cuda.current_stream
+        return _current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -412,11 +420,10 @@ def tp_gqa_paged_attention_workspace_size(h, n_heads, n_kv_heads, N, dtype):
 def tp_gqa_paged_attention_fwd(qkv, kcache, vcache, block_table, total_lens, cu_new, o, lse, T, R,
                                h, n_heads, n_kv_heads, N, n_pages, page_size, max_pages, max_new,
                                causal, dtype, ws, ws_bytes, stream=None):
-    _check(lib().tp_gqa_paged_attention_fwd(*[_ptr(t) for t in (qkv, kcache, vcache, block_table,
-                                                                total_lens, cu_new, o, lse)],
-                                            T, R, h, n_heads, n_kv_heads, N, n_pages, page_size,
-                                            max_pages, max_new, int(causal), int(dtype), _ptr(ws),
-                                            int(ws_bytes), _stream(stream)))
+    _check(lib().tp_gqa_paged_attention_fwd(
+        _ptr(qkv), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(total_lens), _ptr(cu_new),
+        _ptr(o), _ptr(lse), T, R, h, n_heads, n_kv_heads, N, n_pages, page_size, max_pages, max_new,
+        causal, dtype, _ptr(ws), ws_bytes, _stream(stream)))
 
 
 def tp_gqa_paged_workspace_size(T, h, n_heads, n_kv_heads, N, dtype, mode):
