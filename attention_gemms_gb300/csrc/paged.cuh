@@ -51,8 +51,8 @@ struct PagedParams {
 
 // What CTA i left in its two slots: slot 0 the piece of a unit that began in an earlier
 // CTA (head: 1 the unit goes on after this CTA, 2 it ends here), slot 1 the first piece of
-// a unit that goes on after this CTA (tail = 1, with the unit's first row, its tokens, its
-// first query head and their number). 0: nothing.
+// a unit that goes on after this CTA (tail: the CTA where it ends, with the unit's first row,
+// its tokens, its first query head and their number). 0: nothing.
 struct __align__(8) PagedRec {
   int head, tail, row0, tokens, head0, heads;
 };
@@ -162,6 +162,8 @@ __device__ __forceinline__ int64_t paged_prefix(const PagedParams& p, const Page
 // (never none of them: a share that ends within a unit's start cost leaves it to the next).
 struct PagedWalk {
   int64_t left;  // work left after the current segment
+  int64_t stop, total;  // the CTA's end on the line, the line's
+  int ctas;             // those with work
   PagedReq q;
   int r, vh, u, units, tiles, lo, hi;
 
@@ -173,6 +175,11 @@ struct PagedWalk {
     left -= end - x;
     lo = max(x - p.unit_cost, 0);
     hi = max(end - p.unit_cost, 0);
+  }
+  // of a segment that does not end its unit (it is the CTA's last one): where the unit ends
+  __device__ __forceinline__ int last_cta() const {
+    const int64_t end = stop + tiles - hi;
+    return static_cast<int>((end * ctas + total - 1) / total) - 1;
   }
   __device__ __forceinline__ void next(const PagedParams& p) {
     if (left <= 0) {
@@ -232,7 +239,10 @@ __device__ __forceinline__ PagedWalk paged_schedule(const PagedParams& p, PagedS
     before += w < warp ? v : 0;
     total += v;
   }
-  const int64_t begin = div_by(total * cta, ctas), end = div_by(total * (cta + 1), ctas);
+  // every CTA below n has work, so that a unit's pieces lie in consecutive ones
+  const int n = static_cast<int>(min(static_cast<int64_t>(ctas), total));
+  const int64_t begin = cta < n ? div_by(total * cta, n) : total;
+  const int64_t end = cta < n ? div_by(total * (cta + 1), n) : total;
   const int64_t mine = before + inc - sum;  // tiles before this thread's requests
   if (end > begin && begin >= mine && begin < mine + sum) {
     int64_t x = begin - mine;
@@ -250,6 +260,9 @@ __device__ __forceinline__ PagedWalk paged_schedule(const PagedParams& p, PagedS
   PagedWalk w;
   w.lo = w.hi = 0;
   w.left = end - begin;
+  w.stop = end;
+  w.total = total;
+  w.ctas = n;
   w.r = sc.r;
   if (w.left <= 0 || w.r < 0 || w.r >= p.R) {
     w.left = 0;
@@ -279,14 +292,14 @@ __device__ __forceinline__ PagedWalk paged_schedule(const PagedParams& p, PagedS
   return w;
 }
 
-// the tail entry of a unit
-__device__ __forceinline__ void paged_tail(const PagedParams& p, PagedRec& rec, const PagedReq& q,
-                                           int vh, int u) {
-  const int j = vh / p.hs;
-  rec.tail = 1;
-  rec.row0 = q.row0 + u * p.tpu;
-  rec.tokens = min(p.tpu, q.rows - u * p.tpu);
-  rec.head0 = j * p.G + (vh - j * p.hs) * p.Gv;
+// the tail entry of the walk's segment
+__device__ __forceinline__ void paged_tail(const PagedParams& p, PagedRec& rec,
+                                           const PagedWalk& w) {
+  const int j = w.vh / p.hs;
+  rec.tail = w.last_cta();
+  rec.row0 = w.q.row0 + w.u * p.tpu;
+  rec.tokens = min(p.tpu, w.q.rows - w.u * p.tpu);
+  rec.head0 = j * p.G + (w.vh - j * p.hs) * p.Gv;
   rec.heads = min(p.Gv, (j + 1) * p.G - rec.head0);
 }
 

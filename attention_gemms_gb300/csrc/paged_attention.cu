@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
     }
     const bool begins = w.lo == 0, ends = w.hi == w.tiles;
     if (!begins) rec.head = ends ? 2 : 1;
-    if (begins && !ends) paged_tail(p, rec, w.q, w.vh, w.u);
+    if (begins && !ends) paged_tail(p, rec, w);
     float* slot = p.part + static_cast<int64_t>(2 * blockIdx.x + (begins ? 1 : 0)) * RT * (D + 2);
     if (oy < OY) {
 #pragma unroll
@@ -240,115 +240,100 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
   if (tid == 0) p.rec[blockIdx.x] = rec;
 }
 
-// CTA (i, y) joins rows [16 y, 16 y + 16) of the unit whose first piece is CTA i's tail: that
-// piece, then the heads of the following CTAs up to the one where the unit ends. First all
-// pieces' maxima and sums at once (a weight per piece and row, into shared memory), then
-// each thread sums its columns over the pieces, whose loads do not wait for one another. A
-// loop that rescaled piece by piece took 21 us for 25 pieces of 16 x 128.
-constexpr int kJoinRows = 16;
-template <typename T, int D>
+// CTA (i, y) joins a part of the unit whose first piece is CTA i's tail: that piece, then the
+// heads of the following CTAs up to the one where the unit ends. A thread has PER groups of
+// 4 columns of one row: the maximum over the pieces first, then weights, sums and outputs,
+// whose loads do not wait for one another. No shared memory, so that the blocks stand
+// ready beside the kernel before them. (Rescaling piece by piece took 21 us for 25 pieces of
+// 16 x 128; weights in shared memory, with the pieces searched for here, 9 us, and 30 us for
+// 151 pairs of 256 x 128.)
+// Slots of two tiles hold O by groups of 4 columns, (d / 4, rows, 4), as their kernel has a
+// thread per row; the others by rows. Threads follow the slots' order.
+template <typename T, int D, int PER>
 __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedParams p,
                                                                  const int unit_rows,
                                                                  const int tile_rows) {
-  constexpr int kLanes = kThreads / kJoinRows;  // threads of a row in the first part
-  __shared__ int last;
-  __shared__ float wt[kPagedMaxCtas][kJoinRows], lk[kPagedMaxCtas][kJoinRows];
-  __shared__ float ms[kJoinRows][kLanes + 1], ls[kJoinRows][kLanes + 1];
   pdl_wait();  // the previous kernel's results are complete and visible
   pdl_trigger();
-  const int i = blockIdx.x, n = gridDim.x, tid = threadIdx.x;
-  const PagedRec rec = p.rec[i];
-  if (!rec.tail) return;
-  // row of the unit: tiles of tile_rows rows, each of whole tokens
-  const int tpt = tile_rows / p.Gv;
-  auto place = [&](int row, int* token, int* head) -> bool {
-    const int tile = row / tile_rows, x = row - tile * tile_rows;
-    const int tt = x / p.Gv, hh = x - tt * p.Gv;
-    *token = tile * tpt + tt;
-    *head = rec.head0 + hh;
-    return tt < tpt && hh < rec.heads && *token < rec.tokens;
-  };
-  int token, head;
-  place(blockIdx.y * kJoinRows, &token, &head);
-  if (token >= rec.tokens) return;  // tokens ascend with the rows: none of these is one
-  if (tid == 0) last = n;
-  __syncthreads();
-  for (int k = i + 1 + tid; k < n; k += kThreads)
-    if (p.rec[k].head == 2) atomicMin(&last, k);
-  __syncthreads();
-  const int pieces = min(last, n - 1) - i + 1;
-  const int64_t floats = static_cast<int64_t>(unit_rows) * (D + 2);
-  auto slot_of = [&](int k) { return p.part + (2 * static_cast<int64_t>(i + k) + (k == 0)) * floats; };
-  {
-    const int r = tid % kJoinRows, first = tid / kJoinRows;
-    const int row = blockIdx.y * kJoinRows + r;
-    const bool live = place(row, &token, &head);
-    float m = -INFINITY;
-    for (int k = first; k < pieces; k += kLanes) {
-      // a CTA without tiles left no piece; rows that are none have none
-      const bool has = live && (k == 0 || p.rec[i + k].head != 0);
-      const float* s = slot_of(k) + row;
-      const float mk = has ? s[0] : -INFINITY;
-      lk[k][r] = has ? s[unit_rows] : 0.0f;
-      wt[k][r] = mk;
-      m = fmaxf(m, mk);
-    }
-    ms[r][first] = m;
-    __syncthreads();
-    float M = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < kLanes; ++k) M = fmaxf(M, ms[r][k]);
-    float l = 0.0f;
-    for (int k = first; k < pieces; k += kLanes) {
-      const float mk = wt[k][r];
-      const float e = mk == -INFINITY ? 0.0f : exp2f(mk - M);
-      l += lk[k][r] * e;
-      wt[k][r] = e;
-    }
-    ls[r][first] = l;
-    __syncthreads();
-  }
-  // Slots of two tiles hold O by groups of 4 columns, (d / 4, rows, 4), as their kernel has a
-  // thread per row; the others by rows. Threads follow the slots' order.
-  const bool by_cols = unit_rows > tile_rows;
   constexpr int CG = D / 4;
-  for (int e = tid; e < kJoinRows * CG; e += kThreads) {
-    const int r = by_cols ? e % kJoinRows : e / CG, cg = by_cols ? e / kJoinRows : e % CG;
-    const int row = blockIdx.y * kJoinRows + r;
-    if (!place(row, &token, &head)) continue;
-    const int64_t at = 2 * unit_rows +
-                       4 * (by_cols ? static_cast<int64_t>(cg) * unit_rows + row
-                                    : static_cast<int64_t>(row) * CG + cg);
-    float f[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-    for (int k = 0; k < pieces; ++k) {
-      const float w = wt[k][r];
-      float ok[4];
-      load4(slot_of(k) + at, ok);  // of a piece that is none: anything, not used
-#pragma unroll
-      for (int x = 0; x < 4; ++x) f[x] += w == 0.0f ? 0.0f : ok[x] * w;
-    }
-    float l = 0.0f, M = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < kLanes; ++k) {
-      l += ls[r][k];
-      M = fmaxf(M, ms[r][k]);
-    }
-    const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) f[x] *= inv;
-    const int64_t t = static_cast<int64_t>(rec.row0) + token;
-    store4(static_cast<T*>(p.o) + t * p.H * D + static_cast<int64_t>(head) * D + 4 * cg, f);
-    if (cg == 0 && p.lse)
-      p.lse[head * p.T + t] = l > 0.0f ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  const int i = blockIdx.x;
+  const PagedRec rec = p.rec[i];
+  if (rec.tail <= i) return;
+  const int pieces = min(rec.tail, static_cast<int>(gridDim.x) - 1) - i + 1;
+  int row, cg, step;  // this thread's first group of columns, and to its next one
+  if (unit_rows > tile_rows) {
+    const int e = blockIdx.y * kThreads + threadIdx.x;
+    row = e % unit_rows;
+    cg = e / unit_rows * PER;
+    step = unit_rows;
+  } else {
+    const int e = blockIdx.y * kThreads + threadIdx.x;
+    row = e / CG;
+    cg = e % CG;
+    step = 0;
   }
+  const int tile = row / tile_rows, x = row - tile * tile_rows, tpt = tile_rows / p.Gv;
+  const int tt = x / p.Gv, hh = x - tt * p.Gv, token = tile * tpt + tt;
+  if (row >= unit_rows || cg >= CG || tt >= tpt || hh >= rec.heads || token >= rec.tokens) return;
+  const int64_t floats = static_cast<int64_t>(unit_rows) * (D + 2);
+  const float* first = p.part + (2 * static_cast<int64_t>(i) + 1) * floats;  // CTA i's tail
+  const float* heads = p.part + 2 * static_cast<int64_t>(i) * floats;        // + 2 k floats: heads
+  float M = first[row];
+#pragma unroll 8
+  for (int k = 1; k < pieces; ++k) M = fmaxf(M, heads[2 * k * floats + row]);
+  const float mu = M == -INFINITY ? 0.0f : M;
+  const int64_t at = 2 * unit_rows + 4 * (step ? static_cast<int64_t>(cg) * step + row
+                                               : static_cast<int64_t>(row) * CG + cg);
+  float l, f[PER][4];
+  {
+    const float w = exp2f(first[row] - mu);
+    l = first[unit_rows + row] * w;
+#pragma unroll
+    for (int g = 0; g < PER; ++g) {
+      load4(first + at + 4 * g * static_cast<int64_t>(step), f[g]);
+#pragma unroll
+      for (int y = 0; y < 4; ++y) f[g][y] *= w;
+    }
+  }
+#pragma unroll 4
+  for (int k = 1; k < pieces; ++k) {
+    const float* s = heads + 2 * k * floats;
+    const float w = exp2f(s[row] - mu);
+    l += s[unit_rows + row] * w;
+#pragma unroll
+    for (int g = 0; g < PER; ++g) {
+      float o[4];
+      load4(s + at + 4 * g * static_cast<int64_t>(step), o);
+#pragma unroll
+      for (int y = 0; y < 4; ++y) f[g][y] += o[y] * w;
+    }
+  }
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const int64_t t = static_cast<int64_t>(rec.row0) + token;
+  const int head = rec.head0 + hh;
+  T* dst = static_cast<T*>(p.o) + t * p.H * D + static_cast<int64_t>(head) * D + 4 * cg;
+#pragma unroll
+  for (int g = 0; g < PER; ++g) {
+#pragma unroll
+    for (int y = 0; y < 4; ++y) f[g][y] *= inv;
+    store4(dst + 4 * g, f[g]);
+  }
+  if (cg == 0 && p.lse)
+    p.lse[head * p.T + t] = l > 0.0f ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 template <typename T, int D>
 tp_status combine_t(const PagedParams& p, int unit_rows, int tile_rows, int ctas, cudaStream_t st) {
-  const dim3 grid(ctas, unit_rows / kJoinRows);
-  TP_CUDA_TRY(launch_kernel(paged_combine_kernel<T, D>, grid, dim3(kThreads), 0, st, p, unit_rows,
-                            tile_rows));
+  if (unit_rows > tile_rows) {
+    constexpr int PER = 4;
+    TP_CUDA_TRY(launch_kernel(paged_combine_kernel<T, D, PER>,
+                              dim3(ctas, unit_rows * (D / 4 / PER) / kThreads), dim3(kThreads), 0,
+                              st, p, unit_rows, tile_rows));
+  } else {
+    TP_CUDA_TRY(launch_kernel(paged_combine_kernel<T, D, 1>,
+                              dim3(ctas, std::max(1, unit_rows * (D / 4) / kThreads)),
+                              dim3(kThreads), 0, st, p, unit_rows, tile_rows));
+  }
   count_launch();
   return TP_OK;
 }

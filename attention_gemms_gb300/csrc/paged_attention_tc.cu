@@ -214,7 +214,8 @@ struct __align__(16) Seg {
   int n, n0, pair, lo;              // n = 0: no more segments; lo: the first key tile
   int row0, tokens, pos0, kv_end;   // first token's row and position, tokens, keys
   int head0, heads, j, kend;        // first query head, heads, key/value head, unit's keys
-  int r, ends, pad0, pad1;          // request; bit 0: the unit begins here, bit 1: it ends here
+  int r, ends, last, pad;           // request; bit 0: the unit begins here, bit 1: it ends
+                                    // here; else the CTA where it ends
   __device__ __forceinline__ int count(int t) const {  // row tile t's key tiles
     return pair ? (t ? n : n0) : (n + 1 - t) >> 1;
   }
@@ -236,6 +237,7 @@ __device__ __forceinline__ Seg make_seg(const PagedParams& p, const PagedWalk& w
   g.kend = paged_unit_kend(p, w.q, w.u);
   g.r = w.r;
   g.ends = (w.lo == 0 ? 1 : 0) | (w.hi == w.tiles ? 2 : 0);
+  g.last = w.hi == w.tiles ? 0 : w.last_cta();
   g.n0 = g.n;
   if (g.pair && p.causal) {  // the first tile's rows see no key of the last tiles
     const int64_t end = min(static_cast<int64_t>(g.pos0) + tpt, static_cast<int64_t>(g.kv_end));
@@ -722,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const bool begins = g.ends & 1, ends = g.ends & 2;
       if (!begins) rec.head = ends ? 2 : 1;
-      if (begins && !ends) rec = {rec.head, 1, g.row0, g.tokens, g.head0, g.heads};
+      if (begins && !ends) rec = {rec.head, g.last, g.row0, g.tokens, g.head0, g.heads};
       const bool joins = !g.pair && g.count(1) > 0;
       if (!g.pair && t == 1) {
         if (joins) {

@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int tid = threadIdx.x, jr = tid / TPR, jc = (tid % TPR) * 4;
       const bool begins = w.lo == 0, ends = w.hi == w.tiles;
       if (!begins) rec.head = ends ? 2 : 1;
-      if (begins && !ends) paged_tail(p, rec, w.q, w.vh, w.u);
+      if (begins && !ends) paged_tail(p, rec, w);
       float M = -INFINITY, lsum = 0.0f;
       int jtoken = 0, jhead = 0;
       bool jlive = false;
