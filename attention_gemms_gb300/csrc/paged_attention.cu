@@ -242,17 +242,19 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
 
 // CTA (i, y) joins a part of the unit whose first piece is CTA i's tail: that piece, then the
 // heads of the following CTAs up to the one where the unit ends. A thread has PER groups of
-// 4 columns of one row: the maximum over the pieces first, then weights, sums and outputs,
-// whose loads do not wait for one another. No shared memory, so that the blocks stand
-// ready beside the kernel before them. (Rescaling piece by piece took 21 us for 25 pieces of
-// 16 x 128; weights in shared memory, with the pieces searched for here, 9 us, and 30 us for
-// 151 pairs of 256 x 128.)
+// 4 columns of one row and every G-th piece: the maximum over its pieces first, then weights,
+// sums and outputs, whose loads do not wait for one another; the G threads of a row and
+// columns join in shared memory. G = 4 for the slots of few rows, where a long context has
+// tens of pieces, and 1 for those of 256, which have two or three.
 // Slots of two tiles hold O by groups of 4 columns, (d / 4, rows, 4), as their kernel has a
 // thread per row; the others by rows. Threads follow the slots' order.
-template <typename T, int D, int PER>
+template <typename T, int D, int PER, int G>
 __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedParams p,
                                                                  const int unit_rows,
                                                                  const int tile_rows) {
+  static_assert(G == 1 || PER == 1, "");
+  constexpr int kPer = kThreads / G;  // threads of a group of pieces
+  __shared__ float join[G > 1 ? G : 1][6][G > 1 ? kPer : 1];
   pdl_wait();  // the previous kernel's results are complete and visible
   pdl_trigger();
   constexpr int CG = D / 4;
@@ -260,44 +262,42 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedPara
   const PagedRec rec = p.rec[i];
   if (rec.tail <= i) return;
   const int pieces = min(rec.tail, static_cast<int>(gridDim.x) - 1) - i + 1;
+  const int group = threadIdx.x / kPer, et = threadIdx.x % kPer;
+  const int e = blockIdx.y * kPer + et;
   int row, cg, step;  // this thread's first group of columns, and to its next one
   if (unit_rows > tile_rows) {
-    const int e = blockIdx.y * kThreads + threadIdx.x;
     row = e % unit_rows;
     cg = e / unit_rows * PER;
     step = unit_rows;
   } else {
-    const int e = blockIdx.y * kThreads + threadIdx.x;
     row = e / CG;
     cg = e % CG;
     step = 0;
   }
   const int tile = row / tile_rows, x = row - tile * tile_rows, tpt = tile_rows / p.Gv;
   const int tt = x / p.Gv, hh = x - tt * p.Gv, token = tile * tpt + tt;
-  if (row >= unit_rows || cg >= CG || tt >= tpt || hh >= rec.heads || token >= rec.tokens) return;
+  const bool live =
+      row < unit_rows && cg < CG && tt < tpt && hh < rec.heads && token < rec.tokens;
+  if (G == 1 && !live) return;
   const int64_t floats = static_cast<int64_t>(unit_rows) * (D + 2);
-  const float* first = p.part + (2 * static_cast<int64_t>(i) + 1) * floats;  // CTA i's tail
-  const float* heads = p.part + 2 * static_cast<int64_t>(i) * floats;        // + 2 k floats: heads
-  float M = first[row];
+  // piece 0 is CTA i's tail (its second slot), piece k CTA i + k's head
+  const float* base = p.part + 2 * static_cast<int64_t>(i) * floats;
+  auto slot_of = [&](int k) { return base + (2 * static_cast<int64_t>(k) + (k == 0)) * floats; };
+  const int count = live ? pieces : 0;
+  float M = -INFINITY;
 #pragma unroll 8
-  for (int k = 1; k < pieces; ++k) M = fmaxf(M, heads[2 * k * floats + row]);
-  const float mu = M == -INFINITY ? 0.0f : M;
+  for (int k = group; k < count; k += G) M = fmaxf(M, slot_of(k)[row]);
+  float mu = M == -INFINITY ? 0.0f : M;
   const int64_t at = 2 * unit_rows + 4 * (step ? static_cast<int64_t>(cg) * step + row
                                                : static_cast<int64_t>(row) * CG + cg);
-  float l, f[PER][4];
-  {
-    const float w = exp2f(first[row] - mu);
-    l = first[unit_rows + row] * w;
+  float l = 0.0f, f[PER][4];
 #pragma unroll
-    for (int g = 0; g < PER; ++g) {
-      load4(first + at + 4 * g * static_cast<int64_t>(step), f[g]);
+  for (int g = 0; g < PER; ++g)
 #pragma unroll
-      for (int y = 0; y < 4; ++y) f[g][y] *= w;
-    }
-  }
+    for (int y = 0; y < 4; ++y) f[g][y] = 0.0f;
 #pragma unroll 4
-  for (int k = 1; k < pieces; ++k) {
-    const float* s = heads + 2 * k * floats;
+  for (int k = group; k < count; k += G) {
+    const float* s = slot_of(k);
     const float w = exp2f(s[row] - mu);
     l += s[unit_rows + row] * w;
 #pragma unroll
@@ -306,6 +306,27 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedPara
       load4(s + at + 4 * g * static_cast<int64_t>(step), o);
 #pragma unroll
       for (int y = 0; y < 4; ++y) f[g][y] += o[y] * w;
+    }
+  }
+  if constexpr (G > 1) {
+    join[group][0][et] = M;
+    join[group][1][et] = l;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) join[group][2 + y][et] = f[0][y];
+    __syncthreads();
+    if (group > 0 || !live) return;
+#pragma unroll
+    for (int g = 1; g < G; ++g) M = fmaxf(M, join[g][0][et]);
+    mu = M == -INFINITY ? 0.0f : M;
+    l = 0.0f;
+#pragma unroll
+    for (int y = 0; y < 4; ++y) f[0][y] = 0.0f;
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+      const float w = exp2f(join[g][0][et] - mu);
+      l += join[g][1][et] * w;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) f[0][y] += join[g][2 + y][et] * w;
     }
   }
   const float inv = l > 0.0f ? 1.0f / l : 0.0f;
@@ -326,12 +347,13 @@ template <typename T, int D>
 tp_status combine_t(const PagedParams& p, int unit_rows, int tile_rows, int ctas, cudaStream_t st) {
   if (unit_rows > tile_rows) {
     constexpr int PER = 4;
-    TP_CUDA_TRY(launch_kernel(paged_combine_kernel<T, D, PER>,
+    TP_CUDA_TRY(launch_kernel(paged_combine_kernel<T, D, PER, 1>,
                               dim3(ctas, unit_rows * (D / 4 / PER) / kThreads), dim3(kThreads), 0,
                               st, p, unit_rows, tile_rows));
   } else {
-    TP_CUDA_TRY(launch_kernel(paged_combine_kernel<T, D, 1>,
-                              dim3(ctas, std::max(1, unit_rows * (D / 4) / kThreads)),
+    constexpr int G = 4;
+    TP_CUDA_TRY(launch_kernel(paged_combine_kernel<T, D, 1, G>,
+                              dim3(ctas, std::max(1, unit_rows * (D / 4) / (kThreads / G))),
                               dim3(kThreads), 0, st, p, unit_rows, tile_rows));
   }
   count_launch();
