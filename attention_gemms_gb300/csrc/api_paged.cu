@@ -101,7 +101,7 @@ tp_status launch_paged(const PagedArgs& a, const PagedGqa& g, void* ws, cudaStre
     return g.d >= 64 && p.G <= 128 && a.max_new * p.G > 16
                ? launch_paged_tc(p, g.d, a.N, st)
                : launch_paged_decode(p, g.d, st);
-  return launch_paged_simt(p, g.d, a.max_new * p.G > 16, a.dt, st);
+  return launch_paged_simt(p, g.d, a.max_new * p.G > 16, st);
 }
 
 }  // namespace

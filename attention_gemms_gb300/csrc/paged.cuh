@@ -321,9 +321,9 @@ __device__ __forceinline__ int64_t paged_row(const PagedParams& p, const int32_t
 
 #endif  // __CUDACC__
 
-// kernels (bf16 / fp32, CUDA cores) and the join of the partial results
+// fp32 on CUDA cores (wide: chunks), and the join of the partial results (paged_attention.cu)
 constexpr int kPagedMaxCtas = 304;
-tp_status launch_paged_simt(PagedParams p, int d, bool wide, tp_dtype dt, cudaStream_t st);
+tp_status launch_paged_simt(PagedParams p, int d, bool wide, cudaStream_t st);
 // unit_rows: rows of a slot; tile_rows: rows of its tiles (whole tokens each)
 tp_status launch_paged_combine(const PagedParams& p, int d, int unit_rows, int tile_rows, int ctas,
                                tp_dtype dt, cudaStream_t st);

@@ -93,6 +93,28 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
     const int j = w.vh / p.hs;
     const int32_t* tab = p.table + static_cast<int64_t>(w.r) * p.max_pages;
     const int kend = paged_unit_kend(p, w.q, w.u);
+    // rows of the unit that are any: a decoding request beside chunks has few of the 64
+    const int rows = min(p.tpu, w.q.rows - w.u * p.tpu) * p.Gv;
+    // this thread's part of a key tile: its next one is on its way while one is worked on
+    constexpr int NL = kKT * CG / kThreads;
+    static_assert(kKT * CG % kThreads == 0, "whole loads per thread");
+    float fk[NL][4], fv[NL][4];
+    bool has[NL];
+    auto fetch = [&](int k0) {
+#pragma unroll
+      for (int y = 0; y < NL; ++y) {
+        const int e = tid + y * kThreads, k = e / CG, c = (e - k * CG) * 4;
+        const int64_t row = k0 + k < kend ? paged_row(p, tab, j, k0 + k) : -1;
+        has[y] = row >= 0;
+#pragma unroll
+        for (int z = 0; z < 4; ++z) fk[y][z] = fv[y][z] = 0.0f;
+        if (has[y]) {
+          load4(static_cast<const T*>(p.kc) + row * D + c, fk[y]);
+          load4(static_cast<const T*>(p.vc) + row * D + c, fv[y]);
+        }
+      }
+    };
+    fetch(w.lo * kKT);
     __syncthreads();  // the previous segment's readers are done
     for (int e = tid; e < RT * CG; e += kThreads) {
       const int i = e / CG, c = (e - i * CG) * 4;
@@ -108,7 +130,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
     }
     for (int i = tid; i < RT; i += kThreads) {
       ms[i] = -INFINITY;
-      ls[i] = 0.0f;
+      ls[i] = ws[i] = 0.0f;
     }
     float acc[OR][4];
 #pragma unroll
@@ -118,18 +140,14 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
     for (int tile = w.lo; tile < w.hi; ++tile) {
       const int k0 = tile * kKT;
       __syncthreads();
-      for (int e = tid; e < kKT * CG; e += kThreads) {
-        const int k = e / CG, c = (e - k * CG) * 4;
-        float fk[4] = {0.f, 0.f, 0.f, 0.f}, fv[4] = {0.f, 0.f, 0.f, 0.f};
-        const int64_t row = k0 + k < kend ? paged_row(p, tab, j, k0 + k) : -1;
-        if (row >= 0) {
-          load4(static_cast<const T*>(p.kc) + row * D + c, fk);
-          load4(static_cast<const T*>(p.vc) + row * D + c, fv);
-        }
-        store4(Ks + k * LD + c, fk);
-        store4(Vs + k * LD + c, fv);
-        if (c == 0) ok[k] = row >= 0;
+#pragma unroll
+      for (int y = 0; y < NL; ++y) {
+        const int e = tid + y * kThreads, k = e / CG, c = (e - k * CG) * 4;
+        store4(Ks + k * LD + c, fk[y]);
+        store4(Vs + k * LD + c, fv[y]);
+        if (c == 0) ok[k] = has[y];
       }
+      if (tile + 1 < w.hi) fetch(k0 + kKT);
       __syncthreads();
       {
         float s[SR][SK];
@@ -145,6 +163,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
             kv[b] = *reinterpret_cast<const float4*>(Ks + (kx + b * KX) * LD + c);
 #pragma unroll
           for (int a = 0; a < SR; ++a) {
+            if (a * RY >= rows) break;
             const float4 q = *reinterpret_cast<const float4*>(Qs + (ry + a * RY) * LD + c);
 #pragma unroll
             for (int b = 0; b < SK; ++b)
@@ -153,6 +172,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
         }
 #pragma unroll
         for (int a = 0; a < SR; ++a) {
+          if (a * RY >= rows) break;
           const int i = ry + a * RY;
           // keys the row's token sees: all, or up to its own position
           const int64_t lim = p.causal ? static_cast<int64_t>(w.q.total) - w.q.n + w.u * p.tpu +
@@ -166,7 +186,7 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
         }
       }
       __syncthreads();
-      for (int i = warp; i < RT; i += kThreads / 32) {
+      for (int i = warp; i < rows; i += kThreads / 32) {
         const float a = Ps[i * PLD + lane], b = Ps[i * PLD + lane + 32];
         float mx = fmaxf(a, b);
 #pragma unroll
@@ -190,20 +210,25 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
       if (oy < OY) {
 #pragma unroll
         for (int i = 0; i < OR; ++i) {
+          if (i * OY >= rows) break;
           const float wt = ws[oy + i * OY];
 #pragma unroll
           for (int k = 0; k < 4; ++k) acc[i][k] *= wt;
         }
-#pragma unroll 4
-        for (int k = 0; k < kKT; ++k) {
-          const float4 v = *reinterpret_cast<const float4*>(Vs + k * LD + cg * 4);
+#pragma unroll 2
+        for (int k = 0; k < kKT; k += 4) {
+          float4 v[4];
+#pragma unroll
+          for (int z = 0; z < 4; ++z)
+            v[z] = *reinterpret_cast<const float4*>(Vs + (k + z) * LD + cg * 4);
 #pragma unroll
           for (int i = 0; i < OR; ++i) {
-            const float e = Ps[(oy + i * OY) * PLD + k];
-            acc[i][0] += e * v.x;
-            acc[i][1] += e * v.y;
-            acc[i][2] += e * v.z;
-            acc[i][3] += e * v.w;
+            if (i * OY >= rows) break;
+            const float4 e = *reinterpret_cast<const float4*>(Ps + (oy + i * OY) * PLD + k);
+            acc[i][0] += e.x * v[0].x + e.y * v[1].x + e.z * v[2].x + e.w * v[3].x;
+            acc[i][1] += e.x * v[0].y + e.y * v[1].y + e.z * v[2].y + e.w * v[3].y;
+            acc[i][2] += e.x * v[0].z + e.y * v[1].z + e.z * v[2].z + e.w * v[3].z;
+            acc[i][3] += e.x * v[0].w + e.y * v[1].w + e.z * v[2].w + e.w * v[3].w;
           }
         }
       }
@@ -390,8 +415,8 @@ tp_status simt_d(PagedParams& p, int d, bool wide, cudaStream_t st) {
 
 }  // namespace
 
-tp_status launch_paged_simt(PagedParams p, int d, bool wide, tp_dtype dt, cudaStream_t st) {
-  return dt == TP_BF16 ? simt_d<__nv_bfloat16>(p, d, wide, st) : simt_d<float>(p, d, wide, st);
+tp_status launch_paged_simt(PagedParams p, int d, bool wide, cudaStream_t st) {
+  return simt_d<float>(p, d, wide, st);
 }
 
 tp_status launch_paged_combine(const PagedParams& p, int d, int unit_rows, int tile_rows, int ctas,
