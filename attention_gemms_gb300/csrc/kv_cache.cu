@@ -23,7 +23,7 @@
 namespace tp {
 namespace {
 
-constexpr int kTableThreads = 1024;
+constexpr int kTableThreads = 1024;  // at most; a decode step's few rows take fewer
 constexpr int kTableCtas = 8;
 constexpr int kMaxLen = 1 << 30;  // a length, as the sums take it
 
@@ -41,13 +41,13 @@ __global__ void __launch_bounds__(kTableThreads) kv_tables_kernel(const TablesPa
   pdl_wait();  // the previous kernel's results are complete and visible
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int cta = blockIdx.x, ctas = gridDim.x;
+  const int cta = blockIdx.x, ctas = gridDim.x, threads = blockDim.x;
   auto pages_of = [&](int64_t len) {
     const int64_t n = (len + (static_cast<int64_t>(1) << p.ps_log2) - 1) >> p.ps_log2;
     return static_cast<int>(min(n, static_cast<int64_t>(p.max_pages)));
   };
   const int head = min(max(*p.head, 0), p.n_free);
-  const int per = (p.R + kTableThreads - 1) / kTableThreads;
+  const int per = (p.R + threads - 1) / threads;
   const int r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
   int64_t rows = 0, pages = 0;
   for (int r = r0; r < r1; ++r) {
@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kTableThreads) kv_tables_kernel(const TablesPa
   __syncthreads();
   int64_t sr = ir - rows, sp = ip - pages, all_rows = 0, all_pages = 0;
 #pragma unroll 4
-  for (int w = 0; w < kTableThreads / 32; ++w) {
+  for (int w = 0; w < threads / 32; ++w) {
     if (w < warp) sr += wr[w], sp += wp[w];
     all_rows += wr[w], all_pages += wp[w];
   }
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kTableThreads) kv_tables_kernel(const TablesPa
     return i < p.n_free ? p.free_pages[i] : -1;
   };
   // lengths and offsets; the pages of request r: one warp
-  const int gt = cta * kTableThreads + tid, step = ctas * kTableThreads;
+  const int gt = cta * threads + tid, step = ctas * threads;
   for (int r = gt; r <= p.R; r += step) {
     p.cu[r] = cu_s[r];
     if (r < p.R)
@@ -105,26 +105,42 @@ __global__ void __launch_bounds__(kTableThreads) kv_tables_kernel(const TablesPa
       p.table[static_cast<int64_t>(r) * p.max_pages + have + k] = fresh_page(r, k);
   }
   const int live = cu_s[p.R];
-  for (int64_t t = gt; t < p.T; t += step) {
-    int slot = -1, at = -1;
-    if (t < live) {
+  // four rows at a time: their searches and page loads overlap
+  constexpr int kBatch = 4;
+  for (int64_t t0 = gt; t0 < p.T; t0 += kBatch * static_cast<int64_t>(step)) {
+    int at[kBatch], req[kBatch];
+    int64_t page[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int64_t t = t0 + i * static_cast<int64_t>(step);
+      at[i] = -1;
+      page[i] = -1;
+      if (t >= live) continue;
       int lo = 0, hi = p.R;  // cu[lo] <= t < cu[hi]
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (cu_s[mid] <= t) lo = mid;
         else hi = mid;
       }
-      at = ctx_s[lo] + static_cast<int>(t - cu_s[lo]);
-      const int pg = at >> p.ps_log2, have = pages_of(ctx_s[lo]);
-      if (pg < p.max_pages) {
-        const int64_t page = pg < have ? p.table[static_cast<int64_t>(lo) * p.max_pages + pg]
-                                       : fresh_page(lo, pg - have);
-        const int64_t s = (page << p.ps_log2) + (at & ((1 << p.ps_log2) - 1));
-        slot = page >= 0 && s <= kTop ? static_cast<int>(s) : -1;
-      }
+      req[i] = lo;
+      at[i] = ctx_s[lo] + static_cast<int>(t - cu_s[lo]);
     }
-    p.slots[t] = slot;
-    if (p.pos) p.pos[t] = at;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int pg = at[i] >> p.ps_log2;
+      if (at[i] < 0 || pg >= p.max_pages || t0 + i * static_cast<int64_t>(step) >= p.T) continue;
+      const int have = pages_of(ctx_s[req[i]]);
+      page[i] = pg < have ? p.table[static_cast<int64_t>(req[i]) * p.max_pages + pg]
+                          : fresh_page(req[i], pg - have);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int64_t t = t0 + i * static_cast<int64_t>(step);
+      if (t >= p.T) break;
+      const int64_t s = (page[i] << p.ps_log2) + (at[i] & ((1 << p.ps_log2) - 1));
+      p.slots[t] = page[i] >= 0 && s <= kTop ? static_cast<int>(s) : -1;
+      if (p.pos) p.pos[t] = at[i];
+    }
   }
   if (gt == 0) {
     const int64_t left = p.n_free - head;
@@ -202,6 +218,8 @@ tp_status launch_kv_tables(const int32_t* ctx, const int32_t* add, const int32_t
                                      static_cast<int>((3 * kKvMaxRequests + 2) * sizeof(int32_t))));
     mark_device(attr_set);
   }
+  const int64_t most = std::max(T, R);
+  const int threads = static_cast<int>(std::clamp<int64_t>((most + 31) / 32 * 32, 128, kTableThreads));
   const int ctas = static_cast<int>(std::clamp<int64_t>(
       (std::max(T, 32 * R) + 2 * kTableThreads - 1) / (2 * kTableThreads), 1, kTableCtas));
   cudaLaunchConfig_t cfg = {};
@@ -218,7 +236,7 @@ tp_status launch_kv_tables(const int32_t* ctx, const int32_t* add, const int32_t
     ++na;
   }
   cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kTableThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
