@@ -48,6 +48,20 @@ __device__ __forceinline__ void store4(__nv_bfloat16* dst, const float (&f)[4]) 
                                               *reinterpret_cast<const uint32_t*>(&b));
 }
 
+__device__ __forceinline__ float ex2(float x) {  // relative error about 2^-22, 4 fp32 roundings
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 16 bytes of global into shared memory, zeros unless `live` (the address is valid either way)
+__device__ __forceinline__ void copy16(float* dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src), "r"(live ? 16 : 0)
+               : "memory");
+}
+
 // Row i of a unit (tiles of tile_rows rows, each of whole tokens): its token and query
 // head; false when the row is none.
 __device__ __forceinline__ bool unit_row(const PagedParams& p, const PagedReq& q, int u, int vh,
@@ -66,27 +80,35 @@ __device__ __forceinline__ bool unit_row(const PagedParams& p, const PagedReq& q
 template <typename T, int D, int RT>
 struct SimtLayout {
   static constexpr int LD = D + 4;  // padded row: float4 accesses of 8 rows hit 32 banks
-  static constexpr int kQ = 0, kK = RT * LD, kV = kK + kKT * LD, kP = kV + kKT * LD,
-                       kStat = kP + RT * (kKT + 4), kEnd = kStat + 3 * RT + kKT;
+  // Q | two stages of K and V | P | m, l, weight per row | key flags per stage
+  static constexpr int kQ = 0, kKV = RT * LD, kStage = 2 * kKT * LD, kP = kKV + 2 * kStage,
+                       kStat = kP + RT * (kKT + 4), kEnd = kStat + 3 * RT + 2 * kKT;
   static constexpr int kSmem = kEnd * 4;
+  static constexpr int kCtas = kSmem <= 112 * 1024 ? 2 : 1;  // per SM
 };
 
 template <typename T, int D, int RT>
-__global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(kThreads, SimtLayout<T, D, RT>::kCtas)
+    paged_simt_kernel(const PagedParams p) {
   using Lay = SimtLayout<T, D, RT>;
   constexpr int LD = Lay::LD, PLD = kKT + 4;
   extern __shared__ __align__(16) float sm[];
-  float *Qs = sm + Lay::kQ, *Ks = sm + Lay::kK, *Vs = sm + Lay::kV, *Ps = sm + Lay::kP;
+  float *Qs = sm + Lay::kQ, *Ps = sm + Lay::kP;
   float *ms = sm + Lay::kStat, *ls = ms + RT, *ws = ls + RT;
-  int* ok = reinterpret_cast<int*>(ws + RT);  // key is in the cache
+  int* oks = reinterpret_cast<int*>(ws + RT);  // key is in the cache, per stage
   __shared__ PagedSched sc;
   pdl_wait();  // the previous kernel's results are complete and visible
   pdl_trigger();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  // scores: RT / RY rows x 64 / KX keys per thread; output: D / 4 column groups
-  constexpr int KX = RT == 16 ? 32 : 16, RY = kThreads / KX, SR = RT / RY, SK = kKT / KX;
-  constexpr int CG = D / 4, OY = (kThreads / CG) < RT ? (kThreads / CG) : RT, OR = RT / OY;
-  const int kx = tid % KX, ry = tid / KX, cg = tid % CG, oy = tid / CG;
+  // Scores: a warp has 8 lanes of keys x 4 of rows, a thread SK keys and SR rows of the tile,
+  // so that each 16-byte operand access of the warp is one or a half pass over the banks (16
+  // x 2 lanes read four times the bytes and took 2.5 times as long). Likewise the output: CL
+  // lanes of 4 columns x RL of rows.
+  constexpr int RG = RT / 16, SR = 4, SK = kKT / (8 / RG) / 8;  // RG groups of 16 rows
+  const int kx = lane & 7, sk0 = (warp / RG) * 8 * SK + kx, sr0 = (warp % RG) * 16 + (lane >> 3);
+  constexpr int CG = D / 4, CL = CG < 8 ? CG : 8, RL = 32 / CL, CW = CG / CL, RW = 8 / CW;
+  constexpr int OY = RL * RW < RT ? RL * RW : RT, OR = RT / OY;
+  const int cg = (warp % CW) * CL + lane % CL, oy = (warp / CW) * RL + lane / CL;
   PagedRec rec{0, 0, 0, 0, 0, 0};
   PagedWalk w = paged_schedule(p, sc, blockIdx.x, gridDim.x);
   for (; w.valid(); w.next(p)) {
@@ -95,27 +117,24 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
     const int kend = paged_unit_kend(p, w.q, w.u);
     // rows of the unit that are any: a decoding request beside chunks has few of the 64
     const int rows = min(p.tpu, w.q.rows - w.u * p.tpu) * p.Gv;
-    // this thread's part of a key tile: its next one is on its way while one is worked on
-    constexpr int NL = kKT * CG / kThreads;
-    static_assert(kKT * CG % kThreads == 0, "whole loads per thread");
-    float fk[NL][4], fv[NL][4];
-    bool has[NL];
-    auto fetch = [&](int k0) {
-#pragma unroll
-      for (int y = 0; y < NL; ++y) {
-        const int e = tid + y * kThreads, k = e / CG, c = (e - k * CG) * 4;
+    // A key tile's loads run beside the work on the one before it (the first's beside Q's):
+    // copies into shared memory that occupy no registers; missing keys are zeros.
+    auto fetch = [&](int tile) {
+      const int k0 = tile * kKT, stage = (tile - w.lo) & 1;
+      float* Ks = sm + Lay::kKV + stage * Lay::kStage;
+#pragma unroll 4
+      for (int e = tid; e < kKT * CG; e += kThreads) {
+        const int k = e / CG, c = (e - k * CG) * 4;
         const int64_t row = k0 + k < kend ? paged_row(p, tab, j, k0 + k) : -1;
-        has[y] = row >= 0;
-#pragma unroll
-        for (int z = 0; z < 4; ++z) fk[y][z] = fv[y][z] = 0.0f;
-        if (has[y]) {
-          load4(static_cast<const T*>(p.kc) + row * D + c, fk[y]);
-          load4(static_cast<const T*>(p.vc) + row * D + c, fv[y]);
-        }
+        const int64_t at = row < 0 ? 0 : row * D + c;
+        copy16(Ks + k * LD + c, static_cast<const T*>(p.kc) + at, row >= 0);
+        copy16(Ks + (kKT + k) * LD + c, static_cast<const T*>(p.vc) + at, row >= 0);
+        if (c == 0) oks[stage * kKT + k] = row >= 0;
       }
+      asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    fetch(w.lo * kKT);
     __syncthreads();  // the previous segment's readers are done
+    fetch(w.lo);
     for (int e = tid; e < RT * CG; e += kThreads) {
       const int i = e / CG, c = (e - i * CG) * 4;
       int token, head;
@@ -123,8 +142,6 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
       if (unit_row(p, w.q, w.u, w.vh, RT, i, &token, &head)) {
         load4(static_cast<const T*>(p.qkv) + (static_cast<int64_t>(w.q.row0) + token) * p.ldq +
                   paged_qcol<D>(p, head) + c, f);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) f[k] *= p.scale_log2;
       }
       store4(Qs + i * LD + c, f);
     }
@@ -132,22 +149,30 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
       ms[i] = -INFINITY;
       ls[i] = ws[i] = 0.0f;
     }
+    int lim[SR];  // keys a row's token sees: all, or up to its own position
+#pragma unroll
+    for (int a = 0; a < SR; ++a)
+      lim[a] = p.causal ? static_cast<int>(
+                              min(static_cast<int64_t>(w.q.kv_end),
+                                  static_cast<int64_t>(w.q.total) - w.q.n + w.u * p.tpu +
+                                      (sr0 + 4 * a) / p.Gv + 1))
+                        : w.q.kv_end;
     float acc[OR][4];
 #pragma unroll
     for (int i = 0; i < OR; ++i)
 #pragma unroll
       for (int k = 0; k < 4; ++k) acc[i][k] = 0.0f;
     for (int tile = w.lo; tile < w.hi; ++tile) {
-      const int k0 = tile * kKT;
-      __syncthreads();
-#pragma unroll
-      for (int y = 0; y < NL; ++y) {
-        const int e = tid + y * kThreads, k = e / CG, c = (e - k * CG) * 4;
-        store4(Ks + k * LD + c, fk[y]);
-        store4(Vs + k * LD + c, fv[y]);
-        if (c == 0) ok[k] = has[y];
+      const int k0 = tile * kKT, stage = (tile - w.lo) & 1;
+      const float *Ks = sm + Lay::kKV + stage * Lay::kStage, *Vs = Ks + kKT * LD;
+      const int* ok = oks + stage * kKT;
+      if (tile + 1 < w.hi) {
+        if (tile > w.lo) __syncthreads();  // the other stage's readers are done
+        fetch(tile + 1);
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+      } else {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
       }
-      if (tile + 1 < w.hi) fetch(k0 + kKT);
       __syncthreads();
       {
         float s[SR][SK];
@@ -155,56 +180,83 @@ __global__ void __launch_bounds__(kThreads) paged_simt_kernel(const PagedParams 
         for (int a = 0; a < SR; ++a)
 #pragma unroll
           for (int b = 0; b < SK; ++b) s[a][b] = 0.0f;
+        const int rows_here = rows - (warp % RG) * 16;
+        if (rows_here > 0) {
+          auto dot = [&](auto sr) {  // the first sr of this thread's rows
+            constexpr int N = decltype(sr)::value;
 #pragma unroll 4
-        for (int c = 0; c < D; c += 4) {
-          float4 kv[SK];
+            for (int c = 0; c < D; c += 4) {
+              float4 kv[SK];
 #pragma unroll
-          for (int b = 0; b < SK; ++b)
-            kv[b] = *reinterpret_cast<const float4*>(Ks + (kx + b * KX) * LD + c);
+              for (int b = 0; b < SK; ++b)
+                kv[b] = *reinterpret_cast<const float4*>(Ks + (sk0 + 8 * b) * LD + c);
 #pragma unroll
-          for (int a = 0; a < SR; ++a) {
-            if (a * RY >= rows) break;
-            const float4 q = *reinterpret_cast<const float4*>(Qs + (ry + a * RY) * LD + c);
+              for (int a = 0; a < N; ++a) {
+                const float4 q = *reinterpret_cast<const float4*>(Qs + (sr0 + 4 * a) * LD + c);
 #pragma unroll
-            for (int b = 0; b < SK; ++b)
-              s[a][b] += q.x * kv[b].x + q.y * kv[b].y + q.z * kv[b].z + q.w * kv[b].w;
-          }
-        }
-#pragma unroll
-        for (int a = 0; a < SR; ++a) {
-          if (a * RY >= rows) break;
-          const int i = ry + a * RY;
-          // keys the row's token sees: all, or up to its own position
-          const int64_t lim = p.causal ? static_cast<int64_t>(w.q.total) - w.q.n + w.u * p.tpu +
-                                             i / p.Gv + 1
-                                       : w.q.kv_end;
+                for (int b = 0; b < SK; ++b) {
+                  s[a][b] = fmaf(q.x, kv[b].x, s[a][b]);
+                  s[a][b] = fmaf(q.y, kv[b].y, s[a][b]);
+                  s[a][b] = fmaf(q.z, kv[b].z, s[a][b]);
+                  s[a][b] = fmaf(q.w, kv[b].w, s[a][b]);
+                }
+              }
+            }
+          };
+          if (rows_here > 4)
+            dot(std::integral_constant<int, SR>{});
+          else
+            dot(std::integral_constant<int, 1>{});
 #pragma unroll
           for (int b = 0; b < SK; ++b) {
-            const int k = kx + b * KX;
-            Ps[i * PLD + k] = (ok[k] && k0 + k < lim) ? s[a][b] : -INFINITY;
+            const int k = sk0 + 8 * b;
+            const bool there = ok[k];
+#pragma unroll
+            for (int a = 0; a < SR; ++a)
+              Ps[(sr0 + 4 * a) * PLD + k] =
+                  there && k0 + k < lim[a] ? s[a][b] * p.scale_log2 : -INFINITY;
           }
         }
       }
       __syncthreads();
-      for (int i = warp; i < rows; i += kThreads / 32) {
-        const float a = Ps[i * PLD + lane], b = Ps[i * PLD + lane + 32];
-        float mx = fmaxf(a, b);
+      {
+        // a warp's rows side by side: one row's shuffles wait behind another's
+        constexpr int NR = RT / 8;
+        float a[NR], b[NR], mx[NR];
+        auto each = [&](auto f) {
 #pragma unroll
-        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-        const float m0 = ms[i], m1 = fmaxf(m0, mx), mu = m1 == -INFINITY ? 0.0f : m1;
-        const float ea = exp2f(a - mu), eb = exp2f(b - mu);
-        Ps[i * PLD + lane] = ea;
-        Ps[i * PLD + lane + 32] = eb;
-        float sum = ea + eb;
+          for (int y = 0; y < NR; ++y)
+            if (warp + 8 * y < rows) f(y, warp + 8 * y);
+        };
+        each([&](int y, int i) {
+          a[y] = Ps[i * PLD + lane];
+          b[y] = Ps[i * PLD + lane + 32];
+          mx[y] = fmaxf(a[y], b[y]);
+        });
 #pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        for (int o = 16; o; o >>= 1)
+          each([&](int y, int) { mx[y] = fmaxf(mx[y], __shfl_xor_sync(0xFFFFFFFFu, mx[y], o)); });
+        each([&](int y, int i) {
+          const float m0 = ms[i], m1 = fmaxf(m0, mx[y]), mu = m1 == -INFINITY ? 0.0f : m1;
+          a[y] = ex2(a[y] - mu);
+          b[y] = ex2(b[y] - mu);
+          Ps[i * PLD + lane] = a[y];
+          Ps[i * PLD + lane + 32] = b[y];
+          a[y] += b[y];
+          b[y] = ex2(m0 - mu);
+          mx[y] = m1;
+        });
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+          each([&](int y, int) { a[y] += __shfl_xor_sync(0xFFFFFFFFu, a[y], o); });
         __syncwarp();
-        if (lane == 0) {
-          const float wt = exp2f(m0 - mu);
-          ws[i] = wt;
-          ls[i] = ls[i] * wt + sum;
-          ms[i] = m1;
-        }
+        each([&](int y, int i) {
+          if (lane == 0) {
+            ws[i] = b[y];
+            ls[i] = ls[i] * b[y] + a[y];
+            ms[i] = mx[y];
+          }
+        });
       }
       __syncthreads();
       if (oy < OY) {
@@ -395,7 +447,7 @@ tp_status simt_t(PagedParams& p, cudaStream_t st) {
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kSmem));
     mark_device(attr_set);
   }
-  const int ctas = std::min(kPagedMaxCtas, device_sm_count() * (Lay::kSmem <= 100 * 1024 ? 2 : 1));
+  const int ctas = std::min(kPagedMaxCtas, device_sm_count() * Lay::kCtas);
   TP_CUDA_TRY(launch_kernel(paged_simt_kernel<T, D, RT>, dim3(ctas), dim3(kThreads),
                             static_cast<size_t>(Lay::kSmem), st, p));
   count_launch();
