@@ -49,8 +49,16 @@ tp_status check_pages(int64_t n_pages, int64_t page_size, int64_t max_pages, int
               TP_ERR_SHAPE, "page_size must be a power of two from 8 to 256"));
   TP_TRY(need(n_pages < (1ll << 31) && n_pages * page_size <= 2147482623ll / Hkv, TP_ERR_SHAPE,
               "n_pages * page_size * n_kv_heads must be below 2^31 - 1024"));
-  return need(max_pages <= 2147483647ll / page_size, TP_ERR_SHAPE,
-              "max_pages * page_size must be below 2^31");
+  return need(max_pages <= (1ll << 30) / page_size, TP_ERR_SHAPE,
+              "max_pages * page_size must be at most 2^30");
+}
+
+// lengths, tables, offsets and lse: 4-byte elements read one by one
+tp_status check_words(std::initializer_list<const void*> ptrs) {
+  for (const void* q : ptrs)
+    TP_TRY(need(reinterpret_cast<uintptr_t>(q) % 4 == 0, TP_ERR_ALIGNMENT,
+                "int32 and fp32 arrays must be 4-byte aligned"));
+  return TP_OK;
 }
 
 struct PagedArgs {
@@ -68,7 +76,8 @@ struct PagedArgs {
 
 tp_status check_rows(int64_t T, int64_t R, int64_t max_new) {
   TP_TRY(need(T >= 0 && R >= 0 && max_new >= 0, TP_ERR_INVALID_ARG, "need T, R, max_new >= 0"));
-  return need(T < (1ll << 31) && R < (1ll << 31), TP_ERR_SHAPE, "T and R must be below 2^31");
+  TP_TRY(need(T < (1ll << 31), TP_ERR_SHAPE, "T must be below 2^31"));
+  return need(R <= (1 << 20), TP_ERR_SHAPE, "at most 2^20 requests");
 }
 
 tp_status launch_paged(const PagedArgs& a, const PagedGqa& g, void* ws, cudaStream_t st) {
@@ -127,6 +136,8 @@ tp_status tp_kv_tables(const int32_t* ctx_lens, const int32_t* new_lens, const i
   TP_TRY(need(R <= kKvMaxRequests, TP_ERR_SHAPE, "at most 8192 requests"));
   TP_TRY(need(n_free < (1ll << 31), TP_ERR_SHAPE, "n_free must be below 2^31"));
   TP_TRY(check_pages(1, page_size, max_pages, 1));
+  TP_TRY(check_words({ctx_lens, new_lens, free_pages, free_head, free_head_out, block_table,
+                      total_lens, cu_new, slots, positions, counts}));
   TP_TRY(check_device());
   return launch_kv_tables(ctx_lens, new_lens, free_pages, static_cast<int>(n_free), free_head,
                           free_head_out, block_table, total_lens, cu_new, slots, positions, counts,
@@ -145,6 +156,7 @@ tp_status tp_kv_append(const void* qkv, const int32_t* slots, void* kcache, void
   TP_TRY(paged_shape(h, n_heads, n_kv_heads, N, &g));
   TP_TRY(check_pages(n_pages, page_size, 1, n_kv_heads));
   TP_TRY(check_aligned({qkv, kcache, vcache}));
+  TP_TRY(check_words({slots}));
   if (T == 0) return TP_OK;
   TP_TRY(check_device());
   return launch_kv_append(qkv, slots, kcache, vcache, T, g.d, n_kv_heads, g.hkv, g.hq, g.rep, g.W,
@@ -177,6 +189,7 @@ tp_status tp_gqa_paged_attention_fwd(const void* qkv, const void* kcache, const 
   TP_TRY(paged_shape(h, n_heads, n_kv_heads, N, &g));
   TP_TRY(check_pages(n_pages, page_size, max_pages, n_kv_heads));
   TP_TRY(check_aligned({qkv, kcache, vcache, o, ws}));
+  TP_TRY(check_words({block_table, total_lens, cu_new, lse}));
   if (T == 0 || R == 0) return TP_OK;
   TP_TRY(need(ws && ws_bytes >= paged_workspace_bytes(g.d, dtype), TP_ERR_WORKSPACE,
               "workspace smaller than tp_gqa_paged_attention_workspace_size"));
@@ -224,6 +237,7 @@ tp_status tp_gqa_paged_attn_proj_fwd(
     TP_TRY(need((h / N) % 64 == 0, TP_ERR_SHAPE, "bf16 path: h/N must be a multiple of 64"));
   }
   TP_TRY(check_aligned({x, gamma, beta, Wqkv, Wo, xn, mean, rstd, qkv, kcache, vcache, o, out, ws}));
+  TP_TRY(check_words({block_table, total_lens, cu_new, slots, lse}));
   if (T == 0) return TP_OK;
   TP_TRY(need(ws && ws_bytes >= tp_gqa_paged_workspace_size(T, h, n_heads, n_kv_heads, N, dtype, mode),
               TP_ERR_WORKSPACE, "workspace smaller than tp_gqa_paged_workspace_size"));

@@ -206,9 +206,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   } else {
     // ---------------------------------------------------------------- consumers
+    auto timed_out = [&] {
+      atomicCAS(dp.status, 0, static_cast<int>(TP_ERR_TIMEOUT));
+      atomicAdd(dp.status + 1, 1);
+    };
     bool ok = true;
-    if (dp.debug_hang && warp == 0)
+    if (dp.debug_hang && warp == 0) {
       ok = __all_sync(0xFFFFFFFFu, mbar_wait(never, 0, dp.timeout_ns, abort_flag));
+      if (!ok && lane == 0) timed_out();
+    }
     const int row0 = lane >> 2, col = (lane & 3) * 2;
     PagedRec rec{0, 0, 0, 0, 0, 0};
     for (; w.valid(); w.next(p)) {
@@ -246,10 +252,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int st = it % L::kStages, round = it / L::kStages;
         if (ok && !__all_sync(0xFFFFFFFFu, mbar_wait(full(st), round & 1, dp.timeout_ns, abort_flag))) {
           ok = false;
-          if (lane == 0) {
-            atomicCAS(dp.status, 0, static_cast<int>(TP_ERR_TIMEOUT));
-            atomicAdd(dp.status + 1, 1);
-          }
+          if (lane == 0) timed_out();
         }
         if (!ok) continue;
         const uint32_t kt = sb + st * 2 * L::kTile, vt = kt + L::kTile;

@@ -565,8 +565,10 @@ TP_API tp_status tp_gqa_attn_proj_bwd(const void* x, const float* gamma, const v
  * slot = page * page_size + offset. Step: request r has total_lens[r] tokens, the last
  * cu_new[r+1] - cu_new[r] of them new, in rows cu_new[r] .. cu_new[r+1] - 1 of the packed
  * rows; rows from cu_new[R] to T are padding (a captured graph's fixed size).
- * All of these int32 arrays are device memory (4-byte aligned) and are read when the work
- * runs, so a captured step replays with new lengths. Values that do not fit are no error
+ * max_pages * page_size is at most 2^30, R at most 2^20. All of these int32 arrays are
+ * device memory (4-byte aligned, as lse) and are read when the work runs, so a captured
+ * step replays with new lengths. Buffers of one call do not overlap where nothing else is
+ * said. Values that do not fit are no error
  * and nothing is read or written outside the buffers: rows >= T do not exist, a page id
  * outside [0, n_pages) is a page whose keys no row sees, keys past max_pages pages do
  * not exist, negative lengths are zero.

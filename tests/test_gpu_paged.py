@@ -431,3 +431,69 @@ def test_streams_graphs_and_repeats(dtype, new):
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(o1, ref) and torch.equal(o2, full)
+
+
+@pytest.mark.parametrize("d,new,mx", [(64, 1, 1), (128, 1, 1), (64, 40, 40), (128, 40, 40)])
+def test_expired_waits_are_reported_and_recovered_from(d, new, mx):
+    """The injected wait runs out (a barrier that nothing arrives on): the call stops, the
+    status says so, and the next call on the same buffers is right."""
+    lens = [(300, new), (5, 1)]
+    T.tp_set_wait_timeout_ns(20_000_000)
+    T.tp_debug_inject_wait_fault(True)
+    try:
+        H, Hkv, P_ = 8, 2, 16
+        rows, MP = new + 1, -(-(300 + new) // P_)
+        _, qkv = tensor((rows, cols(H, Hkv, 1, d)), 70)
+        _, kc = tensor((2 * MP, Hkv, P_, d), 71)
+        o = torch.zeros(rows, H * d, dtype=torch.bfloat16, device="cuda")
+        wsb = T.tp_gqa_paged_attention_workspace_size(H * d, H, Hkv, 1, T.DType.BF16)
+        ws = torch.zeros(wsb, dtype=torch.uint8, device="cuda")
+        T.tp_gqa_paged_attention_fwd(qkv, kc, kc, i32(np.arange(2 * MP).reshape(2, MP)),
+                                     i32([300 + new, 6]), i32([0, new, rows]), o, None, rows, 2,
+                                     H * d, H, Hkv, 1, 2 * MP, P_, MP, mx, 1, T.DType.BF16, ws, wsb)
+        assert T.tp_check_status() == T.Status.TIMEOUT
+    finally:
+        T.tp_debug_inject_wait_fault(False)
+        T.tp_set_wait_timeout_ns(1_000_000_000)
+    assert T.tp_check_status() == 0
+    run_attention(lens, 8, 2, 1, d, 16, "bf16", 1, seed=12)
+
+
+@pytest.mark.parametrize("H,Hkv,N", [(128, 1, 1), (130, 1, 1), (256, 2, 4), (100, 1, 100), (7, 7, 7)])
+@pytest.mark.parametrize("new", [1, 3])
+def test_wide_and_narrow_groups(H, Hkv, N, new):
+    """Query heads per key/value head from 1 to 130: a row tile's whole tokens, more than one
+    tile's heads, replicas across all shards."""
+    run_attention([(37, new), (0, 2)], H, Hkv, N, 64, 16, "bf16", 1, seed=H)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("bf16", 128), ("f32", 64)])
+def test_chunked_equals_whole(dtype, d):
+    """A prompt in one call and in pieces (the kernel for few rows among them) agree to the
+    rounding of P and the output."""
+    H, Hkv, P_, L = 8, 2, 16, 333
+    h, dt = H * d, (T.DType.BF16 if dtype == "bf16" else T.DType.F32)
+    MP = -(-L // P_)
+    _, qkv = tensor((L, cols(H, Hkv, 1, d)), 80, dtype=dtype)
+    z = lambda *s: torch.zeros(s, dtype=qkv.dtype, device="cuda")
+    kc, vc = z(MP, Hkv, P_, d), z(MP, Hkv, P_, d)
+    tb = i32(np.random.default_rng(1).permutation(MP)[None])
+    wsb = T.tp_gqa_paged_attention_workspace_size(h, H, Hkv, 1, dt)
+    ws = torch.empty(wsb, dtype=torch.uint8, device="cuda")
+    pos = np.arange(L)
+    slots = tb.cpu().numpy()[0][pos // P_] * P_ + pos % P_
+    T.tp_kv_append(qkv, i32(slots), kc, vc, L, h, H, Hkv, 1, MP, P_, dt)
+    outs = []
+    for cuts in ([0, L], [0, 1, 2, 5, 130, 131, 300, L]):
+        o = z(L, h)
+        for a, b in zip(cuts[:-1], cuts[1:]):
+            T.tp_gqa_paged_attention_fwd(qkv[a:], kc, vc, tb, i32([b]), i32([0, b - a]), o[a:], None,
+                                         b - a, 1, h, H, Hkv, 1, MP, P_, MP, b - a, 1, dt, ws, wsb)
+        outs.append(host(o))
+    torch.cuda.synchronize()
+    q, k, v = P.qkv_heads(host(qkv), H, Hkv, 1)
+    ref = P.paged_attention(q, host(kc), host(vc), tb.cpu().numpy(), [L], [0, L], True)
+    tol = 2.0 ** -8 if dtype == "bf16" else U * 2 * L
+    lim = 2 * tol * (ref["A"] + np.abs(ref["o"])) + \
+        2 * ref["A"] * U * (2 * (d + 4) * ref["B"].T[:, :, None] + 2 * L + 64)
+    assert (np.abs(outs[0] - outs[1]).reshape(L, H, d) <= lim).all()

@@ -43,7 +43,8 @@ PROJ = dict(x=A, gamma=A, beta=A, Wqkv=A, Wo=A, xn=A, mean=None, rstd=None, qkv=
     (dict(R=-1), S.INVALID_ARG), (dict(T=-1), S.INVALID_ARG), (dict(R=8193), S.SHAPE),
     (dict(page_size=4), S.SHAPE), (dict(page_size=24), S.SHAPE), (dict(page_size=512), S.SHAPE),
     (dict(max_pages=0), S.INVALID_ARG), (dict(max_pages=1 << 28), S.SHAPE),
-    (dict(n_free=1 << 31), S.SHAPE)])
+    (dict(n_free=1 << 31), S.SHAPE), (dict(ctx_lens=A + 2), S.ALIGNMENT),
+    (dict(slots=A + 1), S.ALIGNMENT), (dict(counts=A + 2), S.ALIGNMENT)])
 def test_tables(kw, want):
     assert _status(T.tp_kv_tables, TABLES, **kw) == want
 
@@ -68,6 +69,8 @@ def test_append(kw, want):
     (dict(cu_new=None), S.INVALID_ARG), (dict(o=None), S.INVALID_ARG), (dict(o=A + 2), S.ALIGNMENT),
     (dict(max_pages=0), S.INVALID_ARG), (dict(max_pages=1 << 28), S.SHAPE),
     (dict(max_new=-1), S.INVALID_ARG), (dict(R=-1), S.INVALID_ARG), (dict(T=3), S.WORKSPACE),
+    (dict(R=(1 << 20) + 1), S.SHAPE), (dict(lse=A + 2), S.ALIGNMENT),
+    (dict(block_table=A + 2), S.ALIGNMENT), (dict(max_pages=(1 << 26) + 1), S.SHAPE),
     (dict(T=3, ws=A, ws_bytes=64), S.WORKSPACE), (dict(ws=A + 8), S.ALIGNMENT), (dict(), S.OK),
     (dict(R=0, T=3), S.OK)])
 def test_attention(kw, want):
