@@ -645,17 +645,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           // exponentials. They hold for every row of the warp unless one's maximum has to
           // move (by more than 8: weights up to 2^8 are harmless in bf16 and fp32, and o / l
           // does not depend on m); then they are formed again.
+          // (A loop, so that the code is there once: a second copy of it slowed every tile.)
           float f = 1.0f;
           uint64_t sum[2];
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          auto weights = [&](bool search) {
+          for (;;) {
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
             const float mu = m == -INFINITY ? 0.0f : m;
             const uint64_t mu2 = pair_of(-mu, -mu);
             sum[0] = sum[1] = 0;
 #pragma unroll
             for (int y = 0; y < 32; ++y) {
               const float s0 = __uint_as_float(v[2 * y]), s1 = __uint_as_float(v[2 * y + 1]);
-              if (search) mx[y & 3] = max3(mx[y & 3], s0, s1);
+              mx[y & 3] = max3(mx[y & 3], s0, s1);
               float a, b;
               split(fma2(pair_of(s0, s1), sc2, mu2), a, b);
               a = ex2(a);
@@ -663,14 +664,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               sum[y & 1] = add2(sum[y & 1], pair_of(a, b));
               pk[y] = pack2(a, b);
             }
-          };
-          weights(true);
-          const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-          const bool move = mb > m + 8.0f;
-          if (__any_sync(0xFFFFFFFFu, move)) {
-            const float m1 = move ? mb : m;
-            f = move ? ex2(m - m1) : 1.0f;
-            m = m1;
+            const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+            const bool move = mb > m + 8.0f;
+            if (!__any_sync(0xFFFFFFFFu, move)) break;
+            if (move) {
+              f = ex2(m - mb);
+              m = mb;
+            }
             if (s > 0) {
               // all earlier P V of the tile have completed when the other half's next S has
               if (!wait_all(s_full(t, h ^ 1), (h ? ns0 + k + 1 : ns1 + k) & 1)) {
@@ -688,8 +688,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_st32(tO(t) + lanes + 32 * c, o);
               }
             }
-            weights(false);
           }
+          if (!ok) break;
           tmem_st32(tP(t) + lanes + L::kPHalf * h, pk);
           float sa, sb2;
           split(add2(sum[0], sum[1]), sa, sb2);
