@@ -106,14 +106,18 @@ tp_status launch_paged(const PagedArgs& a, const PagedGqa& g, void* ws, cudaStre
   p.max_pages = static_cast<int>(a.max_pages);
   p.causal = a.causal != 0;
   p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(g.d));
+  const int64_t rows = a.max_new * p.G;  // most rows of a request per key/value head
+  // The kernel for few rows reads K and V once per 16 rows, the tcgen05 one per 256. 33
+  // requests over 100 to 5000 tokens, 8 key/value heads, us (few rows / tcgen05): d = 128, 16
+  // rows 69 / 81, 20 rows 102 / 83, 64 rows 209 / 85; d = 64, 16 rows 44 / 61, 20 rows 64 / 62,
+  // 32 rows 69 / 61. One token each: 164 / 184 (61 requests), 9.7 / 17 (one).
   if (a.dt == TP_BF16)
-    return g.d >= 64 && p.G <= 128 && a.max_new * p.G > 16
-               ? launch_paged_tc(p, g.d, a.N, st)
-               : launch_paged_decode(p, g.d, st);
+    return rows > 16 && g.d >= 64 && p.G <= 128 ? launch_paged_tc(p, g.d, a.N, st)
+                                                : launch_paged_decode(p, g.d, st);
   // 64-row units where there are many rows, else 16 (measured with 3 requests of 8 heads over
   // 2, head_dim 64 / 128: 1440 rows 32 / 49 us against 25 / 33, 19200 rows 202 / 394 us
   // against 296 / 449)
-  return launch_paged_simt(p, g.d, a.max_new * p.G > 16 && a.T * a.H >= 4096, st);
+  return launch_paged_simt(p, g.d, rows > 16 && a.T * a.H >= 4096, st);
 }
 
 }  // namespace

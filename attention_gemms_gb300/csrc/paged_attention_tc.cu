@@ -12,14 +12,28 @@
 //   eight softmax warps, four per tile, a thread per row: S out of TMEM, the running
 //     maximum (moved lazily) and sum, P as bf16 back into TMEM, O rescaled there when the
 //     maximum moves; at a segment's end O / l, or the piece for the join.
-// The tiles take turns: while one tile's softmax runs, the tensor cores do the other's
-// O += P V and next S. At d = 128, P lies over the S it came from: the MMAs of a thread run
-// in order, so the next S of the tile is written after the P V that reads P. At d = 64 the
-// two products have different shapes and P has columns of its own.
+// A key tile flows in two halves of 64 keys, each with its own S, P and barriers: when a
+// half's P arrives, its MMA warp issues O += P V of the half and the next key tile's S of the
+// half, which lies over that P in TMEM (a thread's MMAs run in the order they were issued), so
+// that the softmax finds the next half ready instead of waiting for both products. With
+// whole tiles a row tile's period was softmax + 1024 cycles of products + the hand-overs
+// (about 3500 cycles against the tensor cores' 2048 for both tiles); S in halves costs more
+// tensor time (N = 64 reads Q twice as often: about 2660) and still takes 3200.
 // A unit of at most 128 rows (drafts, decoding requests beside a chunk, a chunk's end) would
 // leave the second tile idle and the chain S, softmax, P V bare; then both tiles take the
 // same rows, the first the even key tiles, the second the odd ones, and at the segment's end
 // the first tile's warps read both O.
+// What carries it: the walk's scalar work in one warp (in every role it cost more than a
+// tile per unit: 525 -> 412 us for two chunks of 2048 tokens, 64 heads over 8, d = 128, 0 and
+// 6000 cached), MMAs issued by an elected lane of a converged warp (a one-lane branch took
+// 80 to 100 cycles per MMA in moves to uniform registers: 741 -> 650), a start cost per unit
+// in the division of the work (none 721, one tile 640, two 576, three 526 before the walk was
+// moved; now one 427, two 383, three 375, with three slower on the other shapes).
+// Now: those chunks 380 us, 1.42 PFLOP/s, 74 % of the card's matrix rate (bound by the tensor
+// cores' S in halves and the hand-overs; tensor pipe 60 % of the launch); four chunks of 401
+// to 512 tokens, 32 heads over 8, d = 64: 66 us (bound by the softmax warps: P V and S are a
+// third of the time); 33 requests of 2 to 7 drafts, 32 heads over 8, d = 128 (347 MB): 82 us,
+// 4.2 TB/s (the loads, the schedule and the join before and after them).
 // Every wait is bounded; on a timeout the CTA records TP_ERR_TIMEOUT, stops issuing, waits
 // (bounded) for its own copies and MMAs, frees TMEM and returns.
 #include <cuda.h>
@@ -42,8 +56,8 @@ constexpr int kUnitRows = 2 * kTile;
 // and 1, 11: the walk over the CTA's work, and Q loads
 constexpr int kProd = 8, kMma = 9, kWalk = 11, kThreads = 384;
 // Registers: 384 threads launch with 168 each; the third warpgroup gives up its share
-// (128 x 80 + 256 x 208 = 63488 of the launch's 64512) so that a row's 128 scores stay in
-// the softmax threads' registers.
+// (128 x 80 + 256 x 208 = 63488 of the launch's 64512) so that the softmax threads keep a
+// half row's scores and weights in registers.
 constexpr int kRegsLoad = 80, kRegsSoftmax = 208;
 constexpr int kSegs = 4;            // segment descriptors in flight
 constexpr int kSegReaders = 8 + 3;  // softmax warps, K/V loads, MMA
@@ -417,9 +431,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok && lane == 0) timed_out();
     } else if (warp != kWalk) {
       // ---------------------------------------------------------------- MMA issuers
-      // One warp per row tile: the tensor cores' queue holds about five MMAs, so a warp's
-      // waits and loop between its products (about 700 cycles of one turn's 1024) would leave
-      // them idle; now the other tile's products run meanwhile.
+      // One warp per row tile: the tensor cores' queue holds about five MMAs, so one warp's
+      // waits and loop between two products would leave them idle; now the other tile's
+      // products run meanwhile.
       const int t = same(warp - kMma);
       const uint32_t id_s = idesc_bf16_f32(128, kTile / 2, 0, 0);  // Q, K both K-major
       const uint32_t id_o = idesc_bf16_f32(128, D, 0, 1);      // P in TMEM, V MN-major
