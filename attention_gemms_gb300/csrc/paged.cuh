@@ -78,7 +78,8 @@ __device__ __forceinline__ PagedReq paged_req(const PagedParams& p, int r) {
 }
 
 __device__ __forceinline__ int paged_units(const PagedParams& p, const PagedReq& q) {
-  return (q.rows + p.tpu - 1) / p.tpu;
+  const int n = q.rows + p.tpu - 1;
+  return p.tpu_log2 >= 0 ? n >> p.tpu_log2 : n / p.tpu;
 }
 
 // first key that no row of unit u sees
@@ -208,8 +209,9 @@ struct PagedWalk {
 // Scratch of the schedule (shared memory).
 struct PagedSched {
   int64_t warp_sum[32];
-  int64_t x;  // the CTA's first work, from the beginning of request r
-  int r;
+  int64_t x, per_head;  // the CTA's first work, from the beginning of request r; its heads' cost
+  PagedReq q;
+  int r, units;
 };
 
 // Returns the CTA's first segment. Called by every thread of the CTA (blockDim.x a multiple
@@ -227,10 +229,12 @@ __device__ __forceinline__ PagedWalk paged_schedule(const PagedParams& p, PagedS
   };
   const int per = (p.R + nt - 1) / nt;
   const int r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
-  int64_t sum = 0;
+  int64_t sum = 0, head_cost = 0;
+  PagedReq q;
   for (int r = r0; r < r1; ++r) {
-    const PagedReq q = paged_req(p, r);
-    if (q.rows > 0) sum += p.Hv * paged_prefix(p, q, paged_units(p, q));
+    q = paged_req(p, r);
+    head_cost = q.rows > 0 ? paged_prefix(p, q, paged_units(p, q)) : 0;
+    sum += p.Hv * head_cost;
   }
   int64_t inc = sum;
 #pragma unroll
@@ -255,14 +259,18 @@ __device__ __forceinline__ PagedWalk paged_schedule(const PagedParams& p, PagedS
   if (end > begin && begin >= mine && begin < mine + sum) {
     int64_t x = begin - mine;
     int r = r0;
-    for (; r < r1; ++r) {
-      const PagedReq q = paged_req(p, r);
-      const int64_t w = q.rows > 0 ? p.Hv * paged_prefix(p, q, paged_units(p, q)) : 0;
-      if (x < w) break;
-      x -= w;
-    }
+    if (per > 1)  // with one request per thread, it is still at hand
+      for (; r < r1; ++r) {
+        q = paged_req(p, r);
+        head_cost = q.rows > 0 ? paged_prefix(p, q, paged_units(p, q)) : 0;
+        if (x < p.Hv * head_cost) break;
+        x -= p.Hv * head_cost;
+      }
     sc.r = r;
     sc.x = x;
+    sc.q = q;
+    sc.per_head = head_cost;
+    sc.units = paged_units(p, q);
   }
   sync();
   PagedWalk w;
@@ -277,9 +285,9 @@ __device__ __forceinline__ PagedWalk paged_schedule(const PagedParams& p, PagedS
     return w;
   }
   // every warp finds the unit on its own (32 candidates at a time)
-  w.q = paged_req(p, w.r);
-  w.units = paged_units(p, w.q);
-  const int64_t per_head = paged_prefix(p, w.q, w.units);
+  w.q = sc.q;
+  w.units = sc.units;
+  const int64_t per_head = sc.per_head;
   int64_t x = sc.x;
   w.vh = static_cast<int>((static_cast<uint64_t>(x) | static_cast<uint64_t>(per_head)) >> 32
                               ? x / per_head
