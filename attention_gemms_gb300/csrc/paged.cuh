@@ -45,8 +45,6 @@ struct PagedParams {
   int tpu, kt_log2;        // tokens per unit, keys per tile
   int tpu_log2;            // -1: not a power of two
   int unit_cost;           // of a unit, beside its tiles, in tiles
-  int only_rows;           // > 0: only requests of at most that many rows per head group;
-                           // < 0: only requests of more than -only_rows
 };
 
 // What CTA i left in its two slots: slot 0 the piece of a unit that began in an earlier
@@ -72,8 +70,6 @@ __device__ __forceinline__ PagedReq paged_req(const PagedParams& p, int r) {
   q.total = max(p.total[r], 0);
   q.kv_end = static_cast<int>(
       min(static_cast<int64_t>(q.total), static_cast<int64_t>(p.max_pages) << p.ps_log2));
-  const int64_t gr = static_cast<int64_t>(q.rows) * p.Gv;
-  if (p.only_rows > 0 ? gr > p.only_rows : (p.only_rows < 0 && gr <= -p.only_rows)) q.rows = 0;
   return q;
 }
 

@@ -26,19 +26,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kKT = 64;  // keys per tile
 
-template <typename T>
-__device__ __forceinline__ void load4(const T* src, float (&f)[4]);
-template <>
-__device__ __forceinline__ void load4<float>(const float* src, float (&f)[4]) {
+__device__ __forceinline__ void load4(const float* src, float (&f)[4]) {
   const float4 v = *reinterpret_cast<const float4*>(src);
   f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w;
-}
-template <>
-__device__ __forceinline__ void load4<__nv_bfloat16>(const __nv_bfloat16* src, float (&f)[4]) {
-  const uint2 v = *reinterpret_cast<const uint2*>(src);
-  const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.x));
-  const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v.y));
-  f[0] = a.x, f[1] = a.y, f[2] = b.x, f[3] = b.y;
 }
 __device__ __forceinline__ void store4(float* dst, const float (&f)[4]) {
   *reinterpret_cast<float4*>(dst) = make_float4(f[0], f[1], f[2], f[3]);
@@ -79,7 +69,7 @@ __device__ __forceinline__ bool unit_row(const PagedParams& p, const PagedReq& q
 
 // RT rows per unit: 16 for a token or a few, 64 for chunks (a key tile is then read from
 // L2 once per 64 rows instead of 16).
-template <typename T, int D, int RT>
+template <int D, int RT>
 struct SimtLayout {
   static constexpr int LD = D + 4;  // padded row: float4 accesses of 8 rows hit 32 banks
   // Q | two stages of K and V | P | m, l, weight per row | key flags per stage
@@ -89,10 +79,10 @@ struct SimtLayout {
   static constexpr int kCtas = kSmem <= 112 * 1024 ? 2 : 1;  // per SM
 };
 
-template <typename T, int D, int RT>
-__global__ void __launch_bounds__(kThreads, SimtLayout<T, D, RT>::kCtas)
+template <int D, int RT>
+__global__ void __launch_bounds__(kThreads, SimtLayout<D, RT>::kCtas)
     paged_simt_kernel(const PagedParams p) {
-  using Lay = SimtLayout<T, D, RT>;
+  using Lay = SimtLayout<D, RT>;
   constexpr int LD = Lay::LD, PLD = kKT + 4;
   extern __shared__ __align__(16) float sm[];
   float *Qs = sm + Lay::kQ, *Ps = sm + Lay::kP;
@@ -129,8 +119,8 @@ __global__ void __launch_bounds__(kThreads, SimtLayout<T, D, RT>::kCtas)
         const int k = e / CG, c = (e - k * CG) * 4;
         const int64_t row = k0 + k < kend ? paged_row(p, tab, j, k0 + k) : -1;
         const int64_t at = row < 0 ? 0 : row * D + c;
-        copy16(Ks + k * LD + c, static_cast<const T*>(p.kc) + at, row >= 0);
-        copy16(Ks + (kKT + k) * LD + c, static_cast<const T*>(p.vc) + at, row >= 0);
+        copy16(Ks + k * LD + c, static_cast<const float*>(p.kc) + at, row >= 0);
+        copy16(Ks + (kKT + k) * LD + c, static_cast<const float*>(p.vc) + at, row >= 0);
         if (c == 0) oks[stage * kKT + k] = row >= 0;
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -142,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, SimtLayout<T, D, RT>::kCtas)
       int token, head;
       float f[4] = {0.f, 0.f, 0.f, 0.f};
       if (unit_row(p, w.q, w.u, w.vh, RT, i, &token, &head)) {
-        load4(static_cast<const T*>(p.qkv) + (static_cast<int64_t>(w.q.row0) + token) * p.ldq +
+        load4(static_cast<const float*>(p.qkv) + (static_cast<int64_t>(w.q.row0) + token) * p.ldq +
                   paged_qcol<D>(p, head) + c, f);
       }
       store4(Qs + i * LD + c, f);
@@ -303,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, SimtLayout<T, D, RT>::kCtas)
 #pragma unroll
           for (int k = 0; k < 4; ++k) f[k] = acc[i][k] * inv;
           const int64_t t = static_cast<int64_t>(w.q.row0) + token;
-          store4(static_cast<T*>(p.o) + t * p.H * D + static_cast<int64_t>(head) * D + cg * 4, f);
+          store4(static_cast<float*>(p.o) + t * p.H * D + static_cast<int64_t>(head) * D + cg * 4, f);
           if (cg == 0 && p.lse)
             p.lse[head * p.T + t] = l > 0.0f ? (ms[row] + log2f(l)) * 0.6931471805599453f : -INFINITY;
         } else {
@@ -439,38 +429,32 @@ tp_status combine_t(const PagedParams& p, int unit_rows, int tile_rows, int ctas
   return TP_OK;
 }
 
-template <typename T, int D, int RT>
+template <int D, int RT>
 tp_status simt_t(PagedParams& p, cudaStream_t st) {
-  using Lay = SimtLayout<T, D, RT>;
+  using Lay = SimtLayout<D, RT>;
   paged_set_units(p, RT, RT, 6, 1);
   static std::atomic<uint64_t> attr_set{0};
   if (needs_setup(attr_set)) {
-    TP_CUDA_TRY(cudaFuncSetAttribute(paged_simt_kernel<T, D, RT>,
+    TP_CUDA_TRY(cudaFuncSetAttribute(paged_simt_kernel<D, RT>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::kSmem));
     mark_device(attr_set);
   }
   const int ctas = std::min(kPagedMaxCtas, device_sm_count() * Lay::kCtas);
-  TP_CUDA_TRY(launch_kernel(paged_simt_kernel<T, D, RT>, dim3(ctas), dim3(kThreads),
+  TP_CUDA_TRY(launch_kernel(paged_simt_kernel<D, RT>, dim3(ctas), dim3(kThreads),
                             static_cast<size_t>(Lay::kSmem), st, p));
   count_launch();
-  return launch_paged_combine(p, D, RT, RT, ctas, sizeof(T) == 2 ? TP_BF16 : TP_F32, st);
-}
-
-template <typename T>
-tp_status simt_d(PagedParams& p, int d, bool wide, cudaStream_t st) {
-  switch (d) {
-    case 16: return wide ? simt_t<T, 16, 64>(p, st) : simt_t<T, 16, 16>(p, st);
-    case 32: return wide ? simt_t<T, 32, 64>(p, st) : simt_t<T, 32, 16>(p, st);
-    case 64: return wide ? simt_t<T, 64, 64>(p, st) : simt_t<T, 64, 16>(p, st);
-    case 128: return wide ? simt_t<T, 128, 64>(p, st) : simt_t<T, 128, 16>(p, st);
-  }
-  return fail(TP_ERR_SHAPE, "head_dim must be 16, 32, 64 or 128");
+  return launch_paged_combine(p, D, RT, RT, ctas, TP_F32, st);
 }
 
 }  // namespace
 
 tp_status launch_paged_simt(PagedParams p, int d, bool wide, cudaStream_t st) {
-  return simt_d<float>(p, d, wide, st);
+  switch (d) {
+    case 16: return wide ? simt_t<16, 64>(p, st) : simt_t<16, 16>(p, st);
+    case 32: return wide ? simt_t<32, 64>(p, st) : simt_t<32, 16>(p, st);
+    case 64: return wide ? simt_t<64, 64>(p, st) : simt_t<64, 16>(p, st);
+    default: return wide ? simt_t<128, 64>(p, st) : simt_t<128, 16>(p, st);
+  }
 }
 
 tp_status launch_paged_combine(const PagedParams& p, int d, int unit_rows, int tile_rows, int ctas,
@@ -501,7 +485,8 @@ void paged_set_units(PagedParams& p, int tile_rows, int unit_rows, int kt_log2, 
 }
 
 size_t paged_workspace_bytes(int d, tp_dtype dt) {
-  size_t floats = static_cast<size_t>(kPagedMaxCtas) * 2 * 64 * (d + 2);
+  const int rows = dt == TP_F32 ? 64 : 16;  // of a unit of the fp32, the few-row kernel
+  size_t floats = static_cast<size_t>(kPagedMaxCtas) * 2 * rows * (d + 2);
   if (dt == TP_BF16 && d >= 64) floats = std::max(floats, paged_tc_floats(d));
   return align_up(kPagedMaxCtas * sizeof(PagedRec), 256) + floats * 4;
 }

@@ -511,8 +511,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (left > 1 || h == 0) mma_commit(s_full(t, h));
               if (h == 1) {
                 if (left == 2) mma_commit(q_done);
-                if (left == 1) mma_commit(o_done(t));
                 mma_commit(empty(load));
+                // last, so that nothing still arrives once its waiters have gone
+                if (left == 1) mma_commit(o_done(t));
               }
             }
             __syncwarp();

@@ -201,13 +201,6 @@ __global__ void __launch_bounds__(kThreads, 2)
       atomicCAS(dp.status, 0, static_cast<int>(TP_ERR_TIMEOUT));
       atomicAdd(dp.status + 1, 1);
     }
-    if (*abort_flag) {  // the copies this CTA issued have landed
-      volatile int no_abort = 0;
-      for (int s = 0; s < L::kStages; ++s) {
-        const int n = it > s ? (it - 1 - s) / L::kStages : -1;  // last round of stage s
-        if (n >= 0) mbar_wait(full(s), n & 1, kDrainNs, &no_abort);
-      }
-    }
   } else {
     // ---------------------------------------------------------------- consumers
     auto timed_out = [&] {
@@ -426,6 +419,15 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     if (threadIdx.x == 0) p.rec[blockIdx.x] = rec;
+  }
+  // a role that gave up may have left copies in flight (whenever it did): they land first
+  __syncthreads();
+  if (*abort_flag && warp == kConsumers) {
+    volatile int no_abort = 0;
+    for (int s = 0; s < L::kStages; ++s) {
+      const int n = it > s ? (it - 1 - s) / L::kStages : -1;  // last round of stage s
+      if (n >= 0) mbar_wait(full(s), n & 1, kDrainNs, &no_abort);
+    }
   }
   __syncthreads();
 }
