@@ -212,11 +212,12 @@ def exported_names():
 
 
 def _ptr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return x
-    return x.data_ptr()
+    try:  # a tensor, nearly always
+        return x.data_ptr()
+    except AttributeError:
+        if x is None or isinstance(x, int):
+            return x
+        raise
 
 
 _current_stream = None  # returns torch's current stream as an address, once a GPU has been seen
@@ -246,13 +247,17 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+_dtypes = {}  # torch's element types, once torch is imported
+
+
 def dtype_of(t) -> DType:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return DType.BF16
-    if t.dtype == torch.float32:
-        return DType.F32
-    raise TypeError(f"unsupported dtype {t.dtype}")
+    if not _dtypes:
+        import torch
+        _dtypes.update({torch.bfloat16: DType.BF16, torch.float32: DType.F32})
+    try:
+        return _dtypes[t.dtype]
+    except KeyError:
+        raise TypeError(f"unsupported dtype {t.dtype}") from None
 
 
 def _check(status: int):
