@@ -47,12 +47,12 @@ struct PagedParams {
   int unit_cost;           // of a unit, beside its tiles, in tiles
 };
 
-// What CTA i left in its two slots: slot 0 the piece of a unit that began in an earlier
-// CTA (head: 1 the unit goes on after this CTA, 2 it ends here), slot 1 the first piece of
-// a unit that goes on after this CTA (tail: the CTA where it ends, with the unit's first row,
-// its tokens, its first query head and their number). 0: nothing.
-struct __align__(8) PagedRec {
-  int head, tail, row0, tokens, head0, heads;
+// CTA i's two slots: the first holds its piece of a unit that began in an earlier CTA (its
+// head), the second the first piece of a unit that goes on after it (its tail). What the join
+// needs to know of the tail: the CTA where the unit ends (0: no tail), the unit's first row,
+// its tokens, its first query head and their number.
+struct PagedRec {
+  int tail, row0, tokens, head0, heads;
 };
 
 #ifdef __CUDACC__

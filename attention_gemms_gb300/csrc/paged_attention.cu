@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, SimtLayout<D, RT>::kCtas)
   constexpr int CG = D / 4, CL = CG < 8 ? CG : 8, RL = 32 / CL, CW = CG / CL, RW = 8 / CW;
   constexpr int OY = RL * RW < RT ? RL * RW : RT, OR = RT / OY;
   const int cg = (warp % CW) * CL + lane % CL, oy = (warp / CW) * RL + lane / CL;
-  PagedRec rec{0, 0, 0, 0, 0, 0};
+  PagedRec rec{0, 0, 0, 0, 0};
   PagedWalk w = paged_schedule<false>(p, sc, blockIdx.x, gridDim.x);
   for (; w.valid(); w.next(p)) {
     const int j = w.vh / p.hs;
@@ -278,7 +278,6 @@ __global__ void __launch_bounds__(kThreads, SimtLayout<D, RT>::kCtas)
       }
     }
     const bool begins = w.lo == 0, ends = w.hi == w.tiles;
-    if (!begins) rec.head = ends ? 2 : 1;
     if (begins && !ends) paged_tail(p, rec, w);
     float* slot = p.part + static_cast<int64_t>(2 * blockIdx.x + (begins ? 1 : 0)) * RT * (D + 2);
     if (oy < OY) {

@@ -17,8 +17,8 @@
 // half, which lies over that P in TMEM (a thread's MMAs run in the order they were issued), so
 // that the softmax finds the next half ready instead of waiting for both products. With
 // whole tiles a row tile's period was softmax + 1024 cycles of products + the hand-overs
-// (about 3500 cycles against the tensor cores' 2048 for both tiles); S in halves costs more
-// tensor time (N = 64 reads Q twice as often: about 2660) and still takes 3200.
+// (about 3500 cycles against the tensor cores' 2060 for both tiles); S in halves costs more
+// tensor time (N = 64 reads Q twice as often: 2330) and still takes 3200.
 // A unit of at most 128 rows (drafts, decoding requests beside a chunk, a chunk's end) would
 // leave the second tile idle and the chain S, softmax, P V bare; then both tiles take the
 // same rows, the first the even key tiles, the second the odd ones, and at the segment's end
@@ -29,8 +29,9 @@
 // 80 to 100 cycles per MMA in moves to uniform registers: 741 -> 650), a start cost per unit
 // in the division of the work (none 721, one tile 640, two 576, three 526 before the walk was
 // moved; now one 427, two 383, three 375, with three slower on the other shapes).
-// Now: those chunks 380 us, 1.42 PFLOP/s, 74 % of the card's matrix rate (bound by the tensor
-// cores' S in halves and the hand-overs; tensor pipe 60 % of the launch); four chunks of 401
+// Now: those chunks 380 us with the same inputs again, 1.42 PFLOP/s, 74 % of the card's matrix
+// rate, 423 with new ones each time (bound by products and softmax in turn; tensor pipe 60 %
+// of the launch); four chunks of 401
 // to 512 tokens, 32 heads over 8, d = 64: 66 us (bound by the softmax warps: P V and S are a
 // third of the time); 33 requests of 2 to 7 drafts, 32 heads over 8, d = 128 (347 MB): 82 us,
 // 4.2 TB/s (the loads, the schedule and the join before and after them).
@@ -589,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = warp >> 2, x = threadIdx.x & 127;  // tile, row within it = TMEM lane
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const int tpt = p.tpu / 2, tt = x / p.Gv, hh = x - tt * p.Gv;
-    PagedRec rec{0, 0, 0, 0, 0, 0};
+    PagedRec rec{0, 0, 0, 0, 0};
     int ns0 = 0, ns1 = 0, segs_o = 0, joined = 0;  // S halves' completions before the segment
     uint32_t tiles0 = 0;  // key tiles of earlier segments
     bool ok = true, taken = true;
@@ -739,8 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
       const bool begins = g.ends & 1, ends = g.ends & 2;
-      if (!begins) rec.head = ends ? 2 : 1;
-      if (begins && !ends) rec = {rec.head, g.last, g.row0, g.tokens, g.head0, g.heads};
+      if (begins && !ends) rec = {g.last, g.row0, g.tokens, g.head0, g.heads};
       const bool joins = !g.pair && g.count(1) > 0;
       if (!g.pair && t == 1) {
         if (joins) {

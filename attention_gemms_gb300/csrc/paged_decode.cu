@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!ok && lane == 0) timed_out();
     }
     const int row0 = lane >> 2, col = (lane & 3) * 2;
-    PagedRec rec{0, 0, 0, 0, 0, 0};
+    PagedRec rec{0, 0, 0, 0, 0};
     for (; w.valid(); w.next(p)) {
       const int j = w.vh / p.hs;
       const int kend = paged_unit_kend(p, w.q, w.u);
@@ -361,7 +361,6 @@ __global__ void __launch_bounds__(kThreads, 2)
       constexpr int JC = L::kJoinCols, TPR = JC / 4;
       const int tid = threadIdx.x, jr = tid / TPR, jc = (tid % TPR) * 4;
       const bool begins = w.lo == 0, ends = w.hi == w.tiles;
-      if (!begins) rec.head = ends ? 2 : 1;
       if (begins && !ends) paged_tail(p, rec, w);
       float M = -INFINITY, lsum = 0.0f;
       int jtoken = 0, jhead = 0;
