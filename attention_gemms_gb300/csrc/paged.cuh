@@ -210,19 +210,12 @@ struct PagedSched {
   int r, units;
 };
 
-// Returns the CTA's first segment. Called by every thread of the CTA (blockDim.x a multiple
-// of 32, at most 1024; two block-wide barriers), or, kWarp, by one whole warp.
-template <bool kWarp>
+// Every thread of the CTA (blockDim.x a multiple of 32, at most 1024) calls it; returns
+// the CTA's first segment. Two block-wide barriers. (By one warp it took as long for a few
+// requests and grew with their number.)
 __device__ __forceinline__ PagedWalk paged_schedule(const PagedParams& p, PagedSched& sc, int cta,
                                                     int ctas) {
-  const int lane = threadIdx.x & 31;
-  const int tid = kWarp ? lane : threadIdx.x, nt = kWarp ? 32 : blockDim.x, warp = tid >> 5;
-  auto sync = [] {
-    if constexpr (kWarp)
-      __syncwarp();
-    else
-      __syncthreads();
-  };
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.R + nt - 1) / nt;
   const int r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
   int64_t sum = 0, head_cost = 0;
@@ -240,7 +233,7 @@ __device__ __forceinline__ PagedWalk paged_schedule(const PagedParams& p, PagedS
   }
   if (lane == 31) sc.warp_sum[warp] = inc;
   if (tid == 0) sc.r = -1;
-  sync();
+  __syncthreads();
   int64_t before = 0, total = 0;
   for (int w = 0; w < (nt >> 5); ++w) {
     const int64_t v = sc.warp_sum[w];
@@ -268,7 +261,7 @@ __device__ __forceinline__ PagedWalk paged_schedule(const PagedParams& p, PagedS
     sc.per_head = head_cost;
     sc.units = paged_units(p, q);
   }
-  sync();
+  __syncthreads();
   PagedWalk w;
   w.lo = w.hi = 0;
   w.left = end - begin;

@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kThreads, SimtLayout<D, RT>::kCtas)
   constexpr int OY = RL * RW < RT ? RL * RW : RT, OR = RT / OY;
   const int cg = (warp % CW) * CL + lane % CL, oy = (warp / CW) * RL + lane / CL;
   PagedRec rec{0, 0, 0, 0, 0};
-  PagedWalk w = paged_schedule<false>(p, sc, blockIdx.x, gridDim.x);
+  PagedWalk w = paged_schedule(p, sc, blockIdx.x, gridDim.x);
   for (; w.valid(); w.next(p)) {
     const int j = w.vh / p.hs;
     const int32_t* tab = p.table + static_cast<int64_t>(w.r) * p.max_pages;

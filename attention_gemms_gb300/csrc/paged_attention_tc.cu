@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto seg_empty = [&](uint32_t i) { return bar_at(13 + kSegs + i % kSegs); };
   Seg* segs = reinterpret_cast<Seg*>(smem + L::kOffSeg);
   float2* join = reinterpret_cast<float2*>(smem + L::kOffJoin);  // the second tile's (m, l)
-  PagedSched& sc = *reinterpret_cast<PagedSched*>(join);  // until the first segment is published
+  PagedSched& sc = *reinterpret_cast<PagedSched*>(join);  // before any segment
   static_assert(sizeof(PagedSched) <= kTile * 8, "the schedule's scratch lies in the join's");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -332,6 +332,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tS = [&](int t) { return tmem + 128u * t; };
   auto tP = [&](int t) { return tmem + L::kP + L::kPStep * t; };
   auto tO = [&](int t) { return tmem + L::kO + L::kOStep * t; };
+  PagedWalk w = paged_schedule(p, sc, blockIdx.x, gridDim.x);
+  __syncthreads();  // the scratch has been read
   auto entry_at = [&](int e) { return sb + L::kOffRing + e * L::kOp; };
   auto timed_out = [&] {
     atomicCAS(tp_.status, 0, static_cast<int>(TP_ERR_TIMEOUT));
@@ -531,9 +533,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Segment i + 1 is published before segment i's Q is loaded. A Q tile is tpt tokens x G
       // heads, in that order: a box of the qkv rows. Rows past the request's tokens are
       // other requests' or zeros; nothing of them is written.
-      // (the schedule by this warp alone: the other roles' set-up runs meanwhile)
-      PagedWalk w = paged_schedule<true>(p, sc, blockIdx.x, gridDim.x);
-      __syncwarp();
       bool ok = true;
       const int tpt = p.tpu / 2;
       const uint32_t bytes = static_cast<uint32_t>(tpt) * p.G * D * 2;
