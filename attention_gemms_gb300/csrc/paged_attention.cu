@@ -100,6 +100,9 @@ __global__ void __launch_bounds__(kThreads, SimtLayout<D, RT>::kCtas)
   const int kx = lane & 7, sk0 = (warp / RG) * 8 * SK + kx, sr0 = (warp % RG) * 16 + (lane >> 3);
   constexpr int CG = D / 4, CL = CG < 8 ? CG : 8, RL = 32 / CL, CW = CG / CL, RW = 8 / CW;
   constexpr int OY = RL * RW < RT ? RL * RW : RT, OR = RT / OY;
+  // 16 rows: each warp has its own two; 64: the block's warps share all
+  constexpr bool kOwn = RT == 16;
+  constexpr int CPL = D >= 32 ? D / 32 : 1;
   const int cg = (warp % CW) * CL + lane % CL, oy = (warp / CW) * RL + lane / CL;
   PagedRec rec{0, 0, 0, 0, 0};
   PagedWalk w = paged_schedule(p, sc, blockIdx.x, gridDim.x);
@@ -149,6 +152,20 @@ __global__ void __launch_bounds__(kThreads, SimtLayout<D, RT>::kCtas)
                                   static_cast<int64_t>(w.q.total) - w.q.n + w.u * p.tpu +
                                       (sr0 + 4 * a) / p.Gv + 1))
                         : w.q.kv_end;
+    int own_lim[2];
+    float own_m[2], own_l[2], own_o[2][CPL];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      own_lim[r] = p.causal ? static_cast<int>(
+                                  min(static_cast<int64_t>(w.q.kv_end),
+                                      static_cast<int64_t>(w.q.total) - w.q.n + w.u * p.tpu +
+                                          (2 * warp + r) / p.Gv + 1))
+                            : w.q.kv_end;
+      own_m[r] = -INFINITY;
+      own_l[r] = 0.0f;
+#pragma unroll
+      for (int y = 0; y < CPL; ++y) own_o[r][y] = 0.0f;
+    }
     float acc[OR][4];
 #pragma unroll
     for (int i = 0; i < OR; ++i)
@@ -166,6 +183,73 @@ __global__ void __launch_bounds__(kThreads, SimtLayout<D, RT>::kCtas)
         asm volatile("cp.async.wait_group 0;" ::: "memory");
       }
       __syncthreads();
+      if constexpr (kOwn) {
+        // Two rows per warp, a lane two keys' scores and CPL columns of the output: nothing but
+        // the key tile is shared, so no warp waits for another within a tile.
+        const int r0 = 2 * warp;
+        if (r0 < rows) {
+          float s[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll 4
+          for (int c = 0; c < D; c += 4) {
+            const float4 ka = *reinterpret_cast<const float4*>(Ks + lane * LD + c);
+            const float4 kb = *reinterpret_cast<const float4*>(Ks + (lane + 32) * LD + c);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float4 q = *reinterpret_cast<const float4*>(Qs + (r0 + r) * LD + c);
+              s[r][0] = fmaf(q.w, ka.w, fmaf(q.z, ka.z, fmaf(q.y, ka.y, fmaf(q.x, ka.x, s[r][0]))));
+              s[r][1] = fmaf(q.w, kb.w, fmaf(q.z, kb.z, fmaf(q.y, kb.y, fmaf(q.x, kb.x, s[r][1]))));
+            }
+          }
+          const bool oa = ok[lane], ob = ok[lane + 32];
+          float mx[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            s[r][0] = oa && k0 + lane < own_lim[r] ? s[r][0] * p.scale_log2 : -INFINITY;
+            s[r][1] = ob && k0 + lane + 32 < own_lim[r] ? s[r][1] * p.scale_log2 : -INFINITY;
+            mx[r] = fmaxf(s[r][0], s[r][1]);
+          }
+#pragma unroll
+          for (int o = 16; o; o >>= 1)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) mx[r] = fmaxf(mx[r], __shfl_xor_sync(0xFFFFFFFFu, mx[r], o));
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float m1 = fmaxf(own_m[r], mx[r]), mu = m1 == -INFINITY ? 0.0f : m1;
+            const float wt = ex2(own_m[r] - mu), ea = ex2(s[r][0] - mu), eb = ex2(s[r][1] - mu);
+            own_m[r] = m1;
+            own_l[r] = own_l[r] * wt + (ea + eb);  // this lane's keys
+            Ps[(r0 + r) * PLD + lane] = ea;
+            Ps[(r0 + r) * PLD + lane + 32] = eb;
+#pragma unroll
+            for (int y = 0; y < CPL; ++y) own_o[r][y] *= wt;
+          }
+          __syncwarp();
+          if (lane * CPL < D) {
+#pragma unroll 2
+            for (int k = 0; k < kKT; k += 4) {
+              float e[2][4];
+              load4(Ps + r0 * PLD + k, e[0]);
+              load4(Ps + (r0 + 1) * PLD + k, e[1]);
+#pragma unroll
+              for (int z = 0; z < 4; ++z) {
+                const float* v = Vs + (k + z) * LD + lane * CPL;
+                float vv[CPL];
+                if constexpr (CPL == 4) {
+                  load4(v, vv);
+                } else {
+#pragma unroll
+                  for (int y = 0; y < CPL; ++y) vv[y] = v[y];
+                }
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+#pragma unroll
+                  for (int y = 0; y < CPL; ++y) own_o[r][y] = fmaf(e[r][z], vv[y], own_o[r][y]);
+              }
+            }
+          }
+        }
+        continue;
+      }
       {
         float s[SR][SK];
 #pragma unroll
@@ -280,7 +364,34 @@ __global__ void __launch_bounds__(kThreads, SimtLayout<D, RT>::kCtas)
     const bool begins = w.lo == 0, ends = w.hi == w.tiles;
     if (begins && !ends) paged_tail(p, rec, w);
     float* slot = p.part + static_cast<int64_t>(2 * blockIdx.x + (begins ? 1 : 0)) * RT * (D + 2);
-    if (oy < OY) {
+    if constexpr (kOwn) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = 2 * warp + r;
+        float l = own_l[r];
+#pragma unroll
+        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
+        int token, head;
+        if (!unit_row(p, w.q, w.u, w.vh, RT, row, &token, &head)) continue;
+        const int64_t t = static_cast<int64_t>(w.q.row0) + token;
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        const bool whole = begins && ends;
+        float* dst = whole ? static_cast<float*>(p.o) + t * p.H * D + static_cast<int64_t>(head) * D
+                           : slot + 2 * RT + row * D;
+        if (lane * CPL < D)
+#pragma unroll
+          for (int y = 0; y < CPL; ++y) dst[lane * CPL + y] = own_o[r][y] * (whole ? inv : 1.0f);
+        if (lane == 0) {
+          if (!whole) {
+            slot[row] = own_m[r];
+            slot[RT + row] = l;
+          } else if (p.lse) {
+            p.lse[head * p.T + t] =
+                l > 0.0f ? (own_m[r] + log2f(l)) * 0.6931471805599453f : -INFINITY;
+          }
+        }
+      }
+    } else if (oy < OY) {
 #pragma unroll
       for (int i = 0; i < OR; ++i) {
         const int row = oy + i * OY;
