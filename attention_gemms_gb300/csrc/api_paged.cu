@@ -114,10 +114,10 @@ tp_status launch_paged(const PagedArgs& a, const PagedGqa& g, void* ws, cudaStre
   if (a.dt == TP_BF16)
     return rows > 16 && g.d >= 64 && p.G <= 128 ? launch_paged_tc(p, g.d, a.N, st)
                                                 : launch_paged_decode(p, g.d, st);
-  // 64-row units where there are many rows, else 16 (measured with 3 requests of 8 heads over
-  // 2, head_dim 64 / 128: 1440 rows 32 / 49 us against 25 / 33, 19200 rows 202 / 394 us
-  // against 296 / 449)
-  return launch_paged_simt(p, g.d, rows > 16 && a.T * a.H >= 4096, st);
+  // 64-row units where there are many rows, else 16 (three requests of 8 heads over 2,
+  // head_dim 64 / 128, us, 16-row against 64-row units: 4800 rows over all heads 44 / 81
+  // against 51 / 84, 19200 rows 202 / 436 against 184 / 351)
+  return launch_paged_simt(p, g.d, rows > 16 && a.T * a.H >= 8192, st);
 }
 
 }  // namespace
