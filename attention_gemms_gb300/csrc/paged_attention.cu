@@ -10,7 +10,8 @@
 // / sum 2^(m_j - M) l_j, in the order of their keys, so a call's result does not depend on
 // which CTA finished first.
 // FFMA bounds the fp32 kernel where there are rows (three chunks of 2400 tokens, 8 heads over
-// 2, d = 128: 2.0 ms, 22 TFLOP/s of products that are used), latency where there are few (nine requests, one with 130 new tokens, d = 64: 32 us).
+// 2, d = 128: 2.0 ms, 22 TFLOP/s of products that are used), latency where there are few
+// (nine requests, one with 130 new tokens, d = 64: 32 us).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

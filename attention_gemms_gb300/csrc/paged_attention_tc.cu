@@ -514,9 +514,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (left > 1 || h == 0) mma_commit(s_full(t, h));
               if (h == 1) {
                 if (left == 2) mma_commit(q_done);
-                mma_commit(empty(load));
-                // last, so that nothing still arrives once its waiters have gone
+                // (the other order, in the loop's last turn alone, took 15 of 385 us more)
                 if (left == 1) mma_commit(o_done(t));
+                mma_commit(empty(load));
               }
             }
             __syncwarp();
@@ -527,6 +527,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           advance(size);
         }
       }
+      // behind every product and completion of this warp; waited for before the block ends
+      if (elect_one()) mma_commit(drain);
+      __syncwarp();
       if (!ok && lane == 0) timed_out();
     } else {
       // ---------------------------------------------------------------- the walk, Q loads
@@ -858,11 +861,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kProd && lane == 0)
       for (uint32_t l = issued > kLoads ? issued - kLoads : 0; l < issued; ++l)
         mbar_wait(full(l), round_of(l), kDrainNs, &no_abort);
-    if (warp == kMma || warp == kMma + 1) {  // and the MMAs it issued have completed
-      if (elect_one()) mma_commit(drain);
-      __syncwarp();
-      mbar_wait(drain, 0, kDrainNs, &no_abort);
-    }
+  }
+  if (warp == kMma || warp == kMma + 1) {  // the MMAs it issued, and their arrivals, are complete
+    volatile int no_abort = 0;
+    mbar_wait(drain, 0, kDrainNs, &no_abort);
   }
   tc_fence_before();
   __syncthreads();
