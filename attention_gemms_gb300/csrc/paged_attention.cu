@@ -41,6 +41,13 @@ __device__ __forceinline__ void store4(__nv_bfloat16* dst, const float (&f)[4]) 
                                               *reinterpret_cast<const uint32_t*>(&b));
 }
 
+__device__ __forceinline__ void store8(__nv_bfloat16* dst, const float (&a)[4], const float (&b)[4]) {
+  const __nv_bfloat162 v[4] = {__floats2bfloat162_rn(a[0], a[1]), __floats2bfloat162_rn(a[2], a[3]),
+                               __floats2bfloat162_rn(b[0], b[1]), __floats2bfloat162_rn(b[2], b[3])};
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(v);
+  *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 __device__ __forceinline__ float ex2(float x) {  // relative error about 2^-22, 4 fp32 roundings
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -514,10 +521,15 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedPara
   const int head = rec.head0 + hh;
   T* dst = static_cast<T*>(p.o) + t * p.H * D + static_cast<int64_t>(head) * D + 4 * cg;
 #pragma unroll
-  for (int g = 0; g < PER; ++g) {
+  for (int g = 0; g < PER; ++g)
 #pragma unroll
     for (int y = 0; y < 4; ++y) f[g][y] *= inv;
-    store4(dst + 4 * g, f[g]);
+  if constexpr (PER % 2 == 0 && sizeof(T) == 2) {
+#pragma unroll
+    for (int g = 0; g < PER; g += 2) store8(dst + 4 * g, f[g], f[g + 1]);
+  } else {
+#pragma unroll
+    for (int g = 0; g < PER; ++g) store4(dst + 4 * g, f[g]);
   }
   if (cg == 0 && p.lse)
     p.lse[head * p.T + t] = l > 0.0f ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
