@@ -4,11 +4,12 @@
 // The work of one call is a line of key tiles. Request r with n new tokens has, for each
 // of Hv head groups, ceil(n / tpu) units of tpu tokens x Gv query heads that share a
 // key/value head; a unit's tiles are the KT-key tiles that its last token may see (at
-// least one, so that rows that see no key are written too), after a start cost of unit_cost
-// tiles (queries, first loads, the output: what a unit takes beside its tiles). CTA i of g
-// takes [i total / g, (i + 1) total / g) of the line, whatever units that falls into: every
-// CTA gets the same work for any mix of lengths, and a long context is split over the whole
-// GPU without a setting. A unit that lies in one CTA is finished there; else
+// least one, so that rows that see no key are written too), each at the cost that it has in
+// a unit that is more or at most half full, after the unit's start cost (queries, first
+// loads, the output). CTA i of g takes [i total / g, (i + 1) total / g) of the line,
+// whatever units that falls into (a tile belongs to the CTA that holds its end): every CTA
+// gets the same work for any mix of lengths, and a long context is split over the whole GPU
+// without a setting. A unit that lies in one CTA is finished there; else
 // each CTA leaves its rows' (maximum, sum, unnormalised output) in its slot of the
 // workspace and the combine kernel joins them in key order. At most one unit begins and
 // one ends inside other CTAs' ranges, so two slots per CTA are enough for any lengths.
@@ -44,7 +45,7 @@ struct PagedParams {
   int hs, Gv, Hv;          // head groups per key/value head, heads per group, Hkv * hs
   int tpu, kt_log2;        // tokens per unit, keys per tile
   int tpu_log2;            // -1: not a power of two
-  int unit_cost;           // of a unit, beside its tiles, in tiles
+  int unit_cost;           // of a unit, beside its tiles
 };
 
 // CTA i's two slots: the first holds its piece of a unit that began in an earlier CTA (its
@@ -123,44 +124,61 @@ __device__ __forceinline__ int64_t floor_sum(int64_t n, int k, int a, int64_t b)
   return ans;
 }
 
+// The costs of a tile of a unit with more than (full) and at most (half) tpu / 2 tokens are
+// constants of the kernel: at 1 and 1 nothing is left of them.
+template <int FULL, int HALF>
+__device__ __forceinline__ bool paged_half(const PagedParams& p, const PagedReq& q, int u) {
+  return FULL != HALF && 2 * static_cast<int64_t>(min(p.tpu, q.rows - u * p.tpu)) <= p.tpu;
+}
+
+// cost of unit u's tiles
+template <int FULL, int HALF>
+__device__ __forceinline__ int paged_unit_cost(const PagedParams& p, const PagedReq& q, int u) {
+  return paged_unit_tiles(p, q, u) * (paged_half<FULL, HALF>(p, q, u) ? HALF : FULL);
+}
+
 // cost of the first `u` units of a request's head group
+template <int FULL, int HALF>
 __device__ __forceinline__ int64_t paged_prefix(const PagedParams& p, const PagedReq& q, int u) {
   if (u <= 0) return 0;
   const int64_t starts = static_cast<int64_t>(u) * p.unit_cost;
-  if (u == 1) return starts + paged_unit_tiles(p, q, 0);
+  if (u == 1) return starts + paged_unit_cost<FULL, HALF>(p, q, 0);
   const int units = paged_units(p, q);
-  const int c = q.total - q.n;
-  if (!p.causal) return starts + static_cast<int64_t>(u) * paged_unit_tiles(p, q, 0);
-  int64_t s = starts;
-  if (c < 0 || q.kv_end < q.total) {  // tokens outside the cache: no closed form, rare
-    for (int i = 0; i < u; ++i) s += paged_unit_tiles(p, q, i);
-    return s;
-  }
   const int64_t full = min(u, units - 1);  // the last unit may hold fewer tokens
-  const int64_t b = static_cast<int64_t>(c) + p.tpu + (1 << p.kt_log2) - 1;
-  if (p.tpu_log2 >= p.kt_log2) {  // a whole number of tiles more per unit
-    s += ((full * (full - 1) / 2) << (p.tpu_log2 - p.kt_log2)) + full * (b >> p.kt_log2);
-  } else if (p.tpu_log2 >= 0) {  // a tile more every 2^k units
-    const int k = p.kt_log2 - p.tpu_log2;
-    auto below = [&](int64_t n) {  // sum over x < n of x >> k
-      const int64_t a = n >> k, r = n & ((1 << k) - 1);
-      return ((a * (a - 1) / 2) << k) + a * r;
-    };
-    const int64_t x = b >> p.tpu_log2;
-    s += below(x + full) - below(x);
+  const int last = u > full ? paged_unit_cost<FULL, HALF>(p, q, units - 1) : 0;
+  const int c = q.total - q.n;
+  int64_t s = 0;  // tiles of the full units
+  if (!p.causal) {
+    s = full * paged_unit_tiles(p, q, 0);
+  } else if (c < 0 || q.kv_end < q.total) {  // tokens outside the cache: no closed form, rare
+    for (int i = 0; i < full; ++i) s += paged_unit_tiles(p, q, i);
   } else {
-    s += floor_sum(full, p.kt_log2, p.tpu, b);
+    const int64_t b = static_cast<int64_t>(c) + p.tpu + (1 << p.kt_log2) - 1;
+    if (p.tpu_log2 >= p.kt_log2) {  // a whole number of tiles more per unit
+      s = ((full * (full - 1) / 2) << (p.tpu_log2 - p.kt_log2)) + full * (b >> p.kt_log2);
+    } else if (p.tpu_log2 >= 0) {  // a tile more every 2^k units
+      const int k = p.kt_log2 - p.tpu_log2;
+      auto below = [&](int64_t n) {  // sum over x < n of x >> k
+        const int64_t a = n >> k, r = n & ((1 << k) - 1);
+        return ((a * (a - 1) / 2) << k) + a * r;
+      };
+      const int64_t x = b >> p.tpu_log2;
+      s = below(x + full) - below(x);
+    } else {
+      s = floor_sum(full, p.kt_log2, p.tpu, b);
+    }
   }
-  if (u > full) s += paged_unit_tiles(p, q, units - 1);
-  return s;
+  return starts + s * FULL + last;
 }
 
 // A CTA's walk over its work: segment by segment, a segment being tiles [lo, hi) of unit u
-// (never none of them: a share that ends within a unit's start cost leaves it to the next).
+// (never none of them: a share that ends before a unit's first tile does leaves it to the next).
+template <int FULL, int HALF>
 struct PagedWalk {
   int64_t left;  // work left after the current segment
   int64_t stop, total;  // the CTA's end on the line, the line's
   int ctas;             // those with work
+  int rest;             // cost of the segment's unit after it
   PagedReq q;
   int r, vh, u, units, tiles, lo, hi;
 
@@ -168,15 +186,18 @@ struct PagedWalk {
   // from `x` on, counted from the unit's beginning
   __device__ __forceinline__ void take(const PagedParams& p, int x) {
     tiles = paged_unit_tiles(p, q, u);
-    const int end = static_cast<int>(min(static_cast<int64_t>(tiles) + p.unit_cost, x + left));
+    const bool half = paged_half<FULL, HALF>(p, q, u);
+    const int all = tiles * (half ? HALF : FULL) + p.unit_cost;
+    const int end = static_cast<int>(min(static_cast<int64_t>(all), x + left));
     left -= end - x;
-    lo = max(x - p.unit_cost, 0);
-    hi = max(end - p.unit_cost, 0);
+    rest = all - end;
+    const int a = max(x - p.unit_cost, 0), b = max(end - p.unit_cost, 0);
+    lo = half ? a / HALF : a / FULL;
+    hi = half ? b / HALF : b / FULL;
   }
   // of a segment that does not end its unit (it is the CTA's last one): where the unit ends
   __device__ __forceinline__ int last_cta() const {
-    const int64_t end = stop + tiles - hi;
-    return static_cast<int>((end * ctas + total - 1) / total) - 1;
+    return static_cast<int>(((stop + rest) * ctas + total - 1) / total) - 1;
   }
   __device__ __forceinline__ void next(const PagedParams& p) {
     if (left <= 0) {
@@ -213,8 +234,9 @@ struct PagedSched {
 // Every thread of the CTA (blockDim.x a multiple of 32, at most 1024) calls it; returns
 // the CTA's first segment. Two block-wide barriers. (By one warp it took as long for a few
 // requests and grew with their number.)
-__device__ __forceinline__ PagedWalk paged_schedule(const PagedParams& p, PagedSched& sc, int cta,
-                                                    int ctas) {
+template <int FULL = 1, int HALF = 1>
+__device__ __forceinline__ PagedWalk<FULL, HALF> paged_schedule(const PagedParams& p,
+                                                                PagedSched& sc, int cta, int ctas) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.R + nt - 1) / nt;
   const int r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
@@ -222,7 +244,7 @@ __device__ __forceinline__ PagedWalk paged_schedule(const PagedParams& p, PagedS
   PagedReq q;
   for (int r = r0; r < r1; ++r) {
     q = paged_req(p, r);
-    head_cost = q.rows > 0 ? paged_prefix(p, q, paged_units(p, q)) : 0;
+    head_cost = q.rows > 0 ? paged_prefix<FULL, HALF>(p, q, paged_units(p, q)) : 0;
     sum += p.Hv * head_cost;
   }
   int64_t inc = sum;
@@ -240,8 +262,9 @@ __device__ __forceinline__ PagedWalk paged_schedule(const PagedParams& p, PagedS
     before += w < warp ? v : 0;
     total += v;
   }
-  // every CTA below n has work, so that a unit's pieces lie in consecutive ones
-  const int n = static_cast<int>(min(static_cast<int64_t>(ctas), total));
+  // a share holds the end of a tile at least, so that a unit's pieces lie in consecutive CTAs
+  const int64_t shares = max(total / (FULL > HALF ? FULL : HALF), static_cast<int64_t>(1));
+  const int n = static_cast<int>(min(static_cast<int64_t>(ctas), shares));
   const int64_t begin = cta < n ? div_by(total * cta, n) : total;
   const int64_t end = cta < n ? div_by(total * (cta + 1), n) : total;
   const int64_t mine = before + inc - sum;  // tiles before this thread's requests
@@ -251,7 +274,7 @@ __device__ __forceinline__ PagedWalk paged_schedule(const PagedParams& p, PagedS
     if (per > 1)  // with one request per thread, it is still at hand
       for (; r < r1; ++r) {
         q = paged_req(p, r);
-        head_cost = q.rows > 0 ? paged_prefix(p, q, paged_units(p, q)) : 0;
+        head_cost = q.rows > 0 ? paged_prefix<FULL, HALF>(p, q, paged_units(p, q)) : 0;
         if (x < p.Hv * head_cost) break;
         x -= p.Hv * head_cost;
       }
@@ -262,7 +285,7 @@ __device__ __forceinline__ PagedWalk paged_schedule(const PagedParams& p, PagedS
     sc.units = paged_units(p, q);
   }
   __syncthreads();
-  PagedWalk w;
+  PagedWalk<FULL, HALF> w;
   w.lo = w.hi = 0;
   w.left = end - begin;
   w.stop = end;
@@ -286,20 +309,20 @@ __device__ __forceinline__ PagedWalk paged_schedule(const PagedParams& p, PagedS
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32;
     const int cand = min(lo + lane * step, hi);
-    const bool le = cand < hi && paged_prefix(p, w.q, cand) <= x;
+    const bool le = cand < hi && paged_prefix<FULL, HALF>(p, w.q, cand) <= x;
     const int k = __popc(__ballot_sync(0xFFFFFFFFu, le)) - 1;  // lane 0 always holds
     const int base = lo;
     lo = base + k * step;
     hi = min(hi, base + (k + 1) * step);
   }
   w.u = lo;
-  w.take(p, static_cast<int>(x - paged_prefix(p, w.q, lo)));
+  w.take(p, static_cast<int>(x - paged_prefix<FULL, HALF>(p, w.q, lo)));
   return w;
 }
 
 // the tail entry of the walk's segment
-__device__ __forceinline__ void paged_tail(const PagedParams& p, PagedRec& rec,
-                                           const PagedWalk& w) {
+template <class Walk>
+__device__ __forceinline__ void paged_tail(const PagedParams& p, PagedRec& rec, const Walk& w) {
   const int j = w.vh / p.hs;
   rec.tail = w.last_cta();
   rec.row0 = w.q.row0 + w.u * p.tpu;

@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kThreads, SimtLayout<D, RT>::kCtas)
   constexpr int CPL = D >= 32 ? D / 32 : 1;
   const int cg = (warp % CW) * CL + lane % CL, oy = (warp / CW) * RL + lane / CL;
   PagedRec rec{0, 0, 0, 0, 0};
-  PagedWalk w = paged_schedule(p, sc, blockIdx.x, gridDim.x);
+  auto w = paged_schedule(p, sc, blockIdx.x, gridDim.x);
   for (; w.valid(); w.next(p)) {
     const int j = w.vh / p.hs;
     const int32_t* tab = p.table + static_cast<int64_t>(w.r) * p.max_pages;

@@ -53,6 +53,12 @@ namespace {
 
 constexpr int kTile = 128;  // rows of a TMEM tile, keys of a key tile
 constexpr int kUnitRows = 2 * kTile;
+// The schedule's costs: a key tile of a unit with one tile of rows is bound by its softmax
+// and its loads, and takes most of the time of one with two; a start costs about 2.4 tiles.
+// At 1, 1 and a start of 2 a step of chunks and decodes (mixed-step) took 181 us against
+// 163, a 4096-token chunk 383 against 373, 32 requests of 8 drafts 81.4 against 82.5;
+// 7 / 6 / 17, 4 / 3 / 10 and 5 / 4 / 10 lie between.
+constexpr int kTileCost = 5, kHalfTileCost = 4, kStartCost = 12;
 // warps 0-3: softmax of tile 0, 4-7: of tile 1, 8: K and V loads, 9 and 10: MMA of tile 0
 // and 1, 11: the walk over the CTA's work, and Q loads
 constexpr int kProd = 8, kMma = 9, kWalk = 11, kThreads = 384;
@@ -236,7 +242,8 @@ struct __align__(16) Seg {
   }
 };
 
-__device__ __forceinline__ Seg make_seg(const PagedParams& p, const PagedWalk& w) {
+template <class Walk>
+__device__ __forceinline__ Seg make_seg(const PagedParams& p, const Walk& w) {
   Seg g;
   const int tpt = p.tpu / 2, j = w.vh / p.hs;
   g.n = w.hi - w.lo;
@@ -332,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tS = [&](int t) { return tmem + 128u * t; };
   auto tP = [&](int t) { return tmem + L::kP + L::kPStep * t; };
   auto tO = [&](int t) { return tmem + L::kO + L::kOStep * t; };
-  PagedWalk w = paged_schedule(p, sc, blockIdx.x, gridDim.x);
+  auto w = paged_schedule<kTileCost, kHalfTileCost>(p, sc, blockIdx.x, gridDim.x);
   __syncthreads();  // the scratch has been read
   auto entry_at = [&](int e) { return sb + L::kOffRing + e * L::kOp; };
   auto timed_out = [&] {
@@ -895,7 +902,7 @@ tp_status tc_t(PagedTcParams& t, cudaStream_t st) {
 tp_status launch_paged_tc(const PagedParams& p, int d, int N, cudaStream_t st) {
   PagedTcParams t{};
   t.p = p;
-  paged_set_units(t.p, kTile, kUnitRows, 7, 2);
+  paged_set_units(t.p, kTile, kUnitRows, 7, kStartCost);
   const int64_t rows = (static_cast<int64_t>(p.n_pages) * p.Hkv) << p.ps_log2;
   t.cache_rows = static_cast<int>(rows);
   const int box = std::min(1 << p.ps_log2, kTile);

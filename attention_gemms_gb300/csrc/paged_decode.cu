@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   pdl_wait();  // the set-up above overlaps the previous kernel
   pdl_trigger();
-  PagedWalk w = paged_schedule(p, sc, blockIdx.x, gridDim.x);  // has block-wide barriers
+  auto w = paged_schedule(p, sc, blockIdx.x, gridDim.x);  // has block-wide barriers
   int it = 0;  // tiles so far: stage it % kStages, round it / kStages
 
   if (warp == kConsumers) {
