@@ -29,10 +29,10 @@
 // 80 to 100 cycles per MMA in moves to uniform registers: 741 -> 650), a start cost per unit
 // in the division of the work (none 721, one tile 640, two 576, three 526 before the walk was
 // moved; now one 427, two 383, three 375, with three slower on the other shapes).
-// Now: those chunks 380 us with the same inputs again, 1.42 PFLOP/s, 74 % of the card's matrix
-// rate, 423 with new ones each time (bound by products and softmax in turn; tensor pipe 60 %
+// Now: those chunks 373 us with the same inputs again, 1.45 PFLOP/s, 75 % of the card's matrix
+// rate, 403 with new ones each time (bound by products and softmax in turn; tensor pipe 60 %
 // of the launch); four chunks of 401
-// to 512 tokens, 32 heads over 8, d = 64: 66 us (bound by the softmax warps: P V and S are a
+// to 512 tokens, 32 heads over 8, d = 64: 65 us (bound by the softmax warps: P V and S are a
 // third of the time); 33 requests of 2 to 7 drafts, 32 heads over 8, d = 128 (347 MB): 82 us,
 // 4.2 TB/s (the loads, the schedule and the join before and after them).
 // Every wait is bounded; on a timeout the CTA records TP_ERR_TIMEOUT, stops issuing, waits
