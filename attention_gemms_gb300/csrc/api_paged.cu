@@ -106,7 +106,8 @@ tp_status launch_paged(const PagedArgs& a, const PagedGqa& g, void* ws, cudaStre
   p.max_pages = static_cast<int>(a.max_pages);
   p.causal = a.causal != 0;
   p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(g.d));
-  const int64_t rows = a.max_new * p.G;  // most rows of a request per key/value head
+  // most rows of a request per key/value head (no request has more than T tokens)
+  const int64_t rows = std::min(a.max_new, a.T) * p.G;
   // The kernel for few rows reads K and V once per 16 rows, the tcgen05 one per 256. 33
   // requests over 100 to 5000 tokens, 8 key/value heads, us (few rows / tcgen05): d = 128, 16
   // rows 69 / 81, 20 rows 102 / 83, 64 rows 209 / 85; d = 64, 16 rows 44 / 61, 20 rows 64 / 62,

@@ -206,7 +206,7 @@ def test_chunks(H, Hkv, N, d, P_, dtype, causal):
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("max_new", [0, 1, 9, 5000])
+@pytest.mark.parametrize("max_new", [0, 1, 9, 5000, 1 << 62])
 def test_max_new_is_a_hint(dtype, d, max_new):
     run_attention([(20, 9), (300, 1), (0, 40)], 8, 2, 1, d, 16, dtype, 1, seed=5, max_new=max_new)
 
