@@ -113,7 +113,7 @@ tp_status launch_paged(const PagedArgs& a, const PagedGqa& g, void* ws, cudaStre
   // rows 69 / 81, 20 rows 102 / 83, 64 rows 209 / 85; d = 64, 16 rows 44 / 61, 20 rows 64 / 62,
   // 32 rows 69 / 61. One token each: 164 / 184 (61 requests), 9.7 / 17 (one).
   if (a.dt == TP_BF16)
-    return rows > 16 && g.d >= 64 && p.G <= 128 ? launch_paged_tc(p, g.d, a.N, st)
+    return rows > 16 && g.d >= 64 && p.G <= 128 ? launch_paged_tc(p, g.d, a.N, rows <= 128, st)
                                                 : launch_paged_decode(p, g.d, st);
   // 64-row units where there are many rows, else 16 (three requests of 8 heads over 2,
   // head_dim 64 / 128, us, 16-row against 64-row units: 4800 rows over all heads 44 / 81

@@ -362,10 +362,11 @@ tp_status launch_paged_decode(const PagedParams& p, int d, cudaStream_t st);
 // bf16, head_dim 64 or 128, chunks, at most 128 query heads per key/value head
 // (paged_attention_tc.cu)
 constexpr int kPagedTcCtas = 152;
-tp_status launch_paged_tc(const PagedParams& p, int d, int N, cudaStream_t st);
-// tensor map of the queries: rows, shard blocks, heads, dims; box: tpu / 2 tokens x the
+// one: at most 128 rows per request and key/value head are expected
+tp_status launch_paged_tc(const PagedParams& p, int d, int N, bool one, cudaStream_t st);
+// tensor map of the queries: rows, shard blocks, heads, dims; box: `tokens` tokens x the
 // query heads of one key/value head x 64
-tp_status paged_q_map(CUtensorMap* m, const PagedParams& p, int d, int N);
+tp_status paged_q_map(CUtensorMap* m, const PagedParams& p, int d, int N, int tokens);
 size_t paged_tc_floats(int d);  // partial results it may leave
 // tensor map of a cache (rows of d bf16, swizzled): boxes of box_rows x min(64, d)
 tp_status paged_cache_map(CUtensorMap* m, const void* cache, int64_t rows, int d, int box_rows);

@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, SimtLayout<D, RT>::kCtas)
 // sums and outputs, whose loads do not wait for one another; the G threads of a row and
 // columns join in shared memory. G = 4 for the slots of few rows, where a long context has
 // tens of pieces, and 1 for those of 256, which have two or three.
-// Slots of two tiles hold O by groups of 4 columns, (d / 4, rows, 4), as their kernel has a
+// Slots of 128-row tiles hold O by groups of 4 columns, (d / 4, rows, 4), as their kernel has a
 // thread per row; the others by rows. Threads follow the slots' order.
 template <typename T, int D, int PER, int G>
 __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedParams p,
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedPara
   const int group = threadIdx.x / kPer, et = threadIdx.x % kPer;
   const int e = blockIdx.y * kPer + et;
   int row, cg, step;  // this thread's first group of columns, and to its next one
-  if (unit_rows > tile_rows) {
+  if (tile_rows >= 128) {
     row = e % unit_rows;
     cg = e / unit_rows * PER;
     step = unit_rows;
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedPara
 
 template <typename T, int D>
 tp_status combine_t(const PagedParams& p, int unit_rows, int tile_rows, int ctas, cudaStream_t st) {
-  if (unit_rows > tile_rows) {
+  if (tile_rows >= 128) {
     constexpr int PER = 4;
     TP_CUDA_TRY(launch_kernel(paged_combine_kernel<T, D, PER, 1>,
                               dim3(ctas, unit_rows * (D / 4 / PER) / kThreads), dim3(kThreads), 0,

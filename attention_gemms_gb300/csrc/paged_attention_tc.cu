@@ -33,8 +33,8 @@
 // rate, 403 with new ones each time (bound by products and softmax in turn; tensor pipe 60 %
 // of the launch); four chunks of 401
 // to 512 tokens, 32 heads over 8, d = 64: 65 us (bound by the softmax warps: P V and S are a
-// third of the time); 33 requests of 2 to 7 drafts, 32 heads over 8, d = 128 (347 MB): 82 us,
-// 4.2 TB/s (the loads, the schedule and the join before and after them).
+// third of the time); 33 requests of 2 to 7 drafts, 32 heads over 8, d = 128 (347 MB): 77 us,
+// 4.5 TB/s (the loads, the schedule and the join before and after them).
 // Every wait is bounded; on a timeout the CTA records TP_ERR_TIMEOUT, stops issuing, waits
 // (bounded) for its own copies and MMAs, frees TMEM and returns.
 #include <cuda.h>
@@ -52,13 +52,13 @@ namespace tp {
 namespace {
 
 constexpr int kTile = 128;  // rows of a TMEM tile, keys of a key tile
-constexpr int kUnitRows = 2 * kTile;
 // The schedule's costs: a key tile of a unit with one tile of rows is bound by its softmax
 // and its loads, and takes most of the time of one with two; a start costs about 2.4 tiles.
 // At 1, 1 and a start of 2 a step of chunks and decodes (mixed-step) took 181 us against
-// 163, a 4096-token chunk 383 against 373, 32 requests of 8 drafts 81.4 against 82.5;
+// 163, two chunks of 2048 tokens 383 against 373;
 // 7 / 6 / 17, 4 / 3 / 10 and 5 / 4 / 10 lie between.
 constexpr int kTileCost = 5, kHalfTileCost = 4, kStartCost = 12;
+constexpr int kOneStartCost = 3;  // where every unit has one row tile and tiles cost 1 (2 or 5: 1 % more)
 // warps 0-3: softmax of tile 0, 4-7: of tile 1, 8: K and V loads, 9 and 10: MMA of tile 0
 // and 1, 11: the walk over the CTA's work, and Q loads
 constexpr int kProd = 8, kMma = 9, kWalk = 11, kThreads = 384;
@@ -82,12 +82,17 @@ struct PagedTcParams {
   int debug_hang;
 };
 
-template <int D>
+// ONE: units of one row tile, for calls of at most 128 rows per request and key/value head.
+// The second Q tile's place is a sixth place of the ring, and what such calls wait for is
+// their loads: 33 requests of 2 to 7 drafts, 32 heads over 8, d = 128: 77 us against 83, 33 of
+// 32 tokens 84 against 90. At d = 64 an eleventh place changed nothing (56 and 56).
+template <int D, bool ONE>
 struct Lay {
+  static constexpr int kTiles = ONE ? 1 : 2, kUnit = kTiles * kTile;  // row tiles, rows
   static constexpr int kHalves = D / 64;
   static constexpr int kOp = kTile * D * 2;  // a Q, K or V tile
-  static constexpr int kRing = D == 128 ? 5 : 10;
-  static constexpr int kOffRing = 2 * kOp;
+  static constexpr int kRing = (D == 128 ? 7 : 12) - kTiles;
+  static constexpr int kOffRing = kTiles * kOp;
   static constexpr int kOffBar = kOffRing + kRing * kOp;
   static constexpr int kBars = 2 * kLoads + 18 + 2 * kSegs;  // even: 16-byte alignment after
   static constexpr int kOffJoin = kOffBar + kBars * 8 + kBadRing * 4 + 16;
@@ -243,9 +248,9 @@ struct __align__(16) Seg {
 };
 
 template <class Walk>
-__device__ __forceinline__ Seg make_seg(const PagedParams& p, const Walk& w) {
-  Seg g;
-  const int tpt = p.tpu / 2, j = w.vh / p.hs;
+__device__ __forceinline__ Seg make_seg(const PagedParams& p, const Walk& w, int tpt) {
+  Seg g;  // tpt: tokens of a row tile
+  const int j = w.vh / p.hs;
   g.n = w.hi - w.lo;
   g.lo = w.lo;
   g.tokens = min(p.tpu, w.q.rows - w.u * p.tpu);
@@ -269,10 +274,10 @@ __device__ __forceinline__ Seg make_seg(const PagedParams& p, const Walk& w) {
   return g;
 }
 
-template <int D>
+template <int D, bool ONE>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_tc_kernel(const __grid_constant__ PagedTcParams tp_) {
-  using L = Lay<D>;
+  using L = Lay<D, ONE>;
   const PagedParams& p = tp_.p;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -339,7 +344,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tS = [&](int t) { return tmem + 128u * t; };
   auto tP = [&](int t) { return tmem + L::kP + L::kPStep * t; };
   auto tO = [&](int t) { return tmem + L::kO + L::kOStep * t; };
-  auto w = paged_schedule<kTileCost, kHalfTileCost>(p, sc, blockIdx.x, gridDim.x);
+  auto w = paged_schedule<ONE ? 1 : kTileCost, ONE ? 1 : kHalfTileCost>(p, sc, blockIdx.x,
+                                                                        gridDim.x);
   __syncthreads();  // the scratch has been read
   auto entry_at = [&](int e) { return sb + L::kOffRing + e * L::kOp; };
   auto timed_out = [&] {
@@ -544,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // heads, in that order: a box of the qkv rows. Rows past the request's tokens are
       // other requests' or zeros; nothing of them is written.
       bool ok = true;
-      const int tpt = p.tpu / 2;
+      const int tpt = p.tpu / L::kTiles;
       const uint32_t bytes = static_cast<uint32_t>(tpt) * p.G * D * 2;
       Seg g, next;
       g.n = 0;
@@ -553,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (uint32_t i = 0; ok; ++i) {
         const bool more = w.valid();
         if (more) {
-          next = make_seg(p, w);
+          next = make_seg(p, w, tpt);
           w.next(p);
         } else {
           next.n = 0;
@@ -598,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSoftmax));
     const int t = warp >> 2, x = threadIdx.x & 127;  // tile, row within it = TMEM lane
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const int tpt = p.tpu / 2, tt = x / p.Gv, hh = x - tt * p.Gv;
+    const int tpt = p.tpu / L::kTiles, tt = x / p.Gv, hh = x - tt * p.Gv;
     PagedRec rec{0, 0, 0, 0, 0};
     int ns0 = 0, ns1 = 0, segs_o = 0, joined = 0;  // S halves' completions before the segment
     uint32_t tiles0 = 0;  // key tiles of earlier segments
@@ -782,7 +788,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = lj > 0.0f ? 1.0f / lj : 0.0f;
       const float ga = whole ? fa * inv : fa, gb = whole ? fb * inv : fb;
       float* slot =
-          p.part + static_cast<int64_t>(2 * blockIdx.x + (begins ? 1 : 0)) * kUnitRows * (D + 2);
+          p.part + static_cast<int64_t>(2 * blockIdx.x + (begins ? 1 : 0)) * L::kUnit * (D + 2);
       const int ur = (g.pair ? t : 0) * kTile + x;
       int64_t quad_dst[4];  // where the quad's rows go, -1: nowhere
       {
@@ -815,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!whole) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<uint4*>(slot + 2 * kUnitRows + ((8 * c + i) * kUnitRows + ur) * 4) =
+              *reinterpret_cast<uint4*>(slot + 2 * L::kUnit + ((8 * c + i) * L::kUnit + ur) * 4) =
                   make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
         }
@@ -849,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             p.lse[head * p.T + row] = lj > 0.0f ? (mj + log2f(lj)) * 0.6931471805599453f : -INFINITY;
         } else {
           slot[ur] = mj;
-          slot[kUnitRows + ur] = lj;
+          slot[L::kUnit + ur] = lj;
         }
       }
       tc_fence_before();  // O has been read before the next segment's P is handed over
@@ -881,43 +887,44 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D>
-tp_status tc_t(PagedTcParams& t, cudaStream_t st) {
-  using L = Lay<D>;
+template <int D, bool ONE>
+tp_status tc_t(PagedTcParams& t, int N, cudaStream_t st) {
+  using L = Lay<D, ONE>;
+  paged_set_units(t.p, kTile, L::kUnit, 7, ONE ? kOneStartCost : kStartCost);
+  TP_TRY(paged_q_map(&t.tq, t.p, D, N, t.p.tpu / L::kTiles));
   static std::atomic<uint64_t> attr_set{0};
   if (needs_setup(attr_set)) {
-    TP_CUDA_TRY(cudaFuncSetAttribute(paged_tc_kernel<D>,
+    TP_CUDA_TRY(cudaFuncSetAttribute(paged_tc_kernel<D, ONE>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem));
     mark_device(attr_set);
   }
   const int ctas = std::min(kPagedTcCtas, device_sm_count());
-  TP_CUDA_TRY(launch_kernel(paged_tc_kernel<D>, dim3(ctas), dim3(kThreads),
+  TP_CUDA_TRY(launch_kernel(paged_tc_kernel<D, ONE>, dim3(ctas), dim3(kThreads),
                             static_cast<size_t>(L::kSmem), st, t));
   count_launch();
-  return launch_paged_combine(t.p, D, kUnitRows, kTile, ctas, TP_BF16, st);
+  return launch_paged_combine(t.p, D, L::kUnit, kTile, ctas, TP_BF16, st);
 }
 
 }  // namespace
 
-tp_status launch_paged_tc(const PagedParams& p, int d, int N, cudaStream_t st) {
+tp_status launch_paged_tc(const PagedParams& p, int d, int N, bool one, cudaStream_t st) {
   PagedTcParams t{};
   t.p = p;
-  paged_set_units(t.p, kTile, kUnitRows, 7, kStartCost);
   const int64_t rows = (static_cast<int64_t>(p.n_pages) * p.Hkv) << p.ps_log2;
   t.cache_rows = static_cast<int>(rows);
   const int box = std::min(1 << p.ps_log2, kTile);
   TP_TRY(paged_cache_map(&t.tk, p.kc, rows, d, box));
   TP_TRY(paged_cache_map(&t.tv, p.vc, rows, d, box));
-  TP_TRY(paged_q_map(&t.tq, t.p, d, N));
   t.status = device_status_word();
   if (!t.status) return fail(TP_ERR_CUDA, "device status word unavailable");
   t.timeout_ns = wait_timeout_ns();
   t.debug_hang = debug_hang_flag();
-  return d == 64 ? tc_t<64>(t, st) : tc_t<128>(t, st);
+  if (d == 64) return tc_t<64, false>(t, N, st);
+  return one ? tc_t<128, true>(t, N, st) : tc_t<128, false>(t, N, st);
 }
 
 size_t paged_tc_floats(int d) {
-  return static_cast<size_t>(kPagedTcCtas) * 2 * kUnitRows * (d + 2);
+  return static_cast<size_t>(kPagedTcCtas) * 2 * Lay<64, false>::kUnit * (d + 2);
 }
 
 }  // namespace tp

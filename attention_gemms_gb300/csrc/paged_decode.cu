@@ -486,7 +486,7 @@ tp_status paged_cache_map(CUtensorMap* m, const void* cache, int64_t rows, int d
   return TP_OK;
 }
 
-tp_status paged_q_map(CUtensorMap* m, const PagedParams& p, int d, int N) {
+tp_status paged_q_map(CUtensorMap* m, const PagedParams& p, int d, int N, int tokens) {
   EncodeFn enc = encoder();
   if (!enc) return fail(TP_ERR_CUDA, "cuTensorMapEncodeTiled entry point not available");
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(p.hq),
@@ -496,7 +496,7 @@ tp_status paged_q_map(CUtensorMap* m, const PagedParams& p, int d, int N) {
   const int heads = std::min(p.G, p.hq);  // of one shard block
   const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(heads),
                              static_cast<cuuint32_t>(p.G / heads),
-                             static_cast<cuuint32_t>(p.tpu / 2)};
+                             static_cast<cuuint32_t>(tokens)};
   const cuuint32_t estr[4] = {1, 1, 1, 1};
   const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(p.qkv), dims,
                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
