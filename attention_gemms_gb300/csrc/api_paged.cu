@@ -108,10 +108,10 @@ tp_status launch_paged(const PagedArgs& a, const PagedGqa& g, void* ws, cudaStre
   p.scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(g.d));
   // most rows of a request per key/value head (no request has more than T tokens)
   const int64_t rows = std::min(a.max_new, a.T) * p.G;
-  // The kernel for few rows reads K and V once per 16 rows, the tcgen05 one per 256. 33
+  // The kernel for few rows reads K and V once per 16 rows, the tcgen05 one per 128 or 256. 33
   // requests over 100 to 5000 tokens, 8 key/value heads, us (few rows / tcgen05): d = 128, 16
-  // rows 69 / 81, 20 rows 102 / 83, 64 rows 209 / 85; d = 64, 16 rows 44 / 61, 20 rows 64 / 62,
-  // 32 rows 69 / 61. One token each: 164 / 184 (61 requests), 9.7 / 17 (one).
+  // rows 67 / 78, 20 rows 99 / 79, 64 rows 204 / 80; d = 64, 16 rows 44 / 56, 20 rows 63 / 57,
+  // 32 rows 69 / 57. One token each: 161 / 166 (61 requests), 9 / 16 (one).
   if (a.dt == TP_BF16)
     return rows > 16 && g.d >= 64 && p.G <= 128 ? launch_paged_tc(p, g.d, a.N, rows <= 128, st)
                                                 : launch_paged_decode(p, g.d, st);
