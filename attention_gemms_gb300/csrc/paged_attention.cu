@@ -432,7 +432,9 @@ __global__ void __launch_bounds__(kThreads, SimtLayout<D, RT>::kCtas)
 // 4 columns of one row and every G-th piece: the maximum over its pieces first, then weights,
 // sums and outputs, whose loads do not wait for one another; the G threads of a row and
 // columns join in shared memory. G = 4 for the slots of few rows, where a long context has
-// tens of pieces, and 1 for those of 256, which have two or three.
+// tens of pieces, and 1 for those of 256, which have two or three. Slots of 128: 4 where a
+// unit has about ten pieces or more (8 drafts, 32 heads over 8, d = 128, us, with 1 / 4: one
+// request of 3000 tokens 24.7 / 24.0, of 30000 47 / 45; three of 100000 213 / 216).
 // Slots of 128-row tiles hold O by groups of 4 columns, (d / 4, rows, 4), as their kernel has a
 // thread per row; the others by rows. Threads follow the slots' order.
 template <typename T, int D, int PER, int G>
@@ -537,7 +539,8 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedPara
 
 template <typename T, int D>
 tp_status combine_t(const PagedParams& p, int unit_rows, int tile_rows, int ctas, cudaStream_t st) {
-  if (tile_rows >= 128) {
+  const bool few_units = unit_rows == 128 && 10 * static_cast<int64_t>(p.R) * p.Hv <= ctas;
+  if (tile_rows >= 128 && !few_units) {
     constexpr int PER = 4;
     TP_CUDA_TRY(launch_kernel(paged_combine_kernel<T, D, PER, 1>,
                               dim3(ctas, unit_rows * (D / 4 / PER) / kThreads), dim3(kThreads), 0,
