@@ -238,7 +238,8 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&q)[4][4]) {
 // same rows and tile t takes key tiles t, t + 2, ... of n.
 struct __align__(16) Seg {
   int n, n0, pair, lo;              // n = 0: no more segments; lo: the first key tile
-  int row0, tokens, pos0, kv_end;   // first token's row and position, tokens, keys
+  int row0, tokens, pos0, kv_end;   // first token's row and position, tokens, the request's keys
+                                    // that some row sees
   int head0, heads, j, kend;        // first query head, heads, key/value head, unit's keys
   int r, ends, last, pad;           // request; bit 0: the unit begins here, bit 1: it ends
                                     // here; else the CTA where it ends
@@ -258,6 +259,8 @@ __device__ __forceinline__ Seg make_seg(const PagedParams& p, const Walk& w, int
   g.row0 = w.q.row0 + w.u * p.tpu;
   g.pos0 = w.q.total - w.q.n + w.u * p.tpu;
   g.kv_end = w.q.kv_end;
+  if (p.causal)  // rows past T do not exist, and nothing wrote their keys
+    g.kv_end = max(0, min(g.kv_end, w.q.total - w.q.n + w.q.rows));
   g.head0 = j * p.G + (w.vh - j * p.hs) * p.Gv;
   g.heads = min(p.Gv, (j + 1) * p.G - g.head0);
   g.j = j;
@@ -634,7 +637,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         if (h == 0 && k0 + kTile > kv_end) {
-          // V rows past the request's keys may hold anything and 0 * NaN would spoil O
+          // V rows of keys that no row of the request sees may hold anything and 0 * NaN would
+          // spoil O
           const uint32_t ld = tiles0 + i + 1 + mm;  // V's load and place in the ring
           const uint32_t at =
               2 * tiles0 + (mm == g.n - 1 ? 2 * g.n - 1 : g.pair ? 1 + 2 * mm : 2 + 2 * mm);
