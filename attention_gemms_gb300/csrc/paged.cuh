@@ -347,6 +347,13 @@ __device__ __forceinline__ int64_t paged_row(const PagedParams& p, const int32_t
   return (((static_cast<int64_t>(page) * p.Hkv + j) << p.ps_log2)) + (key & ((1 << p.ps_log2) - 1));
 }
 
+// What a row's sum l and maximum m (base 2) give: the factor of its output, and its lse. A
+// row that sees no key has l = 0; one whose scores are NaN has l = NaN, which stays NaN.
+__device__ __forceinline__ float paged_inv(float l) { return l == 0.0f ? 0.0f : 1.0f / l; }
+__device__ __forceinline__ float paged_lse(float m, float l) {
+  return l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
 #endif  // __CUDACC__
 
 // fp32 on CUDA cores (wide: chunks), and the join of the partial results (paged_attention.cu)

@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, SimtLayout<D, RT>::kCtas)
         int token, head;
         if (!unit_row(p, w.q, w.u, w.vh, RT, row, &token, &head)) continue;
         const int64_t t = static_cast<int64_t>(w.q.row0) + token;
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        const float inv = paged_inv(l);
         const bool whole = begins && ends;
         float* dst = whole ? static_cast<float*>(p.o) + t * p.H * D + static_cast<int64_t>(head) * D
                            : slot + 2 * RT + row * D;
@@ -394,8 +394,7 @@ __global__ void __launch_bounds__(kThreads, SimtLayout<D, RT>::kCtas)
             slot[row] = own_m[r];
             slot[RT + row] = l;
           } else if (p.lse) {
-            p.lse[head * p.T + t] =
-                l > 0.0f ? (own_m[r] + log2f(l)) * 0.6931471805599453f : -INFINITY;
+            p.lse[head * p.T + t] = paged_lse(own_m[r], l);
           }
         }
       }
@@ -406,14 +405,13 @@ __global__ void __launch_bounds__(kThreads, SimtLayout<D, RT>::kCtas)
         int token, head;
         if (!unit_row(p, w.q, w.u, w.vh, RT, row, &token, &head)) continue;
         if (begins && ends) {
-          const float l = ls[row], inv = l > 0.0f ? 1.0f / l : 0.0f;
+          const float l = ls[row], inv = paged_inv(l);
           float f[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) f[k] = acc[i][k] * inv;
           const int64_t t = static_cast<int64_t>(w.q.row0) + token;
           store4(static_cast<float*>(p.o) + t * p.H * D + static_cast<int64_t>(head) * D + cg * 4, f);
-          if (cg == 0 && p.lse)
-            p.lse[head * p.T + t] = l > 0.0f ? (ms[row] + log2f(l)) * 0.6931471805599453f : -INFINITY;
+          if (cg == 0 && p.lse) p.lse[head * p.T + t] = paged_lse(ms[row], l);
         } else {
           store4(slot + 2 * RT + row * D + cg * 4, acc[i]);
           if (cg == 0) {
@@ -518,7 +516,7 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedPara
       for (int y = 0; y < 4; ++y) f[0][y] += join[g][2 + y][et] * w;
     }
   }
-  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  const float inv = paged_inv(l);
   const int64_t t = static_cast<int64_t>(rec.row0) + token;
   const int head = rec.head0 + hh;
   T* dst = static_cast<T*>(p.o) + t * p.H * D + static_cast<int64_t>(head) * D + 4 * cg;
@@ -533,8 +531,7 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(const PagedPara
 #pragma unroll
     for (int g = 0; g < PER; ++g) store4(dst + 4 * g, f[g]);
   }
-  if (cg == 0 && p.lse)
-    p.lse[head * p.T + t] = l > 0.0f ? (M + log2f(l)) * 0.6931471805599453f : -INFINITY;
+  if (cg == 0 && p.lse) p.lse[head * p.T + t] = paged_lse(M, l);
 }
 
 template <typename T, int D>

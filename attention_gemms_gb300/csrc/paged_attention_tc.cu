@@ -789,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         lj = l * fa + ml.y * fb;
       }
       const bool whole = begins && ends;
-      const float inv = lj > 0.0f ? 1.0f / lj : 0.0f;
+      const float inv = paged_inv(lj);
       const float ga = whole ? fa * inv : fa, gb = whole ? fb * inv : fb;
       float* slot =
           p.part + static_cast<int64_t>(2 * blockIdx.x + (begins ? 1 : 0)) * L::kUnit * (D + 2);
@@ -855,8 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (live) {
         if (whole) {
-          if (p.lse)
-            p.lse[head * p.T + row] = lj > 0.0f ? (mj + log2f(lj)) * 0.6931471805599453f : -INFINITY;
+          if (p.lse) p.lse[head * p.T + row] = paged_lse(mj, lj);
         } else {
           slot[ur] = mj;
           slot[L::kUnit + ur] = lj;

@@ -368,10 +368,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (jr < kRows) {
 #pragma unroll
         for (int v = 0; v < kConsumers; ++v) M = fmaxf(M, ml[v * kRows + jr].x);
-        if (M != -INFINITY)
+        // (M = -inf: all sums are 0, or NaN where the scores are)
+        const float mu = M == -INFINITY ? 0.0f : M;
 #pragma unroll
-          for (int v = 0; v < kConsumers; ++v)
-            lsum += ml[v * kRows + jr].y * ex2(ml[v * kRows + jr].x - M);
+        for (int v = 0; v < kConsumers; ++v)
+          lsum += ml[v * kRows + jr].y * ex2(ml[v * kRows + jr].x - mu);
         const int tt = jr / p.Gv, g = (w.vh - j * p.hs) * p.Gv + jr - tt * p.Gv;
         jtoken = w.u * p.tpu + tt;
         jhead = j * p.G + g;
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int64_t t = static_cast<int64_t>(w.q.row0) + jtoken;
       float* slot =
           p.part + static_cast<int64_t>(2 * blockIdx.x + (begins ? 1 : 0)) * kRows * (D + 2);
-      const float inv = lsum > 0.0f ? 1.0f / lsum : 0.0f;
+      const float inv = paged_inv(lsum);
 #pragma unroll
       for (int c0 = 0; c0 < D; c0 += JC) {
 #pragma unroll
@@ -408,9 +409,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       if (jlive && jc == 0) {
         if (begins && ends) {
-          if (p.lse)
-            p.lse[jhead * p.T + t] =
-                lsum > 0.0f ? (M + log2f(lsum)) * 0.6931471805599453f : -INFINITY;
+          if (p.lse) p.lse[jhead * p.T + t] = paged_lse(M, lsum);
         } else {
           slot[jr] = M;
           slot[kRows + jr] = lsum;

@@ -607,8 +607,9 @@ TP_API tp_status tp_kv_append(const void* qkv, const int32_t* slots, void* kcach
  * tp_kv_append): row i of request r sits at position total_lens[r] - n + i and sees the
  * keys up to its position (causal != 0) or all total_lens[r].
  *   qkv (T, W): the Q columns are read;  o (T, h) written;  lse (n_heads, T) fp32
- *   written, or NULL. A row that sees no key gets o = 0 and lse = -inf; padding rows of o
- *   and lse are left as they were.
+ *   written, or NULL. A row that sees no key, or none with a score above -inf, gets o = 0
+ *   and lse = -inf; a row with a score that is NaN or +inf (a query that is not finite)
+ *   gets NaN in both. Padding rows of o and lse are left as they were.
  *   max_new: the largest number of new tokens of a request. It chooses kernels only: the
  *   result is right for any value, and the wrong one costs time.
  *   K and V of the positions that a request's rows see must be finite; other positions'

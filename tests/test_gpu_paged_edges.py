@@ -60,3 +60,27 @@ def test_step_with_more_tokens_than_rows(H, Hkv, N, d, dtype):
     assert counts.cpu().tolist() == [70, 5, 0, 25]
     ref = Q.gqa_block_fwd(xo, 1, rows, go, bo, Wsho, Woo, H, Hkv, N, True)["out"]
     assert rel(host(out), ref) <= (BF16_TOL if dtype == "bf16" else F32_TOL)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("causal", [0, 1])
+@pytest.mark.parametrize("lens", [
+    [(700, 1), (3, 1), (130, 1)], [(20000, 1)], [(3000, 5), (40, 3)], [(300, 40), (0, 70), (9, 1)],
+    [(100, 700), (0, 400)]])
+def test_query_that_is_not_finite(dtype, d, causal, lens):
+    """A NaN, or an infinity whose scores are +-inf, in the query of some rows makes o and lse
+    of these rows NaN, and no others: lse = -inf says that a row sees no key."""
+    H, Hkv, N = 8, 2, 2
+    hq, hkv, _ = Q.gqa_split(H, Hkv, N)
+    rows = sum(n for _, n in lens)
+    n0 = lens[0][1]
+    spots = [(0, 0, float("nan")), (n0 - 1, 3, float("inf")), (n0 // 2, 5, float("-inf")),
+             (rows - 1, 7, float("nan"))]
+
+    def fill(qkv, kc, vc, pos):
+        x = qkv.view(-1, N, hq + 2 * hkv, d)
+        for t, h, v in spots:
+            x[t, h // hq, h % hq, 5 + h] = v
+    _, _, ref = attend(lens, H, Hkv, N, d, 16, dtype, causal, seed=3 + d, pad=1, fill=fill)
+    assert ref["lse"].isnan().sum() == len(spots)
