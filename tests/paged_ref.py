@@ -103,16 +103,17 @@ def reference(q, kc, vc, table, tot, cu, causal):
 
 
 def attend(lens, H, Hkv, N, d, P, dtype, causal=1, *, seed=1, rows=None, total=None, pad=0,
-           max_new=None, spare=2, table_edit=None, fill=None, call=None):
+           max_new=None, spare=2, cu=None, width=None, fill=None):
     """The attention call on random data with scattered pages, NaN in every slot that no
     existing row sees and in the workspace; checks every element of o and lse. lens: (cached,
-    new) per request; fill(qkv, keys, values, pos): edits the inputs, pos (n_pages, P) the
+    new) per request, total and cu in their place where given; width: the table's, where the
+    lengths want more; fill(qkv, keys, values, pos): edits the inputs, pos (n_pages, P) the
     position that a slot holds (-1: none)."""
     rng = np.random.default_rng(seed)
     tot = np.array([c + n for c, n in lens] if total is None else total)
-    cu = np.concatenate([[0], np.cumsum([n for _, n in lens])])
+    cu = np.concatenate([[0], np.cumsum([n for _, n in lens])]) if cu is None else np.array(cu)
     rows = int(cu[-1]) + pad if rows is None else rows
-    pages = [-(-int(t) // P) for t in tot]
+    pages = [min(max(-(-int(t) // P), 0), width or 1 << 30) for t in tot]
     n_pages = sum(pages) + spare
     perm = rng.permutation(n_pages)
     table = np.full((len(lens), max(pages + [1])), -1)
@@ -122,8 +123,6 @@ def attend(lens, H, Hkv, N, d, P, dtype, causal=1, *, seed=1, rows=None, total=N
         table[r, :k] = perm[at:at + k]
         pos[perm[at:at + k]] = np.arange(k * P).reshape(k, P)
         at += k
-    if table_edit:
-        table_edit(table)
     tdt = torch.bfloat16 if dtype == "bf16" else torch.float32
     gen = torch.Generator(device="cuda").manual_seed(seed)
     rnd = lambda *s: torch.randn(s, generator=gen, device="cuda").to(tdt)

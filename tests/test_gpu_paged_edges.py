@@ -84,3 +84,17 @@ def test_query_that_is_not_finite(dtype, d, causal, lens):
             x[t, h // hq, h % hq, 5 + h] = v
     _, _, ref = attend(lens, H, Hkv, N, d, 16, dtype, causal, seed=3 + d, pad=1, fill=fill)
     assert ref["lse"].isnan().sum() == len(spots)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("P", [8, 16, 256])
+@pytest.mark.parametrize("max_new", [1, 9, 100])
+@pytest.mark.parametrize("total", [[7, 3, 100, 2 ** 31 - 1], [0, 0, 30, 0], [9, -5, -(2 ** 31), 60]])
+def test_lengths_that_do_not_fit(dtype, d, P, max_new, total):
+    """A negative number of new tokens, one that ends at 2^31 - 1, totals that are negative,
+    below the new tokens or far past the table: rows and keys are those that exist, and rows
+    that no request has stay as they were."""
+    cu, T_rows = [40, 2, 2, 40, 2 ** 31 - 1], 60
+    attend([(0, 0)] * 4, 8, 2, 1, d, P, dtype, 1, seed=d, rows=T_rows, total=total, cu=cu,
+           width=80 // P or 1, max_new=max_new)
