@@ -146,3 +146,32 @@ def test_append_past_31_bits():
         s = 3 * i
         assert torch.equal(kc[s // P, :, s % P], k[i]) and torch.equal(vc[s // P, :, s % P], v[i])
     assert kc.count_nonzero() == k.count_nonzero() and vc.count_nonzero() == v.count_nonzero()
+
+
+@pytest.mark.parametrize("d,new", [(64, 1), (128, 1), (128, 20), (64, 70), (128, 70)])
+def test_expired_waits_with_full_rings(d, new):
+    """The injected wait (a barrier that nothing arrives on) runs out while every block has a
+    ring of loads and several segments ahead: the call ends, the status says so, and the next
+    call is right."""
+    lens, H, Hkv, P = spread(24, 800, 3000, new, new), 32, 8, 16
+    tot = [c + n for c, n in lens]
+    MP, rows = -(-max(tot) // P), 24 * new
+    qkv = torch.randn(rows, cols(H, Hkv, 1, d), device="cuda").bfloat16()
+    kc = torch.randn(24 * MP, Hkv, P, d, device="cuda").bfloat16()
+    table = torch.arange(24 * MP, device="cuda", dtype=torch.int32)
+    cu = torch.arange(25, device="cuda", dtype=torch.int32) * new
+    o = torch.zeros(rows, H * d, dtype=torch.bfloat16, device="cuda")
+    wsb = T.tp_gqa_paged_attention_workspace_size(H * d, H, Hkv, 1, T.DType.BF16)
+    ws = torch.zeros(wsb, dtype=torch.uint8, device="cuda")
+    total = i32(tot)
+    T.tp_set_wait_timeout_ns(20_000_000)
+    T.tp_debug_inject_wait_fault(True)
+    try:
+        T.tp_gqa_paged_attention_fwd(qkv, kc, kc, table, total, cu, o, None, rows, 24, H * d, H, Hkv,
+                                     1, 24 * MP, P, MP, new, 1, T.DType.BF16, ws, wsb)
+        assert T.tp_check_status() == T.Status.TIMEOUT
+    finally:
+        T.tp_debug_inject_wait_fault(False)
+        T.tp_set_wait_timeout_ns(1_000_000_000)
+    assert T.tp_check_status() == 0
+    attend(lens[:9], H, Hkv, 1, d, P, "bf16", 1, seed=d)
