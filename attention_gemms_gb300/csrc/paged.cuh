@@ -98,8 +98,9 @@ __device__ __forceinline__ int64_t div_by(int64_t a, int b) {
              : a / b;
 }
 
-// sum over i < n of floor((a i + b) / 2^k), b >= 0: the Euclid-like recurrence on the
-// lattice points under a line
+// sum over i < n of floor((a i + b) / 2^k), b >= 0: whole parts by their closed form, the rest
+// by the reciprocity of such sums (the lattice points under a line, counted along the other
+// axis: Graham, Knuth, Patashnik, Concrete Mathematics, section 3.5), as in Euclid's algorithm
 __device__ __forceinline__ int64_t floor_sum(int64_t n, int k, int a, int64_t b) {
   int64_t ans = 0;
   int m = 1 << k;

@@ -29,12 +29,13 @@
 // 80 to 100 cycles per MMA in moves to uniform registers: 741 -> 650), a start cost per unit
 // in the division of the work (none 721, one tile 640, two 576, three 526 before the walk was
 // moved; now one 427, two 383, three 375, with three slower on the other shapes).
-// Now: those chunks 373 us with the same inputs again, 1.45 PFLOP/s, 75 % of the card's matrix
-// rate, 403 with new ones each time (bound by products and softmax in turn; tensor pipe 60 %
-// of the launch); four chunks of 401
-// to 512 tokens, 32 heads over 8, d = 64: 65 us (bound by the softmax warps: P V and S are a
-// third of the time); 33 requests of 2 to 7 drafts, 32 heads over 8, d = 128 (347 MB): 77 us,
-// 4.5 TB/s (the loads, the schedule and the join before and after them).
+// Now: those chunks 400 us with new inputs each time, 1.35 PFLOP/s, 70 % of the card's matrix
+// rate (373 with the same inputs again; bound by products and softmax in turn, tensor pipe 60 %
+// of the launch); four chunks of 401 to 512 tokens, 32 heads over 8, d = 64: 65 us (no pipe is
+// full: tensor 24 %, exponentials 25, ALU 29, issue 39; the chain of S, softmax and P V of two
+// row tiles bounds it, and launch, schedule and join, 15 us); 33 requests of 2 to 7 drafts, 32
+// heads over 8, d = 128 (347 MB): 77 us, 4.5 TB/s (the loads, the schedule and the join before
+// and after them).
 // Every wait is bounded; on a timeout the CTA records TP_ERR_TIMEOUT, stops issuing, waits
 // (bounded) for its own copies and MMAs, frees TMEM and returns.
 #include <cuda.h>

@@ -14,12 +14,14 @@
 //     through shared memory with keys as rows; at 16 rows the legacy instruction takes about
 //     a fifth of the loads' time (16 + 16 instructions of 4096 FLOP per 16 keys at d = 128).
 // At a segment's end the warps' pieces join in shared memory, 32 columns at a time.
-// Two CTAs per SM, 96 KB of loads in flight each: one CTA's joins and unit changes overlap
-// the other's stream. Measured: 61 requests of 1 to 8191 tokens, 64 heads over 8, d = 128,
+// Two CTAs per SM, 96 KB of loads in flight each (64 at d = 32, 32 at d = 16): one CTA's joins
+// and unit changes overlap the other's stream. Measured: 61 requests of 1 to 8191 tokens, 64 heads over 8, d = 128,
 // pages of 64 (1026 MB) 164 us, 6.2 TB/s, 92 % of what a copy reaches; three of 90001 to
-// 131071, 32 heads over 4, pages of 128 (679 MB) 112 us, 6.1 TB/s; one of 701, 32 heads over
-// 8, d = 64: 9.7 us, latency. Units of 32 rows (twice the warps, one CTA per SM) took 90 us
-// where the tcgen05 kernel takes 82 (33 requests of 8 to 28 rows).
+// 131071, 32 heads over 4, pages of 128 (679 MB) 111 us, 6.1 TB/s; one of 701, 32 heads over
+// 8, d = 64: 9.3 us, latency. At d = 16 and 32 the time goes by key tiles, not bytes: 64 requests
+// of 2 to 8001 tokens, 32 heads over 8, pages of 16, 78 and 80 us (131 and 262 MB). Units of 32
+// rows (twice the warps, one CTA per SM) took 90 us where the tcgen05 kernel took 82 (33
+// requests of 8 to 28 rows; it takes 77 now).
 // Every wait is bounded. A warp whose wait expired records TP_ERR_TIMEOUT and goes through
 // the rest of its segments without waiting (the join's barrier needs all four warps); the
 // producer waits, bounded, for the copies it issued.

@@ -583,6 +583,10 @@ TP_API tp_status tp_gqa_attn_proj_bwd(const void* x, const float* gamma, const v
  *   row t = cu_new[r] + i: positions[t] = c + i, slots[t] = its slot (-1 without a page);
  *   padding rows: -1 and -1.  *free_head_out: the list's new position (at most n_free)
  *   counts (4): new rows, pages taken, pages missing, new rows that T has no room for.
+ * The list is only taken from: pages of requests that have ended come back when the caller
+ * writes them into free_pages (and n_free or *free_head) between steps. Entries that the list
+ * had no page for stay -1 in later steps too, and their positions without a slot, unless the
+ * caller fills them; rows past T are not written by tp_kv_append either.
  * total_lens may be ctx_lens and free_head_out may be free_head (updated in place); no
  * other buffers may overlap. positions and counts may be NULL. R <= 8192.
  * Errors: TP_ERR_INVALID_ARG, TP_ERR_SHAPE, TP_ERR_CUDA, TP_ERR_UNSUPPORTED. */
