@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <initializer_list>
 #include <vector>
 
 #include "internal.h"
@@ -19,6 +20,29 @@ tp_status check_vocab(int64_t M, int64_t v, int64_t h, int32_t N, tp_dtype dt) {
   TP_TRY(need(N >= 1 && M >= 0 && v >= 1 && h >= 1, TP_ERR_INVALID_ARG,
               "need N >= 1, M >= 0, vocab >= 1, h >= 1"));
   return need(v % N == 0, TP_ERR_SHAPE, "the vocabulary size must be divisible by N");
+}
+
+// ids, targets and per-row numbers: 4-byte elements read one by one
+tp_status check_words(std::initializer_list<const void*> ptrs) {
+  for (const void* q : ptrs)
+    TP_TRY(need(reinterpret_cast<uintptr_t>(q) % 4 == 0, TP_ERR_ALIGNMENT,
+                "int32 and fp32 arrays must be 4-byte aligned"));
+  return TP_OK;
+}
+
+// sizes of the output layer's cross-entropy and of the scaled embedding
+bool ends_ok(int64_t M, int64_t v, int64_t h) {
+  return M >= 0 && v >= 1 && h >= 1 && M <= (1ll << 30) && v <= (1ll << 30) && h <= (1ll << 20) &&
+         extents_ok(M, h, 1) && extents_ok(v, h, 1) && extents_ok(M, v, 1);
+}
+tp_status check_ends(int64_t M, int64_t v, int64_t h, int32_t N, tp_dtype dt) {
+  TP_TRY(check_vocab(M, v, h, N, dt));
+  return need(ends_ok(M, v, h), TP_ERR_SHAPE,
+              "sizes too large (M or vocab > 2^30, h > 2^20, or a matrix >= 2^40 elements)");
+}
+tp_status check_linear_ce(int64_t M, int64_t v, int64_t h, int32_t N, tp_dtype dt) {
+  TP_TRY(check_ends(M, v, h, N, dt));
+  return need(dt != TP_BF16 || h % 8 == 0, TP_ERR_SHAPE, "bf16: h must be a multiple of 8");
 }
 
 // Carving of the GPT workspace: every block 256-byte aligned.
@@ -129,6 +153,86 @@ tp_status tp_vocab_ce_bwd(const void* logits, const int32_t* targets, const floa
   TP_TRY(check_device());
   return launch_vocab_ce_bwd(logits, targets, lse, dlogits, M, vocab, scale, dtype,
                              static_cast<cudaStream_t>(stream));
+}
+
+size_t tp_vocab_linear_ce_workspace_size(int fwd, int64_t M, int64_t vocab, int64_t h, int32_t N,
+                                         tp_dtype dtype) {
+  if ((dtype != TP_BF16 && dtype != TP_F32) || N < 1 || !ends_ok(M, vocab, h) || M == 0 ||
+      vocab % N || (dtype == TP_BF16 && h % 8))
+    return 0;
+  return vocab_linear_ce_ws_bytes(fwd != 0, M, vocab, h, dtype);
+}
+
+tp_status tp_vocab_linear_ce_fwd(const void* x, const void* E, const int32_t* targets, float* lse,
+                                 float* row_loss, float* shard_loss, float* loss, int64_t M,
+                                 int64_t vocab, int64_t h, int32_t N, tp_dtype dtype, void* ws,
+                                 size_t ws_bytes, void* stream) {
+  TP_TRY(check_linear_ce(M, vocab, h, N, dtype));
+  TP_TRY(need(x && E && targets && lse && row_loss && loss, TP_ERR_INVALID_ARG,
+              "x, E, targets, lse, row_loss and loss are required"));
+  TP_TRY(check_aligned({x, E, ws}));
+  TP_TRY(check_words({targets, lse, row_loss, shard_loss, loss}));
+  if (M == 0) return TP_OK;
+  TP_TRY(need(ws && ws_bytes >= vocab_linear_ce_ws_bytes(true, M, vocab, h, dtype),
+              TP_ERR_WORKSPACE, "workspace smaller than tp_vocab_linear_ce_workspace_size"));
+  TP_TRY(check_device());
+  return launch_vocab_linear_ce_fwd(x, E, targets, lse, row_loss, shard_loss, loss, M, vocab, h, N,
+                                    dtype, ws, static_cast<cudaStream_t>(stream));
+}
+
+tp_status tp_vocab_linear_ce_bwd(const void* x, const void* E, const int32_t* targets,
+                                 const float* lse, void* dx, void* dE, int64_t M, int64_t vocab,
+                                 int64_t h, int32_t N, float scale, tp_dtype dtype, void* ws,
+                                 size_t ws_bytes, void* stream) {
+  TP_TRY(check_linear_ce(M, vocab, h, N, dtype));
+  TP_TRY(need(x && E && targets && lse, TP_ERR_INVALID_ARG, "x, E, targets and lse are required"));
+  TP_TRY(need(dx || dE, TP_ERR_INVALID_ARG, "dx or dE is required"));
+  TP_TRY(check_aligned({x, E, dx, dE, ws}));
+  TP_TRY(check_words({targets, lse}));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (M == 0) {  // no rows: dE is a sum of none
+    if (!dE) return TP_OK;
+    TP_TRY(check_device());
+    TP_CUDA_TRY(cudaMemsetAsync(dE, 0, static_cast<size_t>(vocab * h) * elem_size(dtype), st));
+    return TP_OK;
+  }
+  TP_TRY(need(ws && ws_bytes >= vocab_linear_ce_ws_bytes(false, M, vocab, h, dtype),
+              TP_ERR_WORKSPACE, "workspace smaller than tp_vocab_linear_ce_workspace_size"));
+  TP_TRY(check_device());
+  return launch_vocab_linear_ce_bwd(x, E, targets, lse, dx, dE, M, vocab, h, scale, dtype, ws, st);
+}
+
+tp_status tp_vocab_embed_scaled_fwd(const int32_t* ids, const void* E, void* x, int64_t M,
+                                    int64_t vocab, int64_t h, int32_t N, float scale,
+                                    tp_dtype dtype, void* stream) {
+  TP_TRY(check_ends(M, vocab, h, N, dtype));
+  TP_TRY(need(ids && E && x, TP_ERR_INVALID_ARG, "ids, E and x are required"));
+  TP_TRY(check_aligned({E, x}));
+  TP_TRY(check_words({ids}));
+  if (M == 0) return TP_OK;
+  TP_TRY(check_device());
+  return launch_vocab_embed_scaled_fwd(ids, E, x, M, vocab, h, scale, dtype,
+                                       static_cast<cudaStream_t>(stream));
+}
+
+size_t tp_vocab_embed_scaled_workspace_size(int64_t M, int64_t vocab, int64_t h, tp_dtype dtype) {
+  if ((dtype != TP_BF16 && dtype != TP_F32) || !ends_ok(M, vocab, h)) return 0;
+  return vocab_embed_scaled_ws_bytes(M, vocab, h, dtype);
+}
+
+tp_status tp_vocab_embed_scaled_bwd(const int32_t* ids, const void* dx, void* dE, int64_t M,
+                                    int64_t vocab, int64_t h, int32_t N, float scale,
+                                    int accumulate, tp_dtype dtype, void* ws, size_t ws_bytes,
+                                    void* stream) {
+  TP_TRY(check_ends(M, vocab, h, N, dtype));
+  TP_TRY(need(dE && (M == 0 || (ids && dx)), TP_ERR_INVALID_ARG, "ids, dx and dE are required"));
+  TP_TRY(check_aligned({dx, dE, ws}));
+  TP_TRY(check_words({ids}));
+  TP_TRY(need(ws && ws_bytes >= vocab_embed_scaled_ws_bytes(M, vocab, h, dtype), TP_ERR_WORKSPACE,
+              "workspace smaller than tp_vocab_embed_scaled_workspace_size"));
+  TP_TRY(check_device());
+  return launch_vocab_embed_scaled_bwd(ids, dx, dE, M, vocab, h, scale, accumulate != 0, dtype, ws,
+                                       static_cast<cudaStream_t>(stream));
 }
 
 tp_status tp_adamw_step(float* p, const float* g, float* m, float* v, int64_t n, int64_t step,

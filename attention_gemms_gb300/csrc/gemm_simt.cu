@@ -39,6 +39,7 @@ struct SimtParams {
   const float* in0;
   const float* in1;
   int64_t ldo, out_group_stride;
+  CeEpi ce;   // EPI_LSE, EPI_DCE
   int split;  // CTAs of a cluster sharing one output tile's K steps (1: no split)
 };
 
@@ -65,6 +66,37 @@ __device__ __forceinline__ void epi1(const SimtParams& p, int g, int64_t r, int6
   } else if constexpr (EPI == EPI_PAIR) {
     p.out0[i] = a;
     p.out1[i] = b;
+  } else if constexpr (EPI == EPI_DCE) {
+    const int64_t t = p.ce.targets[r];
+    const float q = expf(a - p.ce.lse[r]) - (t == p.ce.col0 + c ? 1.0f : 0.0f);
+    p.out0[i] = t >= 0 && t < p.ce.vocab ? q * p.ce.scale : 0.0f;
+  }
+}
+
+// EPI_LSE of the `rows` rows of the tile's logits in sm (TN floats each), rows r0 .. of the
+// product, columns c0 ..: a warp per row, two columns per lane. As in the tensor-core engine the
+// maximum is kept in base 2; expf and the sum in 32 bits.
+__device__ __forceinline__ void lse_rows(const SimtParams& p, const float* sm, int rows, int64_t r0,
+                                         int64_t c0, int64_t slot) {
+  static_assert(TN == 64, "two columns per lane");
+  constexpr float kLog2e = 1.4426950408889634f;  // log2(e)
+  const int lane = threadIdx.x & 31;
+  for (int rr = threadIdx.x >> 5; rr < rows; rr += 8) {
+    const int64_t r = r0 + rr;
+    if (r >= p.M) break;
+    const int64_t ca = c0 + lane, cb = ca + 32;
+    const float a = ca < p.N ? sm[rr * TN + lane] : -INFINITY;
+    const float b = cb < p.N ? sm[rr * TN + lane + 32] : -INFINITY;
+    const int64_t t = p.ce.targets[r];
+    if (t == ca && ca < p.N) p.ce.hit[r] = a;
+    if (t == cb && cb < p.N) p.ce.hit[r] = b;
+    float m = fmaxf(a, b);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    float s = expf(a - m) + expf(b - m);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if (lane == 0) p.ce.part[slot * p.M + r] = make_float2(m * kLog2e, s);
   }
 }
 
@@ -85,6 +117,9 @@ __global__ void __launch_bounds__(256) gemm_simt_kernel(const SimtParams p) {
   const int64_t m0 = static_cast<int64_t>(blockIdx.y) * TM;
   const int64_t n0 = static_cast<int64_t>(blockIdx.x / split) * TN;
   const int g = blockIdx.z;
+  if constexpr (EPI == EPI_LSE) {
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.ce.counter = 0;
+  }
   float acc[4][4] = {}, acc2[4][4] = {};
   float ra[kPer], rb[NB][kPer];
   // element e of a step: consecutive threads walk the contiguous storage dimension
@@ -160,6 +195,17 @@ __global__ void __launch_bounds__(256) gemm_simt_kernel(const SimtParams p) {
     }
     __syncthreads();
   }
+  if (EPI == EPI_LSE && split == 1) {
+    if constexpr (EPI == EPI_LSE) {  // the tile through shared memory, whose last reads have ended
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sm[(ty * 4 + i) * TN + tx * 4 + j] = acc[i][j];
+      __syncthreads();
+      lse_rows(p, sm, TM, m0, n0, n0 / TN);
+    }
+    return;
+  }
   if (split == 1) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -183,7 +229,12 @@ __global__ void __launch_bounds__(256) gemm_simt_kernel(const SimtParams p) {
       float v = 0.0f;
       for (int q = 0; q < split; ++q) v += ld_cluster_f32(mapa_shared(off, static_cast<uint32_t>(q)));
       const int64_t r = m0 + rr, c = n0 + cc;
-      if (r < p.M && c < p.N) epi1<EPI>(p, g, r, c, v, 0.0f);
+      if constexpr (EPI == EPI_LSE) sm[rr * TN + cc] = v;  // read by this thread alone
+      else if (r < p.M && c < p.N) epi1<EPI>(p, g, r, c, v, 0.0f);
+    }
+    if constexpr (EPI == EPI_LSE) {
+      __syncthreads();
+      lse_rows(p, sm + rank * rows * TN, rows, m0 + rank * rows, n0, n0 / TN);
     }
     cluster_sync_all();  // no CTA leaves while another still reads its tile
   }
@@ -265,10 +316,12 @@ tp_status launch_gemm_simt(const GemmDesc& d, cudaStream_t st) {
   p.out0 = static_cast<float*>(d.out[0]);
   p.out1 = static_cast<float*>(d.out[1]);
   p.out2 = static_cast<float*>(d.out[2]);
-  p.in0 = static_cast<const float*>(d.in[0]);
+  // out_acc: the output is its own residual (each element is read by the thread that writes it)
+  p.in0 = static_cast<const float*>(d.out_acc ? d.out[0] : d.in[0]);
   p.in1 = static_cast<const float*>(d.in[1]);
   p.ldo = d.ldo;
   p.out_group_stride = d.out_group_stride;
+  p.ce = d.ce;
   const int64_t gx = (d.N + TN - 1) / TN, gy = (d.M + TM - 1) / TM;
   if (gx > 2147483647ll || gy > 65535 || d.groups > 65535)
     return fail(TP_ERR_SHAPE, "fp32 GEMM grid too large");
@@ -296,6 +349,11 @@ tp_status launch_gemm_simt(const GemmDesc& d, cudaStream_t st) {
       if (!pr) return fail(TP_ERR_INVALID_ARG, "pair epilogue needs a paired problem");
       e = launch_k<EPI_PAIR, true>(p, grid, st);
       break;
+    case EPI_LSE:
+      *d.ce.slots = static_cast<int>(gx);
+      e = launch_k<EPI_LSE, false>(p, grid, st);
+      break;
+    case EPI_DCE: e = launch_k<EPI_DCE, false>(p, grid, st); break;
     default: return fail(TP_ERR_INVALID_ARG, "unknown epilogue");
   }
   count_launch();

@@ -115,6 +115,8 @@ struct TcParams {  // CUtensorMap members carry their own 128-byte alignment
   int ld32;  // epilogue inputs likewise: 256-bit loads
   int64_t out_group_stride;
   int tma_out;  // pair kernel: the epilogue stages outputs in shared memory, TMA stores them
+  int out_acc;  // EPI_STORE in fp32: added to out0
+  CeEpi ce;     // EPI_LSE, EPI_DCE
   int* status;
   uint64_t timeout_ns;
   int debug_hang;
@@ -195,11 +197,102 @@ __device__ __forceinline__ void ld8(const void* base, int64_t idx, float* v) {
   unpack8(__ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(base) + idx)), v);
 }
 
+__device__ __forceinline__ void add8(float* v, const float4* o) {
+  const float4 a = o[0], b = o[1];
+  v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+  v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+}
+
 // Inputs an epilogue reads (residual / saved activations), 8 columns at a time
 template <int EPI>
 struct EpiInputs {
   static constexpr int n = EPI == EPI_DSWIGLU ? 2 : (EPI == EPI_DGELU || EPI == EPI_STORE ? 1 : 0);
 };
+
+// ---- cross-entropy on the accumulator (EPI_LSE, EPI_DCE): a lane owns a row of the tile, in
+// base 2 as the kernels on stored logits (vocab.cu): exp(l - m) = 2^(l log2(e) - m log2(e)), one
+// fused multiply-add and one ex2.approx (relative error about 2^-22; a term below 2^-126 of the
+// row's largest is dropped) per logit. The logits stay in 32 bits; only the gradient's tile is
+// rounded, to bf16, the operand type of the products that take it.
+constexpr float kCeLog2e = 1.4426950408889634f;  // log2(e)
+
+__device__ __forceinline__ float ce_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+struct CeRow {
+  int t = -1;              // the target's column of the product; outside [0, N): none here
+  bool live = false;       // the row exists and has a target
+  float m = -INFINITY;     // EPI_LSE: running maximum (base 2) and sum
+  float s = 0.0f;
+  float l2 = 0.0f;         // EPI_DCE: lse in base 2
+};
+
+template <int EPI>
+__device__ __forceinline__ CeRow ce_row(const TcParams& p, int64_t row) {
+  CeRow r;
+  if constexpr (EPI == EPI_LSE || EPI == EPI_DCE) {
+    if (row < p.M) {
+      const int64_t t = __ldg(p.ce.targets + row);
+      r.live = t >= 0 && t < p.ce.vocab;
+      if (r.live) r.t = static_cast<int>(t - p.ce.col0);
+      if constexpr (EPI == EPI_DCE) r.l2 = __ldg(p.ce.lse + row) * kCeLog2e;
+    }
+  }
+  return r;
+}
+
+// 32 logits of the row, columns x .. x + 31 of the product (x < N): into the running maximum and
+// sum, the target's logit to hit
+__device__ __forceinline__ void ce_lse32(const TcParams& p, CeRow& r, int64_t row, int x,
+                                         uint32_t* ra) {
+  const int n = static_cast<int>(p.N) - x;
+  if (n < 32) {  // the last columns' tile (the same for every lane)
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (j >= n) ra[j] = 0xFF800000u;  // -inf
+  }
+  const unsigned tj = static_cast<unsigned>(r.t - x);
+  if (__any_sync(0xFFFFFFFFu, r.t >= 0 && tj < 32u)) {
+    float v = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v = tj == j ? __uint_as_float(ra[j]) : v;
+    if (r.t >= 0 && tj < 32u) p.ce.hit[row] = v;
+  }
+  float mx = __uint_as_float(ra[0]);
+#pragma unroll
+  for (int j = 1; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(ra[j]));
+  mx *= kCeLog2e;
+  if (mx > r.m) {
+    r.s *= ce_ex2(r.m - mx);  // 0 at first
+    r.m = mx;
+  }
+  float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) {
+    s0 += ce_ex2(fmaf(__uint_as_float(ra[j]), kCeLog2e, -r.m));
+    s1 += ce_ex2(fmaf(__uint_as_float(ra[j + 1]), kCeLog2e, -r.m));
+  }
+  r.s += s0 + s1;
+}
+
+// the gradient of 32 logits in their place; zeros in a row without a target, whatever its logits
+__device__ __forceinline__ void ce_grad32(const TcParams& p, const CeRow& r, int x, uint32_t* ra) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    ra[j] = __float_as_uint(ce_ex2(fmaf(__uint_as_float(ra[j]), kCeLog2e, -r.l2)));
+  const unsigned tj = static_cast<unsigned>(r.t - x);
+  if (__any_sync(0xFFFFFFFFu, r.t >= 0 && tj < 32u)) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+      if (r.t >= 0 && tj == j) ra[j] = __float_as_uint(__uint_as_float(ra[j]) - 1.0f);
+  }
+#pragma unroll
+  for (int j = 0; j < 32; ++j)
+    ra[j] = r.live ? __float_as_uint(__uint_as_float(ra[j]) * p.ce.scale) : 0u;
+}
 
 // Epilogue of 8 consecutive output columns of one row. a: accumulator values,
 // b: the paired half (gate/up second operand) when the problem is paired. pre0/pre1:
@@ -225,6 +318,7 @@ __device__ __forceinline__ void epi8(const TcParams& p, int g, int64_t row, int6
     if (p.out_f32) {
       float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(p.out0) +
                                             g * p.out_group_stride + idx);
+      if (p.out_acc) add8(v, o);
       o[0] = make_float4(v[0], v[1], v[2], v[3]);
       o[1] = make_float4(v[4], v[5], v[6], v[7]);
     } else {
@@ -257,6 +351,8 @@ __device__ __forceinline__ void epi8(const TcParams& p, int g, int64_t row, int6
   } else if constexpr (EPI == EPI_PAIR) {
     st8(p.out0, idx, a);
     st8(p.out1, idx, b);
+  } else if constexpr (EPI == EPI_DCE) {
+    st8(p.out0, idx, a);
   }
 }
 
@@ -328,10 +424,16 @@ __device__ __forceinline__ void epi16(const TcParams& p, int g, int64_t row, int
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] += w[i];
     }
-    if (p.out_f32)
-      st16_f32(reinterpret_cast<float*>(p.out0) + g * p.out_group_stride + idx, v, wide);
-    else
+    if (p.out_f32) {
+      float* o = reinterpret_cast<float*>(p.out0) + g * p.out_group_stride + idx;
+      if (p.out_acc) {
+        add8(v, reinterpret_cast<const float4*>(o));
+        add8(v + 8, reinterpret_cast<const float4*>(o) + 2);
+      }
+      st16_f32(o, v, wide);
+    } else {
       st16(p.out0, idx, v, wide);
+    }
   } else if constexpr (EPI == EPI_GELU) {
     if (p.out0) st16(p.out0, idx, a, wide);
 #pragma unroll
@@ -359,6 +461,8 @@ __device__ __forceinline__ void epi16(const TcParams& p, int g, int64_t row, int
   } else if constexpr (EPI == EPI_PAIR) {
     st16(p.out0, idx, a, wide);
     st16(p.out1, idx, b, wide);
+  } else if constexpr (EPI == EPI_DCE) {
+    st16(p.out0, idx, a, wide);
   }
 }
 
@@ -388,6 +492,12 @@ struct EpiStager {
       bulk_commit();
     }
   }
+  __device__ __forceinline__ void add(uint32_t i, const CUtensorMap* m, int x, int y, int z) {
+    if (lane == 0) {
+      tma_add_3d(m, box(i), x, y, z);
+      bulk_commit();
+    }
+  }
   __device__ __forceinline__ void publish() {  // the lanes' box writes, visible to TMA
     fence_proxy_async_smem();
     __syncwarp();
@@ -413,10 +523,11 @@ __device__ __forceinline__ void stage_bf16(EpiStager& st, const CUtensorMap* m, 
   st.k ^= 1u;
 }
 
-// 32 fp32 values as two boxes of 16 columns: (x, y, z) and (x + 16, y, z)
+// 32 fp32 values as two boxes of 16 columns: (x, y, z) and (x + 16, y, z); acc: added to
+// what is there (each element by one box, so in no order but the launches')
 template <class F>
 __device__ __forceinline__ void stage_f32(EpiStager& st, const CUtensorMap* m, int x, int y, int z,
-                                          F&& val) {
+                                          bool acc, F&& val) {
 #pragma unroll
   for (int hf = 0; hf < 2; ++hf) {
     st.acquire<1>();
@@ -427,7 +538,8 @@ __device__ __forceinline__ void stage_f32(EpiStager& st, const CUtensorMap* m, i
                    __float_as_uint(val(j + 2)), __float_as_uint(val(j + 3)));
     }
     st.publish();
-    st.store(st.k, m, x + 16 * hf, y, z);
+    if (acc) st.add(st.k, m, x + 16 * hf, y, z);
+    else st.store(st.k, m, x + 16 * hf, y, z);
     st.k ^= 1u;
   }
 }
@@ -451,7 +563,7 @@ __device__ __forceinline__ void epi_chunk_tma(const TcParams& p, EpiStager& st, 
   auto B = [&](int j) { return __uint_as_float(rb[j]); };
   if constexpr (EPI == EPI_STORE) {
     auto v = [&](int j) { return has0 ? A(j) + in_at(pin0, j) : A(j); };
-    if (p.out_f32) stage_f32(st, &p.tmO[0], x, y, g, v);
+    if (p.out_f32) stage_f32(st, &p.tmO[0], x, y, g, p.out_acc != 0, v);
     else stage_bf16(st, &p.tmO[0], x, y, v);
   } else if constexpr (EPI == EPI_GELU) {
     if (p.out0) stage_bf16(st, &p.tmO[0], x, y, A);
@@ -482,6 +594,8 @@ __device__ __forceinline__ void epi_chunk_tma(const TcParams& p, EpiStager& st, 
   } else if constexpr (EPI == EPI_PAIR) {
     stage_bf16(st, &p.tmO[0], x, y, A);
     stage_bf16(st, &p.tmO[1], x, y, B);
+  } else if constexpr (EPI == EPI_DCE) {
+    stage_bf16(st, &p.tmO[0], x, y, A);
   }
 }
 
@@ -544,6 +658,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
   // the set-up above overlaps the previous kernel; operands and outputs are touched after
   pdl_wait();
   pdl_trigger();
+  if constexpr (EPI == EPI_LSE) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.ce.counter = 0;
+  }
 
   const int ntiles = p.tiles_m * p.tiles_n * p.groups;
   const int nkb = p.nseg * p.kb_per_seg;
@@ -694,6 +811,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
       const TileCoord tc = tile_coord(p, t);
       int ok = 1;
       [[maybe_unused]] const long long tw = TP_CLK();
+      const int64_t row = static_cast<int64_t>(tc.mt) * BM + quad * 32 + lane;
+      [[maybe_unused]] CeRow ce = ce_row<EPI>(p, row);
       if (lane == 0) ok = mbar_wait(tfull_bar(acc), acc_phase, p.timeout_ns, abort_flag) ? 1 : 0;
       ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
       [[maybe_unused]] const long long tb = TP_CLK();
@@ -703,7 +822,6 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
         break;
       }
       tc_fence_after();
-      const int64_t row = static_cast<int64_t>(tc.mt) * BM + quad * 32 + lane;
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * BN;
       const int64_t col_base = static_cast<int64_t>(tc.nt) * bn_logical;
       for (int c = 0; c < bn_logical / 32; ++c) {
@@ -711,6 +829,16 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
         tmem_ld32(t_row + c * 32, ra);
         if (p.paired) tmem_ld32(t_row + BN / 2 + c * 32, rb);
         tmem_ld_wait();
+        if constexpr (EPI == EPI_LSE || EPI == EPI_DCE) {
+          const int x = static_cast<int>(col_base) + c * 32;
+          if (x >= p.N) break;
+          if constexpr (EPI == EPI_LSE) {
+            ce_lse32(p, ce, row, x, ra);
+            continue;
+          } else {
+            ce_grad32(p, ce, x, ra);
+          }
+        }
         if (row < p.M) {
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -726,6 +854,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
             }
           }
         }
+      }
+      if constexpr (EPI == EPI_LSE) {
+        if (row < p.M) p.ce.part[tc.nt * p.M + row] = make_float2(ce.m, ce.s);
       }
       tc_fence_before();
       __syncwarp();
@@ -886,6 +1017,9 @@ __global__ void __launch_bounds__(PairCfg<WN>::THREADS, 1)
   // the set-up above overlaps the previous kernel; operands and outputs are touched after
   pdl_wait();
   pdl_trigger();
+  if constexpr (EPI == EPI_LSE) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.ce.counter = 0;
+  }
 
   const int pair = blockIdx.x >> 1;
   const int npairs = gridDim.x >> 1;
@@ -1132,6 +1266,9 @@ __global__ void __launch_bounds__(PairCfg<WN>::THREADS, 1)
       const TileCoord tc = tile_coord(p, t);
       int ok = 1;
       [[maybe_unused]] const long long tw = TP_CLK();
+      const int64_t row =
+          static_cast<int64_t>(tc.mt) * 256 + static_cast<int>(rank) * 128 + quad * 32 + lane;
+      [[maybe_unused]] CeRow ce = ce_row<EPI>(p, row);
       // narrow: the whole accumulator; wide: each half is waited for below
       if (lane == 0 && WN == 1)
         ok = mbar_wait(tfull_bar(acc), acc_phase, p.timeout_ns, abort_flag) ? 1 : 0;
@@ -1143,8 +1280,6 @@ __global__ void __launch_bounds__(PairCfg<WN>::THREADS, 1)
         break;
       }
       tc_fence_after();
-      const int64_t row =
-          static_cast<int64_t>(tc.mt) * 256 + static_cast<int>(rank) * 128 + quad * 32 + lane;
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * 256;
       for (int h = 0; h < WN && ok; ++h) {
         if (WN == 2) {
@@ -1188,6 +1323,16 @@ __global__ void __launch_bounds__(PairCfg<WN>::THREADS, 1)
             }
           }
           tmem_ld_wait();
+          if constexpr (EPI == EPI_LSE || EPI == EPI_DCE) {
+            const int x = static_cast<int>(col_base) + c * 32;
+            if (x >= p.N) break;
+            if constexpr (EPI == EPI_LSE) {
+              ce_lse32(p, ce, row, x, ra);
+              continue;
+            } else {
+              ce_grad32(p, ce, x, ra);
+            }
+          }
           if (p.tma_out) {
             const int64_t x = col_base + c * 32, y = row - lane;  // the warp's first row
             if (y < p.M && x < p.N)
@@ -1222,6 +1367,10 @@ __global__ void __launch_bounds__(PairCfg<WN>::THREADS, 1)
         }
       }
       if (!ok) break;
+      if constexpr (EPI == EPI_LSE) {  // one partial of the tile, or of each set of warps
+        const int slot = kEW == 8 ? 2 * tc.nt + (warp >= kEpiHi0 ? 1 : 0) : tc.nt;
+        if (row < p.M) p.ce.part[slot * p.M + row] = make_float2(ce.m, ce.s);
+      }
       if (warp == 2 && lane == 0) TP_STAT(4, TP_CLK() - tb);
       if (C::NACC == 2) {
         tc_fence_before();
@@ -1386,6 +1535,8 @@ tp_status launch_bn(int epi, const TcParams& prm, int grid, cudaStream_t st) {
     case EPI_DGELU: return launch_bn_epi<BN, EPI_DGELU, DEC>(prm, grid, st);
     case EPI_DSWIGLU: return launch_bn_epi<BN, EPI_DSWIGLU, DEC>(prm, grid, st);
     case EPI_PAIR: return launch_bn_epi<BN, EPI_PAIR, DEC>(prm, grid, st);
+    case EPI_LSE: return launch_bn_epi<BN, EPI_LSE, DEC>(prm, grid, st);
+    case EPI_DCE: return launch_bn_epi<BN, EPI_DCE, DEC>(prm, grid, st);
   }
   return fail(TP_ERR_INVALID_ARG, "unknown epilogue");
 }
@@ -1438,6 +1589,8 @@ tp_status launch_pair_wn(int epi, const TcParams& prm, int64_t ntiles, cudaStrea
     case EPI_DGELU: return launch_pair_epi<EPI_DGELU, WN>(prm, ntiles, st);
     case EPI_DSWIGLU: return launch_pair_epi<EPI_DSWIGLU, WN>(prm, ntiles, st);
     case EPI_PAIR: return launch_pair_epi<EPI_PAIR, WN>(prm, ntiles, st);
+    case EPI_LSE: return launch_pair_epi<EPI_LSE, WN>(prm, ntiles, st);
+    case EPI_DCE: return launch_pair_epi<EPI_DCE, WN>(prm, ntiles, st);
   }
   return fail(TP_ERR_INVALID_ARG, "unknown epilogue");
 }
@@ -1477,7 +1630,8 @@ int epi_out_bytes(const GemmDesc& d) {
 tp_status launch_gemm_tc(const GemmDesc& d, cudaStream_t st) {
   if (d.M <= 0 || d.N <= 0 || d.K <= 0) return TP_OK;
   if (d.paired && d.nseg != 1) return fail(TP_ERR_INVALID_ARG, "paired GEMM needs one K segment");
-  if (d.N % 8 != 0) return fail(TP_ERR_SHAPE, "GEMM output width must be a multiple of 8");
+  if (d.N % 8 != 0 && d.epi != EPI_LSE)  // which stores nothing of D
+    return fail(TP_ERR_SHAPE, "GEMM output width must be a multiple of 8");
   if (d.groups > 1 && d.K % BK != 0)
     return fail(TP_ERR_SHAPE, "per-shard K must be a multiple of 64");
   if (d.nseg < 1 || d.nseg > 3) return fail(TP_ERR_INVALID_ARG, "1 to 3 K segments");
@@ -1582,6 +1736,10 @@ tp_status launch_gemm_tc(const GemmDesc& d, cudaStream_t st) {
   prm.ldo = d.ldo;
   prm.out_f32 = d.out_f32;
   prm.out_group_stride = d.out_group_stride;
+  prm.out_acc = d.out_acc;
+  prm.ce = d.ce;
+  if (epi == EPI_LSE)  // partials of a row: one per tile, or per set of four epilogue warps
+    *d.ce.slots = prm.tiles_n * (pair && (wide ? PairCfg<2>::EPI_WARPS : PairCfg<1>::EPI_WARPS) == 8 ? 2 : 1);
   {
     const int64_t esz = d.out_f32 ? 4 : 2;
     bool ok = (d.ldo * esz) % 32 == 0 && (!d.out_f32 || (d.out_group_stride * 4) % 32 == 0);
@@ -1604,7 +1762,7 @@ tp_status launch_gemm_tc(const GemmDesc& d, cudaStream_t st) {
     const int64_t gstride = groups > 1 ? d.out_group_stride : d.ldo * d.M;
     bool ok = (d.ldo * esz) % 16 == 0 && (gstride * esz) % 16 == 0 && gstride > 0;
     for (void* o : d.out) ok = ok && reinterpret_cast<uintptr_t>(o) % 16 == 0;
-    if (ok) {
+    if (ok && epi != EPI_LSE) {
       for (int o = 0; o < 3; ++o)
         if (d.out[o]) TP_TRY(make_out_map(&prm.tmO[o], d.out[o], d.out_f32, d.N, d.M, d.ldo, groups, gstride));
       prm.tma_out = 1;

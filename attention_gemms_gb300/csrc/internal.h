@@ -129,7 +129,27 @@ enum EpiKind : int {
   EPI_DGELU = 3,    // out[0] = acc * GELU'(in[0])
   EPI_DSWIGLU = 4,  // a = acc, g = in[0], u = in[1]: out[0] = dG, out[1] = dU
   EPI_PAIR = 5,     // paired: out[0] = first half, out[1] = second half
-  EPI_COUNT = 6
+  EPI_LSE = 6,      // the row's maximum and sum of exponentials over the tile (CeEpi), no output
+  EPI_DCE = 7,      // out[0] = scale (exp(acc - lse) - [column == target]) (CeEpi)
+  EPI_COUNT = 8
+};
+
+// Cross-entropy of the logits D = x E^T that a product forms and does not keep. Column n of D is
+// vocabulary entry col0 + n; a row whose target lies outside [0, vocab) has neither a loss nor a
+// gradient.
+struct CeEpi {
+  const int32_t* targets = nullptr;  // (M)
+  int64_t vocab = 0, col0 = 0;
+  // EPI_LSE: part[slot * M + row] = (m, s) of the tiles' columns: m the largest log2(e) * logit,
+  // s the sum of 2^(log2(e) * logit - m); *slots (host) is set to their number, one for every 64
+  // columns or more. hit[row] = the target's logit. *counter is zeroed.
+  float2* part = nullptr;
+  float* hit = nullptr;
+  int32_t* counter = nullptr;
+  int* slots = nullptr;
+  // EPI_DCE
+  const float* lse = nullptr;  // (M)
+  float scale = 0.0f;
 };
 
 // A 2-D row-major tensor in storage order.
@@ -162,7 +182,9 @@ struct GemmDesc {
   const void* in[2] = {nullptr, nullptr};
   int64_t ldo = 0;     // row pitch of outputs and of in[] (elements)
   bool out_f32 = false;  // EPI_STORE: fp32 output (partials), else the element type
+  bool out_acc = false;  // EPI_STORE with out_f32: out[0] += acc
   int64_t out_group_stride = 0;
+  CeEpi ce;
   tp_dtype dtype = TP_BF16;
 };
 
@@ -265,6 +287,28 @@ tp_status launch_vocab_ce_fwd(const void* logits, const int32_t* targets, float*
 tp_status launch_vocab_ce_bwd(const void* logits, const int32_t* targets, const float* lse,
                               void* dlogits, int64_t M, int64_t v, float scale, tp_dtype dt,
                               cudaStream_t st);
+// the shards' losses and their sum / M (the last step of launch_vocab_ce_fwd)
+tp_status launch_vocab_ce_loss(const float* row_loss, const int32_t* targets, float* shard_loss,
+                               float* loss, int64_t M, int64_t v, int N, cudaStream_t st);
+
+// output layer and cross-entropy without logits (vocab_linear.cu); E (v, h), x (M, h)
+size_t vocab_linear_ce_ws_bytes(bool fwd, int64_t M, int64_t v, int64_t h, tp_dtype dt);
+tp_status launch_vocab_linear_ce_fwd(const void* x, const void* E, const int32_t* targets,
+                                     float* lse, float* row_loss, float* shard_loss, float* loss,
+                                     int64_t M, int64_t v, int64_t h, int N, tp_dtype dt, void* ws,
+                                     cudaStream_t st);
+tp_status launch_vocab_linear_ce_bwd(const void* x, const void* E, const int32_t* targets,
+                                     const float* lse, void* dx, void* dE, int64_t M, int64_t v,
+                                     int64_t h, float scale, tp_dtype dt, void* ws,
+                                     cudaStream_t st);
+// scaled embedding lookup and its gradient by sorted tokens (vocab_embed.cu)
+size_t vocab_embed_scaled_ws_bytes(int64_t M, int64_t v, int64_t h, tp_dtype dt);
+tp_status launch_vocab_embed_scaled_fwd(const int32_t* ids, const void* E, void* x, int64_t M,
+                                        int64_t v, int64_t h, float scale, tp_dtype dt,
+                                        cudaStream_t st);
+tp_status launch_vocab_embed_scaled_bwd(const int32_t* ids, const void* dx, void* dE, int64_t M,
+                                        int64_t v, int64_t h, float scale, bool accumulate,
+                                        tp_dtype dt, void* ws, cudaStream_t st);
 tp_status launch_adamw(float* p, const float* g, float* m, float* v, int64_t n, float lr,
                        float b1, float b2, float eps, float wd, float bc1, float bc2,
                        cudaStream_t st);

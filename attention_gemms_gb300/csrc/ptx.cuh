@@ -189,6 +189,15 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* m, uint32_t src,
       "r"(src), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
+// The same box added (fp32) to what is in global memory.
+__device__ __forceinline__ void tma_add_3d(const CUtensorMap* m, uint32_t src, int32_t x,
+                                           int32_t y, int32_t z) {
+  asm volatile(
+      "cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group"
+      " [%0, {%2, %3, %4}], [%1];" ::"l"(reinterpret_cast<uint64_t>(m)),
+      "r"(src), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
 __device__ __forceinline__ void bulk_commit() {
   asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }

@@ -481,8 +481,14 @@ tp_status launch_vocab_ce_fwd(const void* logits, const int32_t* targets, float*
     if (vec) TP_CUDA_TRY(launch_kernel(vocab_ce_fwd_vec_kernel<float>, gw, kThreads, 0, st, L, targets, lse, row_loss, M, v, N));
     else TP_CUDA_TRY(launch_kernel(vocab_ce_fwd_kernel<float>, g, kThreads, 0, st, L, targets, lse, row_loss, v, N));
   }
+  count_launch();
+  return launch_vocab_ce_loss(row_loss, targets, shard_loss, loss, M, v, N, st);
+}
+
+tp_status launch_vocab_ce_loss(const float* row_loss, const int32_t* targets, float* shard_loss,
+                               float* loss, int64_t M, int64_t v, int N, cudaStream_t st) {
   TP_CUDA_TRY(launch_kernel(vocab_ce_loss_kernel, 1, 1024, 0, st, row_loss, targets, shard_loss, loss, M, v, N));
-  count_launch(2);
+  count_launch();
   TP_CUDA_TRY(cudaGetLastError());
   return TP_OK;
 }

@@ -178,6 +178,15 @@ _SIGS = {
     "tp_vocab_embed_bwd": (_ST, [_P, _P, _P, _I64, _I64, _I64, _I32, ctypes.c_int, _ST, _P]),
     "tp_vocab_ce_fwd": (_ST, [_P] * 6 + [_I64, _I64, _I32, _ST, _P]),
     "tp_vocab_ce_bwd": (_ST, [_P] * 4 + [_I64, _I64, _I32, ctypes.c_float, _ST, _P]),
+    "tp_vocab_linear_ce_workspace_size": (_SZ, [ctypes.c_int, _I64, _I64, _I64, _I32, _ST]),
+    "tp_vocab_linear_ce_fwd": (_ST, [_P] * 7 + [_I64, _I64, _I64, _I32, _ST, _P, _SZ, _P]),
+    "tp_vocab_linear_ce_bwd": (_ST, [_P] * 6 + [_I64, _I64, _I64, _I32, ctypes.c_float, _ST, _P,
+                                                _SZ, _P]),
+    "tp_vocab_embed_scaled_fwd": (_ST, [_P, _P, _P, _I64, _I64, _I64, _I32, ctypes.c_float, _ST,
+                                        _P]),
+    "tp_vocab_embed_scaled_workspace_size": (_SZ, [_I64, _I64, _I64, _ST]),
+    "tp_vocab_embed_scaled_bwd": (_ST, [_P, _P, _P, _I64, _I64, _I64, _I32, ctypes.c_float,
+                                        ctypes.c_int, _ST, _P, _SZ, _P]),
     "tp_adamw_step": (_ST, [_P] * 4 + [_I64, _I64] + [ctypes.c_float] * 5 + [_P]),
     "tp_train_step_advance": (_ST, [_P, _P, _P, _I64, _P]),
     "tp_adamw_step_device": (_ST, [_P] * 4 + [_I64, _P] + [ctypes.c_float] * 5 + [_P]),
@@ -495,6 +504,40 @@ def tp_vocab_ce_fwd(logits, targets, lse, row_loss, shard_loss, loss, M, vocab, 
 def tp_vocab_ce_bwd(logits, targets, lse, dlogits, M, vocab, N, scale, dtype, stream=None):
     _check(lib().tp_vocab_ce_bwd(_ptr(logits), _ptr(targets), _ptr(lse), _ptr(dlogits), M, vocab,
                                  N, float(scale), int(dtype), _stream(stream)))
+
+
+def tp_vocab_linear_ce_workspace_size(fwd, M, vocab, h, N, dtype):
+    return int(lib().tp_vocab_linear_ce_workspace_size(int(bool(fwd)), M, vocab, h, N, int(dtype)))
+
+
+def tp_vocab_linear_ce_fwd(x, E, targets, lse, row_loss, shard_loss, loss, M, vocab, h, N, dtype,
+                           ws, ws_bytes, stream=None):
+    _check(lib().tp_vocab_linear_ce_fwd(_ptr(x), _ptr(E), _ptr(targets), _ptr(lse), _ptr(row_loss),
+                                        _ptr(shard_loss), _ptr(loss), M, vocab, h, N, int(dtype),
+                                        _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def tp_vocab_linear_ce_bwd(x, E, targets, lse, dx, dE, M, vocab, h, N, scale, dtype, ws, ws_bytes,
+                           stream=None):
+    _check(lib().tp_vocab_linear_ce_bwd(_ptr(x), _ptr(E), _ptr(targets), _ptr(lse), _ptr(dx),
+                                        _ptr(dE), M, vocab, h, N, float(scale), int(dtype),
+                                        _ptr(ws), int(ws_bytes), _stream(stream)))
+
+
+def tp_vocab_embed_scaled_fwd(ids, E, x, M, vocab, h, N, scale, dtype, stream=None):
+    _check(lib().tp_vocab_embed_scaled_fwd(_ptr(ids), _ptr(E), _ptr(x), M, vocab, h, N,
+                                           float(scale), int(dtype), _stream(stream)))
+
+
+def tp_vocab_embed_scaled_workspace_size(M, vocab, h, dtype):
+    return int(lib().tp_vocab_embed_scaled_workspace_size(M, vocab, h, int(dtype)))
+
+
+def tp_vocab_embed_scaled_bwd(ids, dx, dE, M, vocab, h, N, scale, accumulate, dtype, ws, ws_bytes,
+                              stream=None):
+    _check(lib().tp_vocab_embed_scaled_bwd(_ptr(ids), _ptr(dx), _ptr(dE), M, vocab, h, N,
+                                           float(scale), int(bool(accumulate)), int(dtype),
+                                           _ptr(ws), int(ws_bytes), _stream(stream)))
 
 
 def tp_adamw_step(p, g, m, v, n, step, lr, beta1, beta2, eps, weight_decay, stream=None):

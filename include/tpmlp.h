@@ -756,6 +756,59 @@ TP_API tp_status tp_vocab_ce_bwd(const void* logits, const int32_t* targets, con
                                  void* dlogits, int64_t M, int64_t vocab, int32_t N,
                                  float scale, tp_dtype dtype, void* stream);
 
+/* The output layer and its cross-entropy in one, in pieces of the vocabulary: the logits
+ * x E^T (M, vocab), E (vocab, h) the shared embedding, are formed on chip and not kept, where
+ * tp_vocab_ce_fwd / _bwd take them as a buffer. Results as there [张量并行 notes,
+ * §损失计算层的并行化]: lse, row_loss (M), shard_loss (N, or NULL) and loss (1), fp32.
+ *   x (M, h), E (vocab, h) read, finite (also rows of x without a target); targets (M) int32
+ *   bf16: logits and their sums in fp32, h % 8 == 0, any vocab divisible by N; fp32: any sizes.
+ *   lse, row_loss, shard_loss, loss, targets: 4-byte aligned.
+ *   ws: tp_vocab_linear_ce_workspace_size(1, ...) bytes, uninitialised, for one call at a time
+ *   (calls on one stream may share it). At most 1/16 of the bf16 logits, and 5 bytes per row.
+ * A row whose target lies outside [0, vocab) gets row_loss 0 and its lse. Buffers do not overlap.
+ * M <= 2^30, vocab <= 2^30, h <= 2^20 (here and below). M = 0 launches nothing.
+ * Errors: TP_ERR_INVALID_ARG, SHAPE, DTYPE, ALIGNMENT, WORKSPACE, CUDA, UNSUPPORTED. */
+TP_API size_t tp_vocab_linear_ce_workspace_size(int fwd, int64_t M, int64_t vocab, int64_t h,
+                                                int32_t N, tp_dtype dtype);
+TP_API tp_status tp_vocab_linear_ce_fwd(const void* x, const void* E, const int32_t* targets,
+                                        float* lse, float* row_loss, float* shard_loss,
+                                        float* loss, int64_t M, int64_t vocab, int64_t h,
+                                        int32_t N, tp_dtype dtype, void* ws, size_t ws_bytes,
+                                        void* stream);
+
+/* Its gradients from the forward's lse, q = scale * (softmax(x E^T) - one_hot(targets)):
+ *   dx (M, h) = q E and dE (vocab, h) = q^T x, written (either may be NULL: not wanted).
+ * scale = 1/M for the mean loss. q is a row of zeros where the target lies outside [0, vocab).
+ * The logits are formed again, a piece of the vocabulary at a time; of q one piece is kept in ws
+ * (tp_vocab_linear_ce_workspace_size(0, ...) bytes: at most about 512 MiB, or 256 columns, of q,
+ * and in bf16 fp32 sums of dx where they need several products), rounded to the element type.
+ * The fp32 sums over the vocabulary and over the rows go in a fixed order: results repeat.
+ * M = 0 writes zeros to dE. Errors: as above. */
+TP_API tp_status tp_vocab_linear_ce_bwd(const void* x, const void* E, const int32_t* targets,
+                                        const float* lse, void* dx, void* dE, int64_t M,
+                                        int64_t vocab, int64_t h, int32_t N, float scale,
+                                        tp_dtype dtype, void* ws, size_t ws_bytes, void* stream);
+
+/* tp_vocab_embed_fwd with a factor: x[t] = scale * E[ids[t]] (the product in fp32), a zero row for
+ * ids outside [0, vocab). ids 4-byte aligned. Errors: as tp_vocab_embed_fwd. */
+TP_API tp_status tp_vocab_embed_scaled_fwd(const int32_t* ids, const void* E, void* x, int64_t M,
+                                           int64_t vocab, int64_t h, int32_t N, float scale,
+                                           tp_dtype dtype, void* stream);
+
+/* Its gradient, tokens sorted by id on the device first, so that the work is M + vocab rows (the
+ * scan of tp_vocab_embed_bwd reads all M ids for each of the vocab rows):
+ *   dE[c] = (accumulate: dE[c] +) scale * sum over tokens t with ids[t] == c of dx[t]
+ * summed in fp32 in an order that depends on the ids alone, rounded once. accumulate == 0 writes
+ * every row of dE; else rows without a token are left as they were (bit for bit).
+ *   ws: tp_vocab_embed_scaled_workspace_size(...) bytes, uninitialised, for one call at a time.
+ * Errors: as tp_vocab_embed_bwd, and TP_ERR_WORKSPACE. */
+TP_API size_t tp_vocab_embed_scaled_workspace_size(int64_t M, int64_t vocab, int64_t h,
+                                                   tp_dtype dtype);
+TP_API tp_status tp_vocab_embed_scaled_bwd(const int32_t* ids, const void* dx, void* dE,
+                                           int64_t M, int64_t vocab, int64_t h, int32_t N,
+                                           float scale, int accumulate, tp_dtype dtype, void* ws,
+                                           size_t ws_bytes, void* stream);
+
 /* AdamW with decoupled weight decay over n fp32 values, step >= 1 (bias corrections
  * 1 - beta^step): p <- p (1 - lr wd); m <- b1 m + (1-b1) g; v <- b2 v + (1-b2) g^2;
  * p <- p - lr (m / bc1) / (sqrt(v / bc2) + eps). The listing of the Megatron-LM 实战 04
