@@ -227,7 +227,7 @@ struct CeRow {
   bool live = false;       // the row exists and has a target
   float m = -INFINITY;     // EPI_LSE: running maximum (base 2) and sum
   float s = 0.0f;
-  float l2 = 0.0f;         // EPI_DCE: lse in base 2
+  float l2 = 0.0f;         // EPI_DCE: (lse in base 2) - log2|scale|; inf in a row without a target
 };
 
 template <int EPI>
@@ -238,7 +238,8 @@ __device__ __forceinline__ CeRow ce_row(const TcParams& p, int64_t row) {
       const int64_t t = __ldg(p.ce.targets + row);
       r.live = t >= 0 && t < p.ce.vocab;
       if (r.live) r.t = static_cast<int>(t - p.ce.col0);
-      if constexpr (EPI == EPI_DCE) r.l2 = __ldg(p.ce.lse + row) * kCeLog2e;
+      if constexpr (EPI == EPI_DCE)
+        r.l2 = r.live ? __ldg(p.ce.lse + row) * kCeLog2e - log2f(fabsf(p.ce.scale)) : INFINITY;
     }
   }
   return r;
@@ -278,7 +279,8 @@ __device__ __forceinline__ void ce_lse32(const TcParams& p, CeRow& r, int64_t ro
   r.s += s0 + s1;
 }
 
-// the gradient of 32 logits in their place; zeros in a row without a target, whatever its logits
+// the gradient of 32 logits in their place, |scale| in the exponent: one fused multiply-add and one
+// power each. Zeros in a row without a target.
 __device__ __forceinline__ void ce_grad32(const TcParams& p, const CeRow& r, int x, uint32_t* ra) {
 #pragma unroll
   for (int j = 0; j < 32; ++j)
@@ -287,11 +289,13 @@ __device__ __forceinline__ void ce_grad32(const TcParams& p, const CeRow& r, int
   if (__any_sync(0xFFFFFFFFu, r.t >= 0 && tj < 32u)) {
 #pragma unroll
     for (int j = 0; j < 32; ++j)
-      if (r.t >= 0 && tj == j) ra[j] = __float_as_uint(__uint_as_float(ra[j]) - 1.0f);
+      if (r.t >= 0 && tj == j)
+        ra[j] = __float_as_uint(__uint_as_float(ra[j]) - fabsf(p.ce.scale));
   }
+  if (p.ce.scale < 0.0f) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j)
-    ra[j] = r.live ? __float_as_uint(__uint_as_float(ra[j]) * p.ce.scale) : 0u;
+    for (int j = 0; j < 32; ++j) ra[j] ^= 0x80000000u;
+  }
 }
 
 // Epilogue of 8 consecutive output columns of one row. a: accumulator values,
@@ -1677,7 +1681,10 @@ tp_status launch_gemm_tc(const GemmDesc& d, cudaStream_t st) {
     const bool many = wtiles >= 4 * pairs_n || 18 * waves(wtiles) < 10 * waves(ntiles);
     const int64_t k_tile = static_cast<int64_t>(d.nseg) * d.K;
     const int mode = g_wide_mode.load();
-    wide = mode == 2 || (mode == 1 && d.N % ww == 0 && many &&
+    // the forward cross-entropy's last tile may be ragged; its exponentials count as two bytes
+    // (K = 2048: 8192 x 50304 925 us wide, 1000 narrow; K = 1024: 2048 x 50304 167 and 158)
+    const bool whole = d.N % ww == 0 || (epi == EPI_LSE && d.N >= 8 * ww);
+    wide = mode == 2 || (mode == 1 && whole && many &&
                          k_tile >= static_cast<int64_t>(TP_WIDE_K_PER_BYTE) * epi_out_bytes(d));
   }
   const int tile_w = bn_logical * (wide ? 2 : 1);  // logical output columns of a tile

@@ -3,15 +3,16 @@
 // An id lies in one vocabulary shard, whose rows are consecutive rows of E: the shards' sum is the
 // row itself. Ids outside [0, v) give a zero row and no gradient.
 //
-// The gradient takes three launches.
-//  * Sort: every CTA owns a range of vocabulary rows and reads all ids (4 M bytes out of L2). It
-//    counts its own per row and warp, and the ids below its range, which is where its part of the
-//    sorted list begins: no exchange between CTAs, no order left to chance. It also cuts the line
-//    (row 0's tokens, row 0, row 1's tokens, row 1, ...) into equal units.
-//  * Sum: a group of threads walks a unit, 16 bytes of the columns each, several tokens' loads in
-//    flight whatever rows they belong to, and writes the rows that end in it, those without a token
-//    too. A row of many tokens can lie in several units, which then leave fp32 partials.
-//  * Join: the partials of such rows in order.
+// The gradient takes two launches.
+//  * Sort: CTA g of G (a power of two) owns the rows c with c mod G = g, so that frequent ids that
+//    lie together, as a tokeniser's do, fall to different CTAs. It reads all ids (4 M bytes out of
+//    L2), counts its own per row and warp, and the ids of the CTAs before it, which is where its
+//    part of the sorted list begins: no exchange between CTAs, no order left to chance. It also
+//    cuts the list into equal units, and notes its rows without a token.
+//  * Sum: a group of threads walks a unit, 16 bytes of the columns each, eight tokens' loads in
+//    flight whatever rows they belong to, and writes the rows that end in it. A row of many tokens
+//    can lie in several units, which then leave fp32 partials; the thread that leaves a column's
+//    last one adds them up, in the units' order. Rows without a token are written beside.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -26,9 +27,12 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kMaxRange = 1408;   // rows of a sorting CTA: 32 counters each in shared memory
+constexpr int kMaxRange = 1152;   // rows of a sorting CTA: 32 counters each in shared memory
+constexpr int kKept = 512;        // tokens of its own that a sorting warp remembers
 constexpr int kWhole = 16;        // a row of at most so many tokens is not split
-constexpr int kInFlight = 8;      // tokens whose loads a thread of the sum issues together
+constexpr int kUnitTokens = 16;   // a unit's tokens at the least
+constexpr int kMaxUnits = 1216;   // 8 per SM
+constexpr int kInFlight = 4;      // tokens whose loads a thread of the sum issues together
 
 // VEC consecutive elements of T in fp32
 template <typename T, int VEC>
@@ -127,37 +131,75 @@ __global__ void __launch_bounds__(kThreads) vocab_embed_scaled_fwd_kernel(
 
 // ------------------------------------------------------------------ sort
 
-// Where a unit begins: at token `tok` of the sorted list, in row `row`; mid: after the row's first
-// token, else before the whole row.
+// Where unit u begins: at token `tok` of the sorted list, in row `row`, which has tokens start ..
+// end - 1. Units have L = ceil(total / units) tokens, so tok is u L, or the row's start where the
+// row is short enough to be left whole.
 struct Border {
-  int32_t row, tok, mid, pad;
+  int32_t row, tok, start, end;
+  __device__ __forceinline__ bool mid() const { return tok > start; }
 };
 
+// Row c is row c >> log2_ctas of CTA c mod ctas; the list goes by CTA, then by row, then by warp and
+// the order in which a warp meets its tokens (four at a time per lane: a fixed order).
 __global__ void __launch_bounds__(kSortThreads) vocab_embed_sort_kernel(
     const int32_t* __restrict__ ids, int2* __restrict__ sorted, Border* __restrict__ border,
-    int64_t M, int64_t v, int range, int units, int row_weight) {
+    int32_t* __restrict__ arrived, uint32_t* __restrict__ absent, int32_t M, int32_t v,
+    int log2_ctas, int range, int units, int columns) {
   pdl_wait();  // the previous kernel's results are complete and visible
   pdl_trigger();
-  extern __shared__ int32_t cnt[];           // [warp][range], then the rows' starts
-  int32_t* start = cnt + kSortWarps * range;  // [range + 1]
+  extern __shared__ int32_t cnt[];              // [warp][range]
+  int32_t* start = cnt + kSortWarps * range;    // [range + 1] the rows' starts
+  uint32_t* kept = reinterpret_cast<uint32_t*>(start + range + 1);  // [warp][kKept]
   __shared__ int32_t red[2][kSortWarps];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t lo = static_cast<int64_t>(blockIdx.x) * range;
-  const int n = static_cast<int>(min(static_cast<int64_t>(range), v - lo));
+  const unsigned lower = (1u << lane) - 1u;
+  const int me = blockIdx.x, mask = (1 << log2_ctas) - 1;
+  const int n = (v - me + mask) >> log2_ctas;  // rows of this CTA
   for (int i = threadIdx.x; i < kSortWarps * range; i += kSortThreads) cnt[i] = 0;
   __syncthreads();
-  // warp w takes tokens [w seg, (w + 1) seg), in order
-  const int64_t seg = ((M + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
-  const int64_t t0 = warp * seg, t1 = min(t0 + seg, M);
+  // warp w takes tokens [w seg, (w + 1) seg), 128 at a time: lane l tokens 4 l .. 4 l + 3
+  const int seg = ((M + kSortWarps - 1) / kSortWarps + 127) / 128 * 128;
+  const int64_t t0 = min(static_cast<int64_t>(warp) * seg, static_cast<int64_t>(M));
+  const int64_t t1 = min(t0 + seg, static_cast<int64_t>(M));
   int32_t* mine = cnt + warp * range;
-  int below = 0, total = 0;
-#pragma unroll 8
-  for (int64_t t = t0 + lane; t < t1; t += 32) {
-    const int64_t id = ids[t];
-    const bool in = id >= 0 && id < v;
-    total += in;
-    below += in && id < lo;
-    if (id >= lo && id < lo + n) atomicAdd(mine + (id - lo), 1);
+  uint32_t* list = kept + warp * kKept;
+  const bool quads = reinterpret_cast<uintptr_t>(ids) % 16 == 0;
+  auto load = [&](int64_t tb, int (&id)[4]) {  // -1: outside the vocabulary, or no token
+    const int64_t t = tb + 4 * lane;
+    if (quads && t + 4 <= t1) {
+      const int4 q = *reinterpret_cast<const int4*>(ids + t);
+      id[0] = q.x; id[1] = q.y; id[2] = q.z; id[3] = q.w;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) id[j] = t + j < t1 ? ids[t + j] : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) id[j] = id[j] < v ? id[j] : -1;
+  };
+  // counts; the tokens that are this CTA's are kept, 16 bits of token and of row, while they fit
+  int below = 0, total = 0, have = 0;
+  for (int64_t tb = t0; tb < t1; tb += 512) {
+    int id[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load(tb + 128 * i, id[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int x = id[i][j], g = x & mask;
+        total += x >= 0;
+        below += x >= 0 && g < me;
+        const bool in = x >= 0 && g == me;
+        const unsigned any = __ballot_sync(0xFFFFFFFFu, in);
+        if (any == 0) continue;
+        if (in) {
+          const int r = x >> log2_ctas, at = have + __popc(any & lower);
+          atomicAdd(mine + r, 1);
+          if (at < kKept)
+            list[at] = static_cast<uint32_t>(tb + 128 * i + 4 * lane + j - t0) << 16 | r;
+        }
+        have += __popc(any);
+      }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
@@ -176,120 +218,168 @@ __global__ void __launch_bounds__(kSortThreads) vocab_embed_sort_kernel(
     below += __shfl_xor_sync(0xFFFFFFFFu, below, o);
     total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
   }
-  // each row's tokens before each warp's, and the rows' counts
-  for (int r = threadIdx.x; r < n; r += kSortThreads) {
+  // each row's tokens before each warp's, and the running sum of the rows' counts
+  if (threadIdx.x == 0) start[0] = below;
+  int carry = below;
+  for (int r0 = 0; r0 < n; r0 += kSortThreads) {
+    const int r = r0 + threadIdx.x;
     int run = 0;
-    for (int w = 0; w < kSortWarps; ++w) {
-      const int c = cnt[w * range + r];
-      cnt[w * range + r] = run;
-      run += c;
-    }
-    start[r + 1] = run;
-  }
-  __syncthreads();
-  if (warp == 0) {  // running sum of the counts
-    int run = below;
-    if (lane == 0) start[0] = run;
-    for (int r = 0; r < n; r += 32) {
-      int c = r + lane < n ? start[r + lane + 1] : 0;
+    if (r < n) {
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xFFFFFFFFu, c, o);
-        if (lane >= o) c += y;
+      for (int w = 0; w < kSortWarps; ++w) {
+        const int c = cnt[w * range + r];
+        cnt[w * range + r] = run;
+        run += c;
       }
-      if (r + lane < n) start[r + lane + 1] = run + c;
-      run += __shfl_sync(0xFFFFFFFFu, c, 31);
     }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xFFFFFFFFu, run, o);
+      if (lane >= o) run += y;
+    }
+    __syncthreads();  // red has been read
+    if (lane == 31) red[0][warp] = run;
+    __syncthreads();
+    int all = red[0][lane], before = lane < warp ? all : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
+      all += __shfl_xor_sync(0xFFFFFFFFu, all, o);
+    }
+    if (r < n) start[r + 1] = carry + before + run;
+    carry += all;
   }
   __syncthreads();
-  // the tokens to their places, each warp its own in order
-  for (int64_t tb = t0; tb < t1; tb += 32) {
-    const int64_t t = tb + lane;
-    const int64_t id = t < t1 ? ids[t] : -1;
-    const bool in = id >= lo && id < lo + n;
-    const unsigned any = __ballot_sync(0xFFFFFFFFu, in);
-    if (any == 0) continue;
+  // the tokens to their places, each warp its own in order: up to 32 of them, in the lanes `any`
+  auto place = [&](unsigned any, bool in, int64_t t, int r) {
     if (in) {
-      const int r = static_cast<int>(id - lo);
       const unsigned same = __match_any_sync(any, r);
-      const int before = __popc(same & ((1u << lane) - 1u));
-      const int at = start[r] + mine[r] + before;
-      sorted[at] = make_int2(static_cast<int>(t), static_cast<int>(id));
+      const int before = __popc(same & lower);
+      const int base = mine[r];
+      sorted[start[r] + base + before] = make_int2(static_cast<int>(t), (r << log2_ctas) + me);
       __syncwarp(any);
-      if (before == 0) mine[r] += __popc(same);
+      if (before == 0) mine[r] = base + __popc(same);
       __syncwarp(any);
     }
-  }
-  // the units' borders that fall into this range's part of the line
-  const int64_t len = row_weight * v + total;
-  for (int r = threadIdx.x; r < n; r += kSortThreads) {
-    const int64_t f = row_weight * (lo + r) + start[r];
-    const int c = start[r + 1] - start[r], items = c + row_weight;
-    if (items == 0) continue;
-    for (int64_t u = (f * units + len - 1) / len; u < units && u * len / units < f + items; ++u) {
-      const int off = static_cast<int>(u * len / units - f);
-      Border b;
-      b.pad = 0;
-      if (off == 0 || c <= kWhole) b = {static_cast<int32_t>(lo + r), start[r], 0, 0};
-      else if (off >= c) b = {static_cast<int32_t>(lo + r + 1), start[r + 1], 0, 0};
-      else b = {static_cast<int32_t>(lo + r), start[r] + off, 1, 0};
-      border[u] = b;
+  };
+  if (have <= kKept && seg <= 65536) {
+    for (int k = 0; k < have; k += 32) {
+      const bool in = k + lane < have;
+      const uint32_t x = in ? list[k + lane] : 0u;
+      place(__ballot_sync(0xFFFFFFFFu, in), in, t0 + (x >> 16), static_cast<int>(x & 0xFFFFu));
+    }
+  } else {
+    for (int64_t tb = t0; tb < t1; tb += 128) {
+      int id[4];
+      load(tb, id);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool in = id[j] >= 0 && (id[j] & mask) == me;
+        const unsigned any = __ballot_sync(0xFFFFFFFFu, in);
+        if (any) place(any, in, tb + 4 * lane + j, id[j] >> log2_ctas);
+      }
     }
   }
-  if (blockIdx.x == gridDim.x - 1)  // the end, and the borders of a line without items
-    for (int u = (len == 0 ? 0 : units) + threadIdx.x; u <= units; u += kSortThreads)
-      border[u] = {static_cast<int32_t>(v), total, 0, 0};
+  // the units' borders that fall into this CTA's part of the list
+  const int len = max((total + units - 1) / units, 1);
+  for (int u = (start[0] + len - 1) / len + threadIdx.x; u < units; u += kSortThreads) {
+    const int64_t at = static_cast<int64_t>(u) * len;
+    if (at >= start[n]) break;
+    int lo = 0, hi = n;  // the row that holds token `at`: start[lo] <= at < start[lo + 1]
+    while (hi - lo > 1) {
+      const int m = (lo + hi) / 2;
+      if (start[m] <= at) lo = m;
+      else hi = m;
+    }
+    const int s = start[lo], end = start[lo + 1];
+    border[u] = {(lo << log2_ctas) + me, end - s > kWhole ? static_cast<int>(at) : s, s, end};
+  }
+  if (blockIdx.x == gridDim.x - 1)  // borders past the last token
+    for (int u = (total + len - 1) / len + threadIdx.x; u <= units; u += kSortThreads)
+      border[u] = {v, total, total, total};
+  // the counters of rows that several units share
+  for (int r = warp; r < n; r += kSortWarps) {
+    const int s = start[r], e = start[r + 1];
+    if (e - s > kWhole && s / len != (e - 1) / len)
+      for (int i = lane; i < columns; i += 32) arrived[static_cast<int64_t>(s / len) * columns + i] = 0;
+  }
+  // rows without a token, a bit each
+  const int words = (range + 31) / 32;
+  for (int w = warp; w < words; w += kSortWarps) {
+    const int r = 32 * w + lane;
+    const unsigned bits = __ballot_sync(0xFFFFFFFFu, r < n && start[r + 1] == start[r]);
+    if (lane == 0) absent[static_cast<int64_t>(me) * words + w] = bits;
+  }
 }
 
 // ------------------------------------------------------------------ sum
 
 // blockDim (threads of a unit, units); blockIdx.y: slice of the columns. part: [unit][2][h] fp32
 // sums of rows that the unit does not hold whole: 0 a row begun before it, 1 one begun in it.
+// arrived: [unit a row is begun in][thread's columns], partials of the row that are written.
+// Blocks past the units' write the rows without a token (not where dE is accumulated into), a word of
+// `absent` each: they fill the memory's time while the units wait for their loads.
 template <typename T, int VEC>
-__global__ void __launch_bounds__(kThreads) vocab_embed_sum_kernel(
+__global__ void __launch_bounds__(kThreads, 4) vocab_embed_sum_kernel(
     const int2* __restrict__ sorted, const Border* __restrict__ border, const T* __restrict__ dx,
-    T* dE, float* __restrict__ part, int64_t h, int units, float scale, int accumulate) {
+    T* dE, float* part, int32_t* arrived, const uint32_t* __restrict__ absent, int64_t h, int units,
+    int unit_blocks, int columns, int log2_ctas, int words, float scale, int accumulate) {
   pdl_wait();  // the previous kernel's results are complete and visible
   pdl_trigger();
+  const int col = blockIdx.y * blockDim.x + threadIdx.x;
+  const int64_t c = static_cast<int64_t>(col) * VEC;
+  if (c >= h) return;
+  if (blockIdx.x >= unit_blocks) {
+    const unsigned w = blockIdx.x - unit_blocks;
+    const uint32_t bits = absent[w];
+    const int64_t first = static_cast<int64_t>(w % words * 32) << log2_ctas | w / words;
+    const float zero[VEC] = {};
+    for (int i = threadIdx.y; i < 32; i += blockDim.y)
+      if (bits >> i & 1u)
+        Vec<T, VEC>::store(dE + (first + (static_cast<int64_t>(i) << log2_ctas)) * h + c, zero);
+    return;
+  }
   const int u = blockIdx.x * blockDim.y + threadIdx.y;
-  const int64_t c = (static_cast<int64_t>(blockIdx.y) * blockDim.x + threadIdx.x) * VEC;
-  if (u >= units || c >= h) return;
+  if (u >= units) return;
   const Border b0 = border[u], b1 = border[u + 1];
+  const int total = border[units].tok;
   int row = b0.row;
-  bool lead = b0.mid != 0, any = false;
+  bool lead = b0.mid(), any = false;
   float acc[VEC];
   auto clear = [&]() {
 #pragma unroll
     for (int i = 0; i < VEC; ++i) acc[i] = 0.0f;
   };
-  auto partial = [&](int which) {
-    float* o = part + (static_cast<int64_t>(u) * 2 + which) * h + c;
+  auto write = [&]() {
+    T* o = dE + row * h + c;
+    float f[VEC], g[VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) o[i] = acc[i];
+    for (int i = 0; i < VEC; ++i) f[i] = acc[i] * scale;
+    if (accumulate) {
+      Vec<T, VEC> a;
+      a.load_rw(o);
+      a.get(g);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) f[i] += g[i];
+    }
+    Vec<T, VEC>::store(o, f);
+  };
+  auto part_at = [&](int unit, int which) { return part + (static_cast<int64_t>(unit) * 2 + which) * h + c; };
+  auto leave = [&](int which) {
+    float* p = part_at(u, which);
+    if constexpr (VEC >= 4) {
+#pragma unroll
+      for (int i = 0; i < VEC; i += 4)
+        __stcg(reinterpret_cast<float4*>(p + i), make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]));
+    } else {
+      __stcg(p, acc[0]);
+    }
   };
   auto flush = [&]() {  // the row's end
-    if (lead) {
-      partial(0);
-    } else if (any || !accumulate) {
-      T* o = dE + row * h + c;
-      float f[VEC], g[VEC];
-#pragma unroll
-      for (int i = 0; i < VEC; ++i) f[i] = acc[i] * scale;
-      if (accumulate) {
-        Vec<T, VEC> a;
-        a.load_rw(o);
-        a.get(g);
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) f[i] += g[i];
-      }
-      Vec<T, VEC>::store(o, f);
-    }
+    if (lead) leave(0);
+    else if (any) write();
     lead = any = false;
     clear();
-  };
-  auto zeros = [&](int from, int to) {  // rows without a token
-    if (accumulate) return;
-    for (int r = from; r < to; ++r) Vec<T, VEC>::store(dE + r * h + c, acc);
   };
   clear();
   for (int k = b0.tok; k < b1.tok; k += kInFlight) {
@@ -309,7 +399,6 @@ __global__ void __launch_bounds__(kThreads) vocab_embed_sum_kernel(
       if (r[i] < 0) break;
       if (r[i] != row) {
         flush();
-        zeros(row + 1, r[i]);
         row = r[i];
       }
       float f[VEC];
@@ -319,60 +408,35 @@ __global__ void __launch_bounds__(kThreads) vocab_embed_sum_kernel(
       any = true;
     }
   }
-  if (row < b1.row) {
-    flush();
-    zeros(row + 1, b1.row);
-  } else if (b1.mid) {
-    partial(lead ? 0 : 1);
-  }
-}
-
-// ------------------------------------------------------------------ join
-
-// Rows begun in a unit and ended in a later one: partial 1 of the unit, then partials 0 of the
-// following ones up to the row's end. A CTA takes (row, 32 columns); eight warps share the
-// partials, the warps' sums are added in order.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) vocab_embed_join_kernel(
-    const Border* __restrict__ border, const float* __restrict__ part, T* dE, int64_t h, int units,
-    float scale, int accumulate) {
-  pdl_wait();  // the previous kernel's results are complete and visible
-  pdl_trigger();
-  __shared__ float sm[kThreads / 32][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t slices = (h + 31) / 32;
-  for (int u = blockIdx.x; u < units; u += gridDim.x) {
-    const Border b0 = border[u], b1 = border[u + 1];
-    if (!b1.mid || (b0.mid && b0.row == b1.row)) continue;  // no row is begun here and left open
-    int last = u + 1;  // the last unit with tokens of the row
-    while (last + 1 < units && border[last + 1].mid && border[last + 1].row == b1.row) ++last;
-    for (int64_t sl = blockIdx.y; sl < slices; sl += gridDim.y) {
-      const int64_t c = sl * 32 + lane;
-      float a = 0.0f;
-      if (c < h) {
+  const bool open = b1.mid() && row == b1.row;
+  if (open) leave(lead ? 0 : 1);
+  else if (any) flush();
+  // the rows left in parts, the one begun before this unit and the one left open: whoever leaves a
+  // row's last part in these columns adds them up
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    if (which == 0 ? !b0.mid() : !open || (b0.mid() && b0.row == b1.row)) continue;
+    const Border& b = which == 0 ? b0 : b1;
+    const int len = (total + units - 1) / units, first = b.start / len, last = (b.end - 1) / len;
+    __threadfence();
+    if (atomicAdd(arrived + static_cast<int64_t>(first) * columns + col, 1) != last - first) continue;
+    __threadfence();
+    clear();
 #pragma unroll 4
-        for (int k = u + warp; k <= last; k += kThreads / 32)
-          a += part[(static_cast<int64_t>(k) * 2 + (k == u ? 1 : 0)) * h + c];
-      }
-      __syncthreads();
-      sm[warp][lane] = a;
-      __syncthreads();
-      if (warp == 0 && c < h) {
-        a = 0.0f;
+    for (int k = first; k <= last; ++k) {
+      const float* p = part_at(k, k == first ? 1 : 0);
+      if constexpr (VEC >= 4) {
 #pragma unroll
-        for (int w = 0; w < kThreads / 32; ++w) a += sm[w][lane];
-        T* o = dE + b1.row * h + c;
-        float f = a * scale;
-        if (accumulate) {
-          float g;
-          Vec<T, 1> old;
-          old.load_rw(o);
-          old.get(&g);
-          f += g;
+        for (int i = 0; i < VEC; i += 4) {
+          const float4 f = __ldcg(reinterpret_cast<const float4*>(p + i));
+          acc[i] += f.x; acc[i + 1] += f.y; acc[i + 2] += f.z; acc[i + 3] += f.w;
         }
-        Vec<T, 1>::store(o, &f);
+      } else {
+        acc[0] += __ldcg(p);
       }
     }
+    row = b.row;
+    write();
   }
 }
 
@@ -380,8 +444,9 @@ __global__ void __launch_bounds__(kThreads) vocab_embed_join_kernel(
 
 struct SumPlan {
   int vec, tx, ty, slices;  // elements per thread, threads of a unit, units of a CTA, column slices
-  int units;
-  size_t sorted, border, part, total;
+  int units, columns;       // columns: threads that share a row
+  int log2_ctas, range;     // of the sort
+  size_t sorted, border, arrived, absent, part, total;
 };
 SumPlan sum_plan(int64_t M, int64_t v, int64_t h, tp_dtype dt) {
   SumPlan P{};
@@ -392,12 +457,19 @@ SumPlan sum_plan(int64_t M, int64_t v, int64_t h, tp_dtype dt) {
   while (P.tx < kThreads && P.tx < nv) P.tx *= 2;
   P.ty = kThreads / P.tx;
   P.slices = static_cast<int>((nv + P.tx - 1) / P.tx);
-  // four CTAs per SM at once (152 SMs), but no unit of fewer than 16 items
-  const int64_t most = std::max<int64_t>(4 * 152 / P.slices, 1) * P.ty;
-  P.units = static_cast<int>(std::max<int64_t>(std::min(most, (M + v) / 16), 1));
+  // more than the CTAs that run at once: rows end in some units and not in others
+  P.units = static_cast<int>(std::clamp<int64_t>(M / kUnitTokens, 1, kMaxUnits));
   size_t o = 0;
   P.sorted = o; o += align_up(M * sizeof(int2), 256);
   P.border = o; o += align_up((P.units + 1) * sizeof(Border), 256);
+  P.columns = P.tx * P.slices;
+  // 128 sorting CTAs (one per SM, of 152), fewer where they would have less than 32 rows each, more
+  // where their counters would not fit in shared memory
+  while ((P.log2_ctas < 7 && v >> P.log2_ctas > 32) || (v - 1) >> P.log2_ctas >= kMaxRange)
+    ++P.log2_ctas;
+  P.range = static_cast<int>((v - 1) >> P.log2_ctas) + 1;
+  P.absent = o; o += align_up((static_cast<size_t>((P.range + 31) / 32) << P.log2_ctas) * 4, 256);
+  P.arrived = o; o += align_up(static_cast<size_t>(P.units) * P.columns * 4, 256);
   P.part = o;   o += align_up(static_cast<size_t>(P.units) * 2 * h * 4, 256);
   P.total = o;
   return P;
@@ -419,20 +491,16 @@ tp_status embed_fwd(const int32_t* ids, const void* E, void* x, int64_t M, int64
 template <typename T, int VEC>
 tp_status embed_sum(const SumPlan& P, const void* dx, void* dE, int64_t h, float scale,
                     bool accumulate, char* ws, cudaStream_t st) {
-  const Border* border = reinterpret_cast<const Border*>(ws + P.border);
-  float* part = reinterpret_cast<float*>(ws + P.part);
+  const int words = (P.range + 31) / 32, unit_blocks = (P.units + P.ty - 1) / P.ty;
+  const int64_t blocks = unit_blocks + (accumulate ? 0 : static_cast<int64_t>(words) << P.log2_ctas);
   TP_CUDA_TRY(launch_kernel(
       vocab_embed_sum_kernel<T, VEC>,
-      dim3(static_cast<unsigned>((P.units + P.ty - 1) / P.ty), static_cast<unsigned>(P.slices)),
-      dim3(P.tx, P.ty), 0, st, reinterpret_cast<const int2*>(ws + P.sorted), border,
-      static_cast<const T*>(dx), static_cast<T*>(dE), part, h, P.units, scale, accumulate ? 1 : 0));
+      dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(P.slices)), dim3(P.tx, P.ty), 0, st,
+      reinterpret_cast<const int2*>(ws + P.sorted), reinterpret_cast<const Border*>(ws + P.border),
+      static_cast<const T*>(dx), static_cast<T*>(dE), reinterpret_cast<float*>(ws + P.part),
+      reinterpret_cast<int32_t*>(ws + P.arrived), reinterpret_cast<const uint32_t*>(ws + P.absent), h,
+      P.units, unit_blocks, P.columns, P.log2_ctas, words, scale, accumulate ? 1 : 0));
   count_launch();
-  if (P.units > 1) {
-    const unsigned gx = static_cast<unsigned>(std::min(P.units, 608));
-    TP_CUDA_TRY(launch_kernel(vocab_embed_join_kernel<T>, dim3(gx, 4), kThreads, 0, st, border, part,
-                              static_cast<T*>(dE), h, P.units, scale, accumulate ? 1 : 0));
-    count_launch();
-  }
   return TP_OK;
 }
 
@@ -457,21 +525,20 @@ tp_status launch_vocab_embed_scaled_bwd(const int32_t* ids, const void* dx, void
                                         tp_dtype dt, void* ws, cudaStream_t st) {
   const SumPlan P = sum_plan(M, v, h, dt);
   char* base = static_cast<char*>(ws);
-  // at most one CTA per SM, and no range of fewer than 32 rows
-  const int64_t ctas = std::min<int64_t>((v + 31) / 32, 152);
-  const int range = static_cast<int>(std::min<int64_t>((v + ctas - 1) / ctas, kMaxRange));
-  const size_t smem = (static_cast<size_t>(kSortWarps) * range + range + 1) * 4;
+  const size_t smem = (static_cast<size_t>(kSortWarps) * (P.range + kKept) + P.range + 1) * 4;
   static std::atomic<uint64_t> attr_set{0};
   if (needs_setup(attr_set)) {
     TP_CUDA_TRY(cudaFuncSetAttribute(vocab_embed_sort_kernel,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (kSortWarps * kMaxRange + kMaxRange + 1) * 4));
+                                     (kSortWarps * (kMaxRange + kKept) + kMaxRange + 1) * 4));
     mark_device(attr_set);
   }
-  TP_CUDA_TRY(launch_kernel(vocab_embed_sort_kernel, static_cast<unsigned>((v + range - 1) / range),
-                            kSortThreads, smem, st, ids, reinterpret_cast<int2*>(base + P.sorted),
-                            reinterpret_cast<Border*>(base + P.border), M, v, range, P.units,
-                            accumulate ? 0 : 1));
+  TP_CUDA_TRY(launch_kernel(vocab_embed_sort_kernel, 1u << P.log2_ctas, kSortThreads, smem, st, ids,
+                            reinterpret_cast<int2*>(base + P.sorted),
+                            reinterpret_cast<Border*>(base + P.border),
+                            reinterpret_cast<int32_t*>(base + P.arrived),
+                            reinterpret_cast<uint32_t*>(base + P.absent), static_cast<int32_t>(M),
+                            static_cast<int32_t>(v), P.log2_ctas, P.range, P.units, P.columns));
   count_launch();
   if (dt == TP_BF16)
     return P.vec == 8 ? embed_sum<__nv_bfloat16, 8>(P, dx, dE, h, scale, accumulate, base, st)

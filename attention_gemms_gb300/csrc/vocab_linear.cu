@@ -20,8 +20,9 @@
 namespace tp {
 namespace {
 
-constexpr int kRows = 32;         // rows of a CTA of the join: one per lane
+constexpr int kRows = 8;          // rows of a CTA of the join at the least
 constexpr int kJoinThreads = 1024;
+constexpr int64_t kSms = 152;
 constexpr int kSumShards = 8;     // shards whose losses the join adds up itself
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -33,9 +34,12 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
   m = mm;
 }
 
-// A CTA joins 32 rows: warp w the slots w, w + 32, ..., then warp 0 the warps in order. The CTA
-// that ends last adds the losses up (in the rows' order of CTAs, so the sum does not depend on
-// which one that is): a launch less than a kernel of its own.
+// A CTA joins ROWS rows: its 1024 threads, consecutive ones on consecutive rows, share the slots,
+// warps join by shuffles and warp 0 joins the warps in order. The CTA that ends last adds the losses
+// up (in the order of the CTAs' rows, so the sum does not depend on which one that is): a launch
+// less than a kernel of its own. 32 rows where that gives every SM a CTA (8192 rows x 197 slots: 8
+// us, 11 with 8 rows), else 8 (37 rows x 393 slots: 5 us against 8).
+template <int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) vocab_linear_join_kernel(
     const float2* __restrict__ part, const float* __restrict__ hit,
     const int32_t* __restrict__ targets, float* __restrict__ lse, float* __restrict__ row_loss,
@@ -43,25 +47,29 @@ __global__ void __launch_bounds__(kJoinThreads) vocab_linear_join_kernel(
     int slots, int64_t M, int64_t v, int N) {
   pdl_wait();  // the previous kernel's results are complete and visible
   pdl_trigger();
-  __shared__ float2 sm[32][kRows];
+  __shared__ float2 sm[32][32];
   __shared__ int last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + lane;
+  const int mine = lane % ROWS;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + mine;
   float m = -INFINITY, s = 0.0f;
   if (row < M) {
 #pragma unroll 4
-    for (int i = warp; i < slots; i += 32) {
+    for (int i = threadIdx.x / ROWS; i < slots; i += kJoinThreads / ROWS) {
       const float2 p = part[i * M + row];
       join(m, s, p.x, p.y);
     }
   }
+#pragma unroll
+  for (int o = ROWS; o < 32; o *= 2)
+    join(m, s, __shfl_xor_sync(0xFFFFFFFFu, m, o), __shfl_xor_sync(0xFFFFFFFFu, s, o));
   sm[warp][lane] = make_float2(m, s);
   __syncthreads();
   if (warp == 0) {
     for (int w = 1; w < 32; ++w) join(m, s, sm[w][lane].x, sm[w][lane].y);
     float l = 0.0f;
     int64_t t = -1;
-    if (row < M) {
+    if (row < M && lane < ROWS) {
       const float z = (m + log2f(s)) * kLn2;
       t = targets[row];
       if (t >= 0 && t < v) l = z - hit[row];
@@ -128,7 +136,6 @@ FwdLayout fwd_layout(int64_t M, int64_t v) {
 
 // ---- backward: q of one piece, and (bf16) the fp32 sums of dx where one product does not make it
 constexpr int64_t kPieceBytes = 512ll << 20;
-constexpr int64_t kSms = 152;
 struct BwdPlan {
   int64_t piece;  // vocabulary entries of a piece, whole 256-column tiles; also q's pitch
   int pieces;
@@ -136,6 +143,27 @@ struct BwdPlan {
   bool direct;    // dx leaves one product: no partials
   size_t q, dx, total;
 };
+// Parts of dx's sum over a piece, where its tiles alone would leave SMs idle: the number that
+// takes the least time, whole waves of the tiles (256 x 256 on an SM pair, 128 x 128 on an SM where
+// there are fewer than 256 rows) against the fp32 partials written and read.
+int dx_groups(int64_t M, int64_t h, int64_t piece) {
+  const int64_t tw = M >= 256 ? 256 : 128, at_once = M >= 256 ? kSms / 2 : kSms;
+  const int64_t tiles = (M + tw - 1) / tw * ((h + tw - 1) / tw);
+  if (tiles >= 2 * at_once) return 1;
+  int best = 1;
+  double least = 0.0;
+  for (int g = 1; g <= 32 && (g == 1 || piece / g >= 512); ++g) {
+    const double waves = static_cast<double>((tiles * g + at_once - 1) / at_once);
+    // seconds: a wave's products at 1.7e15 / (152 SMs), the partials at 5e12 bytes
+    const double t = waves * (2.0 * tw * tw * (piece / g)) * at_once / 1.7e15 +
+                     (g > 1 ? g * M * h * 8.0 / 5e12 : 0.0);
+    if (g == 1 || t < least) {
+      best = g;
+      least = t;
+    }
+  }
+  return best;
+}
 BwdPlan bwd_plan(int64_t M, int64_t v, int64_t h, tp_dtype dt) {
   BwdPlan P{};
   const int64_t e = static_cast<int64_t>(elem_size(dt));
@@ -143,14 +171,7 @@ BwdPlan bwd_plan(int64_t M, int64_t v, int64_t h, tp_dtype dt) {
   const int64_t n = (v + most - 1) / most;
   P.piece = ((v + n - 1) / n + 255) / 256 * 256;
   P.pieces = static_cast<int>((v + P.piece - 1) / P.piece);
-  P.groups = 1;
-  if (dt == TP_BF16) {
-    // few tiles of dx: the piece's vocabulary is split, so that the SMs share its sum
-    const int64_t tw = M >= 256 ? 256 : 128;
-    const int64_t tiles = (M + tw - 1) / tw * ((h + tw - 1) / tw) * (tw / 128);
-    if (tiles * 2 <= kSms)
-      P.groups = static_cast<int>(std::min<int64_t>((kSms + tiles - 1) / tiles, (P.piece + 511) / 512));
-  }
+  P.groups = dt == TP_BF16 ? dx_groups(M, h, P.piece) : 1;
   P.direct = dt != TP_BF16 || (P.pieces == 1 && P.groups == 1);
   P.q = a256(M * P.piece * e);
   P.dx = P.direct ? 0 : a256(static_cast<size_t>(P.groups) * M * h * sizeof(float));
@@ -192,9 +213,11 @@ tp_status launch_vocab_linear_ce_fwd(const void* x, const void* E, const int32_t
   d.ce.counter = counter;
   d.ce.slots = &slots;
   TP_TRY(product(d, st));
-  TP_CUDA_TRY(launch_kernel(vocab_linear_join_kernel, static_cast<unsigned>((M + kRows - 1) / kRows),
-                            kJoinThreads, 0, st, d.ce.part, hit, targets, lse, row_loss, shard_loss,
-                            loss, reinterpret_cast<float*>(base + L.cta), counter, slots, M, v, N));
+  const int rows = M >= 32 * kSms ? 32 : kRows;
+  TP_CUDA_TRY(launch_kernel(rows == 32 ? vocab_linear_join_kernel<32> : vocab_linear_join_kernel<kRows>,
+                            static_cast<unsigned>((M + rows - 1) / rows), kJoinThreads, 0, st,
+                            d.ce.part, hit, targets, lse, row_loss, shard_loss, loss,
+                            reinterpret_cast<float*>(base + L.cta), counter, slots, M, v, N));
   count_launch();
   return N > kSumShards ? launch_vocab_ce_loss(row_loss, targets, shard_loss, loss, M, v, N, st)
                         : TP_OK;
