@@ -100,25 +100,56 @@ __device__ __forceinline__ void lse_rows(const SimtParams& p, const float* sm, i
   }
 }
 
+// A and B staging; reused for the partial tile of a split (unpaired only: TM x TN fits)
+constexpr int simt_floats(bool paired) { return TK * (TM + 4) + (paired ? 2 : 1) * TK * (TN + 4); }
+static_assert(simt_floats(false) >= TM * TN, "partial tile must fit the staging buffers");
+
+// row slice `rank` of the tile: the cluster's partial tiles added in rank order, four columns at a
+// time, every load of a thread in flight at once; put(row of the tile, column, sum)
+template <int SPLIT, class F>
+__device__ __forceinline__ void add_partials(const float* sm, int rank, F&& put) {
+  constexpr int rows = TM / SPLIT, kVecs = rows * TN / 4 / 256;  // 2, 1 and (8 ranks) half a vector
+  float4 v[kVecs > 0 ? kVecs : 1][SPLIT];
+#pragma unroll
+  for (int i = 0; i < (kVecs > 0 ? kVecs : 1); ++i) {
+    const int e = (threadIdx.x + i * 256) * 4;
+    if (e < rows * TN) {
+      const uint32_t off = smem_u32(sm + rank * rows * TN + e);
+#pragma unroll
+      for (int q = 0; q < SPLIT; ++q) v[i][q] = ld_cluster_v4(mapa_shared(off, static_cast<uint32_t>(q)));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < (kVecs > 0 ? kVecs : 1); ++i) {
+    const int e = (threadIdx.x + i * 256) * 4;
+    if (e < rows * TN) {
+      float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int q = 0; q < SPLIT; ++q) {
+        a.x += v[i][q].x; a.y += v[i][q].y; a.z += v[i][q].z; a.w += v[i][q].w;
+      }
+      const int rr = rank * rows + e / TN, cc = e % TN;
+      put(rr, cc, a.x);
+      put(rr, cc + 1, a.y);
+      put(rr, cc + 2, a.z);
+      put(rr, cc + 3, a.w);
+    }
+  }
+}
+
+// Output tile (bx, by) of group g; sm: simt_floats(PAIRED) floats of shared memory
 template <int EPI, bool PAIRED>
-__global__ void __launch_bounds__(256) gemm_simt_kernel(const SimtParams p) {
-  pdl_wait();  // the previous kernel's results are complete and visible
-  pdl_trigger();
+__device__ __forceinline__ void simt_tile(const SimtParams& p, int bx, int by, int g, float* sm) {
   constexpr int NB = PAIRED ? 2 : 1;
-  // A and B staging; reused for the partial tile of a split (unpaired only: TM x TN fits)
-  constexpr int kFloats = TK * (TM + 4) + NB * TK * (TN + 4);
-  static_assert(PAIRED || kFloats >= TM * TN, "partial tile must fit the staging buffers");
-  __shared__ __align__(16) float sm[kFloats];
   auto As = reinterpret_cast<float(*)[TM + 4]>(sm);
   auto Bs = reinterpret_cast<float(*)[TK][TN + 4]>(sm + TK * (TM + 4));
   const int split = p.split;
   const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;  // blockIdx.x % split
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.y) * TM;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x / split) * TN;
-  const int g = blockIdx.z;
+  const int64_t m0 = static_cast<int64_t>(by) * TM;
+  const int64_t n0 = static_cast<int64_t>(bx) * TN;
   if constexpr (EPI == EPI_LSE) {
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.ce.counter = 0;
+    if (bx == 0 && by == 0 && rank == 0 && threadIdx.x == 0) *p.ce.counter = 0;
   }
   float acc[4][4] = {}, acc2[4][4] = {};
   float ra[kPer], rb[NB][kPer];
@@ -223,15 +254,14 @@ __global__ void __launch_bounds__(256) gemm_simt_kernel(const SimtParams p) {
       for (int j = 0; j < 4; ++j) sm[(ty * 4 + i) * TN + tx * 4 + j] = acc[i][j];
     cluster_sync_all();  // every CTA's partial tile is in its shared memory
     const int rows = TM / split;
-    for (int e = threadIdx.x; e < rows * TN; e += 256) {
-      const int rr = rank * rows + e / TN, cc = e % TN;
-      const uint32_t off = smem_u32(sm + rr * TN + cc);
-      float v = 0.0f;
-      for (int q = 0; q < split; ++q) v += ld_cluster_f32(mapa_shared(off, static_cast<uint32_t>(q)));
+    auto put = [&](int rr, int cc, float v) {
       const int64_t r = m0 + rr, c = n0 + cc;
       if constexpr (EPI == EPI_LSE) sm[rr * TN + cc] = v;  // read by this thread alone
       else if (r < p.M && c < p.N) epi1<EPI>(p, g, r, c, v, 0.0f);
-    }
+    };
+    if (split == 2) add_partials<2>(sm, rank, put);
+    else if (split == 4) add_partials<4>(sm, rank, put);
+    else add_partials<8>(sm, rank, put);
     if constexpr (EPI == EPI_LSE) {
       __syncthreads();
       lse_rows(p, sm + rank * rows * TN, rows, m0 + rank * rows, n0, n0 / TN);
@@ -240,9 +270,29 @@ __global__ void __launch_bounds__(256) gemm_simt_kernel(const SimtParams p) {
   }
 }
 
+template <int EPI, bool PAIRED>
+__global__ void __launch_bounds__(256) gemm_simt_kernel(const SimtParams p) {
+  pdl_wait();  // the previous kernel's results are complete and visible
+  pdl_trigger();
+  __shared__ __align__(16) float sm[simt_floats(PAIRED)];
+  simt_tile<EPI, PAIRED>(p, blockIdx.x / p.split, blockIdx.y, blockIdx.z, sm);
+}
+
+// Two plain products that do not depend on one another, the second's tiles after the first's: one
+// launch instead of two, which at small sizes is most of their time. Both are split alike.
+__global__ void __launch_bounds__(256)
+    gemm_simt_two_kernel(const SimtParams p0, const SimtParams p1, int tiles0, int gx0, int gx1) {
+  pdl_wait();  // the previous kernel's results are complete and visible
+  pdl_trigger();
+  __shared__ __align__(16) float sm[simt_floats(false)];
+  const int t = blockIdx.x / p0.split;  // a cluster's CTAs share a tile
+  if (t < tiles0) simt_tile<EPI_STORE, false>(p0, t % gx0, t / gx0, 0, sm);
+  else simt_tile<EPI_STORE, false>(p1, (t - tiles0) % gx1, (t - tiles0) / gx1, 0, sm);
+}
+
 // Whether the device can place a cluster of `split` CTAs of this kernel: asked once per
 // device and cluster size (cudaOccupancyMaxActiveClusters), before the first launch.
-template <int EPI, bool PAIRED>
+template <auto kKernel>
 bool cluster_fits(int split) {
   static std::atomic<int> known[64][4];  // 0 unknown, 1 fits, 2 does not
   const int slot = split == 2 ? 0 : split == 4 ? 1 : split == 8 ? 2 : 3;
@@ -260,43 +310,53 @@ bool cluster_fits(int split) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  const bool fits = cudaOccupancyMaxActiveClusters(&n, gemm_simt_kernel<EPI, PAIRED>, &cfg) ==
+  const bool fits = cudaOccupancyMaxActiveClusters(&n, kKernel, &cfg) ==
                         cudaSuccess && n > 0;
   if (!fits) cudaGetLastError();  // the query's own error, not a launch's
   if (dev >= 0) known[dev][slot].store(fits ? 1 : 2);
   return fits;
 }
 
-template <int EPI, bool PAIRED>
-cudaError_t launch_k(const SimtParams& p, dim3 grid, cudaStream_t st) {
-  if (p.split == 1 || !cluster_fits<EPI, PAIRED>(p.split)) {
-    // unsplit: one CTA per tile (also when the device cannot place the cluster)
-    SimtParams q = p;
-    q.split = 1;
-    return launch_kernel(gemm_simt_kernel<EPI, PAIRED>, grid, 256, 0, st, q);
-  }
+// `grid` without the split, which multiplies its x and is the cluster's size
+template <auto kKernel, typename... Args>
+cudaError_t launch_split(int split, dim3 grid, cudaStream_t st, const Args&... args) {
+  if (split == 1) return launch_kernel(kKernel, grid, 256, 0, st, args...);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(p.split);
+  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see launch_kernel
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(grid.x * static_cast<unsigned>(p.split), grid.y, grid.z);
+  cfg.gridDim = dim3(grid.x * static_cast<unsigned>(split), grid.y, grid.z);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, gemm_simt_kernel<EPI, PAIRED>, p);
+  return cudaLaunchKernelEx(&cfg, kKernel, args...);
 }
 
-}  // namespace
+template <int EPI, bool PAIRED>
+cudaError_t launch_k(SimtParams p, dim3 grid, cudaStream_t st) {
+  // unsplit: one CTA per tile (also when the device cannot place the cluster)
+  if (p.split > 1 && !cluster_fits<gemm_simt_kernel<EPI, PAIRED>>(p.split)) p.split = 1;
+  return launch_split<gemm_simt_kernel<EPI, PAIRED>>(p.split, grid, st, p);
+}
 
-tp_status launch_gemm_simt(const GemmDesc& d, cudaStream_t st) {
-  if (d.M <= 0 || d.N <= 0 || d.K <= 0) return TP_OK;
+// split K over a cluster while the tiles (times the split) stay within half the SMs and every CTA
+// keeps at least one K step: at these sizes a K step is a global-load latency, so fewer steps per
+// CTA is a shorter launch
+int simt_split(int64_t tiles, int64_t ksteps) {
+  int split = 1;
+  while (split < 8 && tiles * split * 4 <= device_sm_count() && ksteps >= 2 * split) split *= 2;
+  return split;
+}
+
+int64_t simt_ksteps(const GemmDesc& d) { return (d.K + TK - 1) / TK * d.nseg; }
+
+SimtParams simt_params(const GemmDesc& d) {
   SimtParams p{};
-  if (d.nseg < 1 || d.nseg > 3) return fail(TP_ERR_INVALID_ARG, "1 to 3 K segments");
   for (int s = 0; s < 3; ++s) {
     const int sa = s < d.nseg ? s : 0;
     const int sb = s < (d.paired ? 2 : d.nseg) ? s : 0;
@@ -322,19 +382,21 @@ tp_status launch_gemm_simt(const GemmDesc& d, cudaStream_t st) {
   p.ldo = d.ldo;
   p.out_group_stride = d.out_group_stride;
   p.ce = d.ce;
+  return p;
+}
+
+}  // namespace
+
+tp_status launch_gemm_simt(const GemmDesc& d, cudaStream_t st) {
+  if (d.M <= 0 || d.N <= 0 || d.K <= 0) return TP_OK;
+  if (d.nseg < 1 || d.nseg > 3) return fail(TP_ERR_INVALID_ARG, "1 to 3 K segments");
+  SimtParams p = simt_params(d);
   const int64_t gx = (d.N + TN - 1) / TN, gy = (d.M + TM - 1) / TM;
   if (gx > 2147483647ll || gy > 65535 || d.groups > 65535)
     return fail(TP_ERR_SHAPE, "fp32 GEMM grid too large");
   dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy), static_cast<unsigned>(d.groups));
   const bool pr = d.paired;
-  // split K over a cluster while the tiles (times the split) stay within half the SMs
-  // and every CTA keeps at least one K step: at these sizes a K step is a global-load
-  // latency, so fewer steps per CTA is a shorter launch
-  const int64_t tiles = gx * gy * d.groups, ksteps = (d.K + TK - 1) / TK * d.nseg;
-  p.split = 1;
-  while (!pr && p.split < 8 && tiles * p.split * 4 <= device_sm_count() &&
-         ksteps >= 2 * p.split)
-    p.split *= 2;
+  p.split = pr ? 1 : simt_split(gx * gy * d.groups, simt_ksteps(d));
   cudaError_t e = cudaSuccess;
   switch (d.epi) {
     case EPI_STORE: e = launch_k<EPI_STORE, false>(p, grid, st); break;
@@ -356,6 +418,28 @@ tp_status launch_gemm_simt(const GemmDesc& d, cudaStream_t st) {
     case EPI_DCE: e = launch_k<EPI_DCE, false>(p, grid, st); break;
     default: return fail(TP_ERR_INVALID_ARG, "unknown epilogue");
   }
+  count_launch();
+  TP_CUDA_TRY(e);
+  return TP_OK;
+}
+
+tp_status launch_gemm_simt_two(const GemmDesc& a, const GemmDesc& b, cudaStream_t st) {
+  const int64_t gxa = (a.N + TN - 1) / TN, gya = (a.M + TM - 1) / TM;
+  const int64_t gxb = (b.N + TN - 1) / TN, gyb = (b.M + TM - 1) / TM;
+  const int64_t tiles = gxa * gya + gxb * gyb;
+  if (tiles > device_sm_count()) {  // not the launches, but the tiles take the time
+    if (a.out[0]) TP_TRY(launch_gemm_simt(a, st));
+    return b.out[0] ? launch_gemm_simt(b, st) : TP_OK;
+  }
+  SimtParams pa = simt_params(a), pb = simt_params(b);
+  // by the longer sum (CTAs that the shorter one has no steps for add nothing)
+  int split = simt_split(tiles, std::max(simt_ksteps(a), simt_ksteps(b)));
+  if (split > 1 && !cluster_fits<gemm_simt_two_kernel>(split)) split = 1;
+  pa.split = pb.split = split;
+  const int64_t ta = a.out[0] ? gxa * gya : 0, tb = b.out[0] ? gxb * gyb : 0;
+  const cudaError_t e = launch_split<gemm_simt_two_kernel>(
+      split, static_cast<unsigned>(ta + tb), st, pa, pb, static_cast<int>(ta),
+      static_cast<int>(gxa), static_cast<int>(gxb));
   count_launch();
   TP_CUDA_TRY(e);
   return TP_OK;

@@ -192,6 +192,9 @@ tp_status launch_gemm_tc(const GemmDesc& d, cudaStream_t st);    // bf16, tcgen0
 bool gemv_eligible(const GemmDesc& d);                             // bf16, M <= 4
 tp_status launch_gemv(const GemmDesc& d, cudaStream_t st);
 tp_status launch_gemm_simt(const GemmDesc& d, cudaStream_t st);  // fp32, CUDA cores
+// two independent fp32 products (EPI_STORE, one segment, one group), in one launch if both are
+// small; one without an output is left out, and the other is the same bit for bit
+tp_status launch_gemm_simt_two(const GemmDesc& a, const GemmDesc& b, cudaStream_t st);
 // blocks_per_sm: CTAs of 256 threads per SM of the grid-stride grid (8 saturates HBM
 // alone; 2 leaves room on every SM for a persistent GEMM CTA running beside it).
 // group_stride: elements from one shard's partial to the next (0: M * n), so that a

@@ -35,9 +35,9 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
 }
 
 // A CTA joins ROWS rows: its 1024 threads, consecutive ones on consecutive rows, share the slots,
-// warps join by shuffles and warp 0 joins the warps in order. The CTA that ends last adds the losses
-// up (in the order of the CTAs' rows, so the sum does not depend on which one that is): a launch
-// less than a kernel of its own. 32 rows where that gives every SM a CTA (8192 rows x 197 slots: 8
+// shuffles join a warp's, and a warp per row joins the warps'. The CTA that ends last adds the CTAs'
+// losses up (in an order of their own, whichever CTA that is): a launch less than a kernel of its
+// own. 32 rows where that gives every SM a CTA (8192 rows x 197 slots: 8
 // us, 11 with 8 rows), else 8 (37 rows x 393 slots: 5 us against 8).
 template <int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) vocab_linear_join_kernel(
@@ -47,12 +47,18 @@ __global__ void __launch_bounds__(kJoinThreads) vocab_linear_join_kernel(
     int slots, int64_t M, int64_t v, int N) {
   pdl_wait();  // the previous kernel's results are complete and visible
   pdl_trigger();
-  __shared__ float2 sm[32][32];
+  __shared__ float2 sm[32][ROWS];
+  __shared__ float sum[kSumShards];
   __shared__ int last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int mine = lane % ROWS;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + mine;
+  // the warp that ends row `warp` of the CTA: its target and its target's logit
+  const int64_t own = static_cast<int64_t>(blockIdx.x) * ROWS + warp;
+  const bool ends = warp < ROWS && own < M;
+  int64_t t = ends ? targets[own] : -1;
+  if (t >= v) t = -1;
+  const float at = t >= 0 ? hit[own] : 0.0f;
   float m = -INFINITY, s = 0.0f;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + lane % ROWS;
   if (row < M) {
 #pragma unroll 4
     for (int i = threadIdx.x / ROWS; i < slots; i += kJoinThreads / ROWS) {
@@ -63,54 +69,66 @@ __global__ void __launch_bounds__(kJoinThreads) vocab_linear_join_kernel(
 #pragma unroll
   for (int o = ROWS; o < 32; o *= 2)
     join(m, s, __shfl_xor_sync(0xFFFFFFFFu, m, o), __shfl_xor_sync(0xFFFFFFFFu, s, o));
-  sm[warp][lane] = make_float2(m, s);
+  if (lane < ROWS) sm[warp][lane] = make_float2(m, s);
+  if (threadIdx.x < kSumShards) sum[threadIdx.x] = 0.0f;
   __syncthreads();
-  if (warp == 0) {
-    for (int w = 1; w < 32; ++w) join(m, s, sm[w][lane].x, sm[w][lane].y);
-    float l = 0.0f;
-    int64_t t = -1;
-    if (row < M && lane < ROWS) {
-      const float z = (m + log2f(s)) * kLn2;
-      t = targets[row];
-      if (t >= 0 && t < v) l = z - hit[row];
-      else t = -1;
-      lse[row] = z;
-      row_loss[row] = l;
-    }
-    if (N <= kSumShards) {
-      const int64_t vs = v / N;
-      for (int i = 0; i < N; ++i) {
-        float a = t >= i * vs && t < (i + 1) * vs ? l : 0.0f;
+  float l = 0.0f;
+  if (warp < ROWS) {
+    m = sm[lane][warp].x;
+    s = sm[lane][warp].y;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-        if (lane == 0) cta_loss[static_cast<int64_t>(blockIdx.x) * N + i] = a;
-      }
-      if (lane == 0) {
-        __threadfence();
-        last = atomicAdd(counter, 1) == static_cast<int>(gridDim.x) - 1;
-      }
+    for (int o = 16; o > 0; o >>= 1)
+      join(m, s, __shfl_xor_sync(0xFFFFFFFFu, m, o), __shfl_xor_sync(0xFFFFFFFFu, s, o));
+    const float z = (m + log2f(s)) * kLn2;
+    l = t >= 0 ? z - at : 0.0f;
+    if (ends && lane == 0) {
+      lse[own] = z;
+      row_loss[own] = l;
     }
   }
   if (N > kSumShards) return;
+  __shared__ float losses[ROWS];
+  __shared__ int shard[ROWS];
+  if (warp < ROWS && lane == 0) {
+    losses[warp] = l;
+    shard[warp] = t >= 0 ? static_cast<int>(t / (v / N)) : -1;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    for (int i = 0; i < N; ++i) {
+      float a = lane < ROWS && shard[lane % ROWS] == i ? losses[lane % ROWS] : 0.0f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+      if (lane == 0) {
+        sum[i] = a;
+        if (gridDim.x > 1) cta_loss[static_cast<int64_t>(blockIdx.x) * N + i] = a;
+      }
+    }
+    if (lane == 0) {
+      last = 1;
+      if (gridDim.x > 1) {
+        __threadfence();
+        last = atomicAdd(counter, 1) == static_cast<int>(gridDim.x) - 1;
+        __threadfence();
+      }
+    }
+  }
   __syncthreads();
   if (!last) return;
-  __threadfence();
-  float* red = reinterpret_cast<float*>(sm);  // [N][32 warps]
-  for (int i = 0; i < N; ++i) {
+  if (gridDim.x > 1 && warp < N) {
     float a = 0.0f;
-    for (int64_t c = threadIdx.x; c < gridDim.x; c += kJoinThreads) a += __ldcg(cta_loss + c * N + i);
+#pragma unroll 4
+    for (int64_t c = lane; c < gridDim.x; c += 32) a += __ldcg(cta_loss + c * N + warp);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-    if (lane == 0) red[i * 32 + warp] = a;
+    if (lane == 0) sum[warp] = a;
   }
   __syncthreads();
   if (threadIdx.x == 0) {
     float total = 0.0f;
     for (int i = 0; i < N; ++i) {
-      float a = 0.0f;
-      for (int w = 0; w < 32; ++w) a += red[i * 32 + w];
-      if (shard_loss) shard_loss[i] = a;
-      total += a;
+      if (shard_loss) shard_loss[i] = sum[i];
+      total += sum[i];
     }
     loss[0] = total / static_cast<float>(M);
   }
@@ -139,24 +157,27 @@ constexpr int64_t kPieceBytes = 512ll << 20;
 struct BwdPlan {
   int64_t piece;  // vocabulary entries of a piece, whole 256-column tiles; also q's pitch
   int pieces;
-  int groups;     // parts of dx's sum over a piece, each a partial of its own
-  bool direct;    // dx leaves one product: no partials
-  size_t q, dx, total;
+  int x_parts, e_parts;  // parts of the sums of dx (over a piece) and of dE (over the rows)
+  bool x_direct;         // dx leaves one product
+  size_t q, dx, dE, total;
 };
-// Parts of dx's sum over a piece, where its tiles alone would leave SMs idle: the number that
-// takes the least time, whole waves of the tiles (256 x 256 on an SM pair, 128 x 128 on an SM where
-// there are fewer than 256 rows) against the fp32 partials written and read.
-int dx_groups(int64_t M, int64_t h, int64_t piece) {
-  const int64_t tw = M >= 256 ? 256 : 128, at_once = M >= 256 ? kSms / 2 : kSms;
-  const int64_t tiles = (M + tw - 1) / tw * ((h + tw - 1) / tw);
+// Parts of the sum over K of a product with (rows, cols) outputs, where its tiles alone would leave
+// SMs idle: the number that takes the least time, whole waves of the tiles (256 x 256 on an SM pair,
+// else about 128 x 128 on an SM) against the fp32 partials, written, read and added up by a launch
+// more. No part of fewer than 256 products, no more than 128 MiB of partials.
+int sum_parts(int64_t rows, int64_t cols, int64_t K) {
+  const bool pair = rows >= 256 && cols >= 256;
+  const int64_t tw = pair ? 256 : 128, at_once = pair ? kSms / 2 : kSms;
+  const int64_t tiles = (rows + tw - 1) / tw * ((cols + tw - 1) / tw);
   if (tiles >= 2 * at_once) return 1;
   int best = 1;
   double least = 0.0;
-  for (int g = 1; g <= 32 && (g == 1 || piece / g >= 512); ++g) {
+  for (int g = 1; g <= 32; ++g) {
+    if (g > 1 && (K / g < 256 || g * rows * cols * 4 > (128ll << 20))) break;
     const double waves = static_cast<double>((tiles * g + at_once - 1) / at_once);
-    // seconds: a wave's products at 1.7e15 / (152 SMs), the partials at 5e12 bytes
-    const double t = waves * (2.0 * tw * tw * (piece / g)) * at_once / 1.7e15 +
-                     (g > 1 ? g * M * h * 8.0 / 5e12 : 0.0);
+    // seconds: a wave's products at 1.7e15 / (152 SMs), the partials at 5e12 bytes, their launch
+    const double t = waves * (2.0 * tw * tw * (K / g)) * at_once / 1.7e15 +
+                     (g > 1 ? g * rows * cols * 8.0 / 5e12 + 3e-6 : 0.0);
     if (g == 1 || t < least) {
       best = g;
       least = t;
@@ -171,12 +192,22 @@ BwdPlan bwd_plan(int64_t M, int64_t v, int64_t h, tp_dtype dt) {
   const int64_t n = (v + most - 1) / most;
   P.piece = ((v + n - 1) / n + 255) / 256 * 256;
   P.pieces = static_cast<int>((v + P.piece - 1) / P.piece);
-  P.groups = dt == TP_BF16 ? dx_groups(M, h, P.piece) : 1;
-  P.direct = dt != TP_BF16 || (P.pieces == 1 && P.groups == 1);
+  P.x_parts = dt == TP_BF16 ? sum_parts(M, h, std::min(P.piece, v)) : 1;
+  P.e_parts = dt == TP_BF16 ? sum_parts(std::min(P.piece, v), h, M) : 1;
+  P.x_direct = dt != TP_BF16 || (P.pieces == 1 && P.x_parts == 1);
   P.q = a256(M * P.piece * e);
-  P.dx = P.direct ? 0 : a256(static_cast<size_t>(P.groups) * M * h * sizeof(float));
-  P.total = P.q + P.dx;
+  P.dx = P.x_direct ? 0 : a256(static_cast<size_t>(P.x_parts) * M * h * sizeof(float));
+  P.dE = P.e_parts == 1 ? 0 : a256(static_cast<size_t>(P.e_parts) * P.piece * h * sizeof(float));
+  P.total = P.q + P.dx + P.dE;
   return P;
+}
+
+// a product's sum over K in `parts` parts (1: as it is), each a partial of its own at out
+void split_sum(GemmDesc& d, int parts) {
+  if (parts == 1) return;
+  d.K = ((d.K + parts - 1) / parts + 63) / 64 * 64;
+  d.groups = parts;
+  d.out_group_stride = d.M * d.N;
 }
 
 tp_status product(const GemmDesc& d, cudaStream_t st) {
@@ -230,7 +261,8 @@ tp_status launch_vocab_linear_ce_bwd(const void* x, const void* E, const int32_t
   const BwdPlan P = bwd_plan(M, v, h, dt);
   const int64_t e = static_cast<int64_t>(elem_size(dt));
   void* q = ws;
-  float* sums = reinterpret_cast<float*>(static_cast<char*>(ws) + P.q);
+  float* xs = reinterpret_cast<float*>(static_cast<char*>(ws) + P.q);
+  float* es = reinterpret_cast<float*>(static_cast<char*>(ws) + P.q + P.dx);
   for (int i = 0; i < P.pieces; ++i) {
     const int64_t c0 = i * P.piece, n = std::min(P.piece, v - c0);
     const char* Ei = static_cast<const char*>(E) + c0 * h * e;
@@ -253,42 +285,45 @@ tp_status launch_vocab_linear_ce_bwd(const void* x, const void* E, const int32_t
       d.ce.scale = scale;
       TP_TRY(product(d, st));
     }
-    if (dx) {  // dx (+)= q E
-      GemmDesc d;
-      d.dtype = dt;
-      d.M = M;
-      d.N = h;
-      d.K = P.groups > 1 ? ((n + P.groups - 1) / P.groups + 63) / 64 * 64 : n;
-      d.groups = P.groups;
-      d.A[0] = {q, M, n, P.piece};
-      d.B[0] = {Ei, n, h, h};
-      d.b_mn = true;
-      d.ldo = h;
-      d.epi = EPI_STORE;
-      d.out[0] = P.direct ? dx : sums;
-      d.out_f32 = dt == TP_F32 || !P.direct;
-      d.out_acc = i > 0;
-      d.out_group_stride = P.groups > 1 ? M * h : 0;
-      TP_TRY(product(d, st));
+    GemmDesc gx, ge;
+    // dx (+)= q E
+    gx.dtype = dt;
+    gx.M = M;
+    gx.N = h;
+    gx.K = n;
+    gx.A[0] = {q, M, n, P.piece};
+    gx.B[0] = {Ei, n, h, h};
+    gx.b_mn = true;
+    gx.ldo = h;
+    gx.epi = EPI_STORE;
+    gx.out[0] = P.x_direct || !dx ? dx : xs;
+    gx.out_f32 = dt == TP_F32 || !P.x_direct;
+    gx.out_acc = i > 0;
+    split_sum(gx, P.x_parts);
+    // dE = q^T x, the piece's rows
+    char* dEi = dE ? static_cast<char*>(dE) + c0 * h * e : nullptr;
+    ge.dtype = dt;
+    ge.M = n;
+    ge.N = h;
+    ge.K = M;
+    ge.A[0] = {q, M, n, P.piece};  // q (M, n) read as A(m = n, k = M): MN-major
+    ge.a_mn = true;
+    ge.B[0] = {x, M, h, h};
+    ge.b_mn = true;
+    ge.ldo = h;
+    ge.epi = EPI_STORE;
+    ge.out[0] = P.e_parts > 1 && dE ? static_cast<void*>(es) : dEi;
+    ge.out_f32 = dt == TP_F32 || P.e_parts > 1;
+    split_sum(ge, P.e_parts);
+    if (dt == TP_F32) {
+      TP_TRY(launch_gemm_simt_two(gx, ge, st));
+      continue;
     }
-    if (dE) {  // dE = q^T x, the piece's rows
-      GemmDesc d;
-      d.dtype = dt;
-      d.M = n;
-      d.N = h;
-      d.K = M;
-      d.A[0] = {q, M, n, P.piece};  // q (M, n) read as A(m = n, k = M): MN-major
-      d.a_mn = true;
-      d.B[0] = {x, M, h, h};
-      d.b_mn = true;
-      d.ldo = h;
-      d.epi = EPI_STORE;
-      d.out[0] = static_cast<char*>(dE) + c0 * h * e;
-      d.out_f32 = dt == TP_F32;
-      TP_TRY(product(d, st));
-    }
+    if (dx) TP_TRY(launch_gemm_tc(gx, st));
+    if (dE) TP_TRY(launch_gemm_tc(ge, st));
+    if (dE && P.e_parts > 1) TP_TRY(launch_shard_reduce(es, nullptr, dEi, P.e_parts, n, h, dt, st));
   }
-  if (dx && !P.direct) return launch_shard_reduce(sums, nullptr, dx, P.groups, M, h, dt, st);
+  if (dx && !P.x_direct) return launch_shard_reduce(xs, nullptr, dx, P.x_parts, M, h, dt, st);
   return TP_OK;
 }
 
