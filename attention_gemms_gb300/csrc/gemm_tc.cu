@@ -939,9 +939,9 @@ constexpr uint64_t kPairDrainNs = 20000000ull;
 #ifndef TP_WIDE_STAGES
 #define TP_WIDE_STAGES 4
 #endif
-template <int WN>
+template <int WN, int EW = WN == 2 ? 8 : TP_PAIR_EPI_WARPS>
 struct PairCfg {
-  static constexpr int EPI_WARPS = WN == 2 ? 8 : TP_PAIR_EPI_WARPS;
+  static constexpr int EPI_WARPS = EW;
   static constexpr int THREADS = 32 * (kEpiHi0 + (EPI_WARPS == 8 ? 4 : 0));
   static constexpr int STAGES = WN == 2 ? TP_WIDE_STAGES : TP_PAIR_STAGES;
   static constexpr int B_HALF_BYTES = 128 * BK * 2;                // 128 x 64 bf16
@@ -952,12 +952,13 @@ struct PairCfg {
   static constexpr int STAGING_BYTES = EPI_WARPS * 2 * 2048;
   static constexpr int SMEM = STAGES * STAGE_BYTES + STAGING_BYTES + 1024 + NBARS * 8 + 16;
 };
-static_assert(PairCfg<2>::SMEM <= 232448 && PairCfg<1>::SMEM <= 232448, "shared memory per CTA");
+static_assert(PairCfg<2>::SMEM <= 232448 && PairCfg<1>::SMEM <= 232448 &&
+                  PairCfg<1, 8>::SMEM <= 232448, "shared memory per CTA");
 
-template <int EPI, int WN>
-__global__ void __launch_bounds__(PairCfg<WN>::THREADS, 1)
+template <int EPI, int WN, int EW = PairCfg<WN>::EPI_WARPS>
+__global__ void __launch_bounds__(PairCfg<WN, EW>::THREADS, 1)
     gemm_tc2_kernel(const __grid_constant__ TcParams p) {
-  using C = PairCfg<WN>;
+  using C = PairCfg<WN, EW>;
   constexpr int S = C::STAGES;
   constexpr int A_BYTES = 128 * BK * 2;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -1545,10 +1546,10 @@ tp_status launch_bn(int epi, const TcParams& prm, int grid, cudaStream_t st) {
   return fail(TP_ERR_INVALID_ARG, "unknown epilogue");
 }
 
-template <int EPI, int WN>
+template <int EPI, int WN, int EW = PairCfg<WN>::EPI_WARPS>
 tp_status launch_pair_epi(const TcParams& prm, int64_t ntiles, cudaStream_t st) {
-  auto kern = gemm_tc2_kernel<EPI, WN>;
-  constexpr int kSmem = PairCfg<WN>::SMEM;
+  auto kern = gemm_tc2_kernel<EPI, WN, EW>;
+  constexpr int kSmem = PairCfg<WN, EW>::SMEM;
   static std::atomic<int> max_pairs_dev[64];  // per instantiation and device (0: unknown)
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = -1;
@@ -1561,7 +1562,7 @@ tp_status launch_pair_epi(const TcParams& prm, int64_t ntiles, cudaStream_t st) 
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see launch_kernel
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.blockDim = dim3(PairCfg<WN>::THREADS, 1, 1);
+  cfg.blockDim = dim3(PairCfg<WN, EW>::THREADS, 1, 1);
   cfg.dynamicSmemBytes = kSmem;
   cfg.stream = st;
   cfg.attrs = attr;
@@ -1599,7 +1600,12 @@ tp_status launch_pair_wn(int epi, const TcParams& prm, int64_t ntiles, cudaStrea
   return fail(TP_ERR_INVALID_ARG, "unknown epilogue");
 }
 
-tp_status launch_pair(int epi, bool wide, const TcParams& prm, int64_t ntiles, cudaStream_t st) {
+// epi8: eight epilogue warps beside narrow tiles, see short_sum
+tp_status launch_pair(int epi, bool wide, bool epi8, const TcParams& prm, int64_t ntiles,
+                      cudaStream_t st) {
+  if (epi8 && epi == EPI_STORE) return launch_pair_epi<EPI_STORE, 1, 8>(prm, ntiles, st);
+  if (epi8 && epi == EPI_LSE) return launch_pair_epi<EPI_LSE, 1, 8>(prm, ntiles, st);
+  if (epi8 && epi == EPI_DCE) return launch_pair_epi<EPI_DCE, 1, 8>(prm, ntiles, st);
   return wide ? launch_pair_wn<2>(epi, prm, ntiles, st) : launch_pair_wn<1>(epi, prm, ntiles, st);
 }
 
@@ -1629,6 +1635,14 @@ int epi_out_bytes(const GemmDesc& d) {
   int n = 0;
   for (void* o : d.out) n += o != nullptr;
   return std::max(n, 1) * (d.out_f32 ? 4 : 2);
+}
+
+// Whether a narrow tile's products take so little time that its epilogue is what counts: eight
+// epilogue warps then. Plain stores, us, four / eight warps: 50304 x 2048 with K = 64 85 / 65, 512
+// 101 / 83, 1024 75.5 / 75.8 (50176 x 1024); 8192 x 50304 with K = 512 379 / 313. The forward
+// cross-entropy, 8192 x 50304: K = 256 267 / 225, 512 282 / 288, 1024 501 / 508.
+bool short_sum(int epi, int64_t k_tile) {
+  return epi == EPI_LSE ? k_tile <= 256 : (epi == EPI_STORE || epi == EPI_DCE) && k_tile <= 512;
 }
 
 tp_status launch_gemm_tc(const GemmDesc& d, cudaStream_t st) {
@@ -1671,6 +1685,7 @@ tp_status launch_gemm_tc(const GemmDesc& d, cudaStream_t st) {
   // of them (2 narrow tiles' work at ~10 % more per cycle) still ends first
   // (2048 x 4096 x 2048: 64 wide tiles in one wave, not 128 narrow ones in two)
   bool wide = false;
+  const int64_t k_tile = static_cast<int64_t>(d.nseg) * d.K;
   if (pair) {
     const int64_t ww = 2 * bn_logical;
     const int64_t rows = (d.M + 255) / 256 * d.groups;
@@ -1679,7 +1694,6 @@ tp_status launch_gemm_tc(const GemmDesc& d, cudaStream_t st) {
     const int64_t pairs_n = std::max<int64_t>(device_sm_count() / 2, 1);
     auto waves = [&](int64_t t) { return (t + pairs_n - 1) / pairs_n; };
     const bool many = wtiles >= 4 * pairs_n || 18 * waves(wtiles) < 10 * waves(ntiles);
-    const int64_t k_tile = static_cast<int64_t>(d.nseg) * d.K;
     const int mode = g_wide_mode.load();
     // the forward cross-entropy's last tile may be ragged; its exponentials count as two bytes
     // (K = 2048: 8192 x 50304 925 us wide, 1000 narrow; K = 1024: 2048 x 50304 167 and 158)
@@ -1687,6 +1701,7 @@ tp_status launch_gemm_tc(const GemmDesc& d, cudaStream_t st) {
     wide = mode == 2 || (mode == 1 && whole && many &&
                          k_tile >= static_cast<int64_t>(TP_WIDE_K_PER_BYTE) * epi_out_bytes(d));
   }
+  const bool epi8 = pair && !wide && !d.paired && short_sum(epi, k_tile);
   const int tile_w = bn_logical * (wide ? 2 : 1);  // logical output columns of a tile
   // decode configuration: at most 64 K-major rows of A
   const bool dec = !pair && BN == 128 && !d.a_mn && d.M <= 64;
@@ -1746,7 +1761,7 @@ tp_status launch_gemm_tc(const GemmDesc& d, cudaStream_t st) {
   prm.out_acc = d.out_acc;
   prm.ce = d.ce;
   if (epi == EPI_LSE)  // partials of a row: one per tile, or per set of four epilogue warps
-    *d.ce.slots = prm.tiles_n * (pair && (wide ? PairCfg<2>::EPI_WARPS : PairCfg<1>::EPI_WARPS) == 8 ? 2 : 1);
+    *d.ce.slots = prm.tiles_n * (pair && (wide || epi8 || PairCfg<1>::EPI_WARPS == 8) ? 2 : 1);
   {
     const int64_t esz = d.out_f32 ? 4 : 2;
     bool ok = (d.ldo * esz) % 32 == 0 && (!d.out_f32 || (d.out_group_stride * 4) % 32 == 0);
@@ -1782,7 +1797,7 @@ tp_status launch_gemm_tc(const GemmDesc& d, cudaStream_t st) {
 
   const int64_t ntiles = static_cast<int64_t>(prm.tiles_m) * prm.tiles_n * prm.groups;
   if (ntiles > (1ll << 30)) return fail(TP_ERR_SHAPE, "problem too large");
-  if (pair) return launch_pair(epi, wide, prm, ntiles, st);
+  if (pair) return launch_pair(epi, wide, epi8, prm, ntiles, st);
   const int grid = static_cast<int>(
       std::min<int64_t>(ntiles, static_cast<int64_t>(device_sm_count()) * (dec ? TP_DEC_CTAS_PER_SM : 1)));
   if (dec) return launch_bn<128, true>(epi, prm, grid, st);

@@ -29,9 +29,7 @@ constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxRange = 1152;   // rows of a sorting CTA: 32 counters each in shared memory
 constexpr int kKept = 512;        // tokens of its own that a sorting warp remembers
-constexpr int kWhole = 16;        // a row of at most so many tokens is not split
-constexpr int kUnitTokens = 16;   // a unit's tokens at the least
-constexpr int kMaxUnits = 1216;   // 8 per SM
+constexpr int kWhole = 8;         // a row of at most so many tokens is not split
 constexpr int kInFlight = 4;      // tokens whose loads a thread of the sum issues together
 
 // VEC consecutive elements of T in fp32
@@ -457,8 +455,11 @@ SumPlan sum_plan(int64_t M, int64_t v, int64_t h, tp_dtype dt) {
   while (P.tx < kThreads && P.tx < nv) P.tx *= 2;
   P.ty = kThreads / P.tx;
   P.slices = static_cast<int>((nv + P.tx - 1) / P.tx);
-  // more than the CTAs that run at once: rows end in some units and not in others
-  P.units = static_cast<int>(std::clamp<int64_t>(M / kUnitTokens, 1, kMaxUnits));
+  // 16 tokens of a unit, and up to 8 CTAs of units per SM, more than run at once: rows end in some
+  // units and not in others. Few tokens: 4, whose loads are in flight together (1000 tokens, 5000
+  // rows of 512: 16 us, 20 with 16).
+  P.units = static_cast<int>(std::max<int64_t>(
+      1, std::max(std::min<int64_t>(M / 4, 512), std::min<int64_t>(M / 16, 8 * 152))));
   size_t o = 0;
   P.sorted = o; o += align_up(M * sizeof(int2), 256);
   P.border = o; o += align_up((P.units + 1) * sizeof(Border), 256);
