@@ -104,10 +104,11 @@ __device__ __forceinline__ void lse_rows(const SimtParams& p, const float* sm, i
 constexpr int simt_floats(bool paired) { return TK * (TM + 4) + (paired ? 2 : 1) * TK * (TN + 4); }
 static_assert(simt_floats(false) >= TM * TN, "partial tile must fit the staging buffers");
 
-// row slice `rank` of the tile: the cluster's partial tiles added in rank order, four columns at a
-// time, every load of a thread in flight at once; put(row of the tile, column, sum)
+// row slice `rank` of the tile: the partial tiles of the CTAs `base` .. `base` + SPLIT - 1 of the
+// cluster added in that order, four columns at a time, every load of a thread in flight at once;
+// put(row of the tile, column, sum)
 template <int SPLIT, class F>
-__device__ __forceinline__ void add_partials(const float* sm, int rank, F&& put) {
+__device__ __forceinline__ void add_partials(const float* sm, int rank, int base, F&& put) {
   constexpr int rows = TM / SPLIT, kVecs = rows * TN / 4 / 256;  // 2, 1 and (8 ranks) half a vector
   float4 v[kVecs > 0 ? kVecs : 1][SPLIT];
 #pragma unroll
@@ -116,7 +117,7 @@ __device__ __forceinline__ void add_partials(const float* sm, int rank, F&& put)
     if (e < rows * TN) {
       const uint32_t off = smem_u32(sm + rank * rows * TN + e);
 #pragma unroll
-      for (int q = 0; q < SPLIT; ++q) v[i][q] = ld_cluster_v4(mapa_shared(off, static_cast<uint32_t>(q)));
+      for (int q = 0; q < SPLIT; ++q) v[i][q] = ld_cluster_v4(mapa_shared(off, static_cast<uint32_t>(base + q)));
     }
   }
 #pragma unroll
@@ -137,14 +138,18 @@ __device__ __forceinline__ void add_partials(const float* sm, int rank, F&& put)
   }
 }
 
-// Output tile (bx, by) of group g; sm: simt_floats(PAIRED) floats of shared memory
+// Output tile (bx, by) of group g; sm: simt_floats(PAIRED) floats of shared memory. The p.split CTAs
+// of a tile are consecutive ranks of a cluster, which may hold several tiles (exchange: it has more
+// than one CTA, all of which meet at its barriers).
 template <int EPI, bool PAIRED>
-__device__ __forceinline__ void simt_tile(const SimtParams& p, int bx, int by, int g, float* sm) {
+__device__ __forceinline__ void simt_tile(const SimtParams& p, int bx, int by, int g, float* sm,
+                                          bool exchange) {
   constexpr int NB = PAIRED ? 2 : 1;
   auto As = reinterpret_cast<float(*)[TM + 4]>(sm);
   auto Bs = reinterpret_cast<float(*)[TK][TN + 4]>(sm + TK * (TM + 4));
   const int split = p.split;
-  const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;  // blockIdx.x % split
+  const int in_cluster = exchange ? static_cast<int>(cluster_ctarank()) : 0;
+  const int rank = in_cluster % split, base = in_cluster - rank;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int64_t m0 = static_cast<int64_t>(by) * TM;
   const int64_t n0 = static_cast<int64_t>(bx) * TN;
@@ -245,6 +250,10 @@ __device__ __forceinline__ void simt_tile(const SimtParams& p, int bx, int by, i
         const int64_t r = m0 + ty * 4 + i, c = n0 + tx * 4 + j;
         if (r < p.M && c < p.N) epi1<EPI>(p, g, r, c, acc[i][j], acc2[i][j]);
       }
+    if (exchange) {  // other tiles of the cluster do exchange theirs
+      cluster_sync_all();
+      cluster_sync_all();
+    }
     return;
   }
   if constexpr (!PAIRED) {  // split K (the host splits unpaired problems only)
@@ -259,9 +268,9 @@ __device__ __forceinline__ void simt_tile(const SimtParams& p, int bx, int by, i
       if constexpr (EPI == EPI_LSE) sm[rr * TN + cc] = v;  // read by this thread alone
       else if (r < p.M && c < p.N) epi1<EPI>(p, g, r, c, v, 0.0f);
     };
-    if (split == 2) add_partials<2>(sm, rank, put);
-    else if (split == 4) add_partials<4>(sm, rank, put);
-    else add_partials<8>(sm, rank, put);
+    if (split == 2) add_partials<2>(sm, rank, base, put);
+    else if (split == 4) add_partials<4>(sm, rank, base, put);
+    else add_partials<8>(sm, rank, base, put);
     if constexpr (EPI == EPI_LSE) {
       __syncthreads();
       lse_rows(p, sm + rank * rows * TN, rows, m0 + rank * rows, n0, n0 / TN);
@@ -275,19 +284,22 @@ __global__ void __launch_bounds__(256) gemm_simt_kernel(const SimtParams p) {
   pdl_wait();  // the previous kernel's results are complete and visible
   pdl_trigger();
   __shared__ __align__(16) float sm[simt_floats(PAIRED)];
-  simt_tile<EPI, PAIRED>(p, blockIdx.x / p.split, blockIdx.y, blockIdx.z, sm);
+  simt_tile<EPI, PAIRED>(p, blockIdx.x / p.split, blockIdx.y, blockIdx.z, sm, p.split > 1);
 }
 
-// Two plain products that do not depend on one another, the second's tiles after the first's: one
-// launch instead of two, which at small sizes is most of their time. Both are split alike.
+// Two plain products that do not depend on one another, the second's CTAs (from ctas0 on) after the
+// first's: one launch instead of two, which at small sizes is most of their time. Each has a split of
+// its own that divides the cluster's size; a cluster's last tiles may lie past the product.
 __global__ void __launch_bounds__(256)
-    gemm_simt_two_kernel(const SimtParams p0, const SimtParams p1, int tiles0, int gx0, int gx1) {
+    gemm_simt_two_kernel(const SimtParams p0, const SimtParams p1, int ctas0, int gx0, int gx1,
+                         int cluster) {
   pdl_wait();  // the previous kernel's results are complete and visible
   pdl_trigger();
   __shared__ __align__(16) float sm[simt_floats(false)];
-  const int t = blockIdx.x / p0.split;  // a cluster's CTAs share a tile
-  if (t < tiles0) simt_tile<EPI_STORE, false>(p0, t % gx0, t / gx0, 0, sm);
-  else simt_tile<EPI_STORE, false>(p1, (t - tiles0) % gx1, (t - tiles0) / gx1, 0, sm);
+  const bool first = blockIdx.x < ctas0;
+  const SimtParams& p = first ? p0 : p1;
+  const int gx = first ? gx0 : gx1, t = (blockIdx.x - (first ? 0 : ctas0)) / p.split;
+  simt_tile<EPI_STORE, false>(p, t % gx, t / gx, 0, sm, cluster > 1);
 }
 
 // Whether the device can place a cluster of `split` CTAs of this kernel: asked once per
@@ -424,22 +436,37 @@ tp_status launch_gemm_simt(const GemmDesc& d, cudaStream_t st) {
 }
 
 tp_status launch_gemm_simt_two(const GemmDesc& a, const GemmDesc& b, cudaStream_t st) {
-  const int64_t gxa = (a.N + TN - 1) / TN, gya = (a.M + TM - 1) / TM;
-  const int64_t gxb = (b.N + TN - 1) / TN, gyb = (b.M + TM - 1) / TM;
-  const int64_t tiles = gxa * gya + gxb * gyb;
-  if (tiles > device_sm_count()) {  // not the launches, but the tiles take the time
-    if (a.out[0]) TP_TRY(launch_gemm_simt(a, st));
-    return b.out[0] ? launch_gemm_simt(b, st) : TP_OK;
+  const GemmDesc* d[2] = {&a, &b};
+  int64_t gx[2], tiles[2], steps[2], split[2] = {1, 1};
+  for (int i = 0; i < 2; ++i) {
+    gx[i] = (d[i]->N + TN - 1) / TN;
+    tiles[i] = gx[i] * ((d[i]->M + TM - 1) / TM);
+    steps[i] = simt_ksteps(*d[i]);
   }
-  SimtParams pa = simt_params(a), pb = simt_params(b);
-  // by the longer sum (CTAs that the shorter one has no steps for add nothing)
-  int split = simt_split(tiles, std::max(simt_ksteps(a), simt_ksteps(b)));
-  if (split > 1 && !cluster_fits<gemm_simt_two_kernel>(split)) split = 1;
-  pa.split = pb.split = split;
-  const int64_t ta = a.out[0] ? gxa * gya : 0, tb = b.out[0] ? gxb * gyb : 0;
+  // the longer sum per CTA is halved while it has two steps and four CTAs of an SM hold them all
+  while (true) {
+    const int i = steps[0] / split[0] >= steps[1] / split[1] ? 0 : 1;
+    if (split[i] == 8 || steps[i] < 2 * split[i] ||
+        tiles[0] * split[0] + tiles[1] * split[1] + tiles[i] * split[i] > 4 * device_sm_count())
+      break;
+    split[i] *= 2;
+  }
+  int64_t cluster = std::max(split[0], split[1]);
+  if (cluster > 1 && !cluster_fits<gemm_simt_two_kernel>(static_cast<int>(cluster)))
+    cluster = split[0] = split[1] = 1;
+  SimtParams p[2];
+  int64_t clusters[2];
+  for (int i = 0; i < 2; ++i) {
+    p[i] = simt_params(*d[i]);
+    p[i].split = static_cast<int>(split[i]);
+    clusters[i] = d[i]->out[0] ? (tiles[i] * split[i] + cluster - 1) / cluster : 0;
+  }
+  if ((clusters[0] + clusters[1]) * cluster > 2147483647ll)
+    return fail(TP_ERR_SHAPE, "fp32 GEMM grid too large");
   const cudaError_t e = launch_split<gemm_simt_two_kernel>(
-      split, static_cast<unsigned>(ta + tb), st, pa, pb, static_cast<int>(ta),
-      static_cast<int>(gxa), static_cast<int>(gxb));
+      static_cast<int>(cluster), static_cast<unsigned>(clusters[0] + clusters[1]), st, p[0], p[1],
+      static_cast<int>(clusters[0] * cluster), static_cast<int>(gx[0]), static_cast<int>(gx[1]),
+      static_cast<int>(cluster));
   count_launch();
   TP_CUDA_TRY(e);
   return TP_OK;
