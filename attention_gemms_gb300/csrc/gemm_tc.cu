@@ -82,11 +82,18 @@ constexpr uint64_t kDrainTimeoutNs = 1000000000ull;
 #ifndef TP_DEC_CTAS_PER_SM
 #define TP_DEC_CTAS_PER_SM 2
 #endif
+// 64-column decode tiles (the cross-entropy epilogues over few rows, whose B is E (v, h), K-major): a
+// stage holds two K blocks side by side, so that 256 consecutive bytes of a row of E are asked for
+// together instead of 128 (37 rows x 50257 x 4096: 82 -> 75 us; 8 x 50304 x 8192: 151 -> 137;
+// 64-column tiles of one block, three CTAs per SM: 78 and 139).
 template <int BN, bool DEC = false>
 struct TcCfg {
-  static constexpr int STAGES = DEC ? TP_DEC_STAGES : (BN == 256 ? 4 : 6);
-  static constexpr int A_BYTES = DEC ? 64 * BK * 2 : BM * BK * 2;
-  static constexpr int B_BYTES = BN * BK * 2;
+  static constexpr int KSUB = DEC && BN == 64 ? 2 : 1;  // K blocks of a stage
+  static constexpr int STAGES = KSUB == 2 ? 3 : DEC ? TP_DEC_STAGES : (BN == 256 ? 4 : 6);
+  static constexpr int A_SUB = DEC ? 64 * BK * 2 : BM * BK * 2;
+  static constexpr int B_SUB = BN * BK * 2;
+  static constexpr int A_BYTES = KSUB * A_SUB;
+  static constexpr int B_BYTES = KSUB * B_SUB;
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
   static constexpr int TMEM_COLS = 2 * BN;
   static constexpr int NBARS = 2 * STAGES + 6;
@@ -667,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
   }
 
   const int ntiles = p.tiles_m * p.tiles_n * p.groups;
-  const int nkb = p.nseg * p.kb_per_seg;
+  const int nkb = (p.nseg * p.kb_per_seg + C::KSUB - 1) / C::KSUB;  // stages of a tile
   const int bn_logical = p.paired ? BN / 2 : BN;
   uint32_t issued = 0;      // producer: loads issued
   bool mma_issued = false;  // MMA thread: any MMA issued
@@ -676,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
     if (lane == 0) {
       // ------------------------------------------------------------ producer
       const uint32_t stage_tx =
-          DEC ? static_cast<uint32_t>(p.a_rows * BK * 2 + C::B_BYTES) : C::STAGE_BYTES;
+          DEC ? static_cast<uint32_t>(C::KSUB * p.a_rows * BK * 2 + C::B_BYTES) : C::STAGE_BYTES;
       uint32_t stage = 0, phase = 0;
       bool ok = true;
       [[maybe_unused]] const long long t_start = TP_CLK();
@@ -691,8 +698,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
             break;
           }
           TP_STAT(0, TP_CLK() - tw);
-          const int seg = kb / p.kb_per_seg;
-          const int k0 = p.seg_k0[seg] + static_cast<int>(tc.g * p.K) + (kb - seg * p.kb_per_seg) * BK;
+          const int seg = C::KSUB == 2 ? 0 : kb / p.kb_per_seg;
+          const int k0 = p.seg_k0[seg] + static_cast<int>(tc.g * p.K) +
+                         (kb - seg * p.kb_per_seg) * (C::KSUB * BK);
           const uint32_t a_dst = sbase + stage * C::STAGE_BYTES;
           const uint32_t b_dst = a_dst + C::A_BYTES;
 #ifdef TP_GEMM_STATS
@@ -703,7 +711,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
           }
 #endif
           mbar_arrive_expect_tx(full_bar(stage), stage_tx);
-          if (p.a_mn && p.a3d) {
+          if constexpr (C::KSUB == 2) {  // both operands K-major, one segment
+            tma_load_2d(b_dst, &p.tmB[0], full_bar(stage), k0, n0);
+            tma_load_2d(b_dst + C::B_SUB, &p.tmB[0], full_bar(stage), k0 + BK, n0);
+            tma_load_2d(a_dst, &p.tmA[0], full_bar(stage), k0, m0);
+            tma_load_2d(a_dst + C::A_SUB, &p.tmA[0], full_bar(stage), k0 + BK, m0);
+          } else if (p.a_mn && p.a3d) {
             tma_load_3d(a_dst, &p.tmA[seg], full_bar(stage), 0, k0, m0 / 64);
           } else if (p.a_mn) {
             tma_load_2d(a_dst, &p.tmA[seg], full_bar(stage), m0, k0);
@@ -711,7 +724,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
           } else {
             tma_load_2d(a_dst, &p.tmA[seg], full_bar(stage), k0, m0);
           }
-          if (p.paired && !p.b_mn) {
+          if constexpr (C::KSUB == 2) {
+          } else if (p.paired && !p.b_mn) {
             // K-major halves ((out, in) weights): BN/2 gate rows, then BN/2 up rows
             tma_load_2d(b_dst, &p.tmB[0], full_bar(stage), k0, n0);
             tma_load_2d(b_dst + (BN / 2) * 128, &p.tmB[1], full_bar(stage), k0, n0);
@@ -783,11 +797,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
           const uint32_t a_addr = sbase + stage * C::STAGE_BYTES;
           const uint32_t b_addr = a_addr + C::A_BYTES;
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t ad = sw128_desc(a_addr + kk * a_kstep, a_lbo, 1024u);
-            const uint64_t bd = sw128_desc(b_addr + kk * b_kstep, b_lbo, 1024u);
-            mma_bf16_ss(d_tmem, ad, bd, idesc, (kb | kk) != 0 ? 1u : 0u);
-          }
+          for (int u = 0; u < C::KSUB; ++u)
+#pragma unroll
+            for (int kk = 0; kk < BK / 16; ++kk) {
+              const uint64_t ad = sw128_desc(a_addr + u * C::A_SUB + kk * a_kstep, a_lbo, 1024u);
+              const uint64_t bd = sw128_desc(b_addr + u * C::B_SUB + kk * b_kstep, b_lbo, 1024u);
+              mma_bf16_ss(d_tmem, ad, bd, idesc, (kb | u | kk) != 0 ? 1u : 0u);
+            }
           mma_issued = true;
           mma_commit(empty_bar(stage));
 #ifdef TP_GEMM_STATS
@@ -1540,8 +1556,10 @@ tp_status launch_bn(int epi, const TcParams& prm, int grid, cudaStream_t st) {
     case EPI_DGELU: return launch_bn_epi<BN, EPI_DGELU, DEC>(prm, grid, st);
     case EPI_DSWIGLU: return launch_bn_epi<BN, EPI_DSWIGLU, DEC>(prm, grid, st);
     case EPI_PAIR: return launch_bn_epi<BN, EPI_PAIR, DEC>(prm, grid, st);
-    case EPI_LSE: return launch_bn_epi<BN, EPI_LSE, DEC>(prm, grid, st);
-    case EPI_DCE: return launch_bn_epi<BN, EPI_DCE, DEC>(prm, grid, st);
+  }
+  if constexpr (!DEC) {  // few rows have tiles of their own
+    if (epi == EPI_LSE) return launch_bn_epi<BN, EPI_LSE, false>(prm, grid, st);
+    if (epi == EPI_DCE) return launch_bn_epi<BN, EPI_DCE, false>(prm, grid, st);
   }
   return fail(TP_ERR_INVALID_ARG, "unknown epilogue");
 }
@@ -1675,6 +1693,10 @@ tp_status launch_gemm_tc(const GemmDesc& d, cudaStream_t st) {
     if (pair && 2 * ctas(256, 256) * 2 <= sms) pair = false;
     while (!pair && BN > 64 && 2 * ctas(BM, BN) <= sms) BN /= 2;
   }
+  // few rows against a K-major E: 64-column tiles whose stages hold two K blocks (TcCfg)
+  const bool few = !pair && d.M <= 64 && !d.a_mn && !d.b_mn && d.nseg == 1 && d.groups == 1 &&
+                   (epi == EPI_LSE || epi == EPI_DCE);
+  if (few) BN = 64;
   const int bn_logical = d.paired ? BN / 2 : BN;
   const int tile_m = pair ? 256 : BM;
   // pair tiles twice as wide (256 x 512): 3/4 of the operand bytes per FLOP, but one
@@ -1704,7 +1726,7 @@ tp_status launch_gemm_tc(const GemmDesc& d, cudaStream_t st) {
   const bool epi8 = pair && !wide && !d.paired && short_sum(epi, k_tile);
   const int tile_w = bn_logical * (wide ? 2 : 1);  // logical output columns of a tile
   // decode configuration: at most 64 K-major rows of A
-  const bool dec = !pair && BN == 128 && !d.a_mn && d.M <= 64;
+  const bool dec = few || (!pair && BN == 128 && !d.a_mn && d.M <= 64);
   const int a_rows = dec ? static_cast<int>((d.M + 7) / 8 * 8) : BM;
 
   TcParams prm;
@@ -1800,6 +1822,9 @@ tp_status launch_gemm_tc(const GemmDesc& d, cudaStream_t st) {
   if (pair) return launch_pair(epi, wide, epi8, prm, ntiles, st);
   const int grid = static_cast<int>(
       std::min<int64_t>(ntiles, static_cast<int64_t>(device_sm_count()) * (dec ? TP_DEC_CTAS_PER_SM : 1)));
+  if (few)
+    return epi == EPI_LSE ? launch_bn_epi<64, EPI_LSE, true>(prm, grid, st)
+                          : launch_bn_epi<64, EPI_DCE, true>(prm, grid, st);
   if (dec) return launch_bn<128, true>(epi, prm, grid, st);
   if (BN == 64) return launch_bn<64, false>(epi, prm, grid, st);
   return BN == 256 ? launch_bn<256, false>(epi, prm, grid, st)
