@@ -479,8 +479,10 @@ SumPlan sum_plan(int64_t M, int64_t v, int64_t h, tp_dtype dt) {
 template <typename T, int VEC>
 tp_status embed_fwd(const int32_t* ids, const void* E, void* x, int64_t M, int64_t v, int64_t h,
                     float scale, cudaStream_t st) {
+  // four vectors of a row per thread (65536 rows of 1024, bf16: 31 us, 56 with one; 8192 of 4096: 21
+  // and 25)
   int tx = 4;
-  while (tx < kThreads && tx * VEC < h) tx *= 2;
+  while (tx < kThreads && tx * VEC * 4 < h) tx *= 2;
   const int ty = kThreads / tx;
   TP_CUDA_TRY(launch_kernel(vocab_embed_scaled_fwd_kernel<T, VEC>,
                             dim3(static_cast<unsigned>((M + ty - 1) / ty)), dim3(tx, ty), 0, st, ids,
