@@ -66,18 +66,20 @@ __device__ __forceinline__ void epi1(const SimtParams& p, int g, int64_t r, int6
   } else if constexpr (EPI == EPI_PAIR) {
     p.out0[i] = a;
     p.out1[i] = b;
-  } else if constexpr (EPI == EPI_DCE) {
-    const int64_t t = p.ce.targets[r];
-    const float q = expf(a - p.ce.lse[r]) - (t == p.ce.col0 + c ? 1.0f : 0.0f);
-    p.out0[i] = t >= 0 && t < p.ce.vocab ? q * p.ce.scale : 0.0f;
   }
 }
 
+// The gradient by one logit of a row with target t and this lse
+__device__ __forceinline__ float ce_grad(const SimtParams& p, float a, int64_t t, float lse, int64_t c) {
+  const float q = expf(a - lse) - (t == p.ce.col0 + c ? 1.0f : 0.0f);
+  return t >= 0 && t < p.ce.vocab ? q * p.ce.scale : 0.0f;
+}
+
 // EPI_LSE of the `rows` rows of the tile's logits in sm (TN floats each), rows r0 .. of the
-// product, columns c0 ..: a warp per row, two columns per lane. As in the tensor-core engine the
+// product with these targets, columns c0 ..: a warp per row, two columns per lane. As in the tensor-core engine the
 // maximum is kept in base 2; expf and the sum in 32 bits.
-__device__ __forceinline__ void lse_rows(const SimtParams& p, const float* sm, int rows, int64_t r0,
-                                         int64_t c0, int64_t slot) {
+__device__ __forceinline__ void lse_rows(const SimtParams& p, const float* sm, const int32_t* target,
+                                         int rows, int64_t r0, int64_t c0, int64_t slot) {
   static_assert(TN == 64, "two columns per lane");
   constexpr float kLog2e = 1.4426950408889634f;  // log2(e)
   const int lane = threadIdx.x & 31;
@@ -87,7 +89,7 @@ __device__ __forceinline__ void lse_rows(const SimtParams& p, const float* sm, i
     const int64_t ca = c0 + lane, cb = ca + 32;
     const float a = ca < p.N ? sm[rr * TN + lane] : -INFINITY;
     const float b = cb < p.N ? sm[rr * TN + lane + 32] : -INFINITY;
-    const int64_t t = p.ce.targets[r];
+    const int64_t t = target[rr];
     if (t == ca && ca < p.N) p.ce.hit[r] = a;
     if (t == cb && cb < p.N) p.ce.hit[r] = b;
     float m = fmaxf(a, b);
@@ -153,8 +155,17 @@ __device__ __forceinline__ void simt_tile(const SimtParams& p, int bx, int by, i
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const int64_t m0 = static_cast<int64_t>(by) * TM;
   const int64_t n0 = static_cast<int64_t>(bx) * TN;
-  if constexpr (EPI == EPI_LSE) {
-    if (bx == 0 && by == 0 && rank == 0 && threadIdx.x == 0) *p.ce.counter = 0;
+  // the rows' targets and lse, asked for before the product (read after its barriers)
+  constexpr bool kCe = EPI == EPI_LSE || EPI == EPI_DCE;
+  __shared__ int32_t row_t[kCe ? TM : 1];
+  __shared__ float row_lse[kCe ? TM : 1];
+  if constexpr (kCe) {
+    if (threadIdx.x < TM) {
+      const bool in = m0 + threadIdx.x < p.M;
+      row_t[threadIdx.x] = in ? p.ce.targets[m0 + threadIdx.x] : -1;
+      if constexpr (EPI == EPI_DCE) row_lse[threadIdx.x] = in ? p.ce.lse[m0 + threadIdx.x] : 0.0f;
+    }
+    if (EPI == EPI_LSE && bx == 0 && by == 0 && rank == 0 && threadIdx.x == 0) *p.ce.counter = 0;
   }
   float acc[4][4] = {}, acc2[4][4] = {};
   float ra[kPer], rb[NB][kPer];
@@ -238,7 +249,7 @@ __device__ __forceinline__ void simt_tile(const SimtParams& p, int bx, int by, i
 #pragma unroll
         for (int j = 0; j < 4; ++j) sm[(ty * 4 + i) * TN + tx * 4 + j] = acc[i][j];
       __syncthreads();
-      lse_rows(p, sm, TM, m0, n0, n0 / TN);
+      lse_rows(p, sm, row_t, TM, m0, n0, n0 / TN);
     }
     return;
   }
@@ -248,7 +259,12 @@ __device__ __forceinline__ void simt_tile(const SimtParams& p, int bx, int by, i
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int64_t r = m0 + ty * 4 + i, c = n0 + tx * 4 + j;
-        if (r < p.M && c < p.N) epi1<EPI>(p, g, r, c, acc[i][j], acc2[i][j]);
+        if (r < p.M && c < p.N) {
+          if constexpr (EPI == EPI_DCE)
+            p.out0[r * p.ldo + c] = ce_grad(p, acc[i][j], row_t[ty * 4 + i], row_lse[ty * 4 + i], c);
+          else
+            epi1<EPI>(p, g, r, c, acc[i][j], acc2[i][j]);
+        }
       }
     if (exchange) {  // other tiles of the cluster do exchange theirs
       cluster_sync_all();
@@ -265,15 +281,19 @@ __device__ __forceinline__ void simt_tile(const SimtParams& p, int bx, int by, i
     const int rows = TM / split;
     auto put = [&](int rr, int cc, float v) {
       const int64_t r = m0 + rr, c = n0 + cc;
-      if constexpr (EPI == EPI_LSE) sm[rr * TN + cc] = v;  // read by this thread alone
-      else if (r < p.M && c < p.N) epi1<EPI>(p, g, r, c, v, 0.0f);
+      if constexpr (EPI == EPI_LSE) {
+        sm[rr * TN + cc] = v;  // read by this thread alone
+      } else if (r < p.M && c < p.N) {
+        if constexpr (EPI == EPI_DCE) p.out0[r * p.ldo + c] = ce_grad(p, v, row_t[rr], row_lse[rr], c);
+        else epi1<EPI>(p, g, r, c, v, 0.0f);
+      }
     };
     if (split == 2) add_partials<2>(sm, rank, base, put);
     else if (split == 4) add_partials<4>(sm, rank, base, put);
     else add_partials<8>(sm, rank, base, put);
     if constexpr (EPI == EPI_LSE) {
       __syncthreads();
-      lse_rows(p, sm + rank * rows * TN, rows, m0 + rank * rows, n0, n0 / TN);
+      lse_rows(p, sm + rank * rows * TN, row_t + rank * rows, rows, m0 + rank * rows, n0, n0 / TN);
     }
     cluster_sync_all();  // no CTA leaves while another still reads its tile
   }
@@ -443,10 +463,15 @@ __global__ void __launch_bounds__(256, 2)
       for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
       if (tx == 0 && r < p.M) p.ce.part[n0 / BT * p.M + r] = make_float2(m * kLog2e, s);
     } else {
+      const int64_t t = EPI == EPI_DCE && r < p.M ? p.ce.targets[r] : -1;
+      const float lse = EPI == EPI_DCE && r < p.M ? p.ce.lse[r] : 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int64_t c = n0 + 64 * (j / 4) + tx * 4 + j % 4;
-        if (r < p.M && c < p.N) epi1<EPI>(p, 0, r, c, acc[j], 0.0f);
+        if (r < p.M && c < p.N) {
+          if constexpr (EPI == EPI_DCE) p.out0[r * p.ldo + c] = ce_grad(p, acc[j], t, lse, c);
+          else epi1<EPI>(p, 0, r, c, acc[j], 0.0f);
+        }
       }
     }
   }

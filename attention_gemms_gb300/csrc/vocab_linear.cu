@@ -37,8 +37,8 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
 // A CTA joins ROWS rows: its 1024 threads, consecutive ones on consecutive rows, share the slots,
 // shuffles join a warp's, and a warp per row joins the warps'. The CTA that ends last adds the CTAs'
 // losses up (in an order of their own, whichever CTA that is): a launch less than a kernel of its
-// own. 32 rows where that gives every SM a CTA (8192 rows x 197 slots: 8
-// us, 11 with 8 rows), else 8 (37 rows x 393 slots: 5 us against 8).
+// own. 32 rows where that gives every SM a CTA, else 8, whose slots more threads share; up to 128
+// rows of few slots one CTA, which has no other to wait for.
 template <int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) vocab_linear_join_kernel(
     const float2* __restrict__ part, const float* __restrict__ hit,
@@ -47,18 +47,21 @@ __global__ void __launch_bounds__(kJoinThreads) vocab_linear_join_kernel(
     int slots, int64_t M, int64_t v, int N) {
   pdl_wait();  // the previous kernel's results are complete and visible
   pdl_trigger();
-  __shared__ float2 sm[32][ROWS];
+  // up to 32 rows: a warp ends a row, over the 32 warps' pairs; 128: a thread, over eight
+  constexpr bool kWarpEnds = ROWS <= 32;
+  constexpr int kPairs = kWarpEnds ? 32 : kJoinThreads / ROWS;
+  __shared__ float2 sm[kPairs][ROWS];
   __shared__ float sum[kSumShards];
   __shared__ int last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  // the warp that ends row `warp` of the CTA: its target and its target's logit
-  const int64_t own = static_cast<int64_t>(blockIdx.x) * ROWS + warp;
-  const bool ends = warp < ROWS && own < M;
+  const int mine = kWarpEnds ? warp : threadIdx.x;  // the row of the CTA that this thread ends
+  const int64_t own = static_cast<int64_t>(blockIdx.x) * ROWS + mine;
+  const bool ends = mine < ROWS && own < M;
   int64_t t = ends ? targets[own] : -1;
   if (t >= v) t = -1;
   const float at = t >= 0 ? hit[own] : 0.0f;
   float m = -INFINITY, s = 0.0f;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + lane % ROWS;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x % ROWS;
   if (row < M) {
 #pragma unroll 4
     for (int i = threadIdx.x / ROWS; i < slots; i += kJoinThreads / ROWS) {
@@ -69,19 +72,27 @@ __global__ void __launch_bounds__(kJoinThreads) vocab_linear_join_kernel(
 #pragma unroll
   for (int o = ROWS; o < 32; o *= 2)
     join(m, s, __shfl_xor_sync(0xFFFFFFFFu, m, o), __shfl_xor_sync(0xFFFFFFFFu, s, o));
-  if (lane < ROWS) sm[warp][lane] = make_float2(m, s);
-  if (threadIdx.x < kSumShards) sum[threadIdx.x] = 0.0f;
+  if (kWarpEnds) {
+    if (lane < ROWS) sm[warp][lane % ROWS] = make_float2(m, s);
+  } else {
+    sm[threadIdx.x / ROWS][threadIdx.x % ROWS] = make_float2(m, s);
+  }
   __syncthreads();
   float l = 0.0f;
-  if (warp < ROWS) {
-    m = sm[lane][warp].x;
-    s = sm[lane][warp].y;
+  if (mine < ROWS) {
+    if (kWarpEnds) {
+      m = sm[lane % kPairs][mine].x;
+      s = sm[lane % kPairs][mine].y;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-      join(m, s, __shfl_xor_sync(0xFFFFFFFFu, m, o), __shfl_xor_sync(0xFFFFFFFFu, s, o));
+      for (int o = 16; o > 0; o >>= 1)
+        join(m, s, __shfl_xor_sync(0xFFFFFFFFu, m, o), __shfl_xor_sync(0xFFFFFFFFu, s, o));
+    } else {
+#pragma unroll
+      for (int w = 1; w < kPairs; ++w) join(m, s, sm[w][mine].x, sm[w][mine].y);
+    }
     const float z = (m + log2f(s)) * kLn2;
     l = t >= 0 ? z - at : 0.0f;
-    if (ends && lane == 0) {
+    if (ends && (lane == 0 || !kWarpEnds)) {
       lse[own] = z;
       row_loss[own] = l;
     }
@@ -89,14 +100,17 @@ __global__ void __launch_bounds__(kJoinThreads) vocab_linear_join_kernel(
   if (N > kSumShards) return;
   __shared__ float losses[ROWS];
   __shared__ int shard[ROWS];
-  if (warp < ROWS && lane == 0) {
-    losses[warp] = l;
-    shard[warp] = t >= 0 ? static_cast<int>(t / (v / N)) : -1;
+  if (mine < ROWS && (lane == 0 || !kWarpEnds)) {
+    losses[mine] = l;
+    shard[mine] = t >= 0 ? static_cast<int>(t / (v / N)) : -1;
   }
   __syncthreads();
   if (warp == 0) {
     for (int i = 0; i < N; ++i) {
-      float a = lane < ROWS && shard[lane % ROWS] == i ? losses[lane % ROWS] : 0.0f;
+      float a = 0.0f;
+#pragma unroll
+      for (int r = 0; r < ROWS; r += 32)
+        if (lane + r < ROWS) a += shard[lane + r] == i ? losses[lane + r] : 0.0f;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
       if (lane == 0) {
@@ -244,8 +258,10 @@ tp_status launch_vocab_linear_ce_fwd(const void* x, const void* E, const int32_t
   d.ce.counter = counter;
   d.ce.slots = &slots;
   TP_TRY(product(d, st));
-  const int rows = M >= 32 * kSms ? 32 : kRows;
-  TP_CUDA_TRY(launch_kernel(rows == 32 ? vocab_linear_join_kernel<32> : vocab_linear_join_kernel<kRows>,
+  const int rows = M <= 128 && slots <= 32 ? 128 : M >= 32 * kSms ? 32 : kRows;
+  TP_CUDA_TRY(launch_kernel(rows == 128  ? vocab_linear_join_kernel<128>
+                            : rows == 32 ? vocab_linear_join_kernel<32>
+                                         : vocab_linear_join_kernel<kRows>,
                             static_cast<unsigned>((M + rows - 1) / rows), kJoinThreads, 0, st,
                             d.ce.part, hit, targets, lse, row_loss, shard_loss, loss,
                             reinterpret_cast<float*>(base + L.cta), counter, slots, M, v, N));
