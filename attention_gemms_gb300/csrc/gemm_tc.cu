@@ -1650,6 +1650,7 @@ void set_wide_mode(int v) { g_wide_mode.store(v); }
 #define TP_WIDE_K_PER_BYTE 1024
 #endif
 int epi_out_bytes(const GemmDesc& d) {
+  if (d.epi == EPI_DCE) return 4;
   int n = 0;
   for (void* o : d.out) n += o != nullptr;
   return std::max(n, 1) * (d.out_f32 ? 4 : 2);
@@ -1717,9 +1718,12 @@ tp_status launch_gemm_tc(const GemmDesc& d, cudaStream_t st) {
     auto waves = [&](int64_t t) { return (t + pairs_n - 1) / pairs_n; };
     const bool many = wtiles >= 4 * pairs_n || 18 * waves(wtiles) < 10 * waves(ntiles);
     const int mode = g_wide_mode.load();
-    // the forward cross-entropy's last tile may be ragged; its exponentials count as two bytes
-    // (K = 2048: 8192 x 50304 925 us wide, 1000 narrow; K = 1024: 2048 x 50304 167 and 158)
-    const bool whole = d.N % ww == 0 || (epi == EPI_LSE && d.N >= 8 * ww);
+    // the cross-entropies' last tile may be ragged. Forward, the exponentials count as two bytes
+    // (K = 2048: 8192 x 50304 925 us wide, 1000 narrow; K = 1024: 2048 x 50304 167 and 158); the
+    // gradient, which writes two besides, as four (8192 x 50304 with its products, K = 4096: 5.94 ms
+    // wide, 6.27 narrow; K = 2048: 3.05 both; K = 1024: 1.68 and 1.56)
+    const bool ce = epi == EPI_LSE || epi == EPI_DCE;
+    const bool whole = d.N % ww == 0 || (ce && d.N >= 8 * ww);
     wide = mode == 2 || (mode == 1 && whole && many &&
                          k_tile >= static_cast<int64_t>(TP_WIDE_K_PER_BYTE) * epi_out_bytes(d));
   }

@@ -139,12 +139,18 @@ struct Border {
 
 // Row c is row c >> log2_ctas of CTA c mod ctas; the list goes by CTA, then by row, then by warp and
 // the order in which a warp meets its tokens (four at a time per lane: a fixed order).
+// EARLY: launched ahead of its predecessor's end, and the next kernel ahead of its own, as long as it
+// has no more than a CTA per SM (more CTAs of 1024 threads, launched early, are not safe beside the
+// GEMMs of CTA pairs: vocab_linear_join_kernel).
+template <bool EARLY>
 __global__ void __launch_bounds__(kSortThreads) vocab_embed_sort_kernel(
     const int32_t* __restrict__ ids, int2* __restrict__ sorted, Border* __restrict__ border,
     int32_t* __restrict__ arrived, uint32_t* __restrict__ absent, int32_t M, int32_t v,
     int log2_ctas, int range, int units, int columns) {
-  pdl_wait();  // the previous kernel's results are complete and visible
-  pdl_trigger();
+  if (EARLY) {
+    pdl_wait();  // the previous kernel's results are complete and visible
+    pdl_trigger();
+  }
   extern __shared__ int32_t cnt[];              // [warp][range]
   int32_t* start = cnt + kSortWarps * range;    // [range + 1] the rows' starts
   uint32_t* kept = reinterpret_cast<uint32_t*>(start + range + 1);  // [warp][kKept]
@@ -529,19 +535,30 @@ tp_status launch_vocab_embed_scaled_bwd(const int32_t* ids, const void* dx, void
   const SumPlan P = sum_plan(M, v, h, dt);
   char* base = static_cast<char*>(ws);
   const size_t smem = (static_cast<size_t>(kSortWarps) * (P.range + kKept) + P.range + 1) * 4;
-  static std::atomic<uint64_t> attr_set{0};
-  if (needs_setup(attr_set)) {
-    TP_CUDA_TRY(cudaFuncSetAttribute(vocab_embed_sort_kernel,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (kSortWarps * (kMaxRange + kKept) + kMaxRange + 1) * 4));
-    mark_device(attr_set);
-  }
-  TP_CUDA_TRY(launch_kernel(vocab_embed_sort_kernel, 1u << P.log2_ctas, kSortThreads, smem, st, ids,
-                            reinterpret_cast<int2*>(base + P.sorted),
-                            reinterpret_cast<Border*>(base + P.border),
-                            reinterpret_cast<int32_t*>(base + P.arrived),
-                            reinterpret_cast<uint32_t*>(base + P.absent), static_cast<int32_t>(M),
-                            static_cast<int32_t>(v), P.log2_ctas, P.range, P.units, P.columns));
+  auto sort = [&](auto kern, auto launch) -> tp_status {
+    static std::atomic<uint64_t> attr_set{0};  // per kernel and device
+    if (needs_setup(attr_set)) {
+      TP_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (kSortWarps * (kMaxRange + kKept) + kMaxRange + 1) * 4));
+      mark_device(attr_set);
+    }
+    TP_CUDA_TRY(launch(kern, ids, reinterpret_cast<int2*>(base + P.sorted),
+                       reinterpret_cast<Border*>(base + P.border),
+                       reinterpret_cast<int32_t*>(base + P.arrived),
+                       reinterpret_cast<uint32_t*>(base + P.absent), static_cast<int32_t>(M),
+                       static_cast<int32_t>(v), P.log2_ctas, P.range, P.units, P.columns));
+    return TP_OK;
+  };
+  const unsigned ctas = 1u << P.log2_ctas;
+  if (ctas <= 152)
+    TP_TRY(sort(vocab_embed_sort_kernel<true>, [&](auto kern, auto... a) {
+      return launch_kernel(kern, ctas, kSortThreads, smem, st, a...);
+    }));
+  else
+    TP_TRY(sort(vocab_embed_sort_kernel<false>, [&](auto kern, auto... a) {
+      kern<<<ctas, kSortThreads, smem, st>>>(a...);
+      return cudaGetLastError();
+    }));
   count_launch();
   if (dt == TP_BF16)
     return P.vec == 8 ? embed_sum<__nv_bfloat16, 8>(P, dx, dE, h, scale, accumulate, base, st)

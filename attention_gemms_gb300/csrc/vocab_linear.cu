@@ -37,16 +37,22 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
 // A CTA joins ROWS rows: its 1024 threads, consecutive ones on consecutive rows, share the slots,
 // shuffles join a warp's, and a warp per row joins the warps'. The CTA that ends last adds the CTAs'
 // losses up (in an order of their own, whichever CTA that is): a launch less than a kernel of its
-// own. 32 rows where that gives every SM a CTA, else 8, whose slots more threads share; up to 128
-// rows of few slots one CTA, which has no other to wait for.
-template <int ROWS>
+// own. 8 rows, whose slots more threads share, where that is no more than a CTA per SM, else 32; up to
+// 128 rows of few slots one CTA, which has no other to wait for.
+// EARLY: launched ahead of its predecessor's end (pdl_wait), and the next kernel ahead of its own, for
+// no more than a CTA per SM. 512 CTAs of 1024 threads, two of which fill an SM, launched early between
+// GEMMs of CTA pairs stood still together with the GEMM that came next (16384 rows, six calls without
+// a pause; never with 256). In plain stream order none waits for room that another holds.
+template <int ROWS, bool EARLY>
 __global__ void __launch_bounds__(kJoinThreads) vocab_linear_join_kernel(
     const float2* __restrict__ part, const float* __restrict__ hit,
     const int32_t* __restrict__ targets, float* __restrict__ lse, float* __restrict__ row_loss,
     float* __restrict__ shard_loss, float* __restrict__ loss, float* cta_loss, int32_t* counter,
     int slots, int64_t M, int64_t v, int N) {
-  pdl_wait();  // the previous kernel's results are complete and visible
-  pdl_trigger();
+  if (EARLY) {
+    pdl_wait();  // the previous kernel's results are complete and visible
+    pdl_trigger();
+  }
   // up to 32 rows: a warp ends a row, over the 32 warps' pairs; 128: a thread, over eight
   constexpr bool kWarpEnds = ROWS <= 32;
   constexpr int kPairs = kWarpEnds ? 32 : kJoinThreads / ROWS;
@@ -148,6 +154,15 @@ __global__ void __launch_bounds__(kJoinThreads) vocab_linear_join_kernel(
   }
 }
 
+// launch_kernel, or in plain stream order
+template <typename... KArgs, typename... Args>
+cudaError_t launch_after(bool early, void (*kern)(KArgs...), unsigned grid, unsigned block,
+                         cudaStream_t st, Args&&... args) {
+  if (early) return launch_kernel(kern, grid, block, 0, st, std::forward<Args>(args)...);
+  kern<<<grid, block, 0, st>>>(std::forward<Args>(args)...);
+  return cudaGetLastError();
+}
+
 size_t a256(size_t x) { return align_up(x, 256); }
 
 // ---- forward: partials of every row (a slot for 64 columns at the least), the targets' logits,
@@ -167,6 +182,8 @@ FwdLayout fwd_layout(int64_t M, int64_t v) {
 }
 
 // ---- backward: q of one piece, and (bf16) the fp32 sums of dx where one product does not make it
+// Fewer pieces are faster (8192 x 50304 x 2048: 4 of 256 MiB 3.03 ms, 2 of 512 2.92, one of 1 GiB
+// 2.76), but keep more of q: half of it here.
 constexpr int64_t kPieceBytes = 512ll << 20;
 struct BwdPlan {
   int64_t piece;  // vocabulary entries of a piece, whole 256-column tiles; also q's pitch
@@ -176,22 +193,29 @@ struct BwdPlan {
   size_t q, dx, dE, total;
 };
 // Parts of the sum over K of a product with (rows, cols) outputs, where its tiles alone would leave
-// SMs idle: the number that takes the least time, whole waves of the tiles (256 x 256 on an SM pair,
-// else about 128 x 128 on an SM) against the fp32 partials, written, read and added up by a launch
-// more. No part of fewer than 256 products, no more than 128 MiB of partials.
-int sum_parts(int64_t rows, int64_t cols, int64_t K) {
+// SMs idle: the number that takes the least time by whole waves of the tiles (256 x 512 or 256 x 256
+// on an SM pair, as the engine takes them, else about 128 x 128 on an SM) and by the fp32 partials,
+// written, read and added up by a launch more. No part of fewer than 256 products, no more than 512
+// MiB of partials; `partials`: one part is a partial too. (dx of 8192 x 4096, tiles of 3.4 waves, in two parts: 5.55 ms with the other
+// products, 5.75 in one; 1003 x 1032 in 15: 0.31, 0.36 in four.)
+int sum_parts(int64_t rows, int64_t cols, int64_t K, bool partials) {
   const bool pair = rows >= 256 && cols >= 256;
   const int64_t tw = pair ? 256 : 128, at_once = pair ? kSms / 2 : kSms;
-  const int64_t tiles = (rows + tw - 1) / tw * ((cols + tw - 1) / tw);
-  if (tiles >= 2 * at_once) return 1;
+  const int64_t down = (rows + tw - 1) / tw, tiles = down * ((cols + tw - 1) / tw);
+  auto waves = [&](int64_t n) { return (n + at_once - 1) / at_once; };
   int best = 1;
   double least = 0.0;
   for (int g = 1; g <= 32; ++g) {
-    if (g > 1 && (K / g < 256 || g * rows * cols * 4 > (128ll << 20))) break;
-    const double waves = static_cast<double>((tiles * g + at_once - 1) / at_once);
+    if (g > 1 && (K / g < 256 || g * rows * cols * 4 > (512ll << 20))) break;
+    double w = static_cast<double>(waves(tiles * g));
+    if (pair && cols % 512 == 0 && K / g >= 4096) {
+      const int64_t wide = down * (cols / 512) * g;  // a tile of two, at 10 % more of its work
+      if (wide >= 4 * at_once || 18 * waves(wide) < 10 * waves(tiles * g))
+        w = 1.8 * static_cast<double>(waves(wide));
+    }
     // seconds: a wave's products at 1.7e15 / (152 SMs), the partials at 5e12 bytes, their launch
-    const double t = waves * (2.0 * tw * tw * (K / g)) * at_once / 1.7e15 +
-                     (g > 1 ? g * rows * cols * 8.0 / 5e12 + 3e-6 : 0.0);
+    const double t = w * (2.0 * tw * tw * (K / g)) * at_once / 1.7e15 +
+                     (g > 1 || partials ? g * rows * cols * 8.0 / 5e12 + 3e-6 : 0.0);
     if (g == 1 || t < least) {
       best = g;
       least = t;
@@ -206,8 +230,8 @@ BwdPlan bwd_plan(int64_t M, int64_t v, int64_t h, tp_dtype dt) {
   const int64_t n = (v + most - 1) / most;
   P.piece = ((v + n - 1) / n + 255) / 256 * 256;
   P.pieces = static_cast<int>((v + P.piece - 1) / P.piece);
-  P.x_parts = dt == TP_BF16 ? sum_parts(M, h, std::min(P.piece, v)) : 1;
-  P.e_parts = dt == TP_BF16 ? sum_parts(std::min(P.piece, v), h, M) : 1;
+  P.x_parts = dt == TP_BF16 ? sum_parts(M, h, std::min(P.piece, v), P.pieces > 1) : 1;
+  P.e_parts = dt == TP_BF16 ? sum_parts(std::min(P.piece, v), h, M, false) : 1;
   P.x_direct = dt != TP_BF16 || (P.pieces == 1 && P.x_parts == 1);
   P.q = a256(M * P.piece * e);
   P.dx = P.x_direct ? 0 : a256(static_cast<size_t>(P.x_parts) * M * h * sizeof(float));
@@ -258,13 +282,17 @@ tp_status launch_vocab_linear_ce_fwd(const void* x, const void* E, const int32_t
   d.ce.counter = counter;
   d.ce.slots = &slots;
   TP_TRY(product(d, st));
-  const int rows = M <= 128 && slots <= 32 ? 128 : M >= 32 * kSms ? 32 : kRows;
-  TP_CUDA_TRY(launch_kernel(rows == 128  ? vocab_linear_join_kernel<128>
-                            : rows == 32 ? vocab_linear_join_kernel<32>
-                                         : vocab_linear_join_kernel<kRows>,
-                            static_cast<unsigned>((M + rows - 1) / rows), kJoinThreads, 0, st,
-                            d.ce.part, hit, targets, lse, row_loss, shard_loss, loss,
-                            reinterpret_cast<float*>(base + L.cta), counter, slots, M, v, N));
+  const int rows = M <= 128 && slots <= 32 ? 128 : M <= kRows * kSms ? kRows : 32;
+  const unsigned grid = static_cast<unsigned>((M + rows - 1) / rows);
+  auto join = [&](auto kern, bool early) {
+    return launch_after(early, kern, grid, kJoinThreads, st, d.ce.part, hit, targets, lse, row_loss,
+                        shard_loss, loss, reinterpret_cast<float*>(base + L.cta), counter, slots, M,
+                        v, N);
+  };
+  TP_CUDA_TRY(rows == 128     ? join(vocab_linear_join_kernel<128, true>, true)
+              : rows == kRows ? join(vocab_linear_join_kernel<kRows, true>, true)
+              : grid <= kSms  ? join(vocab_linear_join_kernel<32, true>, true)
+                              : join(vocab_linear_join_kernel<32, false>, false));
   count_launch();
   return N > kSumShards ? launch_vocab_ce_loss(row_loss, targets, shard_loss, loss, M, v, N, st)
                         : TP_OK;

@@ -781,7 +781,8 @@ TP_API tp_status tp_vocab_linear_ce_fwd(const void* x, const void* E, const int3
  * scale = 1/M for the mean loss. q is a row of zeros where the target lies outside [0, vocab).
  * The logits are formed again, a piece of the vocabulary at a time; of q one piece is kept in ws
  * (tp_vocab_linear_ce_workspace_size(0, ...) bytes: at most about 512 MiB, or 256 columns, of q,
- * and in bf16 fp32 sums of dx where they need several products), rounded to the element type.
+ * and in bf16 fp32 sums where one product does not make them: dx's, or up to 512 MiB of parts),
+ * rounded to the element type.
  * The fp32 sums over the vocabulary and over the rows go in a fixed order: results repeat.
  * M = 0 writes zeros to dE. Errors: as above. */
 TP_API tp_status tp_vocab_linear_ce_bwd(const void* x, const void* E, const int32_t* targets,

@@ -265,3 +265,32 @@ def test_words_that_are_not_16_byte_aligned(offset):
     T.tp_vocab_embed_scaled_fwd(ids, E, y, M, v, h, 1, 2.0, T.DType.BF16)
     ref = R.embed_fwd(ids, E, 2.0)
     within(y[:M * h].view(M, h), ref, ref.abs() * 2.0 ** -8 * 1.01)
+
+
+@pytest.mark.parametrize("M", [1300, 5000, 16400])
+def test_many_calls_without_a_pause(M):
+    """Kernels of more and of fewer CTAs than the SMs hold, one behind the other: every call ends, and
+    the last is right."""
+    v, h = 3000, 64
+    x, E, t = ce_case(M, v, h, BF)
+    d, n = T.DType.BF16, 0
+    big = 300_001  # a sort of more CTAs than there are SMs
+    for f in (0, 1):
+        n = max(n, T.tp_vocab_linear_ce_workspace_size(f, M, v, h, 1, d))
+    n = max(n, T.tp_vocab_embed_scaled_workspace_size(M, big, 8, d))
+    ws = poison(n)
+    out = [torch.empty(k, device="cuda") for k in (M, M, 1, 1)]
+    dx, dE = torch.empty(M, h, dtype=BF, device="cuda"), torch.empty(v, h, dtype=BF, device="cuda")
+    dB, g = torch.empty(big, 8, dtype=BF, device="cuda"), rnd(gen(1), M, 8)
+    for _ in range(10):
+        T.tp_vocab_linear_ce_fwd(x, E, t, *out, M, v, h, 1, d, ws, n)
+    for _ in range(5):
+        T.tp_vocab_linear_ce_fwd(x, E, t, *out, M, v, h, 1, d, ws, n)
+        T.tp_vocab_linear_ce_bwd(x, E, t, out[0], dx, dE, M, v, h, 1, 1.0 / M, d, ws, n)
+        T.tp_vocab_embed_scaled_bwd(t, g, dB, M, big, 8, 1, 1.0, 0, d, ws, n)
+    torch.cuda.synchronize()
+    assert T.tp_check_status() == 0
+    want = run_fwd(x, E, t, 1)
+    assert torch.equal(out[0], want[1]) and torch.equal(out[3], want[0])
+    wx, wE = run_bwd(x, E, t, want[1].clone(), 1.0 / M)
+    assert torch.equal(dx, wx) and torch.equal(dE, wE)
