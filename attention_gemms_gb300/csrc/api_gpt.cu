@@ -40,8 +40,10 @@ tp_status check_ends(int64_t M, int64_t v, int64_t h, int32_t N, tp_dtype dt) {
   return need(ends_ok(M, v, h), TP_ERR_SHAPE,
               "sizes too large (M or vocab > 2^30, h > 2^20, or a matrix >= 2^40 elements)");
 }
+constexpr int64_t kLinearCeF32Rows = 64ll * 65535;  // the fp32 engine's grid of 64-row tiles
 tp_status check_linear_ce(int64_t M, int64_t v, int64_t h, int32_t N, tp_dtype dt) {
   TP_TRY(check_ends(M, v, h, N, dt));
+  TP_TRY(need(dt != TP_F32 || M <= kLinearCeF32Rows, TP_ERR_SHAPE, "fp32: at most 64 * 65535 rows"));
   return need(dt != TP_BF16 || h % 8 == 0, TP_ERR_SHAPE, "bf16: h must be a multiple of 8");
 }
 
@@ -158,7 +160,7 @@ tp_status tp_vocab_ce_bwd(const void* logits, const int32_t* targets, const floa
 size_t tp_vocab_linear_ce_workspace_size(int fwd, int64_t M, int64_t vocab, int64_t h, int32_t N,
                                          tp_dtype dtype) {
   if ((dtype != TP_BF16 && dtype != TP_F32) || N < 1 || !ends_ok(M, vocab, h) || M == 0 ||
-      vocab % N || (dtype == TP_BF16 && h % 8))
+      vocab % N || (dtype == TP_BF16 && h % 8) || (dtype == TP_F32 && M > kLinearCeF32Rows))
     return 0;
   return vocab_linear_ce_ws_bytes(fwd != 0, M, vocab, h, dtype);
 }

@@ -761,7 +761,8 @@ TP_API tp_status tp_vocab_ce_bwd(const void* logits, const int32_t* targets, con
  * tp_vocab_ce_fwd / _bwd take them as a buffer. Results as there [张量并行 notes,
  * §损失计算层的并行化]: lse, row_loss (M), shard_loss (N, or NULL) and loss (1), fp32.
  *   x (M, h), E (vocab, h) read, finite (also rows of x without a target); targets (M) int32
- *   bf16: logits and their sums in fp32, h % 8 == 0, any vocab divisible by N; fp32: any sizes.
+ *   bf16: logits and their sums in fp32, h % 8 == 0, any vocab divisible by N; fp32: any sizes
+ *   with M <= 64 * 65535.
  *   lse, row_loss, shard_loss, loss, targets: 4-byte aligned.
  *   ws: tp_vocab_linear_ce_workspace_size(1, ...) bytes, uninitialised, for one call at a time
  *   (calls on one stream may share it). At most 1/16 of the bf16 logits, and 5 bytes per row.

@@ -58,6 +58,9 @@ def test_linear_ce_rules():
     assert status(T.tp_vocab_linear_ce_fwd, FWD, h=60) == S.SHAPE
     assert status(T.tp_vocab_linear_ce_bwd, BWD, h=60) == S.SHAPE
     assert status(T.tp_vocab_linear_ce_bwd, BWD, dx=None, dE=None) == S.INVALID_ARG
+    for fn, base, fwd in ((T.tp_vocab_linear_ce_fwd, FWD, 1), (T.tp_vocab_linear_ce_bwd, BWD, 0)):
+        assert status(fn, base, dtype=F32, M=64 * 65535 + 1) == S.SHAPE
+        assert T.tp_vocab_linear_ce_workspace_size(fwd, 64 * 65535 + 1, 100, 64, 2, F32) == 0
     assert status(T.tp_vocab_linear_ce_fwd, FWD, M=0, ws=None) == S.OK  # nothing launched
     assert status(T.tp_vocab_linear_ce_bwd, BWD, M=0, dE=None, ws=None) == S.OK
     assert status(T.tp_vocab_embed_scaled_fwd, EF, M=0) == S.OK

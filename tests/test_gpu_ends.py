@@ -174,8 +174,10 @@ def test_linear_ce_one_gradient_only(dt):
 
 
 def test_linear_ce_several_pieces():
-    """More of q than a piece holds: the pieces' shares of dx are added up."""
-    for M, v, h, N in ((8192, 50304, 64, 8), (70000, 4111, 72, 1)):
+    """More of q than a piece holds: the pieces' shares of dx are added up, by one-CTA and by pair
+    tiles, in one part and in two."""
+    for M, v, h, N in ((8192, 50304, 64, 8), (70000, 4111, 72, 1), (33000, 8300, 512, 1),
+                       (8192, 33000, 4096, 1)):
         assert M * v * 2 > 512 << 20
         x, E, t = ce_case(M, v, h, BF)
         lse = run_fwd(x, E, t, N)[1].clone()
