@@ -129,6 +129,21 @@ struct TcParams {  // CUtensorMap members carry their own 128-byte alignment
   int debug_hang;
 };
 
+// The problems of a launch: one, or two that do not depend on one another and run with the same tile
+// form (launch_gemm_tc_two), the second's tiles behind the first's.
+template <int NP>
+struct TcSet {
+  TcParams p[NP];
+  int tiles[NP];
+  __device__ __forceinline__ int total() const { return tiles[0] + (NP == 2 ? tiles[NP - 1] : 0); }
+  // the problem of tile t of the launch, which becomes a tile of that problem
+  __device__ __forceinline__ const TcParams& of(int& t) const {
+    if (NP == 1 || t < tiles[0]) return p[0];
+    t -= tiles[0];
+    return p[NP - 1];
+  }
+};
+
 // Optional wait-cycle counters (compile with -DTP_GEMM_STATS; off in normal builds):
 // per CTA, [0] producer waiting for a free stage, [1] MMA waiting for data,
 // [2] MMA waiting for a free accumulator, [3] epilogue waiting for an accumulator,
@@ -610,8 +625,10 @@ __device__ __forceinline__ void epi_chunk_tma(const TcParams& p, EpiStager& st, 
   }
 }
 
-template <int BN, int EPI, bool DEC>
-__global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_constant__ TcParams p) {
+template <int BN, int EPI, bool DEC, int NP>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_tc_kernel(const __grid_constant__ TcSet<NP> set) {
+  const TcParams& p = set.p[0];  // what the problems share; a tile's own p shadows it
   using C = TcCfg<BN, DEC>;
   constexpr int S = C::STAGES;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -657,6 +674,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
       tma_prefetch_desc(&p.tmB[s]);
     }
     if (p.paired) tma_prefetch_desc(&p.tmB[1]);
+    if (NP == 2) {
+      tma_prefetch_desc(&set.p[NP - 1].tmA[0]);
+      tma_prefetch_desc(&set.p[NP - 1].tmB[0]);
+    }
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
@@ -673,9 +694,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.ce.counter = 0;
   }
 
-  const int ntiles = p.tiles_m * p.tiles_n * p.groups;
-  const int nkb = (p.nseg * p.kb_per_seg + C::KSUB - 1) / C::KSUB;  // stages of a tile
+  auto stages_of = [](const TcParams& q) {  // of a tile
+    return (q.nseg * q.kb_per_seg + C::KSUB - 1) / C::KSUB;
+  };
   const int bn_logical = p.paired ? BN / 2 : BN;
+  const int ntiles = set.total();
   uint32_t issued = 0;      // producer: loads issued
   bool mma_issued = false;  // MMA thread: any MMA issued
 
@@ -687,7 +710,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
       uint32_t stage = 0, phase = 0;
       bool ok = true;
       [[maybe_unused]] const long long t_start = TP_CLK();
-      for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+      for (int i = blockIdx.x; i < ntiles && ok; i += gridDim.x) {
+        int t = i;
+        const TcParams& p = set.of(t);
+        const int nkb = stages_of(p);
         const TileCoord tc = tile_coord(p, t);
         const int m0 = tc.mt * BM;
         const int n0 = tc.nt * bn_logical;
@@ -765,14 +791,17 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
   } else if (warp == 1) {
     if (lane == 0) {
       // ------------------------------------------------------------ MMA issuer
-      const uint32_t idesc = idesc_bf16_f32(BM, BN, p.a_mn, p.b_mn);
-      const uint32_t a_lbo = p.a_mn ? 8192u : 16u, b_lbo = p.b_mn ? 8192u : 16u;
-      const uint32_t a_kstep = p.a_mn ? 2048u : 32u, b_kstep = p.b_mn ? 2048u : 32u;
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool ok = true;
       if (p.debug_hang) ok = mbar_wait(never_bar, 0, p.timeout_ns, abort_flag);
       [[maybe_unused]] const long long t_start = TP_CLK();
-      for (int t = blockIdx.x; t < ntiles && ok; t += gridDim.x) {
+      for (int i = blockIdx.x; i < ntiles && ok; i += gridDim.x) {
+        int t = i;
+        const TcParams& p = set.of(t);
+        const int nkb = stages_of(p);
+        const uint32_t idesc = idesc_bf16_f32(BM, BN, p.a_mn, p.b_mn);
+        const uint32_t a_lbo = p.a_mn ? 8192u : 16u, b_lbo = p.b_mn ? 8192u : 16u;
+        const uint32_t a_kstep = p.a_mn ? 2048u : 32u, b_kstep = p.b_mn ? 2048u : 32u;
         [[maybe_unused]] long long tw = TP_CLK();
         if (!mbar_wait(tempty_bar(acc), acc_phase ^ 1u, p.timeout_ns, abort_flag)) {
           ok = false;
@@ -827,7 +856,9 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
     // -------------------------------------------------------------- epilogue
     const int quad = warp & 3;  // TMEM lanes [32*quad, 32*quad + 32)
     uint32_t acc = 0, acc_phase = 0;
-    for (int t = blockIdx.x; t < ntiles; t += gridDim.x) {
+    for (int i = blockIdx.x; i < ntiles; i += gridDim.x) {
+      int t = i;
+      const TcParams& p = set.of(t);
       const TileCoord tc = tile_coord(p, t);
       int ok = 1;
       [[maybe_unused]] const long long tw = TP_CLK();
@@ -971,9 +1002,10 @@ struct PairCfg {
 static_assert(PairCfg<2>::SMEM <= 232448 && PairCfg<1>::SMEM <= 232448 &&
                   PairCfg<1, 8>::SMEM <= 232448, "shared memory per CTA");
 
-template <int EPI, int WN, int EW = PairCfg<WN>::EPI_WARPS>
+template <int EPI, int WN, int EW, int NP>
 __global__ void __launch_bounds__(PairCfg<WN, EW>::THREADS, 1)
-    gemm_tc2_kernel(const __grid_constant__ TcParams p) {
+    gemm_tc2_kernel(const __grid_constant__ TcSet<NP> set) {
+  const TcParams& p = set.p[0];  // what the problems share; a tile's own p shadows it
   using C = PairCfg<WN, EW>;
   constexpr int S = C::STAGES;
   constexpr int A_BYTES = 128 * BK * 2;
@@ -1025,6 +1057,10 @@ __global__ void __launch_bounds__(PairCfg<WN, EW>::THREADS, 1)
       tma_prefetch_desc(&p.tmB[s]);
     }
     if (p.paired) tma_prefetch_desc(&p.tmB[1]);
+    if (NP == 2) {
+      tma_prefetch_desc(&set.p[NP - 1].tmA[0]);
+      tma_prefetch_desc(&set.p[NP - 1].tmB[0]);
+    }
   }
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(tmem_slot), 512);
@@ -1044,9 +1080,8 @@ __global__ void __launch_bounds__(PairCfg<WN, EW>::THREADS, 1)
 
   const int pair = blockIdx.x >> 1;
   const int npairs = gridDim.x >> 1;
-  const int ntiles = p.tiles_m * p.tiles_n * p.groups;
-  const int nkb = p.nseg * p.kb_per_seg;
   const int bn_logical = p.paired ? 128 : 256;
+  const int ntiles = set.total();
   uint32_t issued = 0;
 
   if (warp == 0 || (TP_PAIR_DUAL && warp == 6)) {
@@ -1058,7 +1093,10 @@ __global__ void __launch_bounds__(PairCfg<WN, EW>::THREADS, 1)
       bool ok = true;
       [[maybe_unused]] const long long t_start = TP_CLK();
       const uint32_t lead_full0 = mapa_shared(full_bar(0), 0);
-      for (int t = pair; t < ntiles && ok; t += npairs) {
+      for (int i = pair; i < ntiles && ok; i += npairs) {
+        int t = i;
+        const TcParams& p = set.of(t);
+        const int nkb = p.nseg * p.kb_per_seg;
         const TileCoord tc = tile_coord(p, t);
         const int m0 = tc.mt * 256 + static_cast<int>(rank) * 128;
         const int n0 = tc.nt * bn_logical * WN;
@@ -1136,9 +1174,13 @@ __global__ void __launch_bounds__(PairCfg<WN, EW>::THREADS, 1)
   } else if (warp == 1) {
     if (lane == 0 && leader) {
       // ------------------------------------------------------------ pair MMA issuer
-      const uint32_t idesc = idesc_bf16_f32(256, 256, p.a_mn, p.b_mn);
-      const uint32_t a_lbo = p.a_mn ? 8192u : 16u, b_lbo = p.b_mn ? 8192u : 16u;
-      const uint32_t a_kstep = p.a_mn ? 2048u : 32u, b_kstep = p.b_mn ? 2048u : 32u;
+      uint32_t idesc, a_lbo, b_lbo, a_kstep, b_kstep;
+      auto operands = [&](const TcParams& q) {
+        idesc = idesc_bf16_f32(256, 256, q.a_mn, q.b_mn);
+        a_lbo = q.a_mn ? 8192u : 16u, b_lbo = q.b_mn ? 8192u : 16u;
+        a_kstep = q.a_mn ? 2048u : 32u, b_kstep = q.b_mn ? 2048u : 32u;
+      };
+      operands(p);
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool ok = true;
       if (p.debug_hang) ok = mbar_wait(never_bar, 0, p.timeout_ns, abort_flag);
@@ -1180,7 +1222,11 @@ __global__ void __launch_bounds__(PairCfg<WN, EW>::THREADS, 1)
           phase ^= 1u;
         }
       };
-      for (int t = pair; t < ntiles && ok; t += npairs) {
+      for (int i = pair; i < ntiles && ok; i += npairs) {
+        int t = i;
+        const TcParams& p = set.of(t);
+        const int nkb = p.nseg * p.kb_per_seg;
+        if (NP == 2) operands(p);
         [[maybe_unused]] long long tw = TP_CLK();
         // narrow: accumulator `acc` drained; wide: the first half of the accumulator
         if (!mbar_wait(tempty_bar(WN == 2 ? 0 : acc), acc_phase ^ 1u, p.timeout_ns, abort_flag)) {
@@ -1283,7 +1329,9 @@ __global__ void __launch_bounds__(PairCfg<WN, EW>::THREADS, 1)
     const int epi_slot = warp < 6 ? warp - 2 : warp - kEpiHi0 + 4;
     EpiStager stg{smem_u32(staging) + static_cast<uint32_t>(epi_slot) * 4096u, 0u, lane};
     uint32_t acc = 0, acc_phase = 0;
-    for (int t = pair; t < ntiles; t += npairs) {
+    for (int i = pair; i < ntiles; i += npairs) {
+      int t = i;
+      const TcParams& p = set.of(t);
       const TileCoord tc = tile_coord(p, t);
       int ok = 1;
       [[maybe_unused]] const long long tw = TP_CLK();
@@ -1407,7 +1455,7 @@ __global__ void __launch_bounds__(PairCfg<WN, EW>::THREADS, 1)
       }
     }
     // the staged stores have read shared memory and written their outputs before exit
-    if (p.tma_out) {
+    if (p.tma_out || (NP == 2 && set.p[NP - 1].tma_out)) {
       if (lane == 0) bulk_wait_all();
       __syncwarp();
     }
@@ -1533,40 +1581,40 @@ tp_status make_out_map(CUtensorMap* m, void* ptr, bool f32, int64_t N, int64_t M
   return TP_OK;
 }
 
-template <int BN, int EPI, bool DEC>
-tp_status launch_bn_epi(const TcParams& prm, int grid, cudaStream_t st) {
-  auto kern = gemm_tc_kernel<BN, EPI, DEC>;
+template <int BN, int EPI, bool DEC, int NP = 1>
+tp_status launch_bn_epi(TcSet<NP>& set, int grid, cudaStream_t st) {
+  auto kern = gemm_tc_kernel<BN, EPI, DEC, NP>;
   static std::atomic<uint64_t> attr_set{0};  // per instantiation and device
   if (needs_setup(attr_set)) {
     TP_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      TcCfg<BN, DEC>::SMEM_BYTES));
     mark_device(attr_set);
   }
-  TP_CUDA_TRY(launch_kernel(kern, grid, kThreads, TcCfg<BN, DEC>::SMEM_BYTES, st, prm));
+  TP_CUDA_TRY(launch_kernel(kern, grid, kThreads, TcCfg<BN, DEC>::SMEM_BYTES, st, set));
   count_launch();
   return TP_OK;
 }
 
 template <int BN, bool DEC>
-tp_status launch_bn(int epi, const TcParams& prm, int grid, cudaStream_t st) {
+tp_status launch_bn(int epi, TcSet<1>& set, int grid, cudaStream_t st) {
   switch (epi) {
-    case EPI_STORE: return launch_bn_epi<BN, EPI_STORE, DEC>(prm, grid, st);
-    case EPI_GELU: return launch_bn_epi<BN, EPI_GELU, DEC>(prm, grid, st);
-    case EPI_SWIGLU: return launch_bn_epi<BN, EPI_SWIGLU, DEC>(prm, grid, st);
-    case EPI_DGELU: return launch_bn_epi<BN, EPI_DGELU, DEC>(prm, grid, st);
-    case EPI_DSWIGLU: return launch_bn_epi<BN, EPI_DSWIGLU, DEC>(prm, grid, st);
-    case EPI_PAIR: return launch_bn_epi<BN, EPI_PAIR, DEC>(prm, grid, st);
+    case EPI_STORE: return launch_bn_epi<BN, EPI_STORE, DEC>(set, grid, st);
+    case EPI_GELU: return launch_bn_epi<BN, EPI_GELU, DEC>(set, grid, st);
+    case EPI_SWIGLU: return launch_bn_epi<BN, EPI_SWIGLU, DEC>(set, grid, st);
+    case EPI_DGELU: return launch_bn_epi<BN, EPI_DGELU, DEC>(set, grid, st);
+    case EPI_DSWIGLU: return launch_bn_epi<BN, EPI_DSWIGLU, DEC>(set, grid, st);
+    case EPI_PAIR: return launch_bn_epi<BN, EPI_PAIR, DEC>(set, grid, st);
   }
   if constexpr (!DEC) {  // few rows have tiles of their own
-    if (epi == EPI_LSE) return launch_bn_epi<BN, EPI_LSE, false>(prm, grid, st);
-    if (epi == EPI_DCE) return launch_bn_epi<BN, EPI_DCE, false>(prm, grid, st);
+    if (epi == EPI_LSE) return launch_bn_epi<BN, EPI_LSE, false>(set, grid, st);
+    if (epi == EPI_DCE) return launch_bn_epi<BN, EPI_DCE, false>(set, grid, st);
   }
   return fail(TP_ERR_INVALID_ARG, "unknown epilogue");
 }
 
-template <int EPI, int WN, int EW = PairCfg<WN>::EPI_WARPS>
-tp_status launch_pair_epi(const TcParams& prm, int64_t ntiles, cudaStream_t st) {
-  auto kern = gemm_tc2_kernel<EPI, WN, EW>;
+template <int EPI, int WN, int EW = PairCfg<WN>::EPI_WARPS, int NP = 1>
+tp_status launch_pair_epi(TcSet<NP>& set, cudaStream_t st) {
+  auto kern = gemm_tc2_kernel<EPI, WN, EW, NP>;
   constexpr int kSmem = PairCfg<WN, EW>::SMEM;
   static std::atomic<int> max_pairs_dev[64];  // per instantiation and device (0: unknown)
   int dev = 0;
@@ -1595,36 +1643,37 @@ tp_status launch_pair_epi(const TcParams& prm, int64_t ntiles, cudaStream_t st) 
     max_pairs = n;
     if (dev >= 0) max_pairs_dev[dev].store(n);
   }
+  int64_t ntiles = 0;
+  for (int n : set.tiles) ntiles += n;
   const int pairs = static_cast<int>(std::min<int64_t>(ntiles, max_pairs));
   cfg.gridDim = dim3(2 * static_cast<unsigned>(pairs), 1, 1);
   cfg.numAttrs = pdl_enabled() ? 2 : 1;
-  TP_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, prm));
+  TP_CUDA_TRY(cudaLaunchKernelEx(&cfg, kern, set));
   count_launch();
   return TP_OK;
 }
 
 template <int WN>
-tp_status launch_pair_wn(int epi, const TcParams& prm, int64_t ntiles, cudaStream_t st) {
+tp_status launch_pair_wn(int epi, TcSet<1>& set, cudaStream_t st) {
   switch (epi) {
-    case EPI_STORE: return launch_pair_epi<EPI_STORE, WN>(prm, ntiles, st);
-    case EPI_GELU: return launch_pair_epi<EPI_GELU, WN>(prm, ntiles, st);
-    case EPI_SWIGLU: return launch_pair_epi<EPI_SWIGLU, WN>(prm, ntiles, st);
-    case EPI_DGELU: return launch_pair_epi<EPI_DGELU, WN>(prm, ntiles, st);
-    case EPI_DSWIGLU: return launch_pair_epi<EPI_DSWIGLU, WN>(prm, ntiles, st);
-    case EPI_PAIR: return launch_pair_epi<EPI_PAIR, WN>(prm, ntiles, st);
-    case EPI_LSE: return launch_pair_epi<EPI_LSE, WN>(prm, ntiles, st);
-    case EPI_DCE: return launch_pair_epi<EPI_DCE, WN>(prm, ntiles, st);
+    case EPI_STORE: return launch_pair_epi<EPI_STORE, WN>(set, st);
+    case EPI_GELU: return launch_pair_epi<EPI_GELU, WN>(set, st);
+    case EPI_SWIGLU: return launch_pair_epi<EPI_SWIGLU, WN>(set, st);
+    case EPI_DGELU: return launch_pair_epi<EPI_DGELU, WN>(set, st);
+    case EPI_DSWIGLU: return launch_pair_epi<EPI_DSWIGLU, WN>(set, st);
+    case EPI_PAIR: return launch_pair_epi<EPI_PAIR, WN>(set, st);
+    case EPI_LSE: return launch_pair_epi<EPI_LSE, WN>(set, st);
+    case EPI_DCE: return launch_pair_epi<EPI_DCE, WN>(set, st);
   }
   return fail(TP_ERR_INVALID_ARG, "unknown epilogue");
 }
 
 // epi8: eight epilogue warps beside narrow tiles, see short_sum
-tp_status launch_pair(int epi, bool wide, bool epi8, const TcParams& prm, int64_t ntiles,
-                      cudaStream_t st) {
-  if (epi8 && epi == EPI_STORE) return launch_pair_epi<EPI_STORE, 1, 8>(prm, ntiles, st);
-  if (epi8 && epi == EPI_LSE) return launch_pair_epi<EPI_LSE, 1, 8>(prm, ntiles, st);
-  if (epi8 && epi == EPI_DCE) return launch_pair_epi<EPI_DCE, 1, 8>(prm, ntiles, st);
-  return wide ? launch_pair_wn<2>(epi, prm, ntiles, st) : launch_pair_wn<1>(epi, prm, ntiles, st);
+tp_status launch_pair(int epi, bool wide, bool epi8, TcSet<1>& set, cudaStream_t st) {
+  if (epi8 && epi == EPI_STORE) return launch_pair_epi<EPI_STORE, 1, 8>(set, st);
+  if (epi8 && epi == EPI_LSE) return launch_pair_epi<EPI_LSE, 1, 8>(set, st);
+  if (epi8 && epi == EPI_DCE) return launch_pair_epi<EPI_DCE, 1, 8>(set, st);
+  return wide ? launch_pair_wn<2>(epi, set, st) : launch_pair_wn<1>(epi, set, st);
 }
 
 std::atomic<int> g_debug_hang{0};
@@ -1664,8 +1713,15 @@ bool short_sum(int epi, int64_t k_tile) {
   return epi == EPI_LSE ? k_tile <= 256 : (epi == EPI_STORE || epi == EPI_DCE) && k_tile <= 512;
 }
 
-tp_status launch_gemm_tc(const GemmDesc& d, cudaStream_t st) {
-  if (d.M <= 0 || d.N <= 0 || d.K <= 0) return TP_OK;
+namespace {
+// How a problem is launched: the tile form, and the number of tiles
+struct TcPlan {
+  bool pair = false, wide = false, epi8 = false, few = false, dec = false;
+  int BN = 0;
+  int64_t tiles = 0;
+};
+
+tp_status plan_gemm_tc(const GemmDesc& d, TcParams& prm, TcPlan& plan) {
   if (d.paired && d.nseg != 1) return fail(TP_ERR_INVALID_ARG, "paired GEMM needs one K segment");
   if (d.N % 8 != 0 && d.epi != EPI_LSE)  // which stores nothing of D
     return fail(TP_ERR_SHAPE, "GEMM output width must be a multiple of 8");
@@ -1733,7 +1789,6 @@ tp_status launch_gemm_tc(const GemmDesc& d, cudaStream_t st) {
   const bool dec = few || (!pair && BN == 128 && !d.a_mn && d.M <= 64);
   const int a_rows = dec ? static_cast<int>((d.M + 7) / 8 * 8) : BM;
 
-  TcParams prm;
   memset(&prm, 0, sizeof(prm));
   const int nb = d.paired ? 2 : d.nseg;
   // MN-major operands whose rows are whole 64-column chunks use one 3-D load per stage
@@ -1821,18 +1876,67 @@ tp_status launch_gemm_tc(const GemmDesc& d, cudaStream_t st) {
   prm.timeout_ns = wait_timeout_ns();
   prm.debug_hang = g_debug_hang.load();
 
-  const int64_t ntiles = static_cast<int64_t>(prm.tiles_m) * prm.tiles_n * prm.groups;
-  if (ntiles > (1ll << 30)) return fail(TP_ERR_SHAPE, "problem too large");
-  if (pair) return launch_pair(epi, wide, epi8, prm, ntiles, st);
-  const int grid = static_cast<int>(
-      std::min<int64_t>(ntiles, static_cast<int64_t>(device_sm_count()) * (dec ? TP_DEC_CTAS_PER_SM : 1)));
-  if (few)
-    return epi == EPI_LSE ? launch_bn_epi<64, EPI_LSE, true>(prm, grid, st)
-                          : launch_bn_epi<64, EPI_DCE, true>(prm, grid, st);
-  if (dec) return launch_bn<128, true>(epi, prm, grid, st);
-  if (BN == 64) return launch_bn<64, false>(epi, prm, grid, st);
-  return BN == 256 ? launch_bn<256, false>(epi, prm, grid, st)
-                   : launch_bn<128, false>(epi, prm, grid, st);
+  plan.pair = pair;
+  plan.wide = wide;
+  plan.epi8 = epi8;
+  plan.few = few;
+  plan.dec = dec;
+  plan.BN = BN;
+  plan.tiles = static_cast<int64_t>(prm.tiles_m) * prm.tiles_n * prm.groups;
+  if (plan.tiles > (1ll << 30)) return fail(TP_ERR_SHAPE, "problem too large");
+  return TP_OK;
+}
+}  // namespace
+
+tp_status launch_gemm_tc(const GemmDesc& d, cudaStream_t st) {
+  if (d.M <= 0 || d.N <= 0 || d.K <= 0) return TP_OK;
+  TcSet<1> set;
+  TcPlan plan;
+  TP_TRY(plan_gemm_tc(d, set.p[0], plan));
+  set.tiles[0] = static_cast<int>(plan.tiles);
+  const int epi = d.epi;
+  if (plan.pair) return launch_pair(epi, plan.wide, plan.epi8, set, st);
+  const int grid = static_cast<int>(std::min<int64_t>(
+      plan.tiles, static_cast<int64_t>(device_sm_count()) * (plan.dec ? TP_DEC_CTAS_PER_SM : 1)));
+  if (plan.few)
+    return epi == EPI_LSE ? launch_bn_epi<64, EPI_LSE, true>(set, grid, st)
+                          : launch_bn_epi<64, EPI_DCE, true>(set, grid, st);
+  if (plan.dec) return launch_bn<128, true>(epi, set, grid, st);
+  if (plan.BN == 64) return launch_bn<64, false>(epi, set, grid, st);
+  return plan.BN == 256 ? launch_bn<256, false>(epi, set, grid, st)
+                        : launch_bn<128, false>(epi, set, grid, st);
+}
+
+tp_status launch_gemm_tc_two(const GemmDesc& a, const GemmDesc& b, cudaStream_t st) {
+  // the longer sums first, so that no long tile begins last
+  const bool swap = static_cast<int64_t>(a.nseg) * a.K < static_cast<int64_t>(b.nseg) * b.K;
+  const GemmDesc* d[2] = {swap ? &b : &a, swap ? &a : &b};
+  TcSet<2> set;
+  TcPlan plan[2];
+  for (int i = 0; i < 2; ++i) {
+    TP_TRY(plan_gemm_tc(*d[i], set.p[i], plan[i]));
+    set.tiles[i] = static_cast<int>(plan[i].tiles);
+  }
+  const int64_t tiles = plan[0].tiles + plan[1].tiles;
+  const bool alike = plan[0].pair == plan[1].pair && plan[0].wide == plan[1].wide &&
+                     plan[0].epi8 == plan[1].epi8 && plan[0].BN == plan[1].BN && !plan[0].dec &&
+                     !plan[1].dec;
+  // up to a wave of one-CTA tiles or two of pair tiles; us of dx, dE and the logits' gradient, together
+  // and one by one: 300 x 1500 x 256 15.5 and 19.3, 1000 x 6000 x 512 41 and 44. More lose: one-CTA
+  // tiles that share a CTA, 1000 x 1000 x 1000 34.6 and 29.8; the order in which tiles share operands in
+  // L2, 4878 x 5168 x 1336 217 and 198, 8192 x 50304 x 2048 3370 and 3090.
+  if (!alike || tiles > device_sm_count()) {
+    TP_TRY(launch_gemm_tc(a, st));
+    return launch_gemm_tc(b, st);
+  }
+  if (plan[0].pair)
+    return plan[0].wide   ? launch_pair_epi<EPI_STORE, 2, 8, 2>(set, st)
+           : plan[0].epi8 ? launch_pair_epi<EPI_STORE, 1, 8, 2>(set, st)
+                          : launch_pair_epi<EPI_STORE, 1, PairCfg<1>::EPI_WARPS, 2>(set, st);
+  const int grid = static_cast<int>(std::min<int64_t>(tiles, device_sm_count()));
+  return plan[0].BN == 256   ? launch_bn_epi<256, EPI_STORE, false, 2>(set, grid, st)
+         : plan[0].BN == 128 ? launch_bn_epi<128, EPI_STORE, false, 2>(set, grid, st)
+                             : launch_bn_epi<64, EPI_STORE, false, 2>(set, grid, st);
 }
 
 }  // namespace tp

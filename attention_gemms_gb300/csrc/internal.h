@@ -189,6 +189,9 @@ struct GemmDesc {
 };
 
 tp_status launch_gemm_tc(const GemmDesc& d, cudaStream_t st);    // bf16, tcgen05
+// two independent plain products (EPI_STORE, unpaired), in one launch where they take the same tile form;
+// each is the same bit for bit as by itself
+tp_status launch_gemm_tc_two(const GemmDesc& a, const GemmDesc& b, cudaStream_t st);
 bool gemv_eligible(const GemmDesc& d);                             // bf16, M <= 4
 tp_status launch_gemv(const GemmDesc& d, cudaStream_t st);
 tp_status launch_gemm_simt(const GemmDesc& d, cudaStream_t st);  // fp32, CUDA cores

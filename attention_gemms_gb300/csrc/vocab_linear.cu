@@ -363,8 +363,8 @@ tp_status launch_vocab_linear_ce_bwd(const void* x, const void* E, const int32_t
       TP_TRY(launch_gemm_simt_two(gx, ge, st));
       continue;
     }
-    if (dx) TP_TRY(launch_gemm_tc(gx, st));
-    if (dE) TP_TRY(launch_gemm_tc(ge, st));
+    if (dx && dE) TP_TRY(launch_gemm_tc_two(gx, ge, st));
+    else TP_TRY(launch_gemm_tc(dx ? gx : ge, st));
     if (dE && P.e_parts > 1) TP_TRY(launch_shard_reduce(es, nullptr, dEi, P.e_parts, n, h, dt, st));
   }
   if (dx && !P.x_direct) return launch_shard_reduce(xs, nullptr, dx, P.x_parts, M, h, dt, st);
