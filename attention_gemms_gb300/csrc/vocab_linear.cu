@@ -10,6 +10,11 @@
 // Backward: the vocabulary goes by in pieces. Of each piece the logits are formed again and leave
 // the accumulator as q (EPI_DCE, in the element type: the operand of the next two products), which
 // gives the piece's rows of dE and its share of dx. One piece's q is all that is kept.
+// The products bound both: 2 M v h operations forward, 6 backward. bf16, 8192 rows, v = 50304: h = 2048
+// 0.96 ms (1756 TFLOP/s, the rate that a library product sustains under the power cap) and 3.1 ms (1630),
+// h = 4096 backward 5.98 ms (1694). The exponentials hide: 6 % of their pipe, 17 % of the issue slots,
+// an epilogue of 3.5 k cycles in a tile's 17 k at h = 1032. For few rows HBM does: 37 rows of h = 4096
+// read E at 6 TB/s (74 us with the join).
 #include <cuda_runtime.h>
 
 #include <algorithm>
