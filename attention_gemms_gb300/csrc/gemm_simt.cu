@@ -178,33 +178,47 @@ __device__ __forceinline__ void simt_tile(const SimtParams& p, int bx, int by, i
     nn = p.b_mn ? e % TN : e / TK;
     kk = p.b_mn ? e / TN : e % TK;
   };
-  auto load = [&](int s, int64_t k0) {  // one K step of segment s: global -> registers
-    const float* A = p.A[s];
-    const int64_t lda = p.lda[s];
+  // a thread's elements of an operand's tile and K step (a_idx, b_idx): one pointer, a fixed distance
+  // apart (K-major: 8 rows, MN-major: 4 values of k)
+  static_assert(TM == 64 && TN == 64 && TK == 32, "distances below");
+  auto fetch = [&](const float* X, int64_t ld, bool mn, int64_t x0, int64_t x_end, int64_t kg,
+                   int64_t k0, float* r) {
+    const int t = threadIdx.x;
+    const float* q = X + (mn ? (kg + t / 64) * ld + x0 + t % 64 : (x0 + t / 32) * ld + kg + t % 32);
+    const int64_t step = mn ? 4 * ld : 8 * ld;
+    const bool in = mn ? x0 + t % 64 < x_end : k0 + t % 32 < p.K;
+    // how many of them there are
+    const int64_t n = !in ? 0 : mn ? (p.K - k0 - t / 64 + 3) / 4 : (x_end - x0 - t / 32 + 7) / 8;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      int mm, kk;
-      a_idx(threadIdx.x + i * 256, mm, kk);
-      const int64_t gm = m0 + mm, lk = k0 + kk, gk = p.k0[s] + g * p.K + lk;
-      ra[i] = (gm < p.M && lk < p.K) ? (p.a_mn ? A[gk * lda + gm] : A[gm * lda + gk]) : 0.0f;
+      r[i] = i < n ? *q : 0.0f;
+      q += step;
     }
+  };
+  auto load = [&](int s, int64_t k0) {  // one K step of segment s: global -> registers
+    const int64_t kg = p.k0[s] + g * p.K + k0;
+    fetch(p.A[s], p.lda[s], p.a_mn, m0, p.M, kg, k0, ra);
 #pragma unroll
-    for (int h = 0; h < NB; ++h) {
-      const float* B = p.B[PAIRED ? h : s];
-      const int64_t ldb = p.ldb[PAIRED ? h : s];
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        int nn, kk;
-        b_idx(threadIdx.x + i * 256, nn, kk);
-        const int64_t gn = n0 + nn, lk = k0 + kk, gk = p.k0[s] + g * p.K + lk;
-        rb[h][i] = (gn < p.N && lk < p.K) ? (p.b_mn ? B[gk * ldb + gn] : B[gn * ldb + gk]) : 0.0f;
-      }
-    }
+    for (int h = 0; h < NB; ++h)
+      fetch(p.B[PAIRED ? h : s], p.ldb[PAIRED ? h : s], p.b_mn, n0, p.N, kg, k0, rb[h]);
   };
   const int64_t steps = (p.K + TK - 1) / TK, total = steps * p.nseg;
   const int64_t per = (total + split - 1) / split;  // this CTA's K steps: [it0, it1)
   const int64_t it0 = rank * per, it1 = it0 + per < total ? it0 + per : total;
-  if (it0 < it1) load(static_cast<int>(it0 / steps), (it0 % steps) * TK);
+  int seg = 0;  // the segment and its step that are loaded next
+  int64_t ks = it0;
+  while (ks >= steps && seg + 1 < p.nseg) {
+    ks -= steps;
+    ++seg;
+  }
+  auto load_next = [&]() {
+    load(seg, ks * TK);
+    if (++ks == steps) {
+      ks = 0;
+      ++seg;
+    }
+  };
+  if (it0 < it1) load_next();
   for (int64_t it = it0; it < it1; ++it) {
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {  // registers -> shared (the previous step's reads ended
@@ -219,10 +233,7 @@ __device__ __forceinline__ void simt_tile(const SimtParams& p, int bx, int by, i
       }
     }
     __syncthreads();
-    if (it + 1 < it1) {  // the next step's loads fly while this step's FMAs run
-      const int64_t nx = it + 1;
-      load(static_cast<int>(nx / steps), (nx % steps) * TK);
-    }
+    if (it + 1 < it1) load_next();  // the next step's loads fly while this step's FMAs run
 #pragma unroll
     for (int kk = 0; kk < TK; ++kk) {
       float a[4], b[4], b2[4];
@@ -540,12 +551,12 @@ cudaError_t launch_k(SimtParams p, dim3 grid, cudaStream_t st) {
   return launch_split<gemm_simt_kernel<EPI, PAIRED>>(p.split, grid, st, p);
 }
 
-// split K over a cluster while the tiles (times the split) stay within half the SMs and every CTA
-// keeps at least one K step: at these sizes a K step is a global-load latency, so fewer steps per
-// CTA is a shorter launch
-int simt_split(int64_t tiles, int64_t ksteps) {
+// split K over a cluster while the tiles (times the split) stay within `most` CTAs (half the SMs) and
+// every CTA keeps at least one K step: at these sizes a K step is a global-load latency, so fewer steps
+// per CTA is a shorter launch
+int simt_split(int64_t tiles, int64_t ksteps, int64_t most) {
   int split = 1;
-  while (split < 8 && tiles * split * 4 <= device_sm_count() && ksteps >= 2 * split) split *= 2;
+  while (split < 8 && tiles * split * 2 <= most && ksteps >= 2 * split) split *= 2;
   return split;
 }
 
@@ -609,7 +620,9 @@ tp_status launch_gemm_simt(const GemmDesc& d, cudaStream_t st) {
     return fail(TP_ERR_SHAPE, "fp32 GEMM grid too large");
   dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy), static_cast<unsigned>(d.groups));
   const bool pr = d.paired;
-  p.split = pr ? 1 : simt_split(gx * gy * d.groups, simt_ksteps(d));
+  // (the cross-entropy's products, whose tiles end in exponentials: up to two CTAs per SM)
+  const bool ce = d.epi == EPI_LSE || d.epi == EPI_DCE;
+  p.split = pr ? 1 : simt_split(gx * gy * d.groups, simt_ksteps(d), ce ? 2 * device_sm_count() : device_sm_count() / 2);
   cudaError_t e = cudaSuccess;
   switch (d.epi) {
     case EPI_STORE: e = launch_k<EPI_STORE, false>(p, grid, st); break;
@@ -649,12 +662,16 @@ tp_status launch_gemm_simt_two(const GemmDesc& a, const GemmDesc& b, cudaStream_
     here[i] = here[i] && d[i]->out[0];
   }
   if (!here[0] && !here[1]) return TP_OK;
-  // the longer sum per CTA is halved while it has two steps and four CTAs of an SM hold them all
+  // the longer sum per CTA is halved while it has two steps (one takes a CTA 2 us) and four CTAs of an
+  // SM hold them all
   while (true) {
-    const int i = steps[0] / split[0] >= steps[1] / split[1] ? 0 : 1;
-    if (split[i] == 8 || steps[i] < 2 * split[i] ||
-        tiles[0] * split[0] + tiles[1] * split[1] + tiles[i] * split[i] > 4 * device_sm_count())
-      break;
+    int i = -1;
+    for (int j = 0; j < 2; ++j)
+      if (split[j] < 8 && steps[j] >= 2 * split[j] &&
+          tiles[0] * split[0] + tiles[1] * split[1] + tiles[j] * split[j] <= 4 * device_sm_count() &&
+          (i < 0 || steps[j] * split[i] > steps[i] * split[j]))
+        i = j;
+    if (i < 0) break;
     split[i] *= 2;
   }
   int64_t cluster = std::max(split[0], split[1]);
