@@ -359,3 +359,20 @@ def test_embed_scaled_bwd_agrees_with_the_scan():
     T.tp_vocab_embed_bwd(ids, dx, want, 900, 500, 96, 4, 0, T.DType.F32)
     g_, a, n = R.embed_bwd(ids, dx, 500, 1.0)
     within(run_embed_bwd(ids, dx, 500, 1.0), want.double(), 2 * R.embed_bwd_bound(g_, a, n, 1.0, F32))
+
+
+@pytest.mark.parametrize("M,v,h,dt", [(200_000, 1000, 64, BF), (5, 1_000_003, 64, BF), (70, 600_001, 24, BF),
+                                      (100_000, 130, 8, F32), (3, 400_000, 5, F32)])
+def test_linear_ce_long(M, v, h, dt):
+    check_ce(*ce_case(M, v, h, dt, seed=21), 1)
+
+
+@pytest.mark.parametrize("M,v,h,kind", [(2_200_000, 300, 8, "mixed"), (2_200_000, 40_000, 2, "same"),
+                                        (300, 2_000_000, 16, "mixed"), (900_000, 151_000, 3, "uniform"),
+                                        (131_072, 128 * 1152, 64, "mixed")])
+def test_embed_scaled_bwd_long(M, v, h, kind):
+    """More tokens of a warp than 16 bits number, more rows than 128 CTAs count."""
+    g = gen(31)
+    ids, dx = tokens(g, M, v, kind), rnd(g, M, h)
+    check_embed_bwd(ids, dx, v, 1.25)
+    check_embed_bwd(ids, dx, v, 1.25, rnd(g, v, h))
