@@ -1918,25 +1918,26 @@ tp_status launch_gemm_tc_two(const GemmDesc& a, const GemmDesc& b, cudaStream_t 
     set.tiles[i] = static_cast<int>(plan[i].tiles);
   }
   const int64_t tiles = plan[0].tiles + plan[1].tiles;
-  const bool alike = plan[0].pair == plan[1].pair && plan[0].wide == plan[1].wide &&
+  const bool alike = plan[0].pair == plan[1].pair && !plan[0].wide && !plan[1].wide &&
                      plan[0].epi8 == plan[1].epi8 && plan[0].BN == plan[1].BN && !plan[0].dec &&
-                     !plan[1].dec;
-  // up to a wave of one-CTA tiles or two of pair tiles; us of dx, dE and the logits' gradient, together
-  // and one by one: 300 x 1500 x 256 15.5 and 19.3, 1000 x 6000 x 512 41 and 44. More lose: one-CTA
-  // tiles that share a CTA, 1000 x 1000 x 1000 34.6 and 29.8; the order in which tiles share operands in
-  // L2, 4878 x 5168 x 1336 217 and 198, 8192 x 50304 x 2048 3370 and 3090.
-  if (!alike || tiles > device_sm_count()) {
+                     !plan[1].dec && (plan[0].pair || plan[0].BN < 256);
+  const int64_t k_most = static_cast<int64_t>(d[0]->nseg) * d[0]->K;
+  // up to a wave of one-CTA tiles or two of pair tiles, and sums of up to 1024; us of dx, dE and the
+  // logits' gradient, together and one by one: 300 x 1500 x 256 15.5 and 19.3, 1000 x 6000 x 512 41 and
+  // 44, 512 x 512 x 5120 45 and 50. More lose: one-CTA tiles that share a CTA, 1000 x 1000 x 1000 34.6
+  // and 29.8; longer sums, beside whose tiles the launch is nothing and the operands that both sets
+  // take from L2 are more, 4096 x 4096 x 2048 156 and 143, 8192 x 50304 x 2048 3370 and 3090.
+  if (!alike || tiles > device_sm_count() || k_most > 1024) {
     TP_TRY(launch_gemm_tc(a, st));
     return launch_gemm_tc(b, st);
   }
   if (plan[0].pair)
-    return plan[0].wide   ? launch_pair_epi<EPI_STORE, 2, 8, 2>(set, st)
-           : plan[0].epi8 ? launch_pair_epi<EPI_STORE, 1, 8, 2>(set, st)
-                          : launch_pair_epi<EPI_STORE, 1, PairCfg<1>::EPI_WARPS, 2>(set, st);
+    return plan[0].epi8 ? launch_pair_epi<EPI_STORE, 1, 8, 2>(set, st)
+                        : launch_pair_epi<EPI_STORE, 1, PairCfg<1>::EPI_WARPS, 2>(set, st);
   const int grid = static_cast<int>(std::min<int64_t>(tiles, device_sm_count()));
-  return plan[0].BN == 256   ? launch_bn_epi<256, EPI_STORE, false, 2>(set, grid, st)
-         : plan[0].BN == 128 ? launch_bn_epi<128, EPI_STORE, false, 2>(set, grid, st)
-                             : launch_bn_epi<64, EPI_STORE, false, 2>(set, grid, st);
+  // (a problem keeps 256-wide one-CTA tiles only if more than half the SMs have one)
+  return plan[0].BN == 128 ? launch_bn_epi<128, EPI_STORE, false, 2>(set, grid, st)
+                           : launch_bn_epi<64, EPI_STORE, false, 2>(set, grid, st);
 }
 
 }  // namespace tp

@@ -120,7 +120,8 @@ CE = [(1, 1, 8, 1), (1, 7, 8, 7), (1, 2000, 64, 8), (2, 256, 16, 1), (3, 65, 24,
       (5, 4097, 128, 1), (37, 1000, 136, 8), (63, 129, 64, 3), (64, 5000, 200, 4), (65, 2048, 128, 2),
       (127, 31, 1032, 1), (128, 256, 128, 2), (129, 257, 264, 1), (255, 640, 64, 16),
       (256, 511, 72, 7), (257, 3001, 512, 1), (300, 12345, 64, 3), (1000, 4099, 1032, 1),
-      (2049, 8192, 256, 16), (1300, 20000, 128, 5)]
+      (2049, 8192, 256, 16), (1300, 20000, 128, 5), (400, 500, 6144, 1), (2500, 2000, 304, 1),
+      (1000, 4000, 1024, 1), (10000, 50, 64, 1), (300, 1500, 256, 1)]
 
 
 @pytest.mark.parametrize("M,v,h,N", CE)
