@@ -28,7 +28,7 @@ namespace {
 constexpr int kRows = 8;          // rows of a CTA of the join at the least
 constexpr int kJoinThreads = 1024;
 constexpr int64_t kSms = 152;
-constexpr int kSumShards = 8;     // shards whose losses the join adds up itself
+constexpr int kSumShards = 32;    // shards whose losses the join adds up itself, a warp each
 constexpr float kLn2 = 0.6931471805599453f;
 
 // (m, s) pairs, m in base 2: s 2^m summed
@@ -116,27 +116,25 @@ __global__ void __launch_bounds__(kJoinThreads) vocab_linear_join_kernel(
     shard[mine] = t >= 0 ? static_cast<int>(t / (v / N)) : -1;
   }
   __syncthreads();
-  if (warp == 0) {
-    for (int i = 0; i < N; ++i) {
-      float a = 0.0f;
+  if (warp < N) {
+    float a = 0.0f;
 #pragma unroll
-      for (int r = 0; r < ROWS; r += 32)
-        if (lane + r < ROWS) a += shard[lane + r] == i ? losses[lane + r] : 0.0f;
+    for (int r = 0; r < ROWS; r += 32)
+      if (lane + r < ROWS) a += shard[lane + r] == warp ? losses[lane + r] : 0.0f;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-      if (lane == 0) {
-        sum[i] = a;
-        if (gridDim.x > 1) cta_loss[static_cast<int64_t>(blockIdx.x) * N + i] = a;
-      }
-    }
+    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
     if (lane == 0) {
-      last = 1;
+      sum[warp] = a;
       if (gridDim.x > 1) {
-        __threadfence();
-        last = atomicAdd(counter, 1) == static_cast<int>(gridDim.x) - 1;
+        cta_loss[static_cast<int64_t>(blockIdx.x) * N + warp] = a;
         __threadfence();
       }
     }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    last = gridDim.x == 1 || atomicAdd(counter, 1) == static_cast<int>(gridDim.x) - 1;
+    __threadfence();
   }
   __syncthreads();
   if (!last) return;

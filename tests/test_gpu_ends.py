@@ -121,7 +121,8 @@ CE = [(1, 1, 8, 1), (1, 7, 8, 7), (1, 2000, 64, 8), (2, 256, 16, 1), (3, 65, 24,
       (127, 31, 1032, 1), (128, 256, 128, 2), (129, 257, 264, 1), (255, 640, 64, 16),
       (256, 511, 72, 7), (257, 3001, 512, 1), (300, 12345, 64, 3), (1000, 4099, 1032, 1),
       (2049, 8192, 256, 16), (1300, 20000, 128, 5), (400, 500, 6144, 1), (2500, 2000, 304, 1),
-      (1000, 4000, 1024, 1), (10000, 50, 64, 1), (300, 1500, 256, 1)]
+      (1000, 4000, 1024, 1), (10000, 50, 64, 1), (300, 1500, 256, 1), (130, 990, 64, 33),
+      (5000, 1280, 64, 40)]
 
 
 @pytest.mark.parametrize("M,v,h,N", CE)
@@ -131,7 +132,8 @@ def test_linear_ce_bf16(M, v, h, N):
 
 @pytest.mark.parametrize("M,v,h,N", [(1, 1, 1, 1), (1, 3, 2, 3), (3, 64, 5, 2), (64, 65, 33, 5),
                                      (65, 257, 128, 1), (128, 256, 128, 2), (130, 1000, 77, 8),
-                                     (300, 4097, 64, 17), (700, 3000, 129, 3), (1025, 128, 300, 16)])
+                                     (300, 4097, 64, 17), (700, 3000, 129, 3), (1025, 128, 300, 16),
+                                     (90, 770, 40, 35)])
 def test_linear_ce_fp32(M, v, h, N):
     check_ce(*ce_case(M, v, h, F32, seed=M + v), N)
 
