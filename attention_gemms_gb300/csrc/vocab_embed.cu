@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kSortThreads) vocab_embed_sort_kernel(
     const int s = start[r], e = start[r + 1];
     if (e - s <= kWhole || s / len == (e - 1) / len) continue;
     for (int u = s / len; u <= (e - 1) / len; u = (u / kGroup + 1) * kGroup)
-      for (int i = lane; i < 2 * columns; i += 32) arrived[static_cast<int64_t>(u) * 2 * columns + i] = 0;
+      for (int i = lane; i < 3 * columns; i += 32) arrived[static_cast<int64_t>(u) * 3 * columns + i] = 0;
   }
   // rows without a token, a bit each
   const int words = (range + 31) / 32;
@@ -358,9 +358,10 @@ __global__ void __launch_bounds__(kSortThreads) vocab_embed_sort_kernel(
 
 // blockDim (threads of a unit, units); blockIdx.y: slice of the columns. part: [unit][2][h] fp32
 // sums of rows that the unit does not hold whole: 0 a row begun before it, 1 one begun in it.
-// arrived: [unit][2][thread's columns]: 0 the partials that are written of the row begun in the unit,
-// or, for a row of more than 32 units, of the units of a group of 32 that begins there; 1 the groups of
-// the row that are added up.
+// arrived: [unit][3][thread's columns]: 0 the partials that are written of the row begun in the unit
+// (of its first group of 32 units, where it has more); 1 the groups of that row that are added up; 2 the
+// partials of the group that begins at the unit, of a row begun before it. 0 and 2 are two rows' where
+// the one ends in the unit in which the other begins.
 // Blocks past the units' write the rows without a token (not where dE is accumulated into), a word of
 // `absent` each: they fill the memory's time while the units wait for their loads.
 template <typename T, int VEC>
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 4) vocab_embed_sum_kernel(
   };
   auto arrive = [&](int unit, int which, int of) {  // whether this is the last of `of`
     __threadfence();
-    const bool is = atomicAdd(arrived + (static_cast<int64_t>(unit) * 2 + which) * columns + col, 1) == of - 1;
+    const bool is = atomicAdd(arrived + (static_cast<int64_t>(unit) * 3 + which) * columns + col, 1) == of - 1;
     __threadfence();
     return is;
   };
@@ -506,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 4) vocab_embed_sum_kernel(
     const bool grouped = last - first >= kGroup;
     const int lo = grouped ? max(first, u / kGroup * kGroup) : first;
     const int hi = grouped ? min(last, u / kGroup * kGroup + kGroup - 1) : last;
-    if (!arrive(lo, 0, hi - lo + 1)) continue;
+    if (!arrive(lo, lo == first ? 0 : 2, hi - lo + 1)) continue;
     add_up(first, lo, hi, std::integral_constant<int, 1>());
     if (grouped) {
       leave(lo, lo == first ? 1 : 0);
@@ -550,7 +551,7 @@ SumPlan sum_plan(int64_t M, int64_t v, int64_t h, tp_dtype dt) {
     ++P.log2_ctas;
   P.range = static_cast<int>((v - 1) >> P.log2_ctas) + 1;
   P.absent = o; o += align_up((static_cast<size_t>((P.range + 31) / 32) << P.log2_ctas) * 4, 256);
-  P.arrived = o; o += align_up(static_cast<size_t>(P.units) * 2 * P.columns * 4, 256);
+  P.arrived = o; o += align_up(static_cast<size_t>(P.units) * 3 * P.columns * 4, 256);
   P.part = o;   o += align_up(static_cast<size_t>(P.units) * 2 * h * 4, 256);
   P.total = o;
   return P;

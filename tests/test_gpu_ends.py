@@ -341,6 +341,31 @@ def test_embed_scaled_bwd_rows_of_every_count():
             check_embed_bwd(ids, rnd(g, ids.numel(), h, dt=dt), 60, 1.0)
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("h", [64, 1032, 5])
+@pytest.mark.parametrize("counts", [(260, 3836), (257, 3839), (263, 30, 3803), (516, 9, 3571), (256, 3840),
+                                    (100, 420, 300, 3276), (260, 512, 512, 2812)])
+def test_embed_scaled_bwd_row_ends_where_the_next_begins(counts, h, dt):
+    """4096 tokens are cut into 512 units of 8. A row of more than 32 units ends in a unit that is a
+    multiple of 32, and the next row begins in it and is split as well: each counts its own."""
+    assert sum(counts) == 4096
+    ids = torch.repeat_interleave(torch.arange(len(counts), device="cuda"), torch.tensor(counts, device="cuda"))
+    g = gen(sum(counts[:1]) + h)
+    ids = ids[torch.randperm(4096, generator=g, device="cuda")].to(torch.int32)
+    check_embed_bwd(ids, rnd(g, 4096, h, dt=dt), len(counts), 1.5)
+    check_embed_bwd(ids, rnd(g, 4096, h, dt=dt), len(counts), 1.5, rnd(g, len(counts), h, dt=dt))
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_embed_scaled_bwd_lists_of_every_shape(seed):
+    g = gen(seed)
+    M = 3000 + 5000 * seed
+    v = (3, 7, 40, 700)[seed % 4]
+    u = torch.rand(M, generator=g, device="cuda")
+    ids = (u ** (2 + seed % 3) * v).long().clamp(max=v - 1).to(torch.int32)
+    check_embed_bwd(ids, rnd(g, M, 24), v, 0.75)
+
+
 def test_embed_scaled_bwd_without_tokens():
     for M in (0, 5):
         ids = torch.full((max(M, 1),), -1, dtype=torch.int32, device="cuda")
