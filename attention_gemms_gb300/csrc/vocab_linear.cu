@@ -15,12 +15,15 @@
 // h = 4096 backward 5.98 ms (1694). The exponentials hide: 6 % of their pipe, 17 % of the issue slots,
 // an epilogue of 3.5 k cycles in a tile's 17 k at h = 1032. For few rows HBM does: 37 rows of h = 4096
 // read E at 6 TB/s (74 us with the join).
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace tp {
 namespace {
@@ -157,6 +160,135 @@ __global__ void __launch_bounds__(kJoinThreads) vocab_linear_join_kernel(
   }
 }
 
+// ---- dE = q^T x of up to 64 rows (bf16): next to no arithmetic, every byte of dE written. A CTA keeps
+// 256 columns of x in shared memory and walks over 64-entry pieces of the vocabulary, q's next piece
+// loading while one is worked on; a warp takes 16 entries x 128 columns by mma.m16n8k16 (the tcgen05
+// engine's tiles of a single K block are bound by their hand-over), and the lanes of a quad exchange
+// their pairs, so that each stores 16 bytes. The whole backward, engine -> this: 50304 x 2048, 1 row 150
+// -> 123 us, 16 rows 149 -> 125, 64 rows 156 -> 152; 50257 x 4096, 37 rows 268 -> 243; 128000 x 4096, 64
+// rows 647 -> 621. It is a launch more, in plain stream order: 30000 x 1024, 64 rows 61 -> 59, but 8000 x
+// 512, 64 rows 24.5 -> 24.8 and 1000 x 256, 16 rows 17.1 -> 18.6, so it takes dE from 2^24 elements.
+constexpr int kOuterRows = 64;     // most rows of x
+constexpr int64_t kOuterLeast = 1ll << 24;  // least elements of dE
+constexpr int kOuterCols = 256;    // columns of a CTA
+constexpr int kOuterEntries = 64;  // vocabulary entries of a step
+constexpr int kXPitch = kOuterCols + 8, kQPitch = kOuterEntries + 8;  // no bank conflicts of ldmatrix
+constexpr int kOuterSmem = (kOuterRows * kXPitch + 2 * kOuterRows * kQPitch) * 2;
+
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void mma_16n8k16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                            uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+// p[j] of lane t of a quad becomes p[t] of its lane j
+__device__ __forceinline__ void transpose_quad(uint32_t (&p)[4], int t) {
+#pragma unroll
+  for (int s = 1; s <= 2; s *= 2) {
+    const bool up = (t & s) != 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (j & s) continue;
+      const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? p[j] : p[j + s], s);
+      if (up) p[j] = got;
+      else p[j + s] = got;
+    }
+  }
+}
+
+// blockIdx: column block fastest; q (M, n) with pitch ldq, x (M, h), dE (n, h); h % 8 == 0, ldq % 64 == 0
+__global__ void __launch_bounds__(256, 2)
+    vocab_outer_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ x,
+                       __nv_bfloat16* __restrict__ dE, int M, int64_t n, int64_t h, int64_t ldq,
+                       int col_blocks) {
+  extern __shared__ __align__(16) uint8_t outer_smem[];
+  __nv_bfloat16* xs = reinterpret_cast<__nv_bfloat16*>(outer_smem);
+  __nv_bfloat16* qs = xs + kOuterRows * kXPitch;  // two stages
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t j0 = static_cast<int64_t>(blockIdx.x % col_blocks) * kOuterCols;
+  const int64_t steps = (n + kOuterEntries - 1) / kOuterEntries;
+  const int64_t stride = gridDim.x / col_blocks;
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  for (int i = threadIdx.x; i < kOuterRows * (kOuterCols / 8); i += 256) {
+    const int r = i / (kOuterCols / 8), c = i % (kOuterCols / 8) * 8;
+    *reinterpret_cast<uint4*>(xs + r * kXPitch + c) =
+        r < M && j0 + c < h ? *reinterpret_cast<const uint4*>(x + r * h + j0 + c) : zero;
+  }
+  // q's piece `step`: 64 rows x 8 vectors, two of them a thread's (entries past n, which no row of dE
+  // takes, are whatever the pitch leaves there)
+  auto load = [&](int64_t step, uint4 (&v)[2]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int e = threadIdx.x + 256 * i, r = e / 8;
+      v[i] = r < M ? *reinterpret_cast<const uint4*>(q + r * ldq + step * kOuterEntries + e % 8 * 8) : zero;
+    }
+  };
+  auto put = [&](int st, const uint4 (&v)[2]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int e = threadIdx.x + 256 * i;
+      *reinterpret_cast<uint4*>(qs + (st * kOuterRows + e / 8) * kQPitch + e % 8 * 8) = v[i];
+    }
+  };
+  const int64_t first = blockIdx.x / col_blocks;
+  uint4 next[2];
+  if (first < steps) {
+    load(first, next);
+    put(0, next);
+  }
+  __syncthreads();
+  const int ksteps = (M + 15) / 16, c0 = warp / 2 * 16, w0 = warp % 2 * 128;
+  const uint32_t xa = smem_u32(xs), qa = smem_u32(qs);
+  int st = 0;
+  for (int64_t step = first; step < steps; step += stride, st ^= 1) {
+    const bool more = step + stride < steps;
+    if (more) load(step + stride, next);
+    float acc[16][4] = {};
+    for (int k = 0; k < ksteps; ++k) {
+      uint32_t a[4];  // 16 entries x 16 rows of q^T
+      ldmatrix_x4_trans(a, qa + ((st * kOuterRows + k * 16 + lane / 16 * 8 + lane % 8) * kQPitch + c0 +
+                                 lane / 8 % 2 * 8) * 2);
+#pragma unroll
+      for (int j = 0; j < 16; j += 2) {
+        uint32_t b[4];  // 16 rows x two tiles of 8 columns of x
+        ldmatrix_x4_trans(b, xa + ((k * 16 + lane / 8 % 2 * 8 + lane % 8) * kXPitch + w0 + j * 8 +
+                                   lane / 16 * 8) * 2);
+        mma_16n8k16(acc[j], a, b[0], b[1]);
+        mma_16n8k16(acc[j + 1], a, b[2], b[3]);
+      }
+    }
+    const int t = lane % 4;
+    const int64_t c = step * kOuterEntries + c0 + lane / 4;
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+      const int64_t col = j0 + w0 + (j + t) * 8;  // the tile that this lane stores of the four
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        uint32_t p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = pack_bf16(acc[j + i][2 * hf], acc[j + i][2 * hf + 1]);
+        transpose_quad(p, t);
+        if (c + 8 * hf < n && col < h)
+          *reinterpret_cast<uint4*>(dE + (c + 8 * hf) * h + col) = make_uint4(p[0], p[1], p[2], p[3]);
+      }
+    }
+    if (more) put(st ^ 1, next);  // the other stage, whose reads ended before the last barrier
+    __syncthreads();
+  }
+}
+
 // launch_kernel, or in plain stream order
 template <typename... KArgs, typename... Args>
 cudaError_t launch_after(bool early, void (*kern)(KArgs...), unsigned grid, unsigned block,
@@ -249,6 +381,25 @@ void split_sum(GemmDesc& d, int parts) {
   d.K = ((d.K + parts - 1) / parts + 63) / 64 * 64;
   d.groups = parts;
   d.out_group_stride = d.M * d.N;
+}
+
+tp_status launch_outer(const void* q, const void* x, void* dE, int64_t M, int64_t n, int64_t h,
+                       int64_t ldq, cudaStream_t st) {
+  static std::atomic<uint64_t> attr_set{0};
+  if (needs_setup(attr_set)) {
+    TP_CUDA_TRY(cudaFuncSetAttribute(vocab_outer_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     kOuterSmem));
+    mark_device(attr_set);
+  }
+  const int64_t blocks = (h + kOuterCols - 1) / kOuterCols, steps = (n + kOuterEntries - 1) / kOuterEntries;
+  const int64_t walkers = std::min(steps, std::max<int64_t>(2 * kSms / blocks, 1));  // of a column block
+  // plain stream order: two CTAs fill an SM's registers, which leaves no room beside a GEMM's
+  vocab_outer_kernel<<<static_cast<unsigned>(blocks * walkers), 256, kOuterSmem, st>>>(
+      static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(x),
+      static_cast<__nv_bfloat16*>(dE), static_cast<int>(M), n, h, ldq, static_cast<int>(blocks));
+  TP_CUDA_TRY(cudaGetLastError());
+  count_launch();
+  return TP_OK;
 }
 
 tp_status product(const GemmDesc& d, cudaStream_t st) {
@@ -364,6 +515,11 @@ tp_status launch_vocab_linear_ce_bwd(const void* x, const void* E, const int32_t
     split_sum(ge, P.e_parts);
     if (dt == TP_F32) {
       TP_TRY(launch_gemm_simt_two(gx, ge, st));
+      continue;
+    }
+    if (M <= kOuterRows && n * h >= kOuterLeast) {
+      if (dx) TP_TRY(launch_gemm_tc(gx, st));
+      if (dE) TP_TRY(launch_outer(q, x, dEi, M, n, h, P.piece, st));
       continue;
     }
     if (dx && dE) TP_TRY(launch_gemm_tc_two(gx, ge, st));

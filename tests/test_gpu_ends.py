@@ -389,6 +389,18 @@ def test_embed_scaled_bwd_agrees_with_the_scan():
     within(run_embed_bwd(ids, dx, 500, 1.0), want.double(), 2 * R.embed_bwd_bound(g_, a, n, 1.0, F32))
 
 
+@pytest.mark.parametrize("M,v,h", [(1, 70_000, 264), (15, 65_601, 256), (16, 2049, 8200), (17, 131_080, 136),
+                                   (33, 50_257, 520), (63, 16_385, 1032), (64, 2_100_001, 8), (64, 16_384, 1024),
+                                   (65, 16_385, 1032), (64, 16_383, 1024)])
+def test_linear_ce_few_rows_of_a_large_gradient(M, v, h):
+    """dE of up to 64 rows and from 2^24 elements has a kernel of its own; the sizes on both sides."""
+    x, E, t = ce_case(M, v, h, BF, seed=M)
+    _, dx, dE = check_ce(x, E, t, 1)
+    _, only_x, _ = check_ce(x, E, t, 1, want=(True, False))
+    _, _, only_E = check_ce(x, E, t, 1, want=(False, True))
+    assert torch.equal(only_x, dx) and torch.equal(only_E, dE)
+
+
 @pytest.mark.parametrize("M,v,h,dt", [(200_000, 1000, 64, BF), (5, 1_000_003, 64, BF), (70, 600_001, 24, BF),
                                       (100_000, 130, 8, F32), (3, 400_000, 5, F32)])
 def test_linear_ce_long(M, v, h, dt):

@@ -294,3 +294,37 @@ def test_many_calls_without_a_pause(M):
     assert torch.equal(out[0], want[1]) and torch.equal(out[3], want[0])
     wx, wE = run_bwd(x, E, t, want[1].clone(), 1.0 / M)
     assert torch.equal(dx, wx) and torch.equal(dE, wE)
+
+
+def test_few_rows_of_a_large_gradient_without_a_pause_and_replayed():
+    """dE's own kernel of few rows between the GEMMs: back to back, and captured with new inputs."""
+    M, v, h = 40, 40_000, 512
+    d = T.DType.BF16
+    x, E, t = ce_case(M, v, h, BF)
+    lse = run_fwd(x, E, t, 1)[1].clone()
+    n = T.tp_vocab_linear_ce_workspace_size(0, M, v, h, 1, d)
+    ws = poison(n)
+    dx, dE = torch.empty(M, h, dtype=BF, device="cuda"), torch.empty(v, h, dtype=BF, device="cuda")
+
+    def step():
+        T.tp_vocab_linear_ce_bwd(x, E, t, lse, dx, dE, M, v, h, 1, 1.0 / M, d, ws, n)
+
+    for _ in range(50):
+        step()
+    torch.cuda.synchronize()
+    assert T.tp_check_status() == 0
+    wx, wE = run_bwd(x, E, t, lse, 1.0 / M)
+    assert torch.equal(dx, wx) and torch.equal(dE, wE)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    x2, _, t2 = ce_case(M, v, h, BF, seed=2)
+    x.copy_(x2)
+    t.copy_(t2)
+    lse.copy_(run_fwd(x, E, t, 1)[1])
+    dx.fill_(float("nan"))
+    dE.fill_(float("nan"))
+    graph.replay()
+    torch.cuda.synchronize()
+    wx, wE = run_bwd(x, E, t, lse, 1.0 / M)
+    assert torch.equal(dx, wx) and torch.equal(dE, wE)
