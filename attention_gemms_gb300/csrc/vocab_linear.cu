@@ -104,7 +104,8 @@ __global__ void __launch_bounds__(kJoinThreads) vocab_linear_join_kernel(
 #pragma unroll
       for (int w = 1; w < kPairs; ++w) join(m, s, sm[w][mine].x, sm[w][mine].y);
     }
-    const float z = (m + log2f(s)) * kLn2;
+    // a softmax over one entry is 1: its lse is the logit itself and the loss 0, not a rounding of it
+    const float z = v == 1 && t >= 0 ? at : (m + log2f(s)) * kLn2;
     l = t >= 0 ? z - at : 0.0f;
     if (ends && (lane == 0 || !kWarpEnds)) {
       lse[own] = z;

@@ -248,6 +248,15 @@ def test_linear_ce_agrees_with_the_kernels_on_logits():
         within(g_, r_.double(), 2 * b_)
 
 
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("M", [1, 100, 1300, 5000])
+def test_linear_ce_vocabulary_of_one_entry(M, dt):
+    """The softmax is 1 and every loss 0, not a rounding of it."""
+    x, E, t = ce_case(M, 1, 72, dt, kind="uniform", sigma=2.0)
+    (loss, lse, rows, shards), _, _ = check_ce(x, E, t, 1)
+    assert torch.all(rows == 0) and loss == 0 and shards == 0
+
+
 def test_linear_ce_empty_batch():
     E = rnd(gen(0), 50, 64)
     dE = guarded(50 * 64, BF)
