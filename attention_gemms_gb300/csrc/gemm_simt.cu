@@ -76,12 +76,11 @@ __device__ __forceinline__ float ce_grad(const SimtParams& p, float a, int64_t t
 }
 
 // EPI_LSE of the `rows` rows of the tile's logits in sm (TN floats each), rows r0 .. of the
-// product with these targets, columns c0 ..: a warp per row, two columns per lane. As in the tensor-core engine the
-// maximum is kept in base 2; expf and the sum in 32 bits.
+// product with these targets, columns c0 ..: a warp per row, two columns per lane; expf and the sum in
+// 32 bits.
 __device__ __forceinline__ void lse_rows(const SimtParams& p, const float* sm, const int32_t* target,
                                          int rows, int64_t r0, int64_t c0, int64_t slot) {
   static_assert(TN == 64, "two columns per lane");
-  constexpr float kLog2e = 1.4426950408889634f;  // log2(e)
   const int lane = threadIdx.x & 31;
   for (int rr = threadIdx.x >> 5; rr < rows; rr += 8) {
     const int64_t r = r0 + rr;
@@ -98,7 +97,7 @@ __device__ __forceinline__ void lse_rows(const SimtParams& p, const float* sm, c
     float s = expf(a - m) + expf(b - m);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-    if (lane == 0) p.ce.part[slot * p.M + r] = make_float2(m * kLog2e, s);
+    if (lane == 0) p.ce.part[slot * p.M + r] = make_float2(m, s);
   }
 }
 
@@ -455,7 +454,6 @@ __global__ void __launch_bounds__(256, 2)
     for (int j = 0; j < 4; ++j)
       asm("mov.b64 {%0, %1}, %2;" : "=f"(acc[2 * j]), "=f"(acc[2 * j + 1]) : "l"(acc2[i][j]));
     if constexpr (EPI == EPI_LSE) {  // the row's 128 columns lie in 16 lanes of the warp
-      constexpr float kLog2e = 1.4426950408889634f;  // log2(e)
       const int64_t t = r < p.M ? p.ce.targets[r] : -1;
       float m = -INFINITY;
 #pragma unroll
@@ -472,7 +470,7 @@ __global__ void __launch_bounds__(256, 2)
       for (int j = 0; j < 8; ++j) s += expf(acc[j] - m);
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-      if (tx == 0 && r < p.M) p.ce.part[n0 / BT * p.M + r] = make_float2(m * kLog2e, s);
+      if (tx == 0 && r < p.M) p.ce.part[n0 / BT * p.M + r] = make_float2(m, s);
     } else {
       const int64_t t = EPI == EPI_DCE && r < p.M ? p.ce.targets[r] : -1;
       const float lse = EPI == EPI_DCE && r < p.M ? p.ce.lse[r] : 0.0f;

@@ -231,11 +231,14 @@ struct EpiInputs {
   static constexpr int n = EPI == EPI_DSWIGLU ? 2 : (EPI == EPI_DGELU || EPI == EPI_STORE ? 1 : 0);
 };
 
-// ---- cross-entropy on the accumulator (EPI_LSE, EPI_DCE): a lane owns a row of the tile, in
-// base 2 as the kernels on stored logits (vocab.cu): exp(l - m) = 2^(l log2(e) - m log2(e)), one
-// fused multiply-add and one ex2.approx (relative error about 2^-22; a term below 2^-126 of the
-// row's largest is dropped) per logit. The logits stay in 32 bits; only the gradient's tile is
-// rounded, to bf16, the operand type of the products that take it.
+// ---- cross-entropy on the accumulator (EPI_LSE, EPI_DCE): a lane owns a row of the tile. Powers are
+// of 2, on the special-function unit; the forward takes exp(l - m) = 2^((l - m) log2(e)) from the
+// difference, which is 0 for the largest logit itself, so its power is 1 exactly and a sum no less:
+// with m log2(e) rounded beforehand, a fused multiply-add for each logit, a target with all of the
+// probability got losses of -8e-6 for logits of 100. Subtraction and product go two logits at a time,
+// as many instructions as that. ex2.approx: relative error about 2^-22; a term below 2^-126 of the
+// row's largest is dropped. The logits stay in 32 bits; only the gradient's tile is rounded, to bf16,
+// the operand type of the products that take it.
 constexpr float kCeLog2e = 1.4426950408889634f;  // log2(e)
 
 __device__ __forceinline__ float ce_ex2(float x) {
@@ -244,10 +247,30 @@ __device__ __forceinline__ float ce_ex2(float x) {
   return y;
 }
 
+// two values in one register pair, and arithmetic on both, each rounded as by itself
+__device__ __forceinline__ uint64_t f32x2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split_f32x2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 struct CeRow {
   int t = -1;              // the target's column of the product; outside [0, N): none here
   bool live = false;       // the row exists and has a target
-  float m = -INFINITY;     // EPI_LSE: running maximum (base 2) and sum
+  float m = -INFINITY;     // EPI_LSE: running maximum and sum
   float s = 0.0f;
   float l2 = 0.0f;         // EPI_DCE: (lse in base 2) - log2|scale|; inf in a row without a target
 };
@@ -287,16 +310,19 @@ __device__ __forceinline__ void ce_lse32(const TcParams& p, CeRow& r, int64_t ro
   float mx = __uint_as_float(ra[0]);
 #pragma unroll
   for (int j = 1; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(ra[j]));
-  mx *= kCeLog2e;
   if (mx > r.m) {
-    r.s *= ce_ex2(r.m - mx);  // 0 at first
+    r.s *= ce_ex2((r.m - mx) * kCeLog2e);  // 0 at first
     r.m = mx;
   }
+  const uint64_t down = f32x2(-r.m, -r.m), log2e = f32x2(kCeLog2e, kCeLog2e);
   float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
   for (int j = 0; j < 32; j += 2) {
-    s0 += ce_ex2(fmaf(__uint_as_float(ra[j]), kCeLog2e, -r.m));
-    s1 += ce_ex2(fmaf(__uint_as_float(ra[j + 1]), kCeLog2e, -r.m));
+    const uint64_t l = f32x2(__uint_as_float(ra[j]), __uint_as_float(ra[j + 1]));
+    float a, b;
+    split_f32x2(mul_f32x2(add_f32x2(l, down), log2e), a, b);
+    s0 += ce_ex2(a);
+    s1 += ce_ex2(b);
   }
   r.s += s0 + s1;
 }

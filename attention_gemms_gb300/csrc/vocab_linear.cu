@@ -32,13 +32,12 @@ constexpr int kRows = 8;          // rows of a CTA of the join at the least
 constexpr int kJoinThreads = 1024;
 constexpr int64_t kSms = 152;
 constexpr int kSumShards = 32;    // shards whose losses the join adds up itself, a warp each
-constexpr float kLn2 = 0.6931471805599453f;
 
-// (m, s) pairs, m in base 2: s 2^m summed
+// (m, s) pairs: s exp(m) summed
 __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
   const float mm = fmaxf(m, m2);
   // an empty side (-inf, 0) adds nothing; NaN in either sum stays
-  s = (m == mm ? s : s * exp2f(m - mm)) + (m2 == mm ? s2 : s2 * exp2f(m2 - mm));
+  s = (m == mm ? s : s * expf(m - mm)) + (m2 == mm ? s2 : s2 * expf(m2 - mm));
   m = mm;
 }
 
@@ -104,11 +103,12 @@ __global__ void __launch_bounds__(kJoinThreads) vocab_linear_join_kernel(
 #pragma unroll
       for (int w = 1; w < kPairs; ++w) join(m, s, sm[w][mine].x, sm[w][mine].y);
     }
-    // a softmax over one entry is 1: its lse is the logit itself and the loss 0, not a rounding of it
-    const float z = v == 1 && t >= 0 ? at : (m + log2f(s)) * kLn2;
-    l = t >= 0 ? z - at : 0.0f;
+    // m is a logit and s >= 1: the loss does not go by way of lse, whose rounding is the logits' size,
+    // and is never below 0
+    const float log_s = logf(s);
+    l = t >= 0 ? (m - at) + log_s : 0.0f;
     if (ends && (lane == 0 || !kWarpEnds)) {
-      lse[own] = z;
+      lse[own] = m + log_s;
       row_loss[own] = l;
     }
   }
