@@ -232,11 +232,11 @@ struct EpiInputs {
 };
 
 // ---- cross-entropy on the accumulator (EPI_LSE, EPI_DCE): a lane owns a row of the tile. Powers are
-// of 2, on the special-function unit; the forward takes exp(l - m) = 2^((l - m) log2(e)) from the
-// difference, which is 0 for the largest logit itself, so its power is 1 exactly and a sum no less:
-// with m log2(e) rounded beforehand, a fused multiply-add for each logit, a target with all of the
-// probability got losses of -8e-6 for logits of 100. Subtraction and product go two logits at a time,
-// as many instructions as that. ex2.approx: relative error about 2^-22; a term below 2^-126 of the
+// of 2, on the special-function unit; exp(l - m) = 2^((l - m) log2(e)) is taken from the
+// difference, which is 0 for the largest logit itself, so its power is 1 exactly and a sum no less;
+// the gradient's exp(l - lse) likewise. With m log2(e) rounded beforehand, a fused multiply-add for
+// each logit, a target with all of the probability got losses of -8e-6 for logits of 100, and logits
+// of 1e10 infinite powers. Two logits at a time, these are as many instructions as that. ex2.approx: relative error about 2^-22; a term below 2^-126 of the
 // row's largest is dropped. The logits stay in 32 bits; only the gradient's tile is rounded, to bf16,
 // the operand type of the products that take it.
 constexpr float kCeLog2e = 1.4426950408889634f;  // log2(e)
@@ -266,13 +266,19 @@ __device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
 
 struct CeRow {
   int t = -1;              // the target's column of the product; outside [0, N): none here
   bool live = false;       // the row exists and has a target
   float m = -INFINITY;     // EPI_LSE: running maximum and sum
   float s = 0.0f;
-  float l2 = 0.0f;         // EPI_DCE: (lse in base 2) - log2|scale|; inf in a row without a target
+  float lse = 0.0f;        // EPI_DCE: of a row with a target
+  float ls = -INFINITY;    // EPI_DCE: log2|scale|; -inf in a row without a target
 };
 
 template <int EPI>
@@ -283,8 +289,12 @@ __device__ __forceinline__ CeRow ce_row(const TcParams& p, int64_t row) {
       const int64_t t = __ldg(p.ce.targets + row);
       r.live = t >= 0 && t < p.ce.vocab;
       if (r.live) r.t = static_cast<int>(t - p.ce.col0);
-      if constexpr (EPI == EPI_DCE)
-        r.l2 = r.live ? __ldg(p.ce.lse + row) * kCeLog2e - log2f(fabsf(p.ce.scale)) : INFINITY;
+      if constexpr (EPI == EPI_DCE) {
+        if (r.live) {
+          r.lse = __ldg(p.ce.lse + row);
+          r.ls = log2f(fabsf(p.ce.scale));
+        }
+      }
     }
   }
   return r;
@@ -327,12 +337,18 @@ __device__ __forceinline__ void ce_lse32(const TcParams& p, CeRow& r, int64_t ro
   r.s += s0 + s1;
 }
 
-// the gradient of 32 logits in their place, |scale| in the exponent: one fused multiply-add and one
-// power each. Zeros in a row without a target.
+// the gradient of 32 logits in their place, |scale| in the exponent: a subtraction and a fused
+// multiply-add for two, and one power each. Zeros in a row without a target.
 __device__ __forceinline__ void ce_grad32(const TcParams& p, const CeRow& r, int x, uint32_t* ra) {
+  const uint64_t down = f32x2(-r.lse, -r.lse), log2e = f32x2(kCeLog2e, kCeLog2e), ls = f32x2(r.ls, r.ls);
 #pragma unroll
-  for (int j = 0; j < 32; ++j)
-    ra[j] = __float_as_uint(ce_ex2(fmaf(__uint_as_float(ra[j]), kCeLog2e, -r.l2)));
+  for (int j = 0; j < 32; j += 2) {
+    const uint64_t l = f32x2(__uint_as_float(ra[j]), __uint_as_float(ra[j + 1]));
+    float a, b;
+    split_f32x2(fma_f32x2(add_f32x2(l, down), log2e, ls), a, b);
+    ra[j] = __float_as_uint(ce_ex2(a));
+    ra[j + 1] = __float_as_uint(ce_ex2(b));
+  }
   const unsigned tj = static_cast<unsigned>(r.t - x);
   if (__any_sync(0xFFFFFFFFu, r.t >= 0 && tj < 32u)) {
 #pragma unroll

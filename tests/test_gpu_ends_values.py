@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from tests.helpers import gemm_tiles
-from tests.test_gpu_ends import BF, F32, gen, rnd, run_fwd, within
+from tests.test_gpu_ends import BF, F32, gen, rnd, run_bwd, run_fwd, within
 
 pytestmark = pytest.mark.gpu
 
@@ -93,3 +93,25 @@ def test_logits_of_any_finite_size(M, v, dt):
         # another target: its loss is the distance
         rows = run_fwd(x, E, torch.zeros_like(t), 1)[2]
         assert torch.equal(rows.double(), b)
+
+
+@pytest.mark.parametrize("M,v", [(40, 300), (200, 700), (700, 2200), (2048, 1280)])
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_gradients_of_logits_of_any_finite_size(M, v, dt):
+    for top in (1.0e5, 1.0e10, 1.0e37):
+        x, E, t, a, _ = two_levels(M, v, 64, dt, seed=3, top=top, gap=(top * 0.002, top * 0.01))
+        dx, dE = run_bwd(x, E, t, a.float(), 0.5)
+        assert torch.all(dx == 0) and torch.all(dE == 0)
+        # another target: q is the scale at the largest logit, its negative at the target
+        dx, _ = run_bwd(x, E, torch.zeros_like(t), a.float(), 0.5)
+        want = torch.zeros_like(dx)
+        want[:, 1] = 0.5
+        assert torch.equal(dx, want)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_gradient_of_a_certain_target_is_zero(dt):
+    """exp(l - lse) = 1 where the target's logit is lse itself: no residue of a change of base."""
+    x, E, t, a, _ = two_levels(500, 900, 64, dt, seed=5, gap=(120.0, 130.0))
+    dx, dE = run_bwd(x, E, t, a.float(), 1.0)
+    assert torch.all(dx == 0) and torch.all(dE == 0)  # e^-120 is below every fp32 number
