@@ -16,7 +16,8 @@
 //    running (max, sum of exp) per shard, re-based when the max grows, and the shards'
 //    (m_i, s_i) are combined exactly as the two all-reduces do. Otherwise one CTA per
 //    row makes two plain passes (max, then sum of exp(l - m)).
-//  * The gradient softmax - one_hot, scaled, needs only m + log S per row.
+//  * The gradient softmax - one_hot, scaled, needs only m + log S per row; a row whose target no shard
+//    owns has neither a loss nor a gradient.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -302,6 +303,11 @@ __global__ void __launch_bounds__(kThreads) vocab_ce_bwd_vec_kernel(
   const T* L = logits + row * v;
   T* D = dlogits + row * v;
   const int64_t n8 = v / 8;
+  if (t < 0 || t >= v) {  // no loss, no gradient, whatever the row holds
+    const float zero[8] = {};
+    for (int64_t c8 = threadIdx.x; c8 < n8; c8 += kThreads) st8(D + c8 * 8, zero);
+    return;
+  }
   for (int64_t c8 = threadIdx.x; c8 < n8; c8 += kThreads) {
     float x[8];
     ld8(L + c8 * 8, x);
@@ -354,6 +360,10 @@ __global__ void __launch_bounds__(kThreads) vocab_ce_bwd_kernel(
   const int64_t row = blockIdx.x;
   const float l = lse[row];
   const int64_t t = targets[row];
+  if (t < 0 || t >= v) {
+    for (int64_t c = threadIdx.x; c < v; c += kThreads) stv(dlogits, row * v + c, 0.0f);
+    return;
+  }
   for (int64_t c = threadIdx.x; c < v; c += kThreads) {
     float p = expf(ldv(logits, row * v + c) - l);
     if (c == t) p -= 1.0f;

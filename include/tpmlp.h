@@ -750,8 +750,9 @@ TP_API tp_status tp_vocab_ce_fwd(const void* logits, const int32_t* targets, flo
                                  float* row_loss, float* shard_loss, float* loss, int64_t M,
                                  int64_t vocab, int32_t N, tp_dtype dtype, void* stream);
 
-/* dlogits = scale * (softmax(logits) - one_hot(targets)), from lse; dlogits may be the
- * logits buffer itself (in place). scale = 1/M for the mean loss. */
+/* dlogits = scale * (softmax(logits) - one_hot(targets)), from lse, and zeros in rows whose
+ * target lies outside [0, vocab); dlogits may be the logits buffer itself (in place).
+ * scale = 1/M for the mean loss. */
 TP_API tp_status tp_vocab_ce_bwd(const void* logits, const int32_t* targets, const float* lse,
                                  void* dlogits, int64_t M, int64_t vocab, int32_t N,
                                  float scale, tp_dtype dtype, void* stream);

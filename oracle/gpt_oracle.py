@@ -89,13 +89,16 @@ def vocab_ce_fwd(logits, targets, N):
 
 def vocab_ce_bwd(logits, targets, lse, N, scale):
     """d(loss)/d(logits) block by block: softmax - one_hot(target), times `scale`
-    (1/M for the mean); each shard needs only its columns, m and S."""
+    (1/M for the mean); each shard needs only its columns, m and S. A row whose target no
+    shard holds has no loss and a gradient of zeros."""
     targets = np.asarray(targets).reshape(-1)
     M, v = logits.shape
+    inside = (targets >= 0) & (targets < v)
     blocks = []
     for i in range(N):
         lo, hi = vocab_range(v, N, i)
         P = np.exp(logits[:, lo:hi] - lse[:, None])
+        P[~inside] = 0.0
         own = np.nonzero((targets >= lo) & (targets < hi))[0]
         P[own, targets[own] - lo] -= 1.0
         blocks.append(P * scale)
