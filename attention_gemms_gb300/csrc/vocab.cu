@@ -286,7 +286,9 @@ __global__ void __launch_bounds__(kThreads) vocab_ce_fwd_vec_kernel(
     const float l = (m + log2f(S)) * kLn2;
     const int64_t t = targets[row];
     lse[row] = l;
-    row_loss[row] = (t >= 0 && t < v) ? l - ldv(L, t) : 0.0f;
+    // l's rounding in base 2 can put it below the target's logit: no loss is below 0 (NaN stays)
+    const float d = (t >= 0 && t < v) ? l - ldv(L, t) : 0.0f;
+    row_loss[row] = d < 0.0f ? 0.0f : d;
   }
 }
 

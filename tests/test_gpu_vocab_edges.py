@@ -1,4 +1,4 @@
-"""The cross-entropy of stored logits at its edges: targets outside the vocabulary."""
+"""The cross-entropy of stored logits at its edges: targets outside the vocabulary, small losses."""
 import pytest
 import torch
 
@@ -36,3 +36,25 @@ def test_ce_bwd_of_a_target_outside_the_vocabulary_is_a_row_of_zeros(M, v, N, dt
     # p's exponent: lse in base 2 and the multiply-add round 2^-23 of up to 16 log2(e), the power 2^-22
     tol = (p.abs() * 1.01 * half + (1.0 + p.abs()) * 2.0 ** -18) / M
     within(got[~out], (p / M)[~out], tol[~out], "dlogits")
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+@pytest.mark.parametrize("v,N", [(64, 4), (1000, 5), (77, 7)])
+def test_ce_fwd_has_no_loss_below_zero(v, N, dt):
+    """A target that is above the other logits by 20 to 30: vectorised rows and the others."""
+    g = gen(v)
+    M = 4000
+    a = (torch.rand(M, generator=g, device="cuda") * 200.0 - 100.0).to(BF)
+    L = (a.float()[:, None] - 20.0 - 10.0 * torch.rand(M, v, generator=g, device="cuda")).to(dt)
+    t = torch.randint(0, v, (M,), generator=g, device="cuda").to(torch.int32)
+    L[torch.arange(M, device="cuda"), t.long()] = a.to(dt)
+    e = lambda n: torch.empty(n, device="cuda")
+    lse, rows, shards, loss = e(M), e(M), e(N), e(1)
+    T.tp_vocab_ce_fwd(L, t, lse, rows, shards, loss, M, v, N, DT[dt])
+    torch.cuda.synchronize()
+    assert torch.all(rows >= 0), f"{int((rows < 0).sum())} of {M}, {rows.min().item():.3g}"
+    assert torch.all(shards >= 0) and loss.item() >= 0
+    L[5, 0] = float("nan")
+    T.tp_vocab_ce_fwd(L, t, lse, rows, shards, loss, M, v, N, DT[dt])
+    torch.cuda.synchronize()
+    assert torch.isnan(rows[5]) and torch.isnan(loss)
