@@ -32,12 +32,13 @@ constexpr int kRows = 8;          // rows of a CTA of the join at the least
 constexpr int kJoinThreads = 1024;
 constexpr int64_t kSms = 152;
 constexpr int kSumShards = 32;    // shards whose losses the join adds up itself, a warp each
+constexpr float kLog2e = 1.4426950408889634f;  // log2(e)
 
 // (m, s) pairs: s exp(m) summed
 __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
   const float mm = fmaxf(m, m2);
   // an empty side (-inf, 0) adds nothing; NaN in either sum stays
-  s = (m == mm ? s : s * expf(m - mm)) + (m2 == mm ? s2 : s2 * expf(m2 - mm));
+  s = (m == mm ? s : s * exp2f((m - mm) * kLog2e)) + (m2 == mm ? s2 : s2 * exp2f((m2 - mm) * kLog2e));
   m = mm;
 }
 
