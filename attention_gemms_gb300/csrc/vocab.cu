@@ -305,11 +305,9 @@ __global__ void __launch_bounds__(kThreads) vocab_ce_bwd_vec_kernel(
   const T* L = logits + row * v;
   T* D = dlogits + row * v;
   const int64_t n8 = v / 8;
-  if (t < 0 || t >= v) {  // no loss, no gradient, whatever the row holds
-    const float zero[8] = {};
-    for (int64_t c8 = threadIdx.x; c8 < n8; c8 += kThreads) st8(D + c8 * 8, zero);
-    return;
-  }
+  // no target, no gradient, whatever the row holds (a selection, so that the logits' loads do not wait
+  // for the target's: 4096 x 50304 bf16 133 us, 141 with a branch)
+  const bool in = t >= 0 && t < v;
   for (int64_t c8 = threadIdx.x; c8 < n8; c8 += kThreads) {
     float x[8];
     ld8(L + c8 * 8, x);
@@ -317,7 +315,7 @@ __global__ void __launch_bounds__(kThreads) vocab_ce_bwd_vec_kernel(
     for (int k = 0; k < 8; ++k) {
       float p = exp2f(fmaf(x[k], kLog2e, -l2));  // exp(x - lse)
       if (c8 * 8 + k == t) p -= 1.0f;
-      x[k] = p * scale;
+      x[k] = in ? p * scale : 0.0f;
     }
     st8(D + c8 * 8, x);  // may overwrite the logits in place (same elements)
   }
@@ -362,14 +360,11 @@ __global__ void __launch_bounds__(kThreads) vocab_ce_bwd_kernel(
   const int64_t row = blockIdx.x;
   const float l = lse[row];
   const int64_t t = targets[row];
-  if (t < 0 || t >= v) {
-    for (int64_t c = threadIdx.x; c < v; c += kThreads) stv(dlogits, row * v + c, 0.0f);
-    return;
-  }
+  const bool in = t >= 0 && t < v;
   for (int64_t c = threadIdx.x; c < v; c += kThreads) {
     float p = expf(ldv(logits, row * v + c) - l);
     if (c == t) p -= 1.0f;
-    stv(dlogits, row * v + c, p * scale);  // may overwrite the logits in place
+    stv(dlogits, row * v + c, in ? p * scale : 0.0f);  // may overwrite the logits in place
   }
 }
 
