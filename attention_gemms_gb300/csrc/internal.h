@@ -85,16 +85,22 @@ class SideBranch {
 
 // ------------------------------------------------------------------ launches
 //
-// Programmatic dependent launch: every kernel of the library is launched (launch_kernel)
-// so that its CTAs may start while the kernel before it on the stream is finishing. A
-// kernel calls pdl_wait() before its first access to global memory -- everything the
-// earlier kernels of the stream wrote is then complete and visible, and nothing they
-// still read is overwritten -- and pdl_trigger() right after, which lets the next
-// kernel's CTAs start their own set-up (barrier init, TMEM allocation, tensor-map
-// prefetch) in turn. The next kernel launches only once every CTA of this one has
-// passed its trigger, so a waiting CTA never holds resources an earlier kernel's CTA
-// still needs. Without the attribute (the environment variable TP_NO_PDL=1) the
-// instructions return at once and the stream serialises the kernels as usual.
+// Programmatic dependent launch: a kernel launched by launch_kernel may start its CTAs while the
+// kernel before it on the stream is finishing. Such a kernel calls pdl_wait() before its first access
+// to global memory -- everything the earlier kernels of the stream wrote is then complete and
+// visible, and nothing they still read is overwritten -- and pdl_trigger() right after, which lets
+// the next kernel's CTAs start their own set-up (barrier init, TMEM allocation, tensor-map prefetch)
+// in turn, once every CTA of this one has passed its trigger. Without the attribute (the environment
+// variable TP_NO_PDL=1) the instructions return at once and the stream serialises the kernels as usual.
+//
+// This alone does not make every early launch safe. A kernel of 512 CTAs of 1024 threads (the join of
+// vocab_linear.cu at 16384 rows, two CTAs of which fill an SM), launched early between GEMMs of CTA
+// pairs, stood still with the GEMM after six calls without a pause. No bounded wait of a kernel ran
+// out, so CTAs were not being placed; which waited for which could not be shown. So the kernels whose
+// CTAs fill an SM between those GEMMs -- the join, the token sort, its sums, the few-row gradient -- go
+// early only as may_go_early has it, and otherwise in plain stream order on both sides: no attribute
+// of their own, no trigger for the next. The library's other kernels, the row and elementwise ones of
+// 256 threads among them, have always gone early, and none of them stood still.
 #ifdef __CUDACC__
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {
@@ -116,6 +122,23 @@ cudaError_t launch_kernel(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t 
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = pdl_enabled() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
+// At most one CTA of at most 256 threads for each of the device's SMs: whatever waits leaves seven
+// eighths of every SM's threads, and most of its registers and shared memory, to the kernels around it
+constexpr bool may_go_early(int64_t ctas, int threads, int sms) { return threads <= 256 && ctas <= sms; }
+
+// launch_kernel, or in plain stream order
+template <typename... KArgs, typename... Args>
+cudaError_t launch_kernel_if(bool early, void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                             cudaStream_t st, Args&&... args) {
+  if (early) return launch_kernel(kern, grid, block, smem, st, std::forward<Args>(args)...);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 

@@ -32,9 +32,12 @@ namespace tp {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kSortThreads = 1024;
-constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kMaxRange = 1152;   // rows of a sorting CTA: 32 counters each in shared memory
+// warps of a sorting CTA: 8 for few tokens, whose launch overlaps its predecessor (may_go_early), 32
+// beyond. us: 128 tokens of 256 x 128 7.6 and 10.3, 1000 of 5000 x 512 10.1 and 12.5, 4096 of 50304 x
+// 2048 44 either way, 8192 50 and 47.
+constexpr int kFewWarps = 8, kManyWarps = 32;
+constexpr int64_t kFewTokens = 4096;
+constexpr int kMaxRange = 1152;   // rows of a sorting CTA: a counter for each warp in shared memory
 constexpr int kKept = 512;        // tokens of its own that a sorting warp remembers
 constexpr int kWhole = 8;         // a row of at most so many tokens is not split
 constexpr int kGroup = 32;        // units whose partials of one row are added up on the way
@@ -174,18 +177,16 @@ struct Border {
 
 // Row c is row c >> log2_ctas of CTA c mod ctas; the list goes by CTA, then by row, then by warp and
 // the order in which a warp meets its tokens (four at a time per lane: a fixed order).
-// EARLY: launched ahead of its predecessor's end, and the next kernel ahead of its own, as long as it
-// has no more than a CTA per SM (more CTAs of 1024 threads, launched early, are not safe beside the
-// GEMMs of CTA pairs: vocab_linear_join_kernel).
-template <bool EARLY>
-__global__ void __launch_bounds__(kSortThreads) vocab_embed_sort_kernel(
+// ahead: the sums, which come next on the stream, may start ahead of its end: with no more than a CTA for
+// each SM all of its own are placed by then, and none of them waits for another.
+template <int kSortWarps>
+__global__ void __launch_bounds__(32 * kSortWarps) vocab_embed_sort_kernel(
     const int32_t* __restrict__ ids, int2* __restrict__ sorted, Border* __restrict__ border,
     int32_t* __restrict__ arrived, uint32_t* __restrict__ absent, int32_t M, int32_t v,
-    int log2_ctas, int range, int units, int columns) {
-  if (EARLY) {
-    pdl_wait();  // the previous kernel's results are complete and visible
-    pdl_trigger();
-  }
+    int log2_ctas, int range, int units, int columns, int ahead) {
+  constexpr int kSortThreads = 32 * kSortWarps;
+  pdl_wait();  // the previous kernel's results are complete and visible
+  if (ahead) pdl_trigger();
   extern __shared__ int32_t cnt[];              // [warp][range]
   int32_t* start = cnt + kSortWarps * range;    // [range + 1] the rows' starts
   uint32_t* kept = reinterpret_cast<uint32_t*>(start + range + 1);  // [warp][kKept]
@@ -252,8 +253,8 @@ __global__ void __launch_bounds__(kSortThreads) vocab_embed_sort_kernel(
     red[1][warp] = total;
   }
   __syncthreads();
-  below = red[0][lane];
-  total = red[1][lane];
+  below = lane < kSortWarps ? red[0][lane] : 0;
+  total = lane < kSortWarps ? red[1][lane] : 0;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     below += __shfl_xor_sync(0xFFFFFFFFu, below, o);
@@ -281,7 +282,7 @@ __global__ void __launch_bounds__(kSortThreads) vocab_embed_sort_kernel(
     __syncthreads();  // red has been read
     if (lane == 31) red[0][warp] = run;
     __syncthreads();
-    int all = red[0][lane], before = lane < warp ? all : 0;
+    int all = lane < kSortWarps ? red[0][lane] : 0, before = lane < warp ? all : 0;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       before += __shfl_xor_sync(0xFFFFFFFFu, before, o);
@@ -368,9 +369,9 @@ template <typename T, int VEC>
 __global__ void __launch_bounds__(kThreads, 4) vocab_embed_sum_kernel(
     const int2* __restrict__ sorted, const Border* __restrict__ border, const T* __restrict__ dx,
     T* dE, float* part, int32_t* arrived, const uint32_t* __restrict__ absent, int64_t h, int units,
-    int unit_blocks, int columns, int log2_ctas, int words, float scale, int accumulate) {
-  pdl_wait();  // the previous kernel's results are complete and visible
-  pdl_trigger();
+    int unit_blocks, int columns, int log2_ctas, int words, float scale, int accumulate, int ahead) {
+  pdl_wait();  // the sort's results are complete and visible
+  if (ahead) pdl_trigger();
   const int col = blockIdx.y * blockDim.x + threadIdx.x;
   const int64_t c = static_cast<int64_t>(col) * VEC;
   if (blockIdx.x >= unit_blocks) {
@@ -577,13 +578,16 @@ tp_status embed_sum(const SumPlan& P, const void* dx, void* dE, int64_t h, float
                     bool accumulate, char* ws, cudaStream_t st) {
   const int words = (P.range + 31) / 32, unit_blocks = (P.units + P.ty - 1) / P.ty;
   const int64_t blocks = unit_blocks + (accumulate ? 0 : static_cast<int64_t>(words) << P.log2_ctas);
+  // behind the sort, and ahead of what comes next only where may_go_early has it: its CTAs fill an SM's
+  // registers, and there are more of them than fit at once
+  const bool ahead = may_go_early(blocks * P.slices, kThreads, device_sm_count());
   TP_CUDA_TRY(launch_kernel(
       vocab_embed_sum_kernel<T, VEC>,
       dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(P.slices)), dim3(P.tx, P.ty), 0, st,
       reinterpret_cast<const int2*>(ws + P.sorted), reinterpret_cast<const Border*>(ws + P.border),
       static_cast<const T*>(dx), static_cast<T*>(dE), reinterpret_cast<float*>(ws + P.part),
       reinterpret_cast<int32_t*>(ws + P.arrived), reinterpret_cast<const uint32_t*>(ws + P.absent), h,
-      P.units, unit_blocks, P.columns, P.log2_ctas, words, scale, accumulate ? 1 : 0));
+      P.units, unit_blocks, P.columns, P.log2_ctas, words, scale, accumulate ? 1 : 0, ahead ? 1 : 0));
   count_launch();
   return TP_OK;
 }
@@ -611,31 +615,29 @@ tp_status launch_vocab_embed_scaled_bwd(const int32_t* ids, const void* dx, void
                                         tp_dtype dt, void* ws, cudaStream_t st) {
   const SumPlan P = sum_plan(M, v, h, dt);
   char* base = static_cast<char*>(ws);
-  const size_t smem = (static_cast<size_t>(kSortWarps) * (P.range + kKept) + P.range + 1) * 4;
-  auto sort = [&](auto kern, auto launch) -> tp_status {
+  const unsigned ctas = 1u << P.log2_ctas;
+  auto sort = [&](auto warps) -> tp_status {
+    constexpr int kWarps = decltype(warps)::value;
+    auto kern = vocab_embed_sort_kernel<kWarps>;
     static std::atomic<uint64_t> attr_set{0};  // per kernel and device
     if (needs_setup(attr_set)) {
       TP_CUDA_TRY(cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (kSortWarps * (kMaxRange + kKept) + kMaxRange + 1) * 4));
+                                       (kWarps * (kMaxRange + kKept) + kMaxRange + 1) * 4));
       mark_device(attr_set);
     }
-    TP_CUDA_TRY(launch(kern, ids, reinterpret_cast<int2*>(base + P.sorted),
-                       reinterpret_cast<Border*>(base + P.border),
-                       reinterpret_cast<int32_t*>(base + P.arrived),
-                       reinterpret_cast<uint32_t*>(base + P.absent), static_cast<int32_t>(M),
-                       static_cast<int32_t>(v), P.log2_ctas, P.range, P.units, P.columns));
+    const size_t smem = (static_cast<size_t>(kWarps) * (P.range + kKept) + P.range + 1) * 4;
+    const bool early = may_go_early(ctas, 32 * kWarps, device_sm_count());
+    TP_CUDA_TRY(launch_kernel_if(early, kern, ctas, 32 * kWarps, smem, st, ids,
+                                 reinterpret_cast<int2*>(base + P.sorted),
+                                 reinterpret_cast<Border*>(base + P.border),
+                                 reinterpret_cast<int32_t*>(base + P.arrived),
+                                 reinterpret_cast<uint32_t*>(base + P.absent), static_cast<int32_t>(M),
+                                 static_cast<int32_t>(v), P.log2_ctas, P.range, P.units, P.columns,
+                                 ctas <= static_cast<unsigned>(device_sm_count()) ? 1 : 0));
     return TP_OK;
   };
-  const unsigned ctas = 1u << P.log2_ctas;
-  if (ctas <= 152)
-    TP_TRY(sort(vocab_embed_sort_kernel<true>, [&](auto kern, auto... a) {
-      return launch_kernel(kern, ctas, kSortThreads, smem, st, a...);
-    }));
-  else
-    TP_TRY(sort(vocab_embed_sort_kernel<false>, [&](auto kern, auto... a) {
-      kern<<<ctas, kSortThreads, smem, st>>>(a...);
-      return cudaGetLastError();
-    }));
+  if (M <= kFewTokens) TP_TRY(sort(std::integral_constant<int, kFewWarps>()));
+  else TP_TRY(sort(std::integral_constant<int, kManyWarps>()));
   count_launch();
   if (dt == TP_BF16)
     return P.vec == 8   ? embed_sum<__nv_bfloat16, 8>(P, dx, dE, h, scale, accumulate, base, st)

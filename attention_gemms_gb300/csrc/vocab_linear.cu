@@ -28,10 +28,9 @@
 namespace tp {
 namespace {
 
-constexpr int kRows = 8;          // rows of a CTA of the join at the least
-constexpr int kJoinThreads = 1024;
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 constexpr int64_t kSms = 152;
-constexpr int kSumShards = 32;    // shards whose losses the join adds up itself, a warp each
+constexpr int kSumShards = 32;    // most shards whose losses the join adds up itself
 constexpr float kLog2e = 1.4426950408889634f;  // log2(e)
 
 // (m, s) pairs: s exp(m) summed
@@ -42,42 +41,35 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
   m = mm;
 }
 
-// A CTA joins ROWS rows: its 1024 threads, consecutive ones on consecutive rows, share the slots,
-// shuffles join a warp's, and a warp per row joins the warps'. The CTA that ends last adds the CTAs'
-// losses up (in an order of their own, whichever CTA that is): a launch less than a kernel of its
-// own. 8 rows, whose slots more threads share, where that is no more than a CTA per SM, else 32; up to
-// 128 rows of few slots one CTA, which has no other to wait for.
-// EARLY: launched ahead of its predecessor's end (pdl_wait), and the next kernel ahead of its own, for
-// no more than a CTA per SM. 512 CTAs of 1024 threads, two of which fill an SM, launched early between
-// GEMMs of CTA pairs stood still together with the GEMM that came next (16384 rows, six calls without
-// a pause; never with 256). In plain stream order none waits for room that another holds.
-template <int ROWS, bool EARLY>
+// A CTA joins ROWS rows: its threads, consecutive ones on consecutive rows, share the slots, shuffles
+// join a warp's, and a thread per row the warps'. The CTA that ends last adds the CTAs' losses up (in an
+// order of their own, whichever CTA that is): a launch less than a kernel of its own. early: launched
+// ahead of its predecessor's end, and the next kernel ahead of its own (may_go_early).
+template <int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) vocab_linear_join_kernel(
     const float2* __restrict__ part, const float* __restrict__ hit,
     const int32_t* __restrict__ targets, float* __restrict__ lse, float* __restrict__ row_loss,
     float* __restrict__ shard_loss, float* __restrict__ loss, float* cta_loss, int32_t* counter,
-    int slots, int64_t M, int64_t v, int N) {
-  if (EARLY) {
-    pdl_wait();  // the previous kernel's results are complete and visible
-    pdl_trigger();
-  }
-  // up to 32 rows: a warp ends a row, over the 32 warps' pairs; 128: a thread, over eight
-  constexpr bool kWarpEnds = ROWS <= 32;
-  constexpr int kPairs = kWarpEnds ? 32 : kJoinThreads / ROWS;
+    int slots, int64_t M, int64_t v, int N, int early) {
+  pdl_wait();  // the previous kernel's results are complete and visible
+  if (early) pdl_trigger();
+  // pairs that are left of a row: one of each warp, or of each thread where a warp has 32 rows
+  constexpr int kPairs = ROWS <= 32 ? kJoinWarps : kJoinThreads / ROWS;
   __shared__ float2 sm[kPairs][ROWS];
+  __shared__ float losses[ROWS];
+  __shared__ int shard[ROWS];
   __shared__ float sum[kSumShards];
   __shared__ int last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int mine = kWarpEnds ? warp : threadIdx.x;  // the row of the CTA that this thread ends
-  const int64_t own = static_cast<int64_t>(blockIdx.x) * ROWS + mine;
-  const bool ends = mine < ROWS && own < M;
+  const int64_t own = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x;  // the row that it ends
+  const bool ends = threadIdx.x < ROWS && own < M;
   int64_t t = ends ? targets[own] : -1;
   if (t >= v) t = -1;
   const float at = t >= 0 ? hit[own] : 0.0f;
   float m = -INFINITY, s = 0.0f;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x % ROWS;
   if (row < M) {
-#pragma unroll 4
+#pragma unroll 8
     for (int i = threadIdx.x / ROWS; i < slots; i += kJoinThreads / ROWS) {
       const float2 p = part[i * M + row];
       join(m, s, p.x, p.y);
@@ -86,52 +78,43 @@ __global__ void __launch_bounds__(kJoinThreads) vocab_linear_join_kernel(
 #pragma unroll
   for (int o = ROWS; o < 32; o *= 2)
     join(m, s, __shfl_xor_sync(0xFFFFFFFFu, m, o), __shfl_xor_sync(0xFFFFFFFFu, s, o));
-  if (kWarpEnds) {
-    if (lane < ROWS) sm[warp][lane % ROWS] = make_float2(m, s);
-  } else {
-    sm[threadIdx.x / ROWS][threadIdx.x % ROWS] = make_float2(m, s);
-  }
+  if (ROWS > 32 || lane < ROWS)
+    sm[ROWS <= 32 ? warp : threadIdx.x / ROWS][threadIdx.x % ROWS] = make_float2(m, s);
   __syncthreads();
-  float l = 0.0f;
-  if (mine < ROWS) {
-    if (kWarpEnds) {
-      m = sm[lane % kPairs][mine].x;
-      s = sm[lane % kPairs][mine].y;
+  if (threadIdx.x < ROWS) {
+    float2 p[kPairs];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-        join(m, s, __shfl_xor_sync(0xFFFFFFFFu, m, o), __shfl_xor_sync(0xFFFFFFFFu, s, o));
-    } else {
+    for (int w = 0; w < kPairs; ++w) p[w] = sm[w][threadIdx.x];
+    m = p[0].x;
 #pragma unroll
-      for (int w = 1; w < kPairs; ++w) join(m, s, sm[w][mine].x, sm[w][mine].y);
-    }
+    for (int w = 1; w < kPairs; ++w) m = fmaxf(m, p[w].x);
+    s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kPairs; ++w) s += p[w].y * exp2f((p[w].x - m) * kLog2e);
     // m is a logit and s >= 1: the loss does not go by way of lse, whose rounding is the logits' size,
     // and is never below 0
     const float log_s = logf(s);
-    l = t >= 0 ? (m - at) + log_s : 0.0f;
-    if (ends && (lane == 0 || !kWarpEnds)) {
+    const float l = t >= 0 ? (m - at) + log_s : 0.0f;
+    if (ends) {
       lse[own] = m + log_s;
       row_loss[own] = l;
     }
+    losses[threadIdx.x] = l;
+    shard[threadIdx.x] = t >= 0 ? static_cast<int>(t / (v / N)) : -1;
   }
   if (N > kSumShards) return;
-  __shared__ float losses[ROWS];
-  __shared__ int shard[ROWS];
-  if (mine < ROWS && (lane == 0 || !kWarpEnds)) {
-    losses[mine] = l;
-    shard[mine] = t >= 0 ? static_cast<int>(t / (v / N)) : -1;
-  }
   __syncthreads();
-  if (warp < N) {
+  for (int i = warp; i < N; i += kJoinWarps) {
     float a = 0.0f;
 #pragma unroll
     for (int r = 0; r < ROWS; r += 32)
-      if (lane + r < ROWS) a += shard[lane + r] == warp ? losses[lane + r] : 0.0f;
+      if (lane + r < ROWS) a += shard[lane + r] == i ? losses[lane + r] : 0.0f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
     if (lane == 0) {
-      sum[warp] = a;
+      sum[i] = a;
       if (gridDim.x > 1) {
-        cta_loss[static_cast<int64_t>(blockIdx.x) * N + warp] = a;
+        cta_loss[static_cast<int64_t>(blockIdx.x) * N + i] = a;
         __threadfence();
       }
     }
@@ -143,14 +126,15 @@ __global__ void __launch_bounds__(kJoinThreads) vocab_linear_join_kernel(
   }
   __syncthreads();
   if (!last) return;
-  if (gridDim.x > 1 && warp < N) {
-    float a = 0.0f;
-#pragma unroll 4
-    for (int64_t c = lane; c < gridDim.x; c += 32) a += __ldcg(cta_loss + c * N + warp);
+  if (gridDim.x > 1)
+    for (int i = warp; i < N; i += kJoinWarps) {
+      float a = 0.0f;
+#pragma unroll 8
+      for (int64_t c = lane; c < gridDim.x; c += 32) a += __ldcg(cta_loss + c * N + i);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
-    if (lane == 0) sum[warp] = a;
-  }
+      for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xFFFFFFFFu, a, o);
+      if (lane == 0) sum[i] = a;
+    }
   __syncthreads();
   if (threadIdx.x == 0) {
     float total = 0.0f;
@@ -291,15 +275,6 @@ __global__ void __launch_bounds__(256, 2)
   }
 }
 
-// launch_kernel, or in plain stream order
-template <typename... KArgs, typename... Args>
-cudaError_t launch_after(bool early, void (*kern)(KArgs...), unsigned grid, unsigned block,
-                         cudaStream_t st, Args&&... args) {
-  if (early) return launch_kernel(kern, grid, block, 0, st, std::forward<Args>(args)...);
-  kern<<<grid, block, 0, st>>>(std::forward<Args>(args)...);
-  return cudaGetLastError();
-}
-
 size_t a256(size_t x) { return align_up(x, 256); }
 
 // ---- forward: partials of every row (a slot for 64 columns at the least), the targets' logits,
@@ -307,12 +282,20 @@ size_t a256(size_t x) { return align_up(x, 256); }
 struct FwdLayout {
   size_t part, hit, cta, counter, total;
 };
+// Rows of a CTA of the join where they have many slots. Two with up to a CTA per SM, eight while 32
+// threads of a row count (1300 x 50304 x 64 51 us, 59 with 32 rows; 4864 rows 125 and 134), 32 beyond,
+// where the sums of the CTAs' losses do (8192 rows x 5000 33.0 us, 34.8 with eight; 60000 x 3000 107 and
+// 127).
+int join_rows(int64_t M) { return M <= 2 * kSms ? 2 : M <= 32 * kSms ? 8 : 32; }
+int64_t join_ctas(int64_t M) { return (M + join_rows(M) - 1) / join_rows(M); }
 FwdLayout fwd_layout(int64_t M, int64_t v) {
   FwdLayout L{};
   size_t o = 0;
   L.part = o;    o += a256(static_cast<size_t>((v + 63) / 64) * M * sizeof(float2));
   L.hit = o;     o += a256(M * sizeof(float));
-  L.cta = o;     o += a256((M + kRows - 1) / kRows * kSumShards * sizeof(float));
+  // join_ctas or more, and never less for more rows
+  const int64_t ctas = std::max({kSms, join_ctas(std::min(M, 32 * kSms)), (M + 31) / 32});
+  L.cta = o;     o += a256(ctas * kSumShards * sizeof(float));
   L.counter = o; o += 256;
   L.total = o;
   return L;
@@ -438,17 +421,19 @@ tp_status launch_vocab_linear_ce_fwd(const void* x, const void* E, const int32_t
   d.ce.counter = counter;
   d.ce.slots = &slots;
   TP_TRY(product(d, st));
-  const int rows = M <= 128 && slots <= 32 ? 128 : M <= kRows * kSms ? kRows : 32;
-  const unsigned grid = static_cast<unsigned>((M + rows - 1) / rows);
-  auto join = [&](auto kern, bool early) {
-    return launch_after(early, kern, grid, kJoinThreads, st, d.ce.part, hit, targets, lse, row_loss,
-                        shard_loss, loss, reinterpret_cast<float*>(base + L.cta), counter, slots, M,
-                        v, N);
+  // 128 rows of few slots: one CTA, which has no other to wait for
+  const bool one = M <= 128 && slots <= 32;
+  const unsigned grid = one ? 1u : static_cast<unsigned>(join_ctas(M));
+  const bool early = may_go_early(grid, kJoinThreads, device_sm_count());
+  auto join = [&](auto kern) {
+    return launch_kernel_if(early, kern, grid, kJoinThreads, 0, st, d.ce.part, hit, targets, lse, row_loss,
+                            shard_loss, loss, reinterpret_cast<float*>(base + L.cta), counter, slots, M,
+                            v, N, early ? 1 : 0);
   };
-  TP_CUDA_TRY(rows == 128     ? join(vocab_linear_join_kernel<128, true>, true)
-              : rows == kRows ? join(vocab_linear_join_kernel<kRows, true>, true)
-              : grid <= kSms  ? join(vocab_linear_join_kernel<32, true>, true)
-                              : join(vocab_linear_join_kernel<32, false>, false));
+  TP_CUDA_TRY(one                 ? join(vocab_linear_join_kernel<128>)
+              : join_rows(M) == 2 ? join(vocab_linear_join_kernel<2>)
+              : join_rows(M) == 8 ? join(vocab_linear_join_kernel<8>)
+                                  : join(vocab_linear_join_kernel<32>));
   count_launch();
   return N > kSumShards ? launch_vocab_ce_loss(row_loss, targets, shard_loss, loss, M, v, N, st)
                         : TP_OK;
