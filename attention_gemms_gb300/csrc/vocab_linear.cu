@@ -315,9 +315,12 @@ struct BwdPlan {
 // Parts of the sum over K of a product with (rows, cols) outputs, where its tiles alone would leave
 // SMs idle: the number that takes the least time by whole waves of the tiles (256 x 512 or 256 x 256
 // on an SM pair, as the engine takes them, else about 128 x 128 on an SM) and by the fp32 partials,
-// written, read and added up by a launch more. No part of fewer than 256 products, no more than 512
-// MiB of partials; `partials`: one part is a partial too. (dx of 8192 x 4096, tiles of 3.4 waves, in two parts: 5.55 ms with the other
-// products, 5.75 in one; 1003 x 1032 in 15: 0.31, 0.36 in four.)
+// written, read and added up by a launch more. No part of fewer than 256 products, none that holds
+// nothing, no more than 512 MiB of partials; `partials`: one part is a partial too. (dx of 8192 x 4096,
+// tiles of 3.4 waves, in two parts: 5.55 ms with the other products, 5.75 in one.)
+int64_t part_length(int64_t K, int64_t parts) {  // whole K blocks, where there is more than one part
+  return parts == 1 ? K : ((K + parts - 1) / parts + 63) / 64 * 64;
+}
 int sum_parts(int64_t rows, int64_t cols, int64_t K, bool partials) {
   const bool pair = rows >= 256 && cols >= 256;
   const int64_t tw = pair ? 256 : 128, at_once = pair ? kSms / 2 : kSms;
@@ -327,14 +330,16 @@ int sum_parts(int64_t rows, int64_t cols, int64_t K, bool partials) {
   double least = 0.0;
   for (int g = 1; g <= 32; ++g) {
     if (g > 1 && (K / g < 256 || g * rows * cols * 4 > (512ll << 20))) break;
+    const int64_t k = part_length(K, g);
+    if ((g - 1) * k >= K) continue;  // the last part would hold nothing
     double w = static_cast<double>(waves(tiles * g));
-    if (pair && cols % 512 == 0 && K / g >= 4096) {
+    if (pair && cols % 512 == 0 && k >= 4096) {
       const int64_t wide = down * (cols / 512) * g;  // a tile of two, at 10 % more of its work
       if (wide >= 4 * at_once || 18 * waves(wide) < 10 * waves(tiles * g))
         w = 1.8 * static_cast<double>(waves(wide));
     }
     // seconds: a wave's products at 1.7e15 / (152 SMs), the partials at 5e12 bytes, their launch
-    const double t = w * (2.0 * tw * tw * (K / g)) * at_once / 1.7e15 +
+    const double t = w * (2.0 * tw * tw * k) * at_once / 1.7e15 +
                      (g > 1 || partials ? g * rows * cols * 8.0 / 5e12 + 3e-6 : 0.0);
     if (g == 1 || t < least) {
       best = g;
@@ -363,7 +368,7 @@ BwdPlan bwd_plan(int64_t M, int64_t v, int64_t h, tp_dtype dt) {
 // a product's sum over K in `parts` parts (1: as it is), each a partial of its own at out
 void split_sum(GemmDesc& d, int parts) {
   if (parts == 1) return;
-  d.K = ((d.K + parts - 1) / parts + 63) / 64 * 64;
+  d.K = part_length(d.K, parts);
   d.groups = parts;
   d.out_group_stride = d.M * d.N;
 }
