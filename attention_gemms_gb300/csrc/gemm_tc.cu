@@ -1928,15 +1928,9 @@ tp_status plan_gemm_tc(const GemmDesc& d, TcParams& prm, TcPlan& plan) {
   if (plan.tiles > (1ll << 30)) return fail(TP_ERR_SHAPE, "problem too large");
   return TP_OK;
 }
-}  // namespace
 
-tp_status launch_gemm_tc(const GemmDesc& d, cudaStream_t st) {
-  if (d.M <= 0 || d.N <= 0 || d.K <= 0) return TP_OK;
-  TcSet<1> set;
-  TcPlan plan;
-  TP_TRY(plan_gemm_tc(d, set.p[0], plan));
+tp_status launch_planned(int epi, TcSet<1>& set, const TcPlan& plan, cudaStream_t st) {
   set.tiles[0] = static_cast<int>(plan.tiles);
-  const int epi = d.epi;
   if (plan.pair) return launch_pair(epi, plan.wide, plan.epi8, set, st);
   const int grid = static_cast<int>(std::min<int64_t>(
       plan.tiles, static_cast<int64_t>(device_sm_count()) * (plan.dec ? TP_DEC_CTAS_PER_SM : 1)));
@@ -1948,11 +1942,20 @@ tp_status launch_gemm_tc(const GemmDesc& d, cudaStream_t st) {
   return plan.BN == 256 ? launch_bn<256, false>(epi, set, grid, st)
                         : launch_bn<128, false>(epi, set, grid, st);
 }
+}  // namespace
+
+tp_status launch_gemm_tc(const GemmDesc& d, cudaStream_t st) {
+  if (d.M <= 0 || d.N <= 0 || d.K <= 0) return TP_OK;
+  TcSet<1> set;
+  TcPlan plan;
+  TP_TRY(plan_gemm_tc(d, set.p[0], plan));
+  return launch_planned(d.epi, set, plan, st);
+}
 
 tp_status launch_gemm_tc_two(const GemmDesc& a, const GemmDesc& b, cudaStream_t st) {
+  const int64_t k_a = static_cast<int64_t>(a.nseg) * a.K, k_b = static_cast<int64_t>(b.nseg) * b.K;
   // the longer sums first, so that no long tile begins last
-  const bool swap = static_cast<int64_t>(a.nseg) * a.K < static_cast<int64_t>(b.nseg) * b.K;
-  const GemmDesc* d[2] = {swap ? &b : &a, swap ? &a : &b};
+  const GemmDesc* d[2] = {k_a < k_b ? &b : &a, k_a < k_b ? &a : &b};
   TcSet<2> set;
   TcPlan plan[2];
   for (int i = 0; i < 2; ++i) {
@@ -1963,15 +1966,18 @@ tp_status launch_gemm_tc_two(const GemmDesc& a, const GemmDesc& b, cudaStream_t 
   const bool alike = plan[0].pair == plan[1].pair && !plan[0].wide && !plan[1].wide &&
                      plan[0].epi8 == plan[1].epi8 && plan[0].BN == plan[1].BN && !plan[0].dec &&
                      !plan[1].dec && (plan[0].pair || plan[0].BN < 256);
-  const int64_t k_most = static_cast<int64_t>(d[0]->nseg) * d[0]->K;
   // up to a wave of one-CTA tiles or two of pair tiles, and sums of up to 1024; us of dx, dE and the
   // logits' gradient, together and one by one: 300 x 1500 x 256 15.5 and 19.3, 1000 x 6000 x 512 41 and
   // 44, 512 x 512 x 5120 45 and 50. More lose: one-CTA tiles that share a CTA, 1000 x 1000 x 1000 34.6
   // and 29.8; longer sums, beside whose tiles the launch is nothing and the operands that both sets
   // take from L2 are more, 4096 x 4096 x 2048 156 and 143, 8192 x 50304 x 2048 3370 and 3090.
-  if (!alike || tiles > device_sm_count() || k_most > 1024) {
-    TP_TRY(launch_gemm_tc(a, st));
-    return launch_gemm_tc(b, st);
+  if (!alike || tiles > device_sm_count() || std::max(k_a, k_b) > 1024) {
+    for (const int i : {k_a < k_b ? 1 : 0, k_a < k_b ? 0 : 1}) {  // a, then b, as they are planned
+      TcSet<1> one;
+      one.p[0] = set.p[i];
+      TP_TRY(launch_planned(d[i]->epi, one, plan[i], st));
+    }
+    return TP_OK;
   }
   if (plan[0].pair)
     return plan[0].epi8 ? launch_pair_epi<EPI_STORE, 1, 8, 2>(set, st)
