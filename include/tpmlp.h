@@ -766,7 +766,8 @@ TP_API tp_status tp_vocab_ce_bwd(const void* logits, const int32_t* targets, con
  *   with M <= 64 * 65535.
  *   lse, row_loss, shard_loss, loss, targets: 4-byte aligned.
  *   ws: tp_vocab_linear_ce_workspace_size(1, ...) bytes, uninitialised, for one call at a time
- *   (calls on one stream may share it). At most 1/16 of the bf16 logits, and 20 bytes per row.
+ *   (calls on one stream may share it): at most 8 ceil(vocab / 64) + 20 bytes for each row, and 24
+ *   KiB; a workspace for M rows serves any fewer.
  * A row whose target lies outside [0, vocab) gets row_loss 0 and its lse. Buffers do not overlap.
  * M <= 2^30, vocab <= 2^30, h <= 2^20 (here and below). M = 0 launches nothing.
  * Errors: TP_ERR_INVALID_ARG, SHAPE, DTYPE, ALIGNMENT, WORKSPACE, CUDA, UNSUPPORTED. */
