@@ -103,18 +103,6 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
                "r"(d)
                : "memory");
 }
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-
-// 2^x on the special-function unit (PTX ex2.approx.ftz: relative error about 2^-22,
-// subnormal results flushed to zero); P is rounded to bf16 right after
-__device__ __forceinline__ float ex2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // 32 fp32 values times `mul` as bf16 to global memory (16-byte aligned)
 __device__ __forceinline__ void st_row_bf16(__nv_bfloat16* dst, const uint32_t* v, float mul) {
@@ -323,7 +311,7 @@ __global__ void __launch_bounds__(FwdLayout<NH>::kThreads, kCtasPerSm) attn_fwd_
       const bool move = mb > m2 + 8.0f;
       const float m_new = move ? mb : m2;
       const float m_use = m_new == -INFINITY ? 0.0f : m_new;
-      const float corr = move ? ex2_approx(m2 - m_use) : 1.0f;  // 0 on the first block
+      const float corr = move ? ex2(m2 - m_use) : 1.0f;  // 0 on the first block
       // P may be overwritten and O rescaled once the previous block's P V is complete
       if (j > 0 && !wait_all(o_done(hh), (j - 1) & 1)) {
         ok = false;
@@ -334,7 +322,7 @@ __global__ void __launch_bounds__(FwdLayout<NH>::kThreads, kCtasPerSm) attn_fwd_
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < kKB; ++i) {
-        const float e = ex2_approx(fmaf(__uint_as_float(v[i]), p.scale_log2, -m_use));
+        const float e = ex2(fmaf(__uint_as_float(v[i]), p.scale_log2, -m_use));
         sum += e;
         v[i] = __float_as_uint(e);
       }
@@ -674,9 +662,9 @@ __global__ void __launch_bounds__(kThreadsBwd, 2) attn_bwd_dq_tc_kernel(const __
 #pragma unroll
         for (int i = 0; i < 32; i += 2)
           dk[i >> 1] = pack_bf16x2(
-              ex2_approx(fmaf(__uint_as_float(sv[i]), p.scale_log2, -lse2)) *
+              ex2(fmaf(__uint_as_float(sv[i]), p.scale_log2, -lse2)) *
                   (__uint_as_float(pv[i]) - Dq),
-              ex2_approx(fmaf(__uint_as_float(sv[i + 1]), p.scale_log2, -lse2)) *
+              ex2(fmaf(__uint_as_float(sv[i + 1]), p.scale_log2, -lse2)) *
                   (__uint_as_float(pv[i + 1]) - Dq));
       } else {  // keys beyond the sequence or after the query, rows beyond the sequence
 #pragma unroll
@@ -687,7 +675,7 @@ __global__ void __launch_bounds__(kThreadsBwd, 2) attn_bwd_dq_tc_kernel(const __
             const int key = k0 + i + e;
             const bool live = valid && key < p.s && !(p.causal && key > qi);
             const float pr =
-                live ? ex2_approx(fmaf(__uint_as_float(sv[i + e]), p.scale_log2, -lse2)) : 0.0f;
+                live ? ex2(fmaf(__uint_as_float(sv[i + e]), p.scale_log2, -lse2)) : 0.0f;
             ds[e] = pr * (__uint_as_float(pv[i + e]) - Dq);
           }
           dk[i >> 1] = pack_bf16x2(ds[0], ds[1]);
@@ -938,7 +926,7 @@ __global__ void __launch_bounds__(kThreadsBwd, 2) attn_bwd_dkdv_tc_kernel(const 
         for (int e = 0; e < 2; ++e) {
           const float l2 = e ? l4.z : l4.x, dq = e ? l4.w : l4.y;
           const float x = fmaf(__uint_as_float(sv[i + e]), p.scale_log2, -l2);
-          pr[e] = ex2_approx((live_bits & (1u << (i + e))) ? x : -INFINITY);  // 2^-inf = 0
+          pr[e] = ex2((live_bits & (1u << (i + e))) ? x : -INFINITY);  // 2^-inf = 0
           ds[e] = pr[e] * (__uint_as_float(pv[i + e]) - dq);
         }
         pk[i >> 1] = pack_bf16x2(pr[0], pr[1]);

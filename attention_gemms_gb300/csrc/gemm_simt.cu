@@ -384,16 +384,6 @@ __device__ __forceinline__ void big_put(float (*S)[BT + BPAD], bool mn, const Bi
   }
 }
 
-// two FMAs in one instruction, each rounded as fmaf: (c0, c1) += a (b0, b1)
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void fma2(uint64_t& c, uint64_t a, uint64_t b) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(c) : "l"(a), "l"(b));
-}
-
 template <int EPI>
 __global__ void __launch_bounds__(256, 2)
     gemm_simt_big_kernel(const SimtParams p, int tiles_m, int tiles_n, int vec_a, int vec_b) {
@@ -435,9 +425,9 @@ __global__ void __launch_bounds__(256, 2)
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint64_t aa = pack2(a[i], a[i]);
+        const uint64_t aa = pair_of(a[i], a[i]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) fma2(acc2[i][j], aa, b[j]);
+        for (int j = 0; j < 4; ++j) acc2[i][j] = fma2(aa, b[j], acc2[i][j]);
       }
     }
     if (it + 1 < steps) {  // the other stage: its reads ended before the last barrier
@@ -452,7 +442,7 @@ __global__ void __launch_bounds__(256, 2)
     float acc[8];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      asm("mov.b64 {%0, %1}, %2;" : "=f"(acc[2 * j]), "=f"(acc[2 * j + 1]) : "l"(acc2[i][j]));
+      split_pair(acc2[i][j], acc[2 * j], acc[2 * j + 1]);
     if constexpr (EPI == EPI_LSE) {  // the row's 128 columns lie in 16 lanes of the warp
       const int64_t t = r < p.M ? p.ce.targets[r] : -1;
       float m = -INFINITY;

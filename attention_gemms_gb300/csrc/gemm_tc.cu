@@ -236,41 +236,10 @@ struct EpiInputs {
 // difference, which is 0 for the largest logit itself, so its power is 1 exactly and a sum no less;
 // the gradient's exp(l - lse) likewise. With m log2(e) rounded beforehand, a fused multiply-add for
 // each logit, a target with all of the probability got losses of -8e-6 for logits of 100, and logits
-// of 1e10 infinite powers. Two logits at a time, these are as many instructions as that. ex2.approx: relative error about 2^-22; a term below 2^-126 of the
-// row's largest is dropped. The logits stay in 32 bits; only the gradient's tile is rounded, to bf16,
-// the operand type of the products that take it.
+// of 1e10 infinite powers. Two logits at a time, these are as many instructions as that. A term below
+// 2^-126 of the row's largest is dropped. The logits stay in 32 bits; only the gradient's tile is
+// rounded, to bf16, the operand type of the products that take it.
 constexpr float kCeLog2e = 1.4426950408889634f;  // log2(e)
-
-__device__ __forceinline__ float ce_ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// two values in one register pair, and arithmetic on both, each rounded as by itself
-__device__ __forceinline__ uint64_t f32x2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void split_f32x2(uint64_t v, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
-}
-__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 
 struct CeRow {
   int t = -1;              // the target's column of the product; outside [0, N): none here
@@ -321,18 +290,18 @@ __device__ __forceinline__ void ce_lse32(const TcParams& p, CeRow& r, int64_t ro
 #pragma unroll
   for (int j = 1; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(ra[j]));
   if (mx > r.m) {
-    r.s *= ce_ex2((r.m - mx) * kCeLog2e);  // 0 at first
+    r.s *= ex2((r.m - mx) * kCeLog2e);  // 0 at first
     r.m = mx;
   }
-  const uint64_t down = f32x2(-r.m, -r.m), log2e = f32x2(kCeLog2e, kCeLog2e);
+  const uint64_t down = pair_of(-r.m, -r.m), log2e = pair_of(kCeLog2e, kCeLog2e);
   float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
   for (int j = 0; j < 32; j += 2) {
-    const uint64_t l = f32x2(__uint_as_float(ra[j]), __uint_as_float(ra[j + 1]));
+    const uint64_t l = pair_of(__uint_as_float(ra[j]), __uint_as_float(ra[j + 1]));
     float a, b;
-    split_f32x2(mul_f32x2(add_f32x2(l, down), log2e), a, b);
-    s0 += ce_ex2(a);
-    s1 += ce_ex2(b);
+    split_pair(mul2(add2(l, down), log2e), a, b);
+    s0 += ex2(a);
+    s1 += ex2(b);
   }
   r.s += s0 + s1;
 }
@@ -340,14 +309,14 @@ __device__ __forceinline__ void ce_lse32(const TcParams& p, CeRow& r, int64_t ro
 // the gradient of 32 logits in their place, |scale| in the exponent: a subtraction and a fused
 // multiply-add for two, and one power each. Zeros in a row without a target.
 __device__ __forceinline__ void ce_grad32(const TcParams& p, const CeRow& r, int x, uint32_t* ra) {
-  const uint64_t down = f32x2(-r.lse, -r.lse), log2e = f32x2(kCeLog2e, kCeLog2e), ls = f32x2(r.ls, r.ls);
+  const uint64_t down = pair_of(-r.lse, -r.lse), log2e = pair_of(kCeLog2e, kCeLog2e), ls = pair_of(r.ls, r.ls);
 #pragma unroll
   for (int j = 0; j < 32; j += 2) {
-    const uint64_t l = f32x2(__uint_as_float(ra[j]), __uint_as_float(ra[j + 1]));
+    const uint64_t l = pair_of(__uint_as_float(ra[j]), __uint_as_float(ra[j + 1]));
     float a, b;
-    split_f32x2(fma_f32x2(add_f32x2(l, down), log2e, ls), a, b);
-    ra[j] = __float_as_uint(ce_ex2(a));
-    ra[j + 1] = __float_as_uint(ce_ex2(b));
+    split_pair(fma2(add2(l, down), log2e, ls), a, b);
+    ra[j] = __float_as_uint(ex2(a));
+    ra[j + 1] = __float_as_uint(ex2(b));
   }
   const unsigned tj = static_cast<unsigned>(r.t - x);
   if (__any_sync(0xFFFFFFFFu, r.t >= 0 && tj < 32u)) {

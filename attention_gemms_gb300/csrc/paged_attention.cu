@@ -22,6 +22,7 @@
 
 #include "internal.h"
 #include "paged.cuh"
+#include "ptx.cuh"
 
 namespace tp {
 namespace {
@@ -50,11 +51,6 @@ __device__ __forceinline__ void store8(__nv_bfloat16* dst, const float (&a)[4], 
   *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-__device__ __forceinline__ float ex2(float x) {  // relative error about 2^-22, 4 fp32 roundings
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // 16 bytes of global into shared memory, zeros unless `live` (the address is valid either way)
 __device__ __forceinline__ void copy16(float* dst, const void* src, bool live) {

@@ -181,35 +181,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
   return y;
 }
-// two fp32 values per instruction
-__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void split(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float ex2(float x) {  // relative error about 2^-22
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// P rounded to bf16 (relative 2^-8 of each weight), the operand of the second product
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
 
 // 4 x 4 transpose over the lanes of a quad: chunk i of lane y becomes chunk y of lane i
 __device__ __forceinline__ void quad_transpose(uint32_t (&q)[4][4]) {
@@ -695,11 +666,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float s0 = __uint_as_float(v[2 * y]), s1 = __uint_as_float(v[2 * y + 1]);
               mx[y & 3] = max3(mx[y & 3], s0, s1);
               float a, b;
-              split(fma2(pair_of(s0, s1), sc2, mu2), a, b);
+              split_pair(fma2(pair_of(s0, s1), sc2, mu2), a, b);
               a = ex2(a);
               b = ex2(b);
               sum[y & 1] = add2(sum[y & 1], pair_of(a, b));
-              pk[y] = pack2(a, b);
+              // P rounded to bf16 (relative 2^-8 of each weight), the operand of the second product
+              pk[y] = pack_bf16x2(a, b);
             }
             const float mb = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
             const bool move = mb > m + 8.0f;
@@ -729,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           tmem_st32(tP(t) + lanes + L::kPHalf * h, pk);
           float sa, sb2;
-          split(add2(sum[0], sum[1]), sa, sb2);
+          split_pair(add2(sum[0], sum[1]), sa, sb2);
           l = l * f + (sa + sb2);
           tmem_st_wait();
         }
@@ -839,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int y = 0; y < 4; ++y)
-              q[i][y] = pack2(__uint_as_float(o[8 * i + 2 * y]), __uint_as_float(o[8 * i + 2 * y + 1]));
+              q[i][y] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * y]), __uint_as_float(o[8 * i + 2 * y + 1]));
           quad_transpose(q);
 #pragma unroll
           for (int i = 0; i < 4; ++i)  // row of lane (lane & ~3) + i, its chunk lane & 3

@@ -77,36 +77,6 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
     return r * 32 + ((c ^ ((r >> 2) & 1)) << 4);
 }
 
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
-      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ float ex2(float x) {  // relative error about 2^-22
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// P rounded to bf16 (relative 2^-8 of each weight), the operand of the second product
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
 __device__ __forceinline__ void consumers_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kConsumers * 32) : "memory");
 }
@@ -268,9 +238,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             uint32_t b[4];
-            ldsm4(b, kt + chunk_at<D>(r, 2 * kk + c));
-            mma16816(s[0], q[kk], b[0], b[1]);
-            mma16816(s[1], q[kk], b[2], b[3]);
+            ldmatrix_x4(b, kt + chunk_at<D>(r, 2 * kk + c));
+            mma_16n8k16(s[0], q[kk], b[0], b[1]);
+            mma_16n8k16(s[1], q[kk], b[2], b[3]);
           }
         }
         const uint32_t miss = bad[st];
@@ -327,17 +297,18 @@ __global__ void __launch_bounds__(kThreads, 2)
             s[n][k] = ex2(fmaf(s[n][k], p.scale_log2, -mu[k >> 1]));
             l[k >> 1] += s[n][k];
           }
-        const uint32_t a[4] = {pack2(s[0][0], s[0][1]), pack2(s[0][2], s[0][3]),
-                               pack2(s[1][0], s[1][1]), pack2(s[1][2], s[1][3])};
+        // P rounded to bf16 (relative 2^-8 of each weight), the operand of the second product
+        const uint32_t a[4] = {pack_bf16x2(s[0][0], s[0][1]), pack_bf16x2(s[0][2], s[0][3]),
+                               pack_bf16x2(s[1][0], s[1][1]), pack_bf16x2(s[1][2], s[1][3])};
         {
           // matrices (transposed): keys 0-7 / 8-15 (lane bit 3), dims 0-7 / 8-15 (lane bit 4)
           const int r = rbase + (lane & 15), c = lane >> 4;
 #pragma unroll
           for (int n = 0; n < D / 16; ++n) {
             uint32_t b[4];
-            ldsm4_t(b, vt + chunk_at<D>(r, 2 * n + c));
-            mma16816(o[2 * n], a, b[0], b[1]);
-            mma16816(o[2 * n + 1], a, b[2], b[3]);
+            ldmatrix_x4_trans(b, vt + chunk_at<D>(r, 2 * n + c));
+            mma_16n8k16(o[2 * n], a, b[0], b[1]);
+            mma_16n8k16(o[2 * n + 1], a, b[2], b[3]);
           }
         }
         __syncwarp();
@@ -403,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (begins && ends)
             *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + t * p.H * D +
                                       static_cast<int64_t>(jhead) * D + c0 + jc) =
-                make_uint2(pack2(v.x * inv, v.y * inv), pack2(v.z * inv, v.w * inv));
+                make_uint2(pack_bf16x2(v.x * inv, v.y * inv), pack_bf16x2(v.z * inv, v.w * inv));
           else
             *reinterpret_cast<float4*>(slot + 2 * kRows + jr * D + c0 + jc) = v;
         }

@@ -161,24 +161,6 @@ constexpr int kOuterEntries = 64;  // vocabulary entries of a step
 constexpr int kXPitch = kOuterCols + 8, kQPitch = kOuterEntries + 8;  // no bank conflicts of ldmatrix
 constexpr int kOuterSmem = (kOuterRows * kXPitch + 2 * kOuterRows * kQPitch) * 2;
 
-__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void mma_16n8k16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                            uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&b);
-}
 // p[j] of lane t of a quad becomes p[t] of its lane j
 __device__ __forceinline__ void transpose_quad(uint32_t (&p)[4], int t) {
 #pragma unroll
@@ -264,7 +246,7 @@ __global__ void __launch_bounds__(256, 2)
       for (int hf = 0; hf < 2; ++hf) {
         uint32_t p[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = pack_bf16(acc[j + i][2 * hf], acc[j + i][2 * hf + 1]);
+        for (int i = 0; i < 4; ++i) p[i] = pack_bf16x2(acc[j + i][2 * hf], acc[j + i][2 * hf + 1]);
         transpose_quad(p, t);
         if (c + 8 * hf < n && col < h)
           *reinterpret_cast<uint4*>(dE + (c + 8 * hf) * h + col) = make_uint4(p[0], p[1], p[2], p[3]);
