@@ -122,8 +122,8 @@ struct TcParams {  // CUtensorMap members carry their own 128-byte alignment
   int ld32;  // epilogue inputs likewise: 256-bit loads
   int64_t out_group_stride;
   int tma_out;  // pair kernel: the epilogue stages outputs in shared memory, TMA stores them
-  int out_acc;  // EPI_STORE in fp32: added to out0
-  CeEpi ce;     // EPI_LSE, EPI_DCE
+  int out_acc;  // EPI_STORE and EPI_SCALE in fp32: added to out0
+  CeEpi ce;     // EPI_LSE, EPI_DCE, EPI_SCALE
   int* status;
   uint64_t timeout_ns;
   int debug_hang;
@@ -247,7 +247,7 @@ struct CeRow {
   float m = -INFINITY;     // EPI_LSE: running maximum and sum
   float s = 0.0f;
   float lse = 0.0f;        // EPI_DCE: of a row with a target
-  float ls = -INFINITY;    // EPI_DCE: log2|scale|; -inf in a row without a target
+  float add = -INFINITY;   // EPI_DCE, to the exponents: 0; -inf in a row without a target
 };
 
 template <int EPI>
@@ -261,7 +261,7 @@ __device__ __forceinline__ CeRow ce_row(const TcParams& p, int64_t row) {
       if constexpr (EPI == EPI_DCE) {
         if (r.live) {
           r.lse = __ldg(p.ce.lse + row);
-          r.ls = log2f(fabsf(p.ce.scale));
+          r.add = 0.0f;
         }
       }
     }
@@ -306,15 +306,15 @@ __device__ __forceinline__ void ce_lse32(const TcParams& p, CeRow& r, int64_t ro
   r.s += s0 + s1;
 }
 
-// the gradient of 32 logits in their place, |scale| in the exponent: a subtraction and a fused
-// multiply-add for two, and one power each. Zeros in a row without a target.
-__device__ __forceinline__ void ce_grad32(const TcParams& p, const CeRow& r, int x, uint32_t* ra) {
-  const uint64_t down = pair_of(-r.lse, -r.lse), log2e = pair_of(kCeLog2e, kCeLog2e), ls = pair_of(r.ls, r.ls);
+// softmax - one_hot of 32 logits in their place: a subtraction and a fused multiply-add for two, and one
+// power each. Zeros in a row without a target.
+__device__ __forceinline__ void ce_grad32(const CeRow& r, int x, uint32_t* ra) {
+  const uint64_t down = pair_of(-r.lse, -r.lse), log2e = pair_of(kCeLog2e, kCeLog2e), add = pair_of(r.add, r.add);
 #pragma unroll
   for (int j = 0; j < 32; j += 2) {
     const uint64_t l = pair_of(__uint_as_float(ra[j]), __uint_as_float(ra[j + 1]));
     float a, b;
-    split_pair(fma2(add2(l, down), log2e, ls), a, b);
+    split_pair(fma2(add2(l, down), log2e, add), a, b);
     ra[j] = __float_as_uint(ex2(a));
     ra[j + 1] = __float_as_uint(ex2(b));
   }
@@ -322,12 +322,19 @@ __device__ __forceinline__ void ce_grad32(const TcParams& p, const CeRow& r, int
   if (__any_sync(0xFFFFFFFFu, r.t >= 0 && tj < 32u)) {
 #pragma unroll
     for (int j = 0; j < 32; ++j)
-      if (r.t >= 0 && tj == j)
-        ra[j] = __float_as_uint(__uint_as_float(ra[j]) - fabsf(p.ce.scale));
+      if (r.t >= 0 && tj == j) ra[j] = __float_as_uint(__uint_as_float(ra[j]) - 1.0f);
   }
-  if (p.ce.scale < 0.0f) {
+}
+
+// EPI_SCALE: 32 accumulator values times the scale, after which they are stored as EPI_STORE does
+__device__ __forceinline__ void scale32(const TcParams& p, uint32_t* ra) {
+  const uint64_t by = pair_of(p.ce.scale, p.ce.scale);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) ra[j] ^= 0x80000000u;
+  for (int j = 0; j < 32; j += 2) {
+    float a, b;
+    split_pair(mul2(pair_of(__uint_as_float(ra[j]), __uint_as_float(ra[j + 1])), by), a, b);
+    ra[j] = __float_as_uint(a);
+    ra[j + 1] = __float_as_uint(b);
   }
 }
 
@@ -344,7 +351,7 @@ __device__ __forceinline__ void epi8(const TcParams& p, int g, int64_t row, int6
     if (preloaded) unpack8(pre, dst);
     else ld8(base, idx, dst);
   };
-  if constexpr (EPI == EPI_STORE) {
+  if constexpr (EPI == EPI_STORE || EPI == EPI_SCALE) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = a[i];
     if (p.in0) {
@@ -453,7 +460,7 @@ __device__ __forceinline__ void epi16(const TcParams& p, int g, int64_t row, int
   const int64_t idx = row * p.ldo + col;
   const bool wide = p.st32 != 0;
   float v[16], w[16];
-  if constexpr (EPI == EPI_STORE) {
+  if constexpr (EPI == EPI_STORE || EPI == EPI_SCALE) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) v[i] = a[i];
     if (p.in0) {
@@ -598,7 +605,7 @@ __device__ __forceinline__ void epi_chunk_tma(const TcParams& p, EpiStager& st, 
                                               const uint4* pin0, const uint4* pin1, bool has0) {
   auto A = [&](int j) { return __uint_as_float(ra[j]); };
   auto B = [&](int j) { return __uint_as_float(rb[j]); };
-  if constexpr (EPI == EPI_STORE) {
+  if constexpr (EPI == EPI_STORE || EPI == EPI_SCALE) {
     auto v = [&](int j) { return has0 ? A(j) + in_at(pin0, j) : A(j); };
     if (p.out_f32) stage_f32(st, &p.tmO[0], x, y, g, p.out_acc != 0, v);
     else stage_bf16(st, &p.tmO[0], x, y, v);
@@ -891,6 +898,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(t_row + c * 32, ra);
         if (p.paired) tmem_ld32(t_row + BN / 2 + c * 32, rb);
         tmem_ld_wait();
+        if constexpr (EPI == EPI_SCALE) scale32(p, ra);
         if constexpr (EPI == EPI_LSE || EPI == EPI_DCE) {
           const int x = static_cast<int>(col_base) + c * 32;
           if (x >= p.N) break;
@@ -898,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ce_lse32(p, ce, row, x, ra);
             continue;
           } else {
-            ce_grad32(p, ce, x, ra);
+            ce_grad32(ce, x, ra);
           }
         }
         if (row < p.M) {
@@ -1403,6 +1411,7 @@ __global__ void __launch_bounds__(PairCfg<WN, EW>::THREADS, 1)
             }
           }
           tmem_ld_wait();
+          if constexpr (EPI == EPI_SCALE) scale32(p, ra);
           if constexpr (EPI == EPI_LSE || EPI == EPI_DCE) {
             const int x = static_cast<int>(col_base) + c * 32;
             if (x >= p.N) break;
@@ -1410,7 +1419,7 @@ __global__ void __launch_bounds__(PairCfg<WN, EW>::THREADS, 1)
               ce_lse32(p, ce, row, x, ra);
               continue;
             } else {
-              ce_grad32(p, ce, x, ra);
+              ce_grad32(ce, x, ra);
             }
           }
           if (p.tma_out) {
@@ -1620,6 +1629,7 @@ tp_status launch_bn(int epi, TcSet<1>& set, int grid, cudaStream_t st) {
     if (epi == EPI_LSE) return launch_bn_epi<BN, EPI_LSE, false>(set, grid, st);
     if (epi == EPI_DCE) return launch_bn_epi<BN, EPI_DCE, false>(set, grid, st);
   }
+  if (epi == EPI_SCALE) return launch_bn_epi<BN, EPI_SCALE, DEC>(set, grid, st);
   return fail(TP_ERR_INVALID_ARG, "unknown epilogue");
 }
 
@@ -1675,6 +1685,7 @@ tp_status launch_pair_wn(int epi, TcSet<1>& set, cudaStream_t st) {
     case EPI_PAIR: return launch_pair_epi<EPI_PAIR, WN>(set, st);
     case EPI_LSE: return launch_pair_epi<EPI_LSE, WN>(set, st);
     case EPI_DCE: return launch_pair_epi<EPI_DCE, WN>(set, st);
+    case EPI_SCALE: return launch_pair_epi<EPI_SCALE, WN>(set, st);
   }
   return fail(TP_ERR_INVALID_ARG, "unknown epilogue");
 }
@@ -1682,6 +1693,7 @@ tp_status launch_pair_wn(int epi, TcSet<1>& set, cudaStream_t st) {
 // epi8: eight epilogue warps beside narrow tiles, see short_sum
 tp_status launch_pair(int epi, bool wide, bool epi8, TcSet<1>& set, cudaStream_t st) {
   if (epi8 && epi == EPI_STORE) return launch_pair_epi<EPI_STORE, 1, 8>(set, st);
+  if (epi8 && epi == EPI_SCALE) return launch_pair_epi<EPI_SCALE, 1, 8>(set, st);
   if (epi8 && epi == EPI_LSE) return launch_pair_epi<EPI_LSE, 1, 8>(set, st);
   if (epi8 && epi == EPI_DCE) return launch_pair_epi<EPI_DCE, 1, 8>(set, st);
   return wide ? launch_pair_wn<2>(epi, set, st) : launch_pair_wn<1>(epi, set, st);
@@ -1721,7 +1733,8 @@ int epi_out_bytes(const GemmDesc& d) {
 // 101 / 83, 1024 75.5 / 75.8 (50176 x 1024); 8192 x 50304 with K = 512 379 / 313. The forward
 // cross-entropy, 8192 x 50304: K = 256 267 / 225, 512 282 / 288, 1024 501 / 508.
 bool short_sum(int epi, int64_t k_tile) {
-  return epi == EPI_LSE ? k_tile <= 256 : (epi == EPI_STORE || epi == EPI_DCE) && k_tile <= 512;
+  if (epi == EPI_LSE) return k_tile <= 256;
+  return (epi == EPI_STORE || epi == EPI_SCALE || epi == EPI_DCE) && k_tile <= 512;
 }
 
 namespace {
@@ -1949,12 +1962,12 @@ tp_status launch_gemm_tc_two(const GemmDesc& a, const GemmDesc& b, cudaStream_t 
     return TP_OK;
   }
   if (plan[0].pair)
-    return plan[0].epi8 ? launch_pair_epi<EPI_STORE, 1, 8, 2>(set, st)
-                        : launch_pair_epi<EPI_STORE, 1, PairCfg<1>::EPI_WARPS, 2>(set, st);
+    return plan[0].epi8 ? launch_pair_epi<EPI_SCALE, 1, 8, 2>(set, st)
+                        : launch_pair_epi<EPI_SCALE, 1, PairCfg<1>::EPI_WARPS, 2>(set, st);
   const int grid = static_cast<int>(std::min<int64_t>(tiles, device_sm_count()));
   // (a problem keeps 256-wide one-CTA tiles only if more than half the SMs have one)
-  return plan[0].BN == 128 ? launch_bn_epi<128, EPI_STORE, false, 2>(set, grid, st)
-                           : launch_bn_epi<64, EPI_STORE, false, 2>(set, grid, st);
+  return plan[0].BN == 128 ? launch_bn_epi<128, EPI_SCALE, false, 2>(set, grid, st)
+                           : launch_bn_epi<64, EPI_SCALE, false, 2>(set, grid, st);
 }
 
 }  // namespace tp

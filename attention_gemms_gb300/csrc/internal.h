@@ -153,8 +153,9 @@ enum EpiKind : int {
   EPI_DSWIGLU = 4,  // a = acc, g = in[0], u = in[1]: out[0] = dG, out[1] = dU
   EPI_PAIR = 5,     // paired: out[0] = first half, out[1] = second half
   EPI_LSE = 6,      // the row's maximum and sum of exponentials over the tile (CeEpi), no output
-  EPI_DCE = 7,      // out[0] = scale (exp(acc - lse) - [column == target]) (CeEpi)
-  EPI_COUNT = 8
+  EPI_DCE = 7,      // out[0] = exp(acc - lse) - [column == target] (CeEpi), in fp32 times its scale
+  EPI_SCALE = 8,    // bf16: out[0] = scale * acc (CeEpi's scale)
+  EPI_COUNT = 9
 };
 
 // Cross-entropy of the logits D = x E^T that a product forms and does not keep. Column n of D is
@@ -169,7 +170,7 @@ struct CeEpi {
   float* hit = nullptr;
   int32_t* counter = nullptr;
   int* slots = nullptr;
-  // EPI_DCE
+  // EPI_DCE (scale: the fp32 engine), EPI_SCALE (scale)
   const float* lse = nullptr;  // (M)
   float scale = 0.0f;
 };
@@ -203,15 +204,15 @@ struct GemmDesc {
   void* out[3] = {nullptr, nullptr, nullptr};
   const void* in[2] = {nullptr, nullptr};
   int64_t ldo = 0;     // row pitch of outputs and of in[] (elements)
-  bool out_f32 = false;  // EPI_STORE: fp32 output (partials), else the element type
-  bool out_acc = false;  // EPI_STORE with out_f32: out[0] += acc
+  bool out_f32 = false;  // EPI_STORE, EPI_SCALE: fp32 output (partials), else the element type
+  bool out_acc = false;  // EPI_STORE, EPI_SCALE with out_f32: added to out[0]
   int64_t out_group_stride = 0;
   CeEpi ce;
   tp_dtype dtype = TP_BF16;
 };
 
 tp_status launch_gemm_tc(const GemmDesc& d, cudaStream_t st);    // bf16, tcgen05
-// two independent plain products (EPI_STORE, unpaired), in one launch where they take the same tile form;
+// two independent scaled products (EPI_SCALE, unpaired), in one launch where they take the same tile form;
 // each is the same bit for bit as by itself
 tp_status launch_gemm_tc_two(const GemmDesc& a, const GemmDesc& b, cudaStream_t st);
 bool gemv_eligible(const GemmDesc& d);                             // bf16, M <= 4

@@ -2,14 +2,17 @@
 // the shared embedding E (v, h) [张量并行 notes, §损失计算层的并行化; the tied output layer of the
 // Megatron-LM 实战 04 listing, 核心实现, SmallGPT]:
 //   lse_r = log sum_c exp(l_rc),  loss_r = lse_r - l_{r, t_r}
-//   q_rc = scale (exp(l_rc - lse_r) - [c = t_r]),  dx = q E,  dE = q^T x
+//   q_rc = exp(l_rc - lse_r) - [c = t_r],  dx = scale q E,  dE = scale q^T x
 // Forward: one product whose epilogue (EPI_LSE of the GEMM engines) keeps, per row and column
 // tile, the largest logit and the sum of exponentials, and the target's logit; the tiles of all
 // vocabulary shards are then joined as the pages' two all-reduces join the shards. A logit lives in
 // the accumulator only.
 // Backward: the vocabulary goes by in pieces. Of each piece the logits are formed again and leave
 // the accumulator as q (EPI_DCE, in the element type: the operand of the next two products), which
-// gives the piece's rows of dE and its share of dx. One piece's q is all that is kept.
+// gives the piece's rows of dE and its share of dx. One piece's q is all that is kept. In bf16 q is
+// rounded without the scale, which the products' sums get in 32 bits: rounded with it, a scale that
+// is no power of two shifts every target's term alike (1/1003 by 2.4e-3; 1003 rows 2.9e-3 off in the
+// 2-norm where a rounded perfect result is 1.7e-3, and 1.7e-3 this way).
 // The products bound both: 2 M v h operations forward, 6 backward. bf16, 8192 rows, v = 50304: h = 2048
 // 0.96 ms (1756 TFLOP/s, the rate that a library product sustains under the power cap) and 3.1 ms (1630),
 // h = 4096 backward 5.98 ms (1694). The exponentials hide: 6 % of their pipe, 17 % of the issue slots,
@@ -180,7 +183,7 @@ __device__ __forceinline__ void transpose_quad(uint32_t (&p)[4], int t) {
 __global__ void __launch_bounds__(256, 2)
     vocab_outer_kernel(const __nv_bfloat16* __restrict__ q, const __nv_bfloat16* __restrict__ x,
                        __nv_bfloat16* __restrict__ dE, int M, int64_t n, int64_t h, int64_t ldq,
-                       int col_blocks) {
+                       int col_blocks, float scale) {
   extern __shared__ __align__(16) uint8_t outer_smem[];
   __nv_bfloat16* xs = reinterpret_cast<__nv_bfloat16*>(outer_smem);
   __nv_bfloat16* qs = xs + kOuterRows * kXPitch;  // two stages
@@ -246,7 +249,8 @@ __global__ void __launch_bounds__(256, 2)
       for (int hf = 0; hf < 2; ++hf) {
         uint32_t p[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = pack_bf16x2(acc[j + i][2 * hf], acc[j + i][2 * hf + 1]);
+        for (int i = 0; i < 4; ++i)
+          p[i] = pack_bf16x2(acc[j + i][2 * hf] * scale, acc[j + i][2 * hf + 1] * scale);
         transpose_quad(p, t);
         if (c + 8 * hf < n && col < h)
           *reinterpret_cast<uint4*>(dE + (c + 8 * hf) * h + col) = make_uint4(p[0], p[1], p[2], p[3]);
@@ -356,7 +360,7 @@ void split_sum(GemmDesc& d, int parts) {
 }
 
 tp_status launch_outer(const void* q, const void* x, void* dE, int64_t M, int64_t n, int64_t h,
-                       int64_t ldq, cudaStream_t st) {
+                       int64_t ldq, float scale, cudaStream_t st) {
   static std::atomic<uint64_t> attr_set{0};
   if (needs_setup(attr_set)) {
     TP_CUDA_TRY(cudaFuncSetAttribute(vocab_outer_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -368,7 +372,8 @@ tp_status launch_outer(const void* q, const void* x, void* dE, int64_t M, int64_
   // plain stream order: two CTAs fill an SM's registers, which leaves no room beside a GEMM's
   vocab_outer_kernel<<<static_cast<unsigned>(blocks * walkers), 256, kOuterSmem, st>>>(
       static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(x),
-      static_cast<__nv_bfloat16*>(dE), static_cast<int>(M), n, h, ldq, static_cast<int>(blocks));
+      static_cast<__nv_bfloat16*>(dE), static_cast<int>(M), n, h, ldq, static_cast<int>(blocks),
+      scale);
   TP_CUDA_TRY(cudaGetLastError());
   count_launch();
   return TP_OK;
@@ -467,7 +472,8 @@ tp_status launch_vocab_linear_ce_bwd(const void* x, const void* E, const int32_t
     gx.B[0] = {Ei, n, h, h};
     gx.b_mn = true;
     gx.ldo = h;
-    gx.epi = EPI_STORE;
+    gx.epi = dt == TP_BF16 ? EPI_SCALE : EPI_STORE;
+    gx.ce.scale = scale;
     gx.out[0] = P.x_direct || !dx ? dx : xs;
     gx.out_f32 = dt == TP_F32 || !P.x_direct;
     gx.out_acc = i > 0;
@@ -483,7 +489,8 @@ tp_status launch_vocab_linear_ce_bwd(const void* x, const void* E, const int32_t
     ge.B[0] = {x, M, h, h};
     ge.b_mn = true;
     ge.ldo = h;
-    ge.epi = EPI_STORE;
+    ge.epi = gx.epi;
+    ge.ce.scale = scale;
     ge.out[0] = P.e_parts > 1 && dE ? static_cast<void*>(es) : dEi;
     ge.out_f32 = dt == TP_F32 || P.e_parts > 1;
     split_sum(ge, P.e_parts);
@@ -493,7 +500,7 @@ tp_status launch_vocab_linear_ce_bwd(const void* x, const void* E, const int32_t
     }
     if (M <= kOuterRows && n * h >= kOuterLeast) {
       if (dx) TP_TRY(launch_gemm_tc(gx, st));
-      if (dE) TP_TRY(launch_outer(q, x, dEi, M, n, h, P.piece, st));
+      if (dE) TP_TRY(launch_outer(q, x, dEi, M, n, h, P.piece, scale, st));
       continue;
     }
     if (dx && dE) TP_TRY(launch_gemm_tc_two(gx, ge, st));

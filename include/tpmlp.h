@@ -779,13 +779,14 @@ TP_API tp_status tp_vocab_linear_ce_fwd(const void* x, const void* E, const int3
                                         int32_t N, tp_dtype dtype, void* ws, size_t ws_bytes,
                                         void* stream);
 
-/* Its gradients from the forward's lse, q = scale * (softmax(x E^T) - one_hot(targets)):
- *   dx (M, h) = q E and dE (vocab, h) = q^T x, written (either may be NULL: not wanted).
- * scale = 1/M for the mean loss. q is a row of zeros where the target lies outside [0, vocab).
+/* Its gradients from the forward's lse, q = softmax(x E^T) - one_hot(targets):
+ *   dx (M, h) = scale * q E and dE (vocab, h) = scale * q^T x, written (either may be NULL: not
+ *   wanted). scale = 1/M for the mean loss. q is a row of zeros where the target lies outside
+ *   [0, vocab).
  * The logits are formed again, a piece of the vocabulary at a time; of q one piece is kept in ws
  * (tp_vocab_linear_ce_workspace_size(0, ...) bytes: at most about 512 MiB, or 256 columns, of q,
  * and in bf16 fp32 sums where one product does not make them: dx's, or up to 512 MiB of parts),
- * rounded to the element type.
+ * rounded to the element type (in bf16 without the scale, which the fp32 sums get).
  * The fp32 sums over the vocabulary and over the rows go in a fixed order: results repeat.
  * M = 0 writes zeros to dE. Errors: as above. */
 TP_API tp_status tp_vocab_linear_ce_bwd(const void* x, const void* E, const int32_t* targets,

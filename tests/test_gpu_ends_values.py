@@ -3,6 +3,7 @@ probability, logits of any finite size."""
 import pytest
 import torch
 
+from tests import ends_ref as R
 from tests.helpers import gemm_tiles
 from tests.test_gpu_ends import BF, F32, gen, rnd, run_bwd, run_fwd, within
 
@@ -115,3 +116,24 @@ def test_gradient_of_a_certain_target_is_zero(dt):
     x, E, t, a, _ = two_levels(500, 900, 64, dt, seed=5, gap=(120.0, 130.0))
     dx, dE = run_bwd(x, E, t, a.float(), 1.0)
     assert torch.all(dx == 0) and torch.all(dE == 0)  # e^-120 is below every fp32 number
+
+
+@pytest.mark.parametrize("scale", [1.0 / 1003, -1.0 / 777, 1.0 / 300])
+@pytest.mark.parametrize("M,v,h", [(5, 5003, 1024), (40, 20000, 1024), (100, 5003, 256), (300, 4100, 256),
+                                   (1003, 5003, 256), (700, 9000, 1088), (2100, 6000, 64)])
+def test_gradients_are_not_shifted_by_the_scale(M, v, h, scale):
+    """bf16 holds these more than 1.5e-3 off. What is rounded is p - 1, here about -1: no term may bring
+    such a factor in."""
+    assert abs(torch.tensor(scale).bfloat16().item() / scale - 1) > 1.5e-3
+    g = gen(M)
+    x, E = rnd(g, M, h), rnd(g, v, h, sigma=1e-4)
+    t = torch.randint(0, v, (M,), generator=g, device="cuda").to(torch.int32)
+    lse = torch.logsumexp(x.double() @ E.double().T, 1).float()
+    dx, dE = run_bwd(x, E, t, lse, scale)
+    for got, ref, name in zip((dx, dE), R.ce_bwd(x, E, t, lse, scale), ("dx", "dE")):
+        got = got.double()
+        # p = 1/v within 2 % or so, which p - 1 may lose to its rounding; the results' roundings, up to
+        # 2^-8 each and independent: six of their standard deviations
+        tol = 1.1 / v + 6 * 2.0 ** -8 / 3 ** 0.5 * ((ref ** 4).sum().sqrt() / (ref ** 2).sum()).item()
+        shift = ((got - ref) * ref).sum() / (ref ** 2).sum()
+        assert abs(shift.item()) <= tol < 1e-3, (name, shift.item(), tol)
