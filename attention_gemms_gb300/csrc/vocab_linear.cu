@@ -220,6 +220,7 @@ __global__ void __launch_bounds__(256, 2)
     put(0, next);
   }
   __syncthreads();
+  const uint64_t by = pair_of(scale, scale);
   const int ksteps = (M + 15) / 16, c0 = warp / 2 * 16, w0 = warp % 2 * 128;
   const uint32_t xa = smem_u32(xs), qa = smem_u32(qs);
   int st = 0;
@@ -249,8 +250,11 @@ __global__ void __launch_bounds__(256, 2)
       for (int hf = 0; hf < 2; ++hf) {
         uint32_t p[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          p[i] = pack_bf16x2(acc[j + i][2 * hf] * scale, acc[j + i][2 * hf + 1] * scale);
+        for (int i = 0; i < 4; ++i) {
+          float lo, hi;
+          split_pair(mul2(pair_of(acc[j + i][2 * hf], acc[j + i][2 * hf + 1]), by), lo, hi);
+          p[i] = pack_bf16x2(lo, hi);
+        }
         transpose_quad(p, t);
         if (c + 8 * hf < n && col < h)
           *reinterpret_cast<uint4*>(dE + (c + 8 * hf) * h + col) = make_uint4(p[0], p[1], p[2], p[3]);
