@@ -1949,9 +1949,9 @@ tp_status launch_gemm_tc_two(const GemmDesc& a, const GemmDesc& b, cudaStream_t 
                      plan[0].epi8 == plan[1].epi8 && plan[0].BN == plan[1].BN && !plan[0].dec &&
                      !plan[1].dec && (plan[0].pair || plan[0].BN < 256);
   // up to a wave of one-CTA tiles or two of pair tiles, and sums of up to 1024; us of dx, dE and the
-  // logits' gradient, together and one by one: 300 x 1500 x 256 15.5 and 19.3, 1000 x 6000 x 512 41 and
-  // 44, 512 x 512 x 5120 45 and 50. More lose: one-CTA tiles that share a CTA, 1000 x 1000 x 1000 34.6
-  // and 29.8; longer sums, beside whose tiles the launch is nothing and the operands that both sets
+  // logits' gradient, together and one by one: 300 x 1500 x 256 14.4 and 18.2, 1000 x 6000 x 512 38 and
+  // 43, 512 x 512 x 5120 45 and 49. More lose: one-CTA tiles that share a CTA, 1000 x 1000 x 1000 33.9
+  // and 29.3; longer sums, beside whose tiles the launch is nothing and the operands that both sets
   // take from L2 are more, 4096 x 4096 x 2048 156 and 143, 8192 x 50304 x 2048 3370 and 3090.
   if (!alike || tiles > device_sm_count() || std::max(k_a, k_b) > 1024) {
     for (const int i : {k_a < k_b ? 1 : 0, k_a < k_b ? 0 : 1}) {  // a, then b, as they are planned

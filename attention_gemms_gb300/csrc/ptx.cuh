@@ -1,7 +1,7 @@
 // Inline-PTX wrappers for sm_103a: mbarrier, TMA (cp.async.bulk.tensor),
 // tcgen05 (TMEM alloc, MMA, commit, loads), the shared-memory / instruction
-// descriptors of tcgen05.mma, warp-level MMA and packed arithmetic. Written from the PTX ISA description of these
-// instructions.
+// descriptors of tcgen05.mma, warp-level MMA and packed arithmetic. Written from the
+// PTX ISA description of these instructions.
 #pragma once
 #include <cstdint>
 #include <cuda.h>

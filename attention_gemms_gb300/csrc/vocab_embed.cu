@@ -15,9 +15,9 @@
 //    can lie in several units, which then leave fp32 partials; the thread that leaves a column's
 //    last one adds them up, in the units' order. Rows without a token are written beside.
 // HBM bounds the sum, latency the sort, which moves next to nothing. bf16, ids whose frequency falls
-// as 1 / (id + 1): 8192 tokens of 50304 x 2048 45 us (5.3 TB/s, 80 % of a copy's rate; the sort some 6
-// of it), 65536 of 50257 x 4096 167 us (5.7 TB/s). The same with contiguous ranges of rows for the
-// sorting CTAs, empty rows written by the sort, and a launch of its own for the partials: 54 and 251.
+// as 1 / (id + 1): 8192 tokens of 50304 x 2048 47.5 us (5.0 TB/s, 75 % of a copy's rate; the sort some 6
+// of it), 65536 of 50257 x 4096 169 us (5.6 TB/s). With contiguous ranges of rows for the sorting CTAs,
+// empty rows written by the sort, and a launch of its own for the partials: 54 and 251.
 // The lookup: 8192 rows of 4096 16 us (95 MB that it cannot do without, 5.8 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
