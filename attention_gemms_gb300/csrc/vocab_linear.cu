@@ -11,8 +11,8 @@
 // the accumulator as q (EPI_DCE, in the element type: the operand of the next two products), which
 // gives the piece's rows of dE and its share of dx. One piece's q is all that is kept. In bf16 q is
 // rounded without the scale, which the products' sums get in 32 bits: rounded with it, a scale that
-// is no power of two shifts every target's term alike (1/1003 by 2.4e-3; 1003 rows 2.9e-3 off in the
-// 2-norm where a rounded perfect result is 1.7e-3, and 1.7e-3 this way).
+// is no power of two shifts every target's term alike (1/1003 by 2.4e-3; dx of 1003 rows was 2.9e-3 off
+// in the 2-norm, and is 1.9e-3 this way, a rounded perfect result 1.7e-3).
 // The products bound both: 2 M v h operations forward, 6 backward. bf16, 8192 rows, v = 50304: h = 2048
 // 0.96 ms (1756 TFLOP/s, the rate that a library product sustains under the power cap) and 3.1 ms (1630),
 // h = 4096 backward 5.98 ms (1694). The exponentials hide: 6 % of their pipe, 17 % of the issue slots,
