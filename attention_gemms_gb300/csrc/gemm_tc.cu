@@ -309,7 +309,8 @@ __device__ __forceinline__ void ce_lse32(const TcParams& p, CeRow& r, int64_t ro
 // softmax - one_hot of 32 logits in their place: a subtraction and a fused multiply-add for two, and one
 // power each. Zeros in a row without a target.
 __device__ __forceinline__ void ce_grad32(const CeRow& r, int x, uint32_t* ra) {
-  const uint64_t down = pair_of(-r.lse, -r.lse), log2e = pair_of(kCeLog2e, kCeLog2e), add = pair_of(r.add, r.add);
+  const uint64_t down = pair_of(-r.lse, -r.lse), log2e = pair_of(kCeLog2e, kCeLog2e);
+  const uint64_t add = pair_of(r.add, r.add);
 #pragma unroll
   for (int j = 0; j < 32; j += 2) {
     const uint64_t l = pair_of(__uint_as_float(ra[j]), __uint_as_float(ra[j + 1]));

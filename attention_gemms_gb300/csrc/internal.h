@@ -165,7 +165,8 @@ struct CeEpi {
   const int32_t* targets = nullptr;  // (M)
   int64_t vocab = 0, col0 = 0;
   // EPI_LSE: part[slot * M + row] = (m, s) of the tiles' columns: m the largest logit, s the sum of
-  // exp(logit - m); *slots (host) is set to their number, one for every 64 columns or more. hit[row] = the target's logit. *counter is zeroed.
+  // exp(logit - m); *slots (host) is set to their number, one for every 64 columns or more.
+  // hit[row] = the target's logit. *counter is zeroed.
   float2* part = nullptr;
   float* hit = nullptr;
   int32_t* counter = nullptr;
